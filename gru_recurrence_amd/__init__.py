@@ -29,7 +29,11 @@ EXPORTS = ("rnn_status_str", "rnn_workspace_size", "rnn_plan_describe", "rnn_inp
            "rnn_rec_lstm", "rnn_rec_lstm_noalloc", "rnn_rec_gru", "rnn_fwd_lstm", "rnn_fwd_gru", "rnn_bwd_lstm",
            "rnn_bwd_gru", "rnn_workspace_size_stack", "rnn_fwd_lstm_stack", "rnn_fwd_gru_stack",
            "rnn_workspace_size_chunked", "rnn_fwd_lstm_chunked", "rnn_fwd_gru_chunked",
-           "rnn_bwd_lstm_ckpt", "rnn_bwd_gru_ckpt", "rnn_plan_search", "rnn_workspace_status")
+           "rnn_bwd_lstm_ckpt", "rnn_bwd_gru_ckpt", "rnn_plan_search", "rnn_workspace_status",
+           "rnn_embed_fwd", "rnn_workspace_size_embed_bwd", "rnn_embed_bwd",
+           "rnn_workspace_size_logprobs", "rnn_token_logprobs", "rnn_token_logprobs_bwd",
+           "rnn_workspace_size_linattn", "rnn_linattn_fwd", "rnn_linattn_step",
+           "rnn_linattn_bwd")
 
 
 class Dims(ctypes.Structure):
@@ -654,3 +658,17 @@ def gru_bwd_ckpt(x, W, R, b, h0, h_ckpt, dh_seq, dhT=None, *, chunk: int, ws=Non
 def workspace_status(ws, stream=None) -> int:
     """Synchronise and report a recorded step-wait timeout (RNN_OK if none)."""
     return int(load().rnn_workspace_status(_ptr(ws, "ws"), ws.numel(), _stream(stream)))
+
+
+# The operators around the recurrence (lm.py) need torch at import; they are
+# loaded with their first use.
+_LM = ("embed_fwd", "embed_bwd", "token_logprobs", "token_logprobs_bwd", "linattn_fwd",
+       "linattn_step", "linattn_bwd", "LinDims", "workspace_size_embed_bwd",
+       "workspace_size_logprobs", "workspace_size_linattn", "OP_LIN_FWD", "OP_LIN_BWD")
+
+
+def __getattr__(name):
+    if name in _LM:
+        from . import lm
+        return getattr(lm, name)
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -1,0 +1,736 @@
+// linattn.hip -- linear attention with a decay for each head.
+//
+// For each batch row and head, with a = e^g and a matrix state S [Dk][Dv]:
+//   S_t = a S_{t-1} + k_t^T v_t,     o_t = scale q_t S_t        (t = 0..T-1)
+// and backward, with G_t = dL/dS_t:
+//   dq_t = scale S_t do_t,  G_t = scale q_t^T do_t + a G_{t+1}  (+ dS_T at T-1)
+//   dk_t = G_t v_t,  dv_t = G_t^T k_t,  dS_0 = a G_0
+//
+// One kernel serves all of these.  It computes, over rows r in walking order,
+//   o_r = os ( is sum_{j<=r} a^(r-j) (x_r . y_j) z_j + a^r x_r X )
+// with a carried matrix X ("the state already decayed for the next row") and
+//   X <- a^n X + is sum_j a^(n-j) y_j^T z_j    over n rows:
+//   forward  x,y,z = q,k,v     X = a S_0           is = 1, os = scale
+//   dq       x,y,z = do,v,k    X = a S_0^T         is = 1, os = scale
+//   dk       x,y,z = v,do,q    X = dS_T^T          is = scale, os = 1, backwards in t
+//   dv       x,y,z = k,q,do    X = dS_T            is = scale, os = 1, backwards in t
+// (the final X of dv is dS_0; the forward's S_T takes one decay less).
+//
+// Rows are taken in chunks of C.  Inside a chunk the masked, decayed product
+// P = (x y^T) o a^(r-j) is formed and applied to z; the rest goes through X.
+// Exponents are never negative, so no decay overflows, a = 0 included.
+//
+// Layout: a workgroup of four waves owns (batch row, head, 64 columns of z, a
+// segment of the rows); wave w owns 16 columns and the whole X for them.  In
+// the 16x16 matrix instructions a lane holds, for its column, four
+// consecutive rows of a result; with the operand's depth numbered so that a
+// lane's eight depth elements are rows 4g..4g+3 of two neighbouring 16-row
+// tiles (g = lane / 16), a result is an operand as it stands: P and X never
+// leave the registers.  y and z are needed along their rows too: LDS is read
+// through the transposing 16-bit loads of gfx950.
+//
+// Arithmetic: x, y, z as given (bf16 or float32), all sums float32.  P, X and
+// the decayed z are operands of further products; in bf16 calls each is split
+// into a bf16 and the bf16 of what that leaves (about 17 bits together), so
+// results carry one rounding, the output's.  float32 calls use the float32
+// matrix instructions.
+//
+// Few (batch row, head) pairs leave the chip empty, so the rows are cut into
+// segments: a first launch forms each segment's own X from nothing, a second
+// carries X across segments, and the main launch runs all segments at once.
+#include <algorithm>
+#include <mutex>
+
+#include "lm.h"
+
+namespace rnn355 {
+namespace lm {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kCols = 64;    // columns of z of one workgroup
+
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// One product with the sequences' heads, operands, ranges and scales.
+struct Role {
+    LinSeq x, y, z;
+    int gx, gy, gz;         // heads that share one of the operand's (head h uses h / g)
+    int Da, Db;             // depth of x.y, columns of z
+    const float *init;      // X before the first row, [B][NH][Dk][Dv], or null
+    int init_t;             // read it transposed
+    int init_decay;         // times a
+    float *fin;             // final state, [B][NH][Da][Db], or null
+    int fin_less;           // with one decay less (the forward's S_T)
+    int rev;                // rows run backwards in t
+    float is, os;
+    void *o;                // [T][B][NH][Db]
+    int o_f32;              // float32 whatever the call's type (partial sums of shared heads)
+    float *part;            // carried X of the segments, in fragment order
+};
+struct LinArgs {
+    Role role[3];
+    int nroles, T, B, NH;
+    const float *g;
+    int nseg, seg_rows, slices;  // segments of seg_rows rows; slices of kCols columns
+};
+
+// ---- element types
+template <typename T>
+struct Frag;  // eight depth elements of a lane
+template <>
+struct Frag<uint16_t> { bf16x8 v; };
+template <>
+struct Frag<float> { float v[8]; };
+
+// d += A B over a depth of 32
+__device__ __forceinline__ void mma(f32x4 &d, const Frag<uint16_t> &a, const Frag<uint16_t> &b) {
+    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, d, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(f32x4 &d, const Frag<float> &a, const Frag<float> &b) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        d = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], d, 0, 0, 0);
+}
+
+// A float32 operand: as it is, or as a bf16 and the rest's bf16.
+template <typename T>
+struct Wide;
+template <>
+struct Wide<float> {
+    Frag<float> f;
+    __device__ void set(const float *x) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f.v[e] = x[e];
+    }
+};
+template <>
+struct Wide<uint16_t> {
+    Frag<uint16_t> hi, lo;
+    __device__ void set(const float *x) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const __bf16 h = (__bf16)x[e];
+            hi.v[e] = h;
+            lo.v[e] = (__bf16)(x[e] - (float)h);
+        }
+    }
+};
+__device__ __forceinline__ void mma(f32x4 &d, const Frag<float> &a, const Wide<float> &b) { mma(d, a, b.f); }
+__device__ __forceinline__ void mma(f32x4 &d, const Wide<float> &a, const Frag<float> &b) { mma(d, a.f, b); }
+__device__ __forceinline__ void mma(f32x4 &d, const Frag<uint16_t> &a, const Wide<uint16_t> &b) {
+    mma(d, a, b.hi);
+    mma(d, a, b.lo);
+}
+__device__ __forceinline__ void mma(f32x4 &d, const Wide<uint16_t> &a, const Frag<uint16_t> &b) {
+    mma(d, a.hi, b);
+    mma(d, a.lo, b);
+}
+
+// Depth elements of row `row`, depths [32 kb, 32 kb + 32), from a row-major
+// LDS tile.
+__device__ __forceinline__ void along(Frag<uint16_t> &f, const uint16_t *t, int ld, int row, int kb, int g) {
+    const uint2 a = *(const uint2 *)(t + row * ld + kb * 32 + 4 * g);
+    const uint2 b = *(const uint2 *)(t + row * ld + kb * 32 + 16 + 4 * g);
+    const uint4 w = make_uint4(a.x, a.y, b.x, b.y);
+    f.v = __builtin_bit_cast(bf16x8, w);
+}
+__device__ __forceinline__ void along(Frag<float> &f, const float *t, int ld, int row, int kb, int g) {
+    const float4 a = *(const float4 *)(t + row * ld + kb * 32 + 4 * g);
+    const float4 b = *(const float4 *)(t + row * ld + kb * 32 + 16 + 4 * g);
+    f.v[0] = a.x; f.v[1] = a.y; f.v[2] = a.z; f.v[3] = a.w;
+    f.v[4] = b.x; f.v[5] = b.y; f.v[6] = b.z; f.v[7] = b.w;
+}
+// Depth runs over the tile's rows [32 kb, 32 kb + 32) at column col0 + lane % 16.
+__device__ __forceinline__ void across(Frag<uint16_t> &f, const uint16_t *t, int ld, int col0, int kb,
+                                       int g, int c) {
+    // each 16 lanes: four rows of 16 columns in, four rows of one column out
+    const uint16_t *p = t + (kb * 32 + 4 * g + (c >> 2)) * ld + col0 + 4 * (c & 3);
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * ld));
+    const __attribute__((ext_vector_type(8))) short w = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    f.v = __builtin_bit_cast(bf16x8, w);
+}
+__device__ __forceinline__ void across(Frag<float> &f, const float *t, int ld, int col0, int kb, int g,
+                                       int c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f.v[e] = t[(kb * 32 + (e >> 2) * 16 + 4 * g + (e & 3)) * ld + col0 + c];
+}
+__device__ __forceinline__ void unpack(float *x, const Frag<uint16_t> &f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = (float)f.v[e];
+}
+__device__ __forceinline__ void unpack(float *x, const Frag<float> &f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = f.v[e];
+}
+
+// A [C][W] tile of a sequence operand on its way from memory to LDS: each
+// thread holds R pieces of 16 bytes.
+template <typename T, int C, int W>
+struct Tile {
+    static constexpr int N = 16 / sizeof(T), PR = W / N, R = C * PR / kThreads;
+    static_assert(C * PR % kThreads == 0, "whole pieces per thread");
+    Unit<T, N> r[R];
+    // rows row0.. of n (walking order, t = rev ? T-1-row : row), columns [0, D) of `src`
+    __device__ void fetch(const T *src, int64_t st, int T_, int rev, int row0, int n, int D, bool vec) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int q = i * kThreads + threadIdx.x, row = q / PR, c = (q % PR) * N;
+            const int at = row0 + row;
+            const T *p = src + (int64_t)(rev ? T_ - 1 - at : at) * st + c;
+            if (row < n && vec && c + N <= D) {
+                r[i] = *(const Unit<T, N> *)p;
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    r[i].v[e] = row < n && c + e < D ? p[e] : from_f32<T>(0.0f);
+            }
+        }
+    }
+    __device__ void put(T *t, int ld) const {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int q = i * kThreads + threadIdx.x;
+            *(Unit<T, N> *)(t + (q / PR) * ld + (q % PR) * N) = r[i];
+        }
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ bool rows_aligned(const T *p, int64_t st, int D) {
+    constexpr int N = 16 / sizeof(T);
+    return ((uintptr_t)p & 15) == 0 && st % N == 0 && D % N == 0;
+}
+
+template <typename T>
+struct Shape;
+template <>
+struct Shape<uint16_t> { static constexpr int C = 64, pad = 16; };
+template <>
+struct Shape<float> { static constexpr int C = 32, pad = 8; };
+
+template <typename T, int DA>
+constexpr size_t lds_bytes() {
+    return sizeof(T) * Shape<T>::C * (2 * (DA + Shape<T>::pad) + kCols + Shape<T>::pad);
+}
+
+// Fragment order of one workgroup's X: [wave][DA/16 tiles][lane][4].
+template <int DA>
+__device__ __forceinline__ int64_t part_at(const LinArgs &a, int bh, int slice, int seg, int tile) {
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t wg = ((int64_t)bh * a.slices + slice) * a.nseg + seg;
+    return (((wg * 4 + w) * (DA / 16) + tile) * 64 + lane) * 4;
+}
+
+// STATE: only the segment's own X, from nothing, into its slot of `part`.
+template <typename T, int DA, bool STATE>
+__global__ __launch_bounds__(kThreads) void lin_kernel(LinArgs a) {
+    constexpr int C = Shape<T>::C, PAD = Shape<T>::pad, LD = DA + PAD, LDZ = kCols + PAD;
+    constexpr int KB = DA / 32, RB = C / 32, RT = C / 16;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    T *xs = (T *)smem, *ys = xs + (STATE ? 0 : C * LD), *zs = ys + C * LD;
+
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, c = lane & 15;
+    // slices of one (role, row, head, segment) go to the same XCD (workgroups
+    // go round the eight of them), where they share x and y in its L2
+    const int nsegs = STATE ? a.nseg - 1 : a.nseg;
+    const int groups = a.nroles * a.B * a.NH * nsegs;
+    const int slice = (blockIdx.x >> 3) % a.slices;
+    const int grp = ((blockIdx.x >> 3) / a.slices) * 8 + (blockIdx.x & 7);
+    if (grp >= groups) return;
+    const int seg = grp % nsegs, rest = grp / nsegs;
+    const int bh = rest % (a.B * a.NH);
+    const Role &R = a.role[rest / (a.B * a.NH)];
+    const int b = bh / a.NH, h = bh % a.NH;
+    const int col0 = slice * kCols;
+    if (col0 >= R.Db) return;
+    const int nc = min(R.Db - col0, kCols);
+
+    const T *x = (const T *)R.x.p + (int64_t)b * R.x.sb + (int64_t)(h / R.gx) * R.Da;
+    const T *y = (const T *)R.y.p + (int64_t)b * R.y.sb + (int64_t)(h / R.gy) * R.Da;
+    const T *z = (const T *)R.z.p + (int64_t)b * R.z.sb + (int64_t)(h / R.gz) * R.Db + col0;
+    const bool vx = !STATE && rows_aligned(x, R.x.st, R.Da), vy = rows_aligned(y, R.y.st, R.Da);
+    const bool vz = rows_aligned(z, R.z.st, R.Db);
+
+    // log2 of the decay; kept finite so that 0 times it is 0 (a = 0)
+    const float g2 = fmaxf(a.g[h] * kLog2e, -1e30f);
+    auto power = [&](int n) { return __builtin_amdgcn_exp2f(g2 * (float)n); };
+
+    const int row_lo = seg * a.seg_rows, row_hi = min(row_lo + a.seg_rows, a.T);
+
+    f32x4 X[DA / 16];
+    // element r of tile t: depth 16 t + 4 g + r, column 16 w + c
+    const int col = col0 + 16 * w + c;
+    const bool wave_on = 16 * w < nc;
+#pragma unroll
+    for (int t = 0; t < DA / 16; ++t) X[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (!STATE) {
+        if (seg > 0) {
+#pragma unroll
+            for (int t = 0; t < DA / 16; ++t)
+                X[t] = *(const f32x4 *)(R.part + part_at<DA>(a, bh, slice, seg, t));
+        }
+        if (R.init) {
+            const float f = power(row_lo + (R.init_decay ? 1 : 0));
+            const float *S = R.init + (int64_t)bh * R.Da * R.Db;
+#pragma unroll
+            for (int t = 0; t < DA / 16; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int d = 16 * t + 4 * g + r;
+                    if (d < R.Da && col < R.Db)
+                        X[t][r] += f * (R.init_t ? S[(int64_t)col * R.Da + d] : S[(int64_t)d * R.Db + col]);
+                }
+        }
+    }
+
+    Tile<T, C, DA> tx, ty;
+    Tile<T, C, kCols> tz;
+    auto fetch = [&](int row0) {
+        const int n = min(C, row_hi - row0);
+        if constexpr (!STATE) tx.fetch(x, R.x.st, a.T, R.rev, row0, n, R.Da, vx);
+        ty.fetch(y, R.y.st, a.T, R.rev, row0, n, R.Da, vy);
+        tz.fetch(z, R.z.st, a.T, R.rev, row0, n, nc, vz);
+    };
+    fetch(row_lo);
+    for (int row0 = row_lo; row0 < row_hi; row0 += C) {
+        const int n = min(C, row_hi - row0);
+        __syncthreads();
+        if constexpr (!STATE) tx.put(xs, LD);
+        ty.put(ys, LD);
+        tz.put(zs, LDZ);
+        __syncthreads();
+        if (row0 + C < row_hi) fetch(row0 + C);
+        if (!wave_on) continue;
+
+        // this wave's columns of z, depth along the chunk's rows
+        Frag<T> zf[RB];
+#pragma unroll
+        for (int kb = 0; kb < RB; ++kb) across(zf[kb], zs, LDZ, 16 * w, kb, g, c);
+
+        if constexpr (!STATE) {
+            Wide<T> Xw[KB];
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                float e[8];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) e[r] = X[2 * kb][r], e[4 + r] = X[2 * kb + 1][r];
+                Xw[kb].set(e);
+            }
+#pragma unroll
+            for (int it = 0; it < RT; ++it) {
+                if (it * 16 >= n) break;
+                Frag<T> xf[KB];
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) along(xf[kb], xs, LD, it * 16 + c, kb, g);
+                // o^T tile: rows are z's columns, columns are the chunk's rows
+                f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) mma(o, Xw[kb], xf[kb]);
+                const float f = power(it * 16 + c);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[r] *= f;
+                // P^T tiles, two at a time: one operand of depth 32
+#pragma unroll
+                for (int jb = 0; jb <= it / 2; ++jb) {
+                    float pe[8];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int jt = 2 * jb + half;
+                        f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
+                        if (jt <= it) {
+#pragma unroll
+                            for (int kb = 0; kb < KB; ++kb) {
+                                Frag<T> yf;
+                                along(yf, ys, LD, jt * 16 + c, kb, g);
+                                mma(p, yf, xf[kb]);
+                            }
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int lag = (it - jt) * 16 + c - 4 * g - r;
+                            pe[4 * half + r] = lag >= 0 ? p[r] * (R.is * power(max(lag, 0))) : 0.0f;
+                        }
+                    }
+                    Wide<T> pw;
+                    pw.set(pe);
+                    mma(o, zf[jb], pw);
+                }
+                // lane: row it*16 + c, z columns 16 w + 4 g ..+3
+                const int row = row0 + it * 16 + c;
+                if (it * 16 + c < n) {
+                    const int64_t at = (((int64_t)(R.rev ? a.T - 1 - row : row) * a.B + b) * a.NH + h) * R.Db +
+                                       col0 + 16 * w + 4 * g;
+                    const int left = nc - 16 * w - 4 * g;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        if (r >= left) break;
+                        if (R.o_f32)
+                            ((float *)R.o)[at + r] = o[r] * R.os;
+                        else
+                            ((T *)R.o)[at + r] = from_f32<T>(o[r] * R.os);
+                    }
+                }
+            }
+        }
+        // X <- a^n X + y^T (decayed z); the forward's final state takes one decay less
+        const bool last = row0 + C >= a.T;
+        if (STATE || row0 + C < row_hi || (last && R.fin)) {
+            const int m = n - (last && R.fin_less ? 1 : 0);
+            const float f = power(m);
+#pragma unroll
+            for (int t = 0; t < DA / 16; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) X[t][r] *= f;
+#pragma unroll
+            for (int kb = 0; kb < RB; ++kb) {
+                float e[8];
+                unpack(e, zf[kb]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int j = kb * 32 + (i >> 2) * 16 + 4 * g + (i & 3);
+                    e[i] *= R.is * power(max(m - j, 0));  // rows past n are zero in z
+                }
+                Wide<T> zw;
+                zw.set(e);
+#pragma unroll
+                for (int t = 0; t < DA / 16; ++t) {
+                    Frag<T> yf;
+                    across(yf, ys, LD, 16 * t, kb, g, c);
+                    mma(X[t], yf, zw);
+                }
+            }
+        }
+    }
+    if constexpr (STATE) {
+        // this segment's own X, in the slot of the segment it is carried into
+#pragma unroll
+        for (int t = 0; t < DA / 16; ++t)
+            *(f32x4 *)(R.part + part_at<DA>(a, bh, slice, seg + 1, t)) = X[t];
+    } else if (R.fin && seg == a.nseg - 1 && wave_on) {
+        float *S = R.fin + (int64_t)bh * R.Da * R.Db;
+#pragma unroll
+        for (int t = 0; t < DA / 16; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int d = 16 * t + 4 * g + r;
+                if (d < R.Da && col < R.Db) S[(int64_t)d * R.Db + col] = X[t][r];
+            }
+    }
+}
+
+// Carries X across segments in place: slot s holds segment s-1's own X and
+// gets sum_{s' < s} a^(L (s-1-s')) of them, L rows to a segment.
+template <int DA>
+__global__ __launch_bounds__(256) void lin_carry_kernel(LinArgs a) {
+    constexpr int E = DA * kCols;  // values of one workgroup's X
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t per = (int64_t)a.B * a.NH * a.slices * (E / 4);
+    if (i >= per * a.nroles) return;
+    const Role &R = a.role[i / per];
+    const int64_t j = i % per, wg = j / (E / 4);
+    const int h = (int)(wg / a.slices % a.NH);
+    const float f = __builtin_amdgcn_exp2f(fmaxf(a.g[h] * kLog2e, -1e30f) * (float)a.seg_rows);
+    f32x4 *p = (f32x4 *)R.part + wg * a.nseg * (E / 4) + j % (E / 4);
+    f32x4 X{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 1; s < a.nseg; ++s) {
+        f32x4 &q = p[(int64_t)s * (E / 4)];
+        const f32x4 own = q;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) X[r] = f * X[r] + own[r];
+        q = X;
+    }
+}
+
+// Gradients of a shared head: the sum over its `grp` heads, in order.
+template <typename T>
+__global__ __launch_bounds__(256) void lin_share_kernel(const float *__restrict__ in, T *__restrict__ out,
+                                                        int64_t n, int grp, int D) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const int64_t head = i / D;
+    const float *p = in + head * grp * D + i % D;
+    float s = 0.0f;
+    for (int j = 0; j < grp; ++j) s += p[(int64_t)j * D];
+    out[i] = from_f32<T>(s);
+}
+
+// One token: S' = a S + k^T v, o = scale q S'.  A workgroup owns 64 columns of
+// a (row, head)'s state, 16 lanes of 4 columns by 16 groups of rows.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(256) void lin_step_kernel(LinDims d, LinSeq q, LinSeq k, LinSeq v,
+                                                       const float *g, float scale, const float *S0,
+                                                       T *o, float *S1, int slices) {
+    __shared__ float sum[16][kCols];
+    const int bh = blockIdx.x / slices, col0 = (blockIdx.x % slices) * kCols;
+    const int b = bh / d.NH, h = bh % d.NH, hk = h / (d.NH / d.NKV);
+    const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4;
+    const T *qp = (const T *)q.p + (int64_t)b * q.sb + (int64_t)h * d.Dk;
+    const T *kp = (const T *)k.p + (int64_t)b * k.sb + (int64_t)hk * d.Dk;
+    const T *vp = (const T *)v.p + (int64_t)b * v.sb + (int64_t)hk * d.Dv;
+    const float a = exp_fast(g[h]);
+    const int c = col0 + 4 * lane, n = min(d.Dv - c, 4);
+    float vv[4], acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) vv[e] = e < n ? to_f32<T>(vp[c + e]) : 0.0f;
+    const int64_t base = (int64_t)bh * d.Dk * d.Dv + c;
+#pragma unroll 4
+    for (int r = grp; r < d.Dk; r += 16) {
+        const float kk = to_f32<T>(kp[r]), qq = to_f32<T>(qp[r]);
+        const int64_t at = base + (int64_t)r * d.Dv;
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (S0) {
+            if constexpr (VEC) {
+                if (n > 0) {
+                    const float4 w = *(const float4 *)(S0 + at);
+                    s[0] = w.x; s[1] = w.y; s[2] = w.z; s[3] = w.w;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < n) s[e] = S0[at + e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s[e] = a * s[e] + kk * vv[e];
+            acc[e] += qq * s[e];
+        }
+        if (S1) {
+            if constexpr (VEC) {
+                if (n > 0) *(float4 *)(S1 + at) = make_float4(s[0], s[1], s[2], s[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < n) S1[at + e] = s[e];
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[grp][4 * lane + e] = acc[e];
+    __syncthreads();
+    if (threadIdx.x < kCols && col0 + (int)threadIdx.x < d.Dv) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s += sum[i][threadIdx.x];
+        o[((int64_t)b * d.NH + h) * d.Dv + col0 + threadIdx.x] = from_f32<T>(s * scale);
+    }
+}
+
+// ------------------------------------------------------------------- host
+size_t up(size_t v) { return (v + 255) & ~(size_t)255; }
+int pad_depth(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+int slices_of(int Db) { return (Db + kCols - 1) / kCols; }
+
+// Segments: enough workgroups for the chip's 256 CUs several times over, at
+// least two chunks to a segment (each costs a pass over y and z and a state).
+struct Cut {
+    int nseg, rows;
+};
+Cut cut(int T, int C, long wgs) {
+    const int chunks = (T + C - 1) / C;
+    long want = std::max(1L, 1024 / std::max(1L, wgs));
+    want = std::min(want, (long)std::max(1, chunks / 2));
+    const int per = (int)((chunks + want - 1) / want);
+    return {(chunks + per - 1) / per, per * C};
+}
+
+size_t part_bytes(const LinDims &d, int DA, int slices, int nseg) {
+    return nseg > 1 ? up(sizeof(float) * (size_t)d.B * d.NH * slices * nseg * DA * kCols) : 0;
+}
+
+template <typename T, int DA, bool STATE>
+hipError_t lin_launch(const LinArgs &a, hipStream_t s) {
+    constexpr size_t lds = STATE ? lds_bytes<T, DA>() - sizeof(T) * Shape<T>::C * (DA + Shape<T>::pad)
+                                 : lds_bytes<T, DA>();
+    static std::once_flag once;
+    static hipError_t attr = hipSuccess;
+    std::call_once(once, [] {
+        attr = hipFuncSetAttribute(reinterpret_cast<const void *>(&lin_kernel<T, DA, STATE>),
+                                   hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    });
+    if (attr != hipSuccess) return attr;
+    const long groups = (long)a.nroles * a.B * a.NH * (STATE ? a.nseg - 1 : a.nseg);
+    const long blocks = (groups + 7) / 8 * 8 * a.slices;
+    if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((lin_kernel<T, DA, STATE>), dim3((unsigned)blocks), dim3(kThreads), lds, s, a);
+    return hipGetLastError();
+}
+
+template <typename T, int DA>
+hipError_t lin_run(const LinArgs &a, hipStream_t s) {
+    if (a.nseg > 1) {
+        hipError_t e = lin_launch<T, DA, true>(a, s);
+        if (e != hipSuccess) return e;
+        const long n = (long)a.nroles * a.B * a.NH * a.slices * (DA * kCols / 4);
+        hipLaunchKernelGGL(lin_carry_kernel<DA>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return lin_launch<T, DA, false>(a, s);
+}
+
+template <typename T>
+hipError_t lin_run_depth(const LinArgs &a, int DA, hipStream_t s) {
+    switch (DA) {
+        case 32: return lin_run<T, 32>(a, s);
+        case 64: return lin_run<T, 64>(a, s);
+        case 128: return lin_run<T, 128>(a, s);
+        default: return lin_run<T, 256>(a, s);
+    }
+}
+
+hipError_t lin_run_any(const LinArgs &a, bool bf16, int DA, hipStream_t s) {
+    return bf16 ? lin_run_depth<uint16_t>(a, DA, s) : lin_run_depth<float>(a, DA, s);
+}
+
+int chunk_of(bool bf16) { return bf16 ? Shape<uint16_t>::C : Shape<float>::C; }
+
+// The backward's launches: roles with the same padded depth share one.
+struct BwdPlan {
+    int n;             // launches
+    int roles[2];      // roles of each
+    int DA[2], slices[2];
+    Cut c[2];
+    size_t part[2], shared_k, shared_v, total;
+};
+BwdPlan bwd_plan(const LinDims &d, bool bf16) {
+    BwdPlan p{};
+    // dq, dk: depth Dv, columns Dk;  dv: depth Dk, columns Dv
+    const int da = pad_depth(d.Dv), db = pad_depth(d.Dk), C = chunk_of(bf16);
+    const long bh = (long)d.B * d.NH;
+    size_t off = 0;
+    if (da == db) {
+        p.n = 1;
+        p.roles[0] = 3;
+        p.DA[0] = da;
+        p.slices[0] = std::max(slices_of(d.Dk), slices_of(d.Dv));
+    } else {
+        p.n = 2;
+        p.roles[0] = 2;
+        p.DA[0] = da;
+        p.slices[0] = slices_of(d.Dk);
+        p.roles[1] = 1;
+        p.DA[1] = db;
+        p.slices[1] = slices_of(d.Dv);
+    }
+    for (int i = 0; i < p.n; ++i) {
+        p.c[i] = cut(d.T, C, bh * p.slices[i] * p.roles[i]);
+        p.part[i] = off;
+        off += p.roles[i] * part_bytes(d, p.DA[i], p.slices[i], p.c[i].nseg);
+    }
+    p.shared_k = p.shared_v = off;
+    if (d.NH != d.NKV) {
+        const size_t n = (size_t)d.T * d.B * d.NH;
+        p.shared_k = off; off += up(sizeof(float) * n * d.Dk);
+        p.shared_v = off; off += up(sizeof(float) * n * d.Dv);
+    }
+    p.total = off;
+    return p;
+}
+
+template <typename T>
+hipError_t share(const float *in, void *out, int64_t n, int grp, int D, hipStream_t s) {
+    hipLaunchKernelGGL(lin_share_kernel<T>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, in,
+                       (T *)out, n, grp, D);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t lin_fwd_bytes(const LinDims &d, bool bf16) {
+    const int DA = pad_depth(d.Dk), sl = slices_of(d.Dv);
+    const Cut c = cut(d.T, chunk_of(bf16), (long)d.B * d.NH * sl);
+    return part_bytes(d, DA, sl, c.nseg);
+}
+
+size_t lin_bwd_bytes(const LinDims &d, bool bf16) { return bwd_plan(d, bf16).total; }
+
+hipError_t launch_lin_step(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSeq v,
+                           const float *g, float scale, const float *S0, void *o, float *S1,
+                           hipStream_t s) {
+    const int sl = slices_of(d.Dv);
+    const long blocks = (long)d.B * d.NH * sl;
+    if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)blocks), thr(256);
+    const bool vec = d.Dv % 4 == 0;
+    if (bf16 && vec)
+        hipLaunchKernelGGL((lin_step_kernel<uint16_t, true>), grid, thr, 0, s, d, q, k, v, g, scale,
+                           S0, (uint16_t *)o, S1, sl);
+    else if (bf16)
+        hipLaunchKernelGGL((lin_step_kernel<uint16_t, false>), grid, thr, 0, s, d, q, k, v, g, scale,
+                           S0, (uint16_t *)o, S1, sl);
+    else if (vec)
+        hipLaunchKernelGGL((lin_step_kernel<float, true>), grid, thr, 0, s, d, q, k, v, g, scale, S0,
+                           (float *)o, S1, sl);
+    else
+        hipLaunchKernelGGL((lin_step_kernel<float, false>), grid, thr, 0, s, d, q, k, v, g, scale, S0,
+                           (float *)o, S1, sl);
+    return hipGetLastError();
+}
+
+hipError_t launch_lin_fwd(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSeq v,
+                          const float *g, float scale, const float *S0, void *o, float *ST,
+                          void *ws, hipStream_t s) {
+    if (d.T == 1) return launch_lin_step(d, bf16, q, k, v, g, scale, S0, o, ST, s);
+    LinArgs a{};
+    const int grp = d.NH / d.NKV, DA = pad_depth(d.Dk);
+    a.nroles = 1;
+    a.T = d.T; a.B = d.B; a.NH = d.NH;
+    a.g = g;
+    a.slices = slices_of(d.Dv);
+    const Cut c = cut(d.T, chunk_of(bf16), (long)d.B * d.NH * a.slices);
+    a.nseg = c.nseg;
+    a.seg_rows = c.rows;
+    a.role[0] = Role{q, k, v, 1, grp, grp, d.Dk, d.Dv, S0, 0, 1, ST, 1, 0, 1.0f, scale, o, 0,
+                     (float *)ws};
+    return lin_run_any(a, bf16, DA, s);
+}
+
+hipError_t launch_lin_bwd(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSeq v,
+                          const float *g, float scale, const float *S0, LinSeq dO,
+                          const float *dST, void *dq, void *dk, void *dv, float *dS0, void *ws,
+                          hipStream_t s) {
+    const BwdPlan p = bwd_plan(d, bf16);
+    const int grp = d.NH / d.NKV;
+    char *base = (char *)ws;
+    float *pk = (float *)(base + p.shared_k), *pv = (float *)(base + p.shared_v);
+    const Role rq{dO, v, k, 1, grp, grp, d.Dv, d.Dk, S0, 1, 1, nullptr, 0, 0, 1.0f, scale, dq, 0, nullptr};
+    const Role rk{v, dO, q, grp, 1, 1, d.Dv, d.Dk, dST, 1, 0, nullptr, 0, 1, scale, 1.0f,
+                  grp > 1 ? (void *)pk : dk, grp > 1, nullptr};
+    const Role rv{k, q, dO, grp, 1, 1, d.Dk, d.Dv, dST, 0, 0, dS0, 0, 1, scale, 1.0f,
+                  grp > 1 ? (void *)pv : dv, grp > 1, nullptr};
+    const Role *order[3] = {&rq, &rk, &rv};
+    int next = 0;
+    for (int i = 0; i < p.n; ++i) {
+        LinArgs a{};
+        a.nroles = p.roles[i];
+        a.T = d.T; a.B = d.B; a.NH = d.NH;
+        a.g = g;
+        a.slices = p.slices[i];
+        a.nseg = p.c[i].nseg;
+        a.seg_rows = p.c[i].rows;
+        const size_t each = part_bytes(d, p.DA[i], p.slices[i], a.nseg);
+        for (int j = 0; j < a.nroles; ++j) {
+            a.role[j] = *order[next++];
+            a.role[j].part = (float *)(base + p.part[i] + j * each);
+        }
+        hipError_t e = lin_run_any(a, bf16, p.DA[i], s);
+        if (e != hipSuccess) return e;
+    }
+    if (grp > 1) {
+        const int64_t n = (int64_t)d.T * d.B * d.NKV;
+        hipError_t e = bf16 ? share<uint16_t>(pk, dk, n * d.Dk, grp, d.Dk, s)
+                            : share<float>(pk, dk, n * d.Dk, grp, d.Dk, s);
+        if (e != hipSuccess) return e;
+        return bf16 ? share<uint16_t>(pv, dv, n * d.Dv, grp, d.Dv, s)
+                    : share<float>(pv, dv, n * d.Dv, grp, d.Dv, s);
+    }
+    return hipSuccess;
+}
+
+}  // namespace lm
+}  // namespace rnn355

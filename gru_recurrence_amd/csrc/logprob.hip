@@ -1,0 +1,398 @@
+// logprob.hip -- log probabilities of given tokens with entropy and the top
+// alternatives, and their gradient.
+//
+// For a row l[0..V) of logits and a token y, with m = max l:
+//   lse = m + log s,  s = sum_v e^(l_v - m)
+//   logp = l_y - lse,  H = log s - t / s,  t = sum_v (l_v - m) e^(l_v - m)
+//   top: the K largest l_v, ties to the lowest index, as l_v - lse
+// and backward, p_v = e^(l_v - lse):
+//   dl_v = dlogp ([v = y] - p_v) - dH p_v (l_v - lse + H)
+//
+// The forward reads every logit once: a workgroup holds a chunk of 8192 of a
+// row in registers, takes the chunk's maximum, sums and K candidates from
+// there, and a second launch joins a row's chunks (only where V needs more
+// than one).  Chunks rather than whole rows: a few rows with a long
+// vocabulary then fill the chip, and small workgroups hide each other's
+// reductions.  All sums are float32.
+//
+// The K candidates of a chunk: the K-th largest of the 256 threads' maxima is
+// a bound that at least K entries reach, and few more do.  Those that reach
+// it are collected (any order) and ranked by counting over the unique keys
+// (value, index), so the result does not depend on the order.  Where ties or
+// a sorted row let more than kCand through, the K-th key is found exactly by
+// bisection over value and index instead.
+#include "lm.h"
+
+namespace rnn355 {
+namespace lm {
+
+namespace {
+
+constexpr int kThreads = 256, kPer = 32, kChunk = kThreads * kPer;
+constexpr int kCand = 1024;
+// e^z is 0 in float32 from z = -104 down; z is held above this where it
+// multiplies e^z, as 0 * -inf would be NaN
+constexpr float kFloor = -200.0f;
+
+// Order-preserving key of a value: -0 equals +0, NaN above everything.
+__device__ __forceinline__ uint32_t order_key(float x) {
+    if (x != x) return 0xFFFFFFFFu;
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    if (k == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
+    return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ uint64_t pair_key(float x, int idx) {
+    return ((uint64_t)order_key(x) << 32) | (uint32_t)~(uint32_t)idx;
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+    return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+}
+
+// A row seen as 16-byte units from the aligned address at or before its
+// start: entry i of unit u is value u*N + i - off.
+template <typename T>
+struct Row {
+    static constexpr int N = 16 / sizeof(T);
+    const T *base;
+    int off, V;
+    __device__ Row(const T *row, int V_) : V(V_) {
+        off = (int)(((uintptr_t)row & 15) / sizeof(T));
+        base = row - off;
+    }
+    // N values of unit u; entries outside the row are -inf
+    __device__ void load(int u, float *x) const {
+        const int i0 = u * N - off;
+        if (i0 >= 0 && i0 + N <= V) {
+            const Unit<T, N> q = *(const Unit<T, N> *)(base + (int64_t)u * N);
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[e] = to_f32<T>(q.v[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                x[e] = i0 + e >= 0 && i0 + e < V ? to_f32<T>(base[(int64_t)u * N + e]) : -INFINITY;
+        }
+    }
+};
+
+// What a chunk leaves for the join.
+struct Part {
+    float m, s, t, pad;
+};
+
+struct Final {
+    float lse, ent;
+};
+// s, t relative to m -> lse, entropy.  A row with nothing allowed (m = -inf):
+// lse -inf, entropy 0.
+__device__ __forceinline__ Final finish(float m, float s, float t) {
+    if (m == -INFINITY && s == 0.0f) return {-INFINITY, 0.0f};
+    const float ls = logf(s);
+    return {m + ls, ls - t / s};
+}
+__device__ __forceinline__ float minus_lse(float x, float lse) {
+    return lse == -INFINITY ? -INFINITY : x - lse;
+}
+
+template <typename T>
+__device__ __forceinline__ void write_row(const LogpArgs &a, int row, const Final &f) {
+    const int64_t id = a.i64 ? ((const int64_t *)a.tok)[row] : (int64_t)((const int32_t *)a.tok)[row];
+    float lp = 0.0f;  // no token
+    if (id >= 0 && id < a.V)
+        lp = minus_lse(to_f32<T>(((const T *)a.logits)[(int64_t)row * a.ld + id]), f.lse);
+    a.logp[row] = lp;
+    if (a.entropy) a.entropy[row] = f.ent;
+    if (a.lse) a.lse[row] = f.lse;
+}
+
+// Ranks n unique keys (LDS) by counting and hands (rank, key) of the K
+// largest to out.
+template <typename F>
+__device__ __forceinline__ void rank_keys(const uint64_t *key, int n, int K, F out) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const uint64_t mine = key[i];
+        int r = 0;
+        for (int j = 0; j < n; ++j) r += key[j] > mine;
+        if (r < K) out(r, mine);
+    }
+}
+
+// Number of threads' entries that satisfy a predicate, over the workgroup.
+__device__ __forceinline__ int block_count(int mine, int *tmp) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) mine += __shfl_xor(mine, o);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = mine;
+    __syncthreads();
+    return tmp[0] + tmp[1] + tmp[2] + tmp[3];
+}
+
+template <typename T, bool TOP>
+__global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
+    constexpr int N = Row<T>::N, U = kPer / N;
+    __shared__ float wm[4], ws[4], wt[4];
+    __shared__ __attribute__((aligned(16))) float tm[kThreads];
+    __shared__ uint64_t cand[TOP ? kCand : 1];
+    __shared__ int ncand, tmp[4];
+    __shared__ float bound;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int row = blockIdx.x / nch, ch = blockIdx.x - row * nch;
+    const Row<T> r((const T *)a.logits + (int64_t)row * a.ld, a.V);
+    const int u0 = ch * (kChunk / N);
+    float x[kPer];
+#pragma unroll
+    for (int j = 0; j < U; ++j) r.load(u0 + j * kThreads + tid, x + j * N);
+    auto index = [&](int i) { return (u0 + (i / N) * kThreads + tid) * N + (i % N) - r.off; };
+
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) m = fmaxf(m, x[i]);
+    if constexpr (TOP) {
+        tm[tid] = m != m ? INFINITY : m;  // nothing but NaN: a bound all the same
+        if (tid == 0) ncand = 0;
+    }
+    m = wave_max(m);
+    if (lane == 0) wm[w] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(wm[0], wm[1]), fmaxf(wm[2], wm[3]));
+    // a chunk of nothing but -inf: weights e^(-inf - 0) = 0
+    const float ref = m == -INFINITY ? 0.0f : m;
+    float s = 0.0f, t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const float z = x[i] - ref, e = exp_fast(z);
+        s += e;
+        t += e * fmaxf(z, kFloor);
+    }
+    s = wave_sum(s);
+    t = wave_sum(t);
+    if (lane == 0) ws[w] = s, wt[w] = t;
+    if constexpr (TOP) {
+        // rank of this thread's maximum among all (ties by thread)
+        const float mine = tm[tid];
+        int above = 0;
+        const float4 *q = (const float4 *)tm;
+        for (int j = 0; j < kThreads / 4; ++j) {
+            const float4 v = q[j];
+            above += (v.x > mine || (v.x == mine && 4 * j < tid));
+            above += (v.y > mine || (v.y == mine && 4 * j + 1 < tid));
+            above += (v.z > mine || (v.z == mine && 4 * j + 2 < tid));
+            above += (v.w > mine || (v.w == mine && 4 * j + 3 < tid));
+        }
+        if (above == a.K - 1) bound = mine;
+    }
+    __syncthreads();
+    s = ws[0] + ws[1] + ws[2] + ws[3];
+    t = wt[0] + wt[1] + wt[2] + wt[3];
+    const Final f = finish(m, s, t);
+    if (nch == 1) {
+        if (tid == 0) write_row<T>(a, row, f);
+    } else if (tid == 0) {
+        ((Part *)a.ws)[blockIdx.x] = Part{m, s, t, 0.0f};
+    }
+    if constexpr (TOP) {
+        const float tau = bound;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int idx = index(i);
+            if (!(x[i] < tau) && idx >= 0 && idx < a.V) {
+                const int at = atomicAdd(&ncand, 1);
+                if (at < kCand) cand[at] = pair_key(x[i], idx);
+            }
+        }
+        __syncthreads();
+        int n = ncand;
+        if (n > kCand) {
+            // exact K-th: the largest value key that at least K entries reach
+            uint32_t vk = 0;
+            for (int b = 31; b >= 0; --b) {
+                const uint32_t c = vk | (1u << b);
+                int k = 0;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const int idx = index(i);
+                    k += idx >= 0 && idx < a.V && order_key(x[i]) >= c;
+                }
+                if (block_count(k, tmp) >= a.K) vk = c;
+            }
+            // and the lowest index bound that completes K among its equals
+            int more = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int idx = index(i);
+                more += idx >= 0 && idx < a.V && order_key(x[i]) > vk;
+            }
+            const int need = a.K - block_count(more, tmp);
+            int lo = 0, hi = a.V - 1;
+            while (lo < hi) {
+                const int mid = lo + (hi - lo) / 2;
+                int k = 0;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const int idx = index(i);
+                    k += idx >= 0 && idx <= mid && order_key(x[i]) == vk;
+                }
+                if (block_count(k, tmp) >= need)
+                    hi = mid;
+                else
+                    lo = mid + 1;
+            }
+            if (tid == 0) ncand = 0;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int idx = index(i);
+                const uint32_t k = order_key(x[i]);
+                if (idx >= 0 && idx < a.V && (k > vk || (k == vk && idx <= lo)))
+                    cand[atomicAdd(&ncand, 1)] = pair_key(x[i], idx);
+            }
+            __syncthreads();
+            n = ncand;
+        }
+        if (nch == 1) {
+            rank_keys(cand, n, a.K, [&](int k, uint64_t key) {
+                a.top_id[(int64_t)row * a.K + k] = (int)~(uint32_t)key;
+                a.top_logp[(int64_t)row * a.K + k] =
+                    minus_lse(key_value((uint32_t)(key >> 32)), f.lse);
+            });
+        } else {
+            uint64_t *out = (uint64_t *)((Part *)a.ws + (int64_t)a.M * nch) + (int64_t)blockIdx.x * a.K;
+            // a chunk with fewer than K entries leaves the lowest key for the rest
+            for (int k = n + tid; k < a.K; k += kThreads) out[k] = 0;
+            rank_keys(cand, n, a.K, [&](int k, uint64_t key) { out[k] = key; });
+        }
+    }
+}
+
+// Joins the chunks of a row.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void logp_join_kernel(LogpArgs a, int nch) {
+    extern __shared__ __attribute__((aligned(16))) uint64_t keys[];
+    const int row = blockIdx.x, tid = threadIdx.x;
+    const Part *p = (const Part *)a.ws + (int64_t)row * nch;
+    const uint64_t *in = (const uint64_t *)((const Part *)a.ws + (int64_t)a.M * nch) +
+                         (int64_t)row * nch * a.K;
+    for (int i = tid; i < nch * a.K; i += kThreads) keys[i] = in[i];
+    float m = -INFINITY;
+    for (int c = 0; c < nch; ++c) m = fmaxf(m, p[c].m);
+    float s = 0.0f, t = 0.0f;
+    for (int c = 0; c < nch; ++c) {
+        const Part q = p[c];
+        if (q.m == -INFINITY && q.s == 0.0f) continue;  // nothing allowed in it
+        const float d = q.m - m, e = exp_fast(d);
+        s += q.s * e;
+        t += (q.t + q.s * fmaxf(d, kFloor)) * e;
+    }
+    const Final f = finish(m, s, t);
+    if (tid == 0) write_row<T>(a, row, f);
+    __syncthreads();
+    if (a.K)
+        rank_keys(keys, nch * a.K, a.K, [&](int k, uint64_t key) {
+            if (key == 0) return;
+            a.top_id[(int64_t)row * a.K + k] = (int)~(uint32_t)key;
+            a.top_logp[(int64_t)row * a.K + k] =
+                minus_lse(key_value((uint32_t)(key >> 32)), f.lse);
+        });
+}
+
+// dl for 4 units of 256 threads each.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void logp_bwd_kernel(LogpBwdArgs a, int nch) {
+    constexpr int N = Row<T>::N;
+    const int row = blockIdx.x / nch, ch = blockIdx.x - row * nch;
+    const Row<T> r((const T *)a.logits + (int64_t)row * a.ld, a.V);
+    T *out = (T *)a.dlogits + (int64_t)row * a.ldd;
+    const bool whole = (int)(((uintptr_t)out & 15) / sizeof(T)) == r.off;  // same place in its 16 bytes
+    const float lse = a.lse[row];
+    float dy = a.dlogp ? a.dlogp[row] : 0.0f;
+    const float dh = a.dent ? a.dent[row] : 0.0f, H = a.dent ? a.entropy[row] : 0.0f;
+    const int64_t id = a.i64 ? ((const int64_t *)a.tok)[row] : (int64_t)((const int32_t *)a.tok)[row];
+    const int y = id >= 0 && id < a.V ? (int)id : -1;
+    if (y < 0) dy = 0.0f;  // no token: its log probability is the constant 0
+    const bool none = lse == -INFINITY;  // nothing allowed: no gradient
+    float x[4][N];
+    const int u0 = ch * 4 * kThreads + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.load(u0 + j * kThreads, x[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int u = u0 + j * kThreads, i0 = u * N - r.off;
+        if (i0 >= a.V) break;
+        Unit<T, N> o;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float lp = x[j][e] - lse, p = exp_fast(lp);
+            // at p = 0 (ruled out, or underflow) p log p is 0, not 0 * -inf
+            float d = -p * (dy + dh * (fmaxf(lp, kFloor) + H));
+            if (i0 + e == y) d += dy;
+            o.v[e] = from_f32<T>(none ? 0.0f : d);
+        }
+        if (whole && i0 >= 0 && i0 + N <= a.V) {
+            *(Unit<T, N> *)(out + i0) = o;
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (i0 + e >= 0 && i0 + e < a.V) out[i0 + e] = o.v[e];
+        }
+    }
+}
+
+// chunks of `per` values that a row of V takes wherever it starts in its 16 bytes
+int chunks(int V, int per, size_t elt) {
+    return (int)(((long)V + (long)(16 / elt) - 1 + per - 1) / per);
+}
+
+template <typename T>
+hipError_t logp_t(const LogpArgs &a, hipStream_t s) {
+    const int nch = chunks(a.V, kChunk, sizeof(T));
+    const dim3 grid((unsigned)((long)a.M * nch));
+    if (a.K)
+        hipLaunchKernelGGL((logp_kernel<T, true>), grid, dim3(kThreads), 0, s, a, nch);
+    else
+        hipLaunchKernelGGL((logp_kernel<T, false>), grid, dim3(kThreads), 0, s, a, nch);
+    if (nch > 1)
+        hipLaunchKernelGGL(logp_join_kernel<T>, dim3((unsigned)a.M), dim3(kThreads),
+                           (size_t)nch * a.K * 8, s, a, nch);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t logp_bwd_t(const LogpBwdArgs &a, hipStream_t s) {
+    const int nch = chunks(a.V, 4 * kThreads * Row<T>::N, sizeof(T));
+    hipLaunchKernelGGL(logp_bwd_kernel<T>, dim3((unsigned)((long)a.M * nch)), dim3(kThreads), 0, s,
+                       a, nch);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t logp_bytes(int M, int V, int K) {
+    // the larger chunk count of the two types
+    const long nch = chunks(V, kChunk, 2);
+    return nch > 1 ? (size_t)M * nch * (sizeof(Part) + 8 * (size_t)K) : 0;
+}
+
+bool logp_grid_ok(int M, int V) {
+    return (long)M * chunks(V, 4 * kThreads * Row<float>::N, 2) <= 0x7fffffffL;
+}
+
+hipError_t launch_logp(const LogpArgs &a, bool bf16, hipStream_t s) {
+    return bf16 ? logp_t<uint16_t>(a, s) : logp_t<float>(a, s);
+}
+
+hipError_t launch_logp_bwd(const LogpBwdArgs &a, bool bf16, hipStream_t s) {
+    return bf16 ? logp_bwd_t<uint16_t>(a, s) : logp_bwd_t<float>(a, s);
+}
+
+}  // namespace lm
+}  // namespace rnn355

@@ -409,6 +409,130 @@ rnn_status rnn_bwd_gru(const rnn_dims *d, rnn_dtype dt,
  */
 rnn_status rnn_workspace_status(const void *ws, size_t ws_bytes, hipStream_t stream);
 
+/*
+ * Operators around the recurrence of a language model: token ids to x, logits
+ * to log probabilities, and the matrix-state recurrence.  They share the rules
+ * above (caller-owned device memory, everything checked on the host before
+ * anything is enqueued, stream order, no allocation, no synchronisation).
+ * Views (ids, tables, logits, the sequences of linear attention) may start at
+ * any element and have any strides, given in elements; dense arrays (outputs,
+ * states, workspaces) are 16-byte aligned.
+ */
+typedef enum { RNN_I32 = 0, RNN_I64 = 1 } rnn_itype;  /* type of token ids */
+
+/* Token ids [T][B]: id (t, b) at data + t*stride_t + b*stride_b. */
+typedef struct {
+    const void *data;
+    rnn_itype type;
+    int64_t stride_t, stride_b;
+} rnn_ids;
+
+/*
+ * Embedding lookup with scaling:
+ *   x[t][b][:] = scale * table[id(t, b)][:]
+ * An id outside [0, V) (padding) gives a row of zeros.  table [V] rows of D
+ * values at stride ld (>= D), x [T][B][D], both in dtype dt; the product is
+ * formed in float32 and rounded once.
+ */
+rnn_status rnn_embed_fwd(int T, int B, int V, int D, rnn_dtype dt, const rnn_ids *ids,
+                         const void *table, int64_t ld, float scale, void *x,
+                         hipStream_t stream);
+
+/*
+ * Its gradient, summed by sorted ids:
+ *   dtable[v][:] = scale * sum over (t, b) with id(t, b) = v of dx[t][b][:]
+ * dx [T][B][D] in dtype dt (the dx of rnn_bwd_lstm / rnn_bwd_gru is float32),
+ * dtable [V][D] float32, every row written.  Sums are float32 in an order
+ * that only the ids set, so results repeat bit for bit.
+ */
+size_t rnn_workspace_size_embed_bwd(int T, int B, int V, int D);
+rnn_status rnn_embed_bwd(int T, int B, int V, int D, rnn_dtype dt, const rnn_ids *ids,
+                         const void *dx, float scale, float *dtable, void *ws, size_t ws_bytes,
+                         hipStream_t stream);
+
+/*
+ * Log probabilities of given tokens, with entropy and the top alternatives.
+ * For every row l[0..V) of logits (dtype dt, rows at stride ld >= V; -inf
+ * rules an entry out) with p = softmax(l):
+ *   lse = log sum e^l,  logp = l[tok] - lse,  entropy = -sum p log p,
+ *   top_id, top_logp [M][K]: the K largest, largest first, ties to the lowest
+ *   index (-0 equals 0), as l - lse.
+ * tok [M] of type it; a token outside [0, V) has logp 0.  A row that rules
+ * everything out has lse and every log probability -inf and entropy 0.  A row
+ * with a NaN or +inf gives NaN.  entropy, lse may be NULL; top_id, top_logp
+ * are required where K > 0.  0 <= K <= min(V, 64), V <= 1000000 (else
+ * RNN_ERR_UNSUPPORTED).  Float32 throughout, each logit read once.
+ */
+size_t rnn_workspace_size_logprobs(int M, int V, int K);
+rnn_status rnn_token_logprobs(int M, int V, rnn_dtype dt, const void *logits, int64_t ld,
+                              const void *tok, rnn_itype it, int K, float *logp, float *entropy,
+                              float *lse, float *top_logp, int *top_id, void *ws,
+                              size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Gradient of sum(dlogp * logp) + sum(dentropy * entropy) with respect to the
+ * logits, given the forward's lse and entropy:
+ *   dlogits[v] = dlogp (1[v = tok] - p_v) - dentropy p_v (log p_v + entropy)
+ * dlogp or dentropy may be NULL (0); entropy is needed with dentropy.  A
+ * token outside [0, V) passes no dlogp; a row that rules everything out gets
+ * zeros.  dlogits in dtype dt, rows at stride ldd >= V; it may be the logits
+ * themselves (same pointer and stride).
+ */
+rnn_status rnn_token_logprobs_bwd(int M, int V, rnn_dtype dt, const void *logits, int64_t ld,
+                                  const void *tok, rnn_itype it, const float *lse,
+                                  const float *entropy, const float *dlogp,
+                                  const float *dentropy, void *dlogits, int64_t ldd,
+                                  hipStream_t stream);
+
+/*
+ * Linear attention with a decay for each head: the recurrence with a matrix
+ * state S [Dk][Dv] per batch row and head,
+ *   S_t = a_h S_{t-1} + k_t^T v_t,   o_t = scale q_t S_t,   a_h = e^{g_h}.
+ * NH query heads share NKV heads of keys and values (NH % NKV == 0; head h
+ * uses key head h / (NH / NKV)); each query head has its own decay and state.
+ * Sequences are views: row (t, b) of q at data + t*stride_t + b*stride_b holds
+ * [NH][Dk] contiguous values (k: [NKV][Dk], v: [NKV][Dv], dO: [NH][Dv]) in
+ * dtype dt, so slices of a fused projection and batch-first arrays are read as
+ * they are.  g [NH] float32 (log decay, <= 0; -inf forgets everything; a
+ * constant, no gradient).  States [B][NH][Dk][Dv] float32.  Outputs are dense
+ * [T][B][heads][D] in dtype dt.  Dk, Dv <= 256 (else RNN_ERR_UNSUPPORTED).
+ * bf16 calls accumulate in float32 and keep every intermediate to about 17
+ * bits; the outputs' rounding is the only one to bf16.  Inputs are finite; a
+ * value that is not may reach every output of its batch row and head.
+ */
+typedef struct {
+    int T, B, NH, NKV, Dk, Dv;
+} rnn_lin_dims;
+typedef struct {
+    const void *data;
+    int64_t stride_t, stride_b;
+} rnn_seq;
+
+typedef enum { RNN_OP_LIN_FWD = 0, RNN_OP_LIN_BWD = 1 } rnn_lin_op;
+/* 0 where none is needed (then ws may be NULL) or the dims are invalid. */
+size_t rnn_workspace_size_linattn(rnn_lin_op op, const rnn_lin_dims *d, rnn_dtype dt);
+
+/* Forward over T tokens.  S0 may be NULL (zeros); ST may be NULL, or be S0. */
+rnn_status rnn_linattn_fwd(const rnn_lin_dims *d, rnn_dtype dt, const rnn_seq *q,
+                           const rnn_seq *k, const rnn_seq *v, const float *g, float scale,
+                           const float *S0, void *o, float *ST, void *ws, size_t ws_bytes,
+                           hipStream_t stream);
+
+/* One token (d->T == 1) for each batch row: reads S, writes S_out, which may
+ * be S itself.  Both are required; no workspace. */
+rnn_status rnn_linattn_step(const rnn_lin_dims *d, rnn_dtype dt, const rnn_seq *q,
+                            const rnn_seq *k, const rnn_seq *v, const float *g, float scale,
+                            const float *S, void *o, float *S_out, hipStream_t stream);
+
+/* Gradients for the loss sum(dO * o) + sum(dST * S_T): dq, dk, dv (dense, in
+ * dtype dt; dk and dv summed over the heads that share them) and dS0
+ * (float32).  S0, dST may be NULL (zeros), dS0 may be NULL. */
+rnn_status rnn_linattn_bwd(const rnn_lin_dims *d, rnn_dtype dt, const rnn_seq *q,
+                           const rnn_seq *k, const rnn_seq *v, const float *g, float scale,
+                           const float *S0, const rnn_seq *dO, const float *dST, void *dq,
+                           void *dk, void *dv, float *dS0, void *ws, size_t ws_bytes,
+                           hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
