@@ -9,8 +9,8 @@
 // The gradient's sums must not depend on timing, so rows are added in the
 // order of a stable sort of the ids, never by atomics:
 //  1. a least-significant-digit radix sort of (id, m), stable by ranking each
-//     wave's 64 items at a time with ballots; up to 16384 ids in one
-//     workgroup's LDS, more in blocks of 16384 (count, then scatter);
+//     wave's 64 items at a time with ballots; up to 4096 ids in one
+//     workgroup's LDS, more in blocks (count, then scatter);
 //  2. the sorted positions and the table's rows are merged into one sequence
 //     (each row's end marker after its positions) that is cut into equal
 //     pieces, one for each wave (the merge-path split: a binary search along
@@ -20,8 +20,6 @@
 //     carry;
 //  3. the carries of each run of pieces with the same open row are added to
 //     that row, in order.
-#include <mutex>
-
 #include "common.h"
 #include "lm.h"
 
@@ -92,9 +90,11 @@ hipError_t embed_fwd_t(const Ids &ids, int V, int D, const T *table, int64_t ld,
 }
 
 // -------------------------------------------------------------------- sort
-constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kSortRounds = 16;
-constexpr int kSortBlock = kSortThreads * kSortRounds;  // items of one workgroup
+// A workgroup sorts ROUNDS items per thread.
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kSortOne = 4 * kSortThreads;  // most items of the one-workgroup sort
 constexpr int kMaxDigits = 512;
+constexpr int kMaxBlocks = 64;  // each block adds up the others' counts
 
 int key_bits(int V) { return 32 - __builtin_clz((unsigned)V); }  // keys 0..V
 int sort_passes(int V) { return (key_bits(V) + 8) / 9; }
@@ -102,31 +102,30 @@ int digit_bits(int V) { return (key_bits(V) + sort_passes(V) - 1) / sort_passes(
 
 // Rank of each of this wave's items among the wave's earlier items of the
 // same digit; cnt[digit] ends as the wave's count.  Items are dealt in order:
-// wave w holds items [w*rounds*64, (w+1)*rounds*64), round r lane l the item
-// r*64 + l of those.
-__device__ __forceinline__ void rank_items(const uint32_t *key, int rounds, int nmine, int shift,
+// wave w holds items [w*R*64, (w+1)*R*64), round r lane l the item r*64 + l of
+// those.
+template <int R>
+__device__ __forceinline__ void rank_items(const uint32_t *key, int nmine, int shift,
                                            int rb, int *cnt, int *rank) {
     const int lane = threadIdx.x & 63;
     const uint64_t below = ((uint64_t)1 << lane) - 1;
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-        if (r < rounds) {
-            const bool have = r * 64 + lane < nmine;
-            const int d = (int)((key[r] >> shift) & ((1u << rb) - 1));
-            uint64_t peers = __ballot(have);
-            for (int b = 0; b < rb; ++b) {
-                const uint64_t one = __ballot((d >> b) & 1);
-                peers &= ((d >> b) & 1) ? one : ~one;
-            }
-            int before = 0;
-            if (have) before = cnt[d];
-            rank[r] = before + __popcll(peers & below);
-            // the last of each group of peers writes the new count; the reads of
-            // this round came first (one wave, LDS operations in order)
-            if (have && (peers >> lane) == 1) cnt[d] = rank[r] + 1;
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+    for (int r = 0; r < R; ++r) {
+        const bool have = r * 64 + lane < nmine;
+        const int d = (int)((key[r] >> shift) & ((1u << rb) - 1));
+        uint64_t peers = __ballot(have);
+        for (int b = 0; b < rb; ++b) {
+            const uint64_t one = __ballot((d >> b) & 1);
+            peers &= ((d >> b) & 1) ? one : ~one;
         }
+        int before = 0;
+        if (have) before = cnt[d];
+        rank[r] = before + __popcll(peers & below);
+        // the last of each group of peers writes the new count; the reads of
+        // this round came first (one wave, LDS operations in order)
+        if (have && (peers >> lane) == 1) cnt[d] = rank[r] + 1;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
@@ -148,36 +147,33 @@ __device__ __forceinline__ void scan_digits(int *tot, int ND, int *tmp) {
     __syncthreads();
 }
 
-// All passes in one workgroup (M <= kSortBlock).
+// All passes in one workgroup.
+template <int R>
 __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(Ids ids, int V, int rb, int passes,
                                                                 uint32_t *okey, uint32_t *opos) {
-    extern __shared__ __attribute__((aligned(16))) char smem[];
-    uint32_t *skey = (uint32_t *)smem;
-    uint16_t *spos = (uint16_t *)(smem + 4 * kSortBlock);
-    int *cnt = (int *)(smem + 6 * kSortBlock);  // [kSortWaves][ND]
+    __shared__ uint32_t skey[kSortThreads * R];
+    __shared__ uint16_t spos[kSortThreads * R];
+    __shared__ int cnt[kSortWaves * kMaxDigits];
     __shared__ int tot[kMaxDigits], tmp[kSortWaves];
     const int M = ids.T * ids.B, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const int rounds = (M + kSortThreads - 1) / kSortThreads;
-    const int first = w * rounds * 64, nmine = min(max(M - first, 0), rounds * 64);
+    const int first = w * R * 64, nmine = min(max(M - first, 0), R * 64);
     const int ND = 1 << rb;
-    uint32_t key[kSortRounds], pos[kSortRounds];
-    int rank[kSortRounds];
+    uint32_t key[R], pos[R];
+    int rank[R];
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
+    for (int r = 0; r < R; ++r) {
         const int i = r * 64 + lane;
-        key[r] = pos[r] = 0;
-        if (r < rounds && i < nmine) {
-            key[r] = (uint32_t)load_id(ids, first + i, V);
-            pos[r] = (uint32_t)(first + i);
-        }
+        key[r] = i < nmine ? (uint32_t)load_id(ids, first + i, V) : 0;
+        pos[r] = (uint32_t)(first + i);
     }
     for (int p = 0; p < passes; ++p) {
         for (int i = tid; i < kSortWaves * ND; i += kSortThreads) cnt[i] = 0;
         __syncthreads();
-        rank_items(key, rounds, nmine, p * rb, rb, cnt + w * ND, rank);
+        rank_items<R>(key, nmine, p * rb, rb, cnt + w * ND, rank);
         __syncthreads();
         if (tid < ND) {  // counts of earlier waves, total
             int s = 0;
+#pragma unroll
             for (int i = 0; i < kSortWaves; ++i) {
                 const int c = cnt[i * ND + tid];
                 cnt[i * ND + tid] = s;
@@ -188,7 +184,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(Ids ids, int V, 
         __syncthreads();
         scan_digits(tot, ND, tmp);
 #pragma unroll
-        for (int r = 0; r < kSortRounds; ++r)
+        for (int r = 0; r < R; ++r)
             if (r * 64 + lane < nmine) {
                 const int d = (int)((key[r] >> (p * rb)) & (ND - 1));
                 const int at = tot[d] + cnt[w * ND + d] + rank[r];
@@ -196,30 +192,30 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(Ids ids, int V, 
                 spos[at] = (uint16_t)pos[r];
             }
         __syncthreads();
-        if (p + 1 < passes) {
 #pragma unroll
-            for (int r = 0; r < kSortRounds; ++r)
-                if (r * 64 + lane < nmine) {
-                    key[r] = skey[first + r * 64 + lane];
-                    pos[r] = spos[first + r * 64 + lane];
-                }
+        for (int r = 0; r < R; ++r)
+            if (r * 64 + lane < nmine) {
+                key[r] = skey[first + r * 64 + lane];
+                pos[r] = spos[first + r * 64 + lane];
+            }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (r * 64 + lane < nmine) {
+            okey[first + r * 64 + lane] = key[r];
+            opos[first + r * 64 + lane] = pos[r];
         }
-    }
-    for (int i = tid; i < M; i += kSortThreads) {
-        okey[i] = skey[i];
-        opos[i] = spos[i];
-    }
 }
 
-// One pass in blocks: each block's digit counts.
+// One pass in blocks of n items: each block's digit counts.
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(Ids ids, int V, int shift, int rb,
-                                                                  const uint32_t *ikey,
+                                                                  int block, const uint32_t *ikey,
                                                                   int *hist) {
     __shared__ int h[kMaxDigits];
     const int M = ids.T * ids.B, tid = threadIdx.x, ND = 1 << rb;
     if (tid < ND) h[tid] = 0;
     __syncthreads();
-    const int first = blockIdx.x * kSortBlock, n = min(M - first, kSortBlock);
+    const int first = blockIdx.x * block, n = min(M - first, block);
     for (int i = tid; i < n; i += kSortThreads) {
         const uint32_t k = ikey ? ikey[first + i] : (uint32_t)load_id(ids, first + i, V);
         atomicAdd(&h[(k >> shift) & (ND - 1)], 1);  // whole numbers: any order, one sum
@@ -230,6 +226,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(Ids ids, int V
 
 // The same pass's scatter: a block's place for a digit is the count of all
 // smaller digits plus that of the digit in earlier blocks.
+template <int R>
 __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
     Ids ids, int V, int shift, int rb, const uint32_t *ikey, const uint32_t *ipos, const int *hist,
     uint32_t *okey, uint32_t *opos) {
@@ -237,38 +234,37 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
     __shared__ int tot[kMaxDigits], tmp[kSortWaves];
     const int M = ids.T * ids.B, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int ND = 1 << rb, nb = gridDim.x, blk = blockIdx.x;
-    const int base = blk * kSortBlock, n = min(M - base, kSortBlock);
-    const int rounds = (n + kSortThreads - 1) / kSortThreads;
-    const int first = w * rounds * 64, nmine = min(max(n - first, 0), rounds * 64);
-    uint32_t key[kSortRounds], pos[kSortRounds];
-    int rank[kSortRounds];
+    const int base = blk * kSortThreads * R, n = min(M - base, kSortThreads * R);
+    const int first = w * R * 64, nmine = min(max(n - first, 0), R * 64);
+    uint32_t key[R], pos[R];
+    int rank[R];
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-        const int i = r * 64 + lane;
+    for (int r = 0; r < R; ++r) {
+        const int i = r * 64 + lane, at = base + first + i;
         key[r] = pos[r] = 0;
-        if (r < rounds && i < nmine) {
-            const int at = base + first + i;
+        if (i < nmine) {
             key[r] = ikey ? ikey[at] : (uint32_t)load_id(ids, at, V);
             pos[r] = ipos ? ipos[at] : (uint32_t)at;
         }
     }
-    for (int i = tid; i < kSortWaves * ND; i += kSortThreads) cnt[i] = 0;
-    __syncthreads();
-    rank_items(key, rounds, nmine, shift, rb, cnt + w * ND, rank);
-    int mine = 0;
+    int mine = 0;  // the digit's count in earlier blocks
     if (tid < ND) {
         int all = 0;
+#pragma unroll 16
         for (int b = 0; b < nb; ++b) {
             const int c = hist[b * ND + tid];
             all += c;
-            if (b < blk) mine += c;
+            mine += b < blk ? c : 0;
         }
         tot[tid] = all;
     }
+    for (int i = tid; i < kSortWaves * ND; i += kSortThreads) cnt[i] = 0;
     __syncthreads();
-    scan_digits(tot, ND, tmp);
+    rank_items<R>(key, nmine, shift, rb, cnt + w * ND, rank);
+    scan_digits(tot, ND, tmp);  // its barriers also order cnt
     if (tid < ND) {
         int s = tot[tid] + mine;
+#pragma unroll
         for (int i = 0; i < kSortWaves; ++i) {
             const int c = cnt[i * ND + tid];
             cnt[i * ND + tid] = s;
@@ -277,7 +273,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
     }
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r)
+    for (int r = 0; r < R; ++r)
         if (r * 64 + lane < nmine) {
             const int at = cnt[w * ND + (int)((key[r] >> shift) & (ND - 1))] + rank[r];
             okey[at] = key[r];
@@ -331,17 +327,23 @@ struct Cols {
 
 // First position of the piece that starts at item `d` of the merge of the
 // positions with the row ends 0..V (position p before row end v iff
-// key[p] <= v); its first row end is d minus that.
+// key[p] <= v); its first row end is d minus that.  The 32 lanes of each half
+// wave search together, 33 ways at a time: the loads of a plain bisection
+// would follow each other.  The halves may search different cuts.
 __device__ __forceinline__ int merge_cut(const uint32_t *key, int M, int V, long d) {
-    long lo = d > (long)V + 1 ? d - (V + 1) : 0, hi = d < M ? d : M;
-    while (lo < hi) {
-        const long mid = (lo + hi) >> 1;
-        if ((long)key[mid] <= d - 1 - mid)
-            lo = mid + 1;
-        else
-            hi = mid;
+    int lo = (int)max(d - ((long)V + 1), 0l), hi = (int)min(d, (long)M);
+    const int l = threadIdx.x & 31;
+    // position p comes before the cut iff key[p] <= d - 1 - p: true, then false
+    while (__any(lo < hi)) {
+        const int step = (hi - lo) / 33 + 1;
+        const long p = (long)lo + (long)(l + 1) * step - 1;  // the last of the lane's share
+        const bool before = p < hi && (long)key[p] <= d - 1 - p;
+        const uint32_t mask = (uint32_t)(__ballot(before) >> (threadIdx.x & 32));
+        const int k = __popc(mask);  // lanes wholly before the cut
+        lo += k * step;
+        hi = min(hi, lo + step - 1);
     }
-    return (int)lo;
+    return lo;
 }
 
 template <typename T, int N, bool VEC>
@@ -357,9 +359,8 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(int M, int V, int D, int
     if (w >= pieces) return;
     const long items = (long)M + V + 1;
     const long d0 = (long)w * kPiece, d1 = min(d0 + kPiece, items);
-    // lanes 0 and 1 search the two cuts
-    const int cut = merge_cut(key, M, V, (lane & 1) ? d1 : d0);
-    const int p0 = __builtin_amdgcn_readlane(cut, 0), p1 = __builtin_amdgcn_readlane(cut, 1);
+    const int cut = merge_cut(key, M, V, lane < 32 ? d0 : d1);
+    const int p0 = __builtin_amdgcn_readlane(cut, 0), p1 = __builtin_amdgcn_readlane(cut, 32);
     int v = (int)(d0 - p0);
     const int v1 = (int)(d1 - p1);
     uint32_t k = V, at = 0;
@@ -444,19 +445,27 @@ __global__ __launch_bounds__(256) void embed_carry_kernel(int V, int D, int piec
 size_t up(size_t v) { return (v + 255) & ~(size_t)255; }
 long pieces_of(long M, long V) { return (M + V + 1 + kPiece - 1) / kPiece; }
 
+// Items per thread of the blocked sort: few blocks' counts to add up, and yet
+// many blocks.
+int sort_rounds(int M) {
+    return M <= kMaxBlocks * kSortThreads ? 1 : M <= 4 * kMaxBlocks * kSortThreads ? 4 : 16;
+}
+
 struct BwdWs {
     size_t key[2], pos[2], hist, crow, carry, total;
 };
 BwdWs bwd_ws(int M, int V, int D) {
     BwdWs w{};
     size_t off = 0;
-    const int nb = (M + kSortBlock - 1) / kSortBlock;
     for (int i = 0; i < 2; ++i) {
         w.key[i] = off; off += up(4 * (size_t)M);
         w.pos[i] = off; off += up(4 * (size_t)M);
-        if (nb == 1) { w.key[1] = w.key[0]; w.pos[1] = w.pos[0]; break; }
+        if (M <= kSortOne) { w.key[1] = w.key[0]; w.pos[1] = w.pos[0]; break; }
     }
-    w.hist = off; off += nb > 1 ? up(sizeof(int) * (size_t)nb * kMaxDigits) : 0;
+    if (M > kSortOne) {
+        const int per = kSortThreads * sort_rounds(M);
+        w.hist = off; off += up(sizeof(int) * (size_t)((M + per - 1) / per) * kMaxDigits);
+    }
     w.crow = off; off += up(sizeof(int) * (size_t)pieces_of(M, V));
     w.carry = off; off += up(sizeof(float) * (size_t)pieces_of(M, V) * D);
     w.total = off;
@@ -504,33 +513,36 @@ hipError_t launch_embed_bwd(const Ids &ids, int V, int D, bool bf16, const void 
     const int M = ids.T * ids.B;
     const BwdWs w = bwd_ws(M, V, D);
     char *base = (char *)ws;
-    const int nb = (M + kSortBlock - 1) / kSortBlock, passes = sort_passes(V), rb = digit_bits(V);
+    const int passes = sort_passes(V), rb = digit_bits(V);
     uint32_t *key[2], *pos[2];
     for (int i = 0; i < 2; ++i) {
         key[i] = (uint32_t *)(base + w.key[i]);
         pos[i] = (uint32_t *)(base + w.pos[i]);
     }
     int last = 0;
-    if (nb == 1) {
-        const size_t lds = 6 * kSortBlock + sizeof(int) * (size_t)kSortWaves * (1 << rb);
-        static std::once_flag once;
-        static hipError_t attr = hipSuccess;
-        std::call_once(once, [] {
-            attr = hipFuncSetAttribute(reinterpret_cast<const void *>(&sort_one_kernel),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(6 * kSortBlock + sizeof(int) * kSortWaves * kMaxDigits));
-        });
-        if (attr != hipSuccess) return attr;
-        hipLaunchKernelGGL(sort_one_kernel, dim3(1), dim3(kSortThreads), lds, s, ids, V, rb, passes,
+    if (M <= kSortThreads) {
+        hipLaunchKernelGGL(sort_one_kernel<1>, dim3(1), dim3(kSortThreads), 0, s, ids, V, rb, passes,
+                           key[0], pos[0]);
+    } else if (M <= kSortOne) {
+        hipLaunchKernelGGL(sort_one_kernel<4>, dim3(1), dim3(kSortThreads), 0, s, ids, V, rb, passes,
                            key[0], pos[0]);
     } else {
         int *hist = (int *)(base + w.hist);
+        const int R = sort_rounds(M), per = kSortThreads * R;
+        const dim3 grid((M + per - 1) / per), thr(kSortThreads);
         for (int p = 0; p < passes; ++p) {
             const uint32_t *ik = p ? key[(p - 1) & 1] : nullptr, *ip = p ? pos[(p - 1) & 1] : nullptr;
-            hipLaunchKernelGGL(sort_count_kernel, dim3(nb), dim3(kSortThreads), 0, s, ids, V, p * rb,
-                               rb, ik, hist);
-            hipLaunchKernelGGL(sort_scatter_kernel, dim3(nb), dim3(kSortThreads), 0, s, ids, V,
-                               p * rb, rb, ik, ip, hist, key[p & 1], pos[p & 1]);
+            uint32_t *ok = key[p & 1], *op = pos[p & 1];
+            hipLaunchKernelGGL(sort_count_kernel, grid, thr, 0, s, ids, V, p * rb, rb, per, ik, hist);
+            if (R == 1)
+                hipLaunchKernelGGL(sort_scatter_kernel<1>, grid, thr, 0, s, ids, V, p * rb, rb, ik, ip,
+                                   hist, ok, op);
+            else if (R == 4)
+                hipLaunchKernelGGL(sort_scatter_kernel<4>, grid, thr, 0, s, ids, V, p * rb, rb, ik, ip,
+                                   hist, ok, op);
+            else
+                hipLaunchKernelGGL(sort_scatter_kernel<16>, grid, thr, 0, s, ids, V, p * rb, rb, ik, ip,
+                                   hist, ok, op);
             last = p & 1;
         }
     }

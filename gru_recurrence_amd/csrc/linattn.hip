@@ -20,20 +20,23 @@
 // P = (x y^T) o a^(r-j) is formed and applied to z; the rest goes through X.
 // Exponents are never negative, so no decay overflows, a = 0 included.
 //
-// Layout: a workgroup of four waves owns (batch row, head, 64 columns of z, a
-// segment of the rows); wave w owns 16 columns and the whole X for them.  In
-// the 16x16 matrix instructions a lane holds, for its column, four
-// consecutive rows of a result; with the operand's depth numbered so that a
-// lane's eight depth elements are rows 4g..4g+3 of two neighbouring 16-row
-// tiles (g = lane / 16), a result is an operand as it stands: P and X never
-// leave the registers.  y and z are needed along their rows too: LDS is read
-// through the transposing 16-bit loads of gfx950.
+// Layout: a workgroup of four waves owns (batch row, head, 64 or 128 columns of
+// z, a segment of the rows); wave w owns 16 or 32 of the columns and the whole
+// X for them.  In the 16x16 matrix instructions a lane holds, for its column,
+// four consecutive rows of a result; with the operand's depth numbered so that
+// a lane's eight depth elements are rows 4g..4g+3 of two neighbouring 16-row
+// tiles (g = lane / 16), a result is an operand as it stands: X never leaves
+// the registers, and P, which all four waves need, is formed once, a tile at a
+// time by one of them, and passed through LDS in operand order.  y and z are
+// needed along their rows too: LDS is read through the transposing 16-bit
+// loads of gfx950.
 //
 // Arithmetic: x, y, z as given (bf16 or float32), all sums float32.  P, X and
 // the decayed z are operands of further products; in bf16 calls each is split
-// into a bf16 and the bf16 of what that leaves (about 17 bits together), so
-// results carry one rounding, the output's.  float32 calls use the float32
-// matrix instructions.
+// into a bf16 and the bf16 of what that leaves (2^-17 of it), so that outputs
+// carry one rounding, their own.  Where a float32 state is returned the decayed
+// z is split in three, which keeps the state to float32.  float32 calls use the
+// float32 matrix instructions.
 //
 // Few (batch row, head) pairs leave the chip empty, so the rows are cut into
 // segments: a first launch forms each segment's own X from nothing, a second
@@ -49,7 +52,6 @@ namespace lm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kCols = 64;    // columns of z of one workgroup
 
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -74,7 +76,7 @@ struct LinArgs {
     Role role[3];
     int nroles, T, B, NH;
     const float *g;
-    int nseg, seg_rows, slices;  // segments of seg_rows rows; slices of kCols columns
+    int nseg, seg_rows, slices;  // segments of seg_rows rows; slices of the columns of z
 };
 
 // ---- element types
@@ -95,7 +97,11 @@ __device__ __forceinline__ void mma(f32x4 &d, const Frag<float> &a, const Frag<f
         d = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], d, 0, 0, 0);
 }
 
-// A float32 operand: as it is, or as a bf16 and the rest's bf16.
+typedef __attribute__((ext_vector_type(2))) float f32x2;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+
+// A float32 operand: as it is, or as a bf16 and the bf16 of what that leaves.
 template <typename T>
 struct Wide;
 template <>
@@ -106,16 +112,23 @@ struct Wide<float> {
         for (int e = 0; e < 8; ++e) f.v[e] = x[e];
     }
 };
+// a pair's bf16 parts, what they leave in x
+__device__ __forceinline__ uint32_t split2(float *x) {
+    const uint32_t h = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x[0], x[1]}, bf16x2));
+    x[0] -= __uint_as_float(h << 16);
+    x[1] -= __uint_as_float(h & 0xFFFF0000u);
+    return h;
+}
+__device__ __forceinline__ void split8(Frag<uint16_t> &f, float *x) {
+    const u32x4 w{split2(x), split2(x + 2), split2(x + 4), split2(x + 6)};
+    f.v = __builtin_bit_cast(bf16x8, w);
+}
 template <>
 struct Wide<uint16_t> {
     Frag<uint16_t> hi, lo;
-    __device__ void set(const float *x) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const __bf16 h = (__bf16)x[e];
-            hi.v[e] = h;
-            lo.v[e] = (__bf16)(x[e] - (float)h);
-        }
+    __device__ void set(float *x) {
+        split8(hi, x);
+        split8(lo, x);
     }
 };
 __device__ __forceinline__ void mma(f32x4 &d, const Frag<float> &a, const Wide<float> &b) { mma(d, a, b.f); }
@@ -127,6 +140,32 @@ __device__ __forceinline__ void mma(f32x4 &d, const Frag<uint16_t> &a, const Wid
 __device__ __forceinline__ void mma(f32x4 &d, const Wide<uint16_t> &a, const Frag<uint16_t> &b) {
     mma(d, a.hi, b);
     mma(d, a.lo, b);
+}
+
+// P^T in LDS: operands of depth 32 (pairs of tiles), each in lane order.  A
+// tile is half an operand: four of a lane's eight elements.
+constexpr int kOperand = 64 * 32;  // bytes of one, of either type
+__device__ __forceinline__ void put_half(char *o, int half, float *x, uint16_t) {
+    const int lane = threadIdx.x & 63;
+    uint2 h, l;
+    h.x = split2(x), h.y = split2(x + 2);
+    l.x = split2(x), l.y = split2(x + 2);
+    *(uint2 *)(o + lane * 16 + half * 8) = h;
+    *(uint2 *)(o + 1024 + lane * 16 + half * 8) = l;
+}
+__device__ __forceinline__ void put_half(char *o, int half, float *x, float) {
+    *(float4 *)(o + half * 1024 + (threadIdx.x & 63) * 16) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void get_operand(Wide<uint16_t> &w, const char *o) {
+    const int lane = threadIdx.x & 63;
+    w.hi.v = *(const bf16x8 *)(o + lane * 16);
+    w.lo.v = *(const bf16x8 *)(o + 1024 + lane * 16);
+}
+__device__ __forceinline__ void get_operand(Wide<float> &w, const char *o) {
+    const int lane = threadIdx.x & 63;
+    const float4 a = *(const float4 *)(o + lane * 16), b = *(const float4 *)(o + 1024 + lane * 16);
+    w.f.v[0] = a.x; w.f.v[1] = a.y; w.f.v[2] = a.z; w.f.v[3] = a.w;
+    w.f.v[4] = b.x; w.f.v[5] = b.y; w.f.v[6] = b.z; w.f.v[7] = b.w;
 }
 
 // Depth elements of row `row`, depths [32 kb, 32 kb + 32), from a row-major
@@ -199,6 +238,29 @@ struct Tile {
     }
 };
 
+// Four neighbouring values, or the `left` of them that exist.
+__device__ __forceinline__ void store4(float *p, const f32x4 &v, int left, bool vec) {
+    if (vec && left >= 4) {
+        *(f32x4 *)p = v;
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (r < left) p[r] = v[r];
+    }
+}
+__device__ __forceinline__ void store4(uint16_t *p, const f32x4 &v, int left, bool vec) {
+    if (vec && left >= 4) {
+        uint2 u;
+        u.x = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[0], v[1]}, bf16x2));
+        u.y = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2], v[3]}, bf16x2));
+        *(uint2 *)p = u;
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (r < left) p[r] = f32_to_bf16_rne(v[r]);
+    }
+}
+
 template <typename T>
 __device__ __forceinline__ bool rows_aligned(const T *p, int64_t st, int D) {
     constexpr int N = 16 / sizeof(T);
@@ -212,28 +274,42 @@ struct Shape<uint16_t> { static constexpr int C = 64, pad = 16; };
 template <>
 struct Shape<float> { static constexpr int C = 32, pad = 8; };
 
-template <typename T, int DA>
-constexpr size_t lds_bytes() {
-    return sizeof(T) * Shape<T>::C * (2 * (DA + Shape<T>::pad) + kCols + Shape<T>::pad);
-}
+// Where each part of the workgroup's LDS starts.
+template <typename T, int DA, int VT, bool STATE>
+struct Lds {
+    static constexpr int C = Shape<T>::C, RT = C / 16;
+    static constexpr int LD = DA + Shape<T>::pad, LDZ = 64 * VT + Shape<T>::pad;
+    // operands of P: depth blocks up to each 16-row tile's own
+    static constexpr int operands = (RT / 2) * (RT / 2 + 1);
+    static constexpr size_t y = 0, z = y + sizeof(T) * C * LD, w = z + sizeof(T) * C * LDZ,
+                            x = w + sizeof(float) * C, p = x + sizeof(T) * C * LD,
+                            bytes = STATE ? x : p + operands * kOperand;
+};
 
-// Fragment order of one workgroup's X: [wave][DA/16 tiles][lane][4].
-template <int DA>
-__device__ __forceinline__ int64_t part_at(const LinArgs &a, int bh, int slice, int seg, int tile) {
+// Fragment order of one workgroup's X: [wave][VT][DA/16 tiles][lane][4].
+template <int DA, int VT>
+__device__ __forceinline__ int64_t part_at(const LinArgs &a, int bh, int slice, int seg, int ct, int tile) {
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int64_t wg = ((int64_t)bh * a.slices + slice) * a.nseg + seg;
-    return (((wg * 4 + w) * (DA / 16) + tile) * 64 + lane) * 4;
+    return ((((wg * 4 + w) * VT + ct) * (DA / 16) + tile) * 64 + lane) * 4;
 }
 
 // STATE: only the segment's own X, from nothing, into its slot of `part`.
-template <typename T, int DA, bool STATE>
-__global__ __launch_bounds__(kThreads) void lin_kernel(LinArgs a) {
-    constexpr int C = Shape<T>::C, PAD = Shape<T>::pad, LD = DA + PAD, LDZ = kCols + PAD;
-    constexpr int KB = DA / 32, RB = C / 32, RT = C / 16;
+// Two workgroups to a CU where their LDS allows it: one's barriers and loads
+// then hide behind the other's products.
+template <typename T, int DA, int VT, bool STATE>
+__global__ __launch_bounds__(kThreads, (2 * Lds<T, DA, VT, STATE>::bytes <= 160 * 1024 ? 2 : 1))
+void lin_kernel(LinArgs a) {
+    using L = Lds<T, DA, VT, STATE>;
+    constexpr int C = L::C, LD = L::LD, LDZ = L::LDZ, COLS = 64 * VT;
+    constexpr int KB = DA / 32, RB = C / 32, RT = C / 16, DT = DA / 16;
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    T *xs = (T *)smem, *ys = xs + (STATE ? 0 : C * LD), *zs = ys + C * LD;
+    T *ys = (T *)(smem + L::y), *zs = (T *)(smem + L::z), *xs = (T *)(smem + L::x);
+    float *wz = (float *)(smem + L::w);  // decays of z's rows towards the next chunk
+    char *ps = smem + L::p;
 
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, c = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     // slices of one (role, row, head, segment) go to the same XCD (workgroups
     // go round the eight of them), where they share x and y in its L2
     const int nsegs = STATE ? a.nseg - 1 : a.nseg;
@@ -245,9 +321,9 @@ __global__ __launch_bounds__(kThreads) void lin_kernel(LinArgs a) {
     const int bh = rest % (a.B * a.NH);
     const Role &R = a.role[rest / (a.B * a.NH)];
     const int b = bh / a.NH, h = bh % a.NH;
-    const int col0 = slice * kCols;
+    const int col0 = slice * COLS;
     if (col0 >= R.Db) return;
-    const int nc = min(R.Db - col0, kCols);
+    const int nc = min(R.Db - col0, COLS);
 
     const T *x = (const T *)R.x.p + (int64_t)b * R.x.sb + (int64_t)(h / R.gx) * R.Da;
     const T *y = (const T *)R.y.p + (int64_t)b * R.y.sb + (int64_t)(h / R.gy) * R.Da;
@@ -261,146 +337,197 @@ __global__ __launch_bounds__(kThreads) void lin_kernel(LinArgs a) {
 
     const int row_lo = seg * a.seg_rows, row_hi = min(row_lo + a.seg_rows, a.T);
 
-    f32x4 X[DA / 16];
-    // element r of tile t: depth 16 t + 4 g + r, column 16 w + c
-    const int col = col0 + 16 * w + c;
-    const bool wave_on = 16 * w < nc;
+    // element r of X[ct][t]: depth 16 t + 4 g + r, column wcol + 16 ct + c
+    f32x4 X[VT][DT];
+    const int wcol = 16 * VT * w;
+    const bool wave_on = wcol < nc;
 #pragma unroll
-    for (int t = 0; t < DA / 16; ++t) X[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int ct = 0; ct < VT; ++ct)
+#pragma unroll
+        for (int t = 0; t < DT; ++t) X[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (!STATE) {
         if (seg > 0) {
 #pragma unroll
-            for (int t = 0; t < DA / 16; ++t)
-                X[t] = *(const f32x4 *)(R.part + part_at<DA>(a, bh, slice, seg, t));
+            for (int ct = 0; ct < VT; ++ct)
+#pragma unroll
+                for (int t = 0; t < DT; ++t)
+                    X[ct][t] = *(const f32x4 *)(R.part + part_at<DA, VT>(a, bh, slice, seg, ct, t));
         }
         if (R.init) {
             const float f = power(row_lo + (R.init_decay ? 1 : 0));
             const float *S = R.init + (int64_t)bh * R.Da * R.Db;
 #pragma unroll
-            for (int t = 0; t < DA / 16; ++t)
+            for (int ct = 0; ct < VT; ++ct)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int d = 16 * t + 4 * g + r;
-                    if (d < R.Da && col < R.Db)
-                        X[t][r] += f * (R.init_t ? S[(int64_t)col * R.Da + d] : S[(int64_t)d * R.Db + col]);
-                }
+                for (int t = 0; t < DT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int d = 16 * t + 4 * g + r, col = col0 + wcol + 16 * ct + c;
+                        if (d < R.Da && col < R.Db)
+                            X[ct][t][r] += f * (R.init_t ? S[(int64_t)col * R.Da + d]
+                                                         : S[(int64_t)d * R.Db + col]);
+                    }
         }
+        // the tiles above the diagonal that share an operand with one on it
+        for (int i = tid; i < L::operands * kOperand / 16; i += kThreads)
+            ((uint4 *)ps)[i] = make_uint4(0, 0, 0, 0);
     }
 
     Tile<T, C, DA> tx, ty;
-    Tile<T, C, kCols> tz;
+    Tile<T, C, COLS> tz;
     auto fetch = [&](int row0) {
         const int n = min(C, row_hi - row0);
-        if constexpr (!STATE) tx.fetch(x, R.x.st, a.T, R.rev, row0, n, R.Da, vx);
         ty.fetch(y, R.y.st, a.T, R.rev, row0, n, R.Da, vy);
         tz.fetch(z, R.z.st, a.T, R.rev, row0, n, nc, vz);
+        if constexpr (!STATE) tx.fetch(x, R.x.st, a.T, R.rev, row0, n, R.Da, vx);
     };
     fetch(row_lo);
     for (int row0 = row_lo; row0 < row_hi; row0 += C) {
         const int n = min(C, row_hi - row0);
-        __syncthreads();
-        if constexpr (!STATE) tx.put(xs, LD);
+        const bool last = row0 + C >= a.T;
+        // rows that X moves on by; the forward's final state takes one decay less
+        const int m = n - (last && R.fin_less ? 1 : 0);
+        lds_barrier();
         ty.put(ys, LD);
         tz.put(zs, LDZ);
-        __syncthreads();
+        if constexpr (!STATE) tx.put(xs, LD);
+        if (tid < C) wz[tid] = R.is * power(max(m - tid, 0));  // rows past n are zero in z
+        lds_barrier();
         if (row0 + C < row_hi) fetch(row0 + C);
+
+        f32x4 o[STATE ? 1 : RT][VT];
+        if constexpr (!STATE) {
+            // P^T, tile by tile: rows j of y, columns i of x
+            for (int p = w; p < RT * (RT + 1) / 2; p += 4) {
+                int it = 0;
+                while ((it + 1) * (it + 2) / 2 <= p) ++it;
+                const int jt = p - it * (it + 1) / 2;
+                if (it * 16 >= n) break;
+                f32x4 d{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    Frag<T> yf, xf;
+                    along(yf, ys, LD, jt * 16 + c, kb, g);
+                    along(xf, xs, LD, it * 16 + c, kb, g);
+                    mma(d, yf, xf);
+                }
+                float e[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int lag = (it - jt) * 16 + c - 4 * g - r;
+                    e[r] = lag >= 0 ? d[r] * (R.is * power(max(lag, 0))) : 0.0f;
+                }
+                // operands before this tile row's: 1, 1, 2, 2, ... each
+                put_half(ps + ((it / 2) * (it / 2 + 1) + (it & 1) * (it / 2 + 1) + jt / 2) * kOperand,
+                         jt & 1, e, T());
+            }
+            // what the carried X gives
+#pragma unroll
+            for (int it = 0; it < RT; ++it)
+#pragma unroll
+                for (int ct = 0; ct < VT; ++ct) o[it][ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (wave_on) {
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    Wide<T> Xw[VT];
+#pragma unroll
+                    for (int ct = 0; ct < VT; ++ct) {
+                        float e[8];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) e[r] = X[ct][2 * kb][r], e[4 + r] = X[ct][2 * kb + 1][r];
+                        Xw[ct].set(e);
+                    }
+#pragma unroll
+                    for (int it = 0; it < RT; ++it) {
+                        Frag<T> xf;
+                        along(xf, xs, LD, it * 16 + c, kb, g);
+#pragma unroll
+                        for (int ct = 0; ct < VT; ++ct) mma(o[it][ct], Xw[ct], xf);
+                    }
+                }
+#pragma unroll
+                for (int it = 0; it < RT; ++it) {
+                    const float f = power(it * 16 + c);
+#pragma unroll
+                    for (int ct = 0; ct < VT; ++ct)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) o[it][ct][r] *= f;
+                }
+            }
+            lds_barrier();
+        }
         if (!wave_on) continue;
 
         // this wave's columns of z, depth along the chunk's rows
-        Frag<T> zf[RB];
+        Frag<T> zf[VT][RB];
 #pragma unroll
-        for (int kb = 0; kb < RB; ++kb) across(zf[kb], zs, LDZ, 16 * w, kb, g, c);
+        for (int ct = 0; ct < VT; ++ct)
+#pragma unroll
+            for (int kb = 0; kb < RB; ++kb) across(zf[ct][kb], zs, LDZ, wcol + 16 * ct, kb, g, c);
 
         if constexpr (!STATE) {
-            Wide<T> Xw[KB];
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                float e[8];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) e[r] = X[2 * kb][r], e[4 + r] = X[2 * kb + 1][r];
-                Xw[kb].set(e);
-            }
-#pragma unroll
-            for (int it = 0; it < RT; ++it) {
-                if (it * 16 >= n) break;
-                Frag<T> xf[KB];
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) along(xf[kb], xs, LD, it * 16 + c, kb, g);
-                // o^T tile: rows are z's columns, columns are the chunk's rows
-                f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) mma(o, Xw[kb], xf[kb]);
-                const float f = power(it * 16 + c);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[r] *= f;
-                // P^T tiles, two at a time: one operand of depth 32
+            for (int it = 0; it < RT; ++it)
 #pragma unroll
                 for (int jb = 0; jb <= it / 2; ++jb) {
-                    float pe[8];
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int jt = 2 * jb + half;
-                        f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
-                        if (jt <= it) {
-#pragma unroll
-                            for (int kb = 0; kb < KB; ++kb) {
-                                Frag<T> yf;
-                                along(yf, ys, LD, jt * 16 + c, kb, g);
-                                mma(p, yf, xf[kb]);
-                            }
-                        }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int lag = (it - jt) * 16 + c - 4 * g - r;
-                            pe[4 * half + r] = lag >= 0 ? p[r] * (R.is * power(max(lag, 0))) : 0.0f;
-                        }
-                    }
                     Wide<T> pw;
-                    pw.set(pe);
-                    mma(o, zf[jb], pw);
-                }
-                // lane: row it*16 + c, z columns 16 w + 4 g ..+3
-                const int row = row0 + it * 16 + c;
-                if (it * 16 + c < n) {
-                    const int64_t at = (((int64_t)(R.rev ? a.T - 1 - row : row) * a.B + b) * a.NH + h) * R.Db +
-                                       col0 + 16 * w + 4 * g;
-                    const int left = nc - 16 * w - 4 * g;
+                    get_operand(pw, ps + ((it / 2) * (it / 2 + 1) + (it & 1) * (it / 2 + 1) + jb) * kOperand);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        if (r >= left) break;
-                        if (R.o_f32)
-                            ((float *)R.o)[at + r] = o[r] * R.os;
-                        else
-                            ((T *)R.o)[at + r] = from_f32<T>(o[r] * R.os);
-                    }
+                    for (int ct = 0; ct < VT; ++ct) mma(o[it][ct], zf[ct][jb], pw);
+                }
+            // lane: row it*16 + c, columns wcol + 16 ct + 4 g ..+3
+#pragma unroll
+            for (int it = 0; it < RT; ++it) {
+                const int row = row0 + it * 16 + c;
+                if (it * 16 + c >= n) continue;
+#pragma unroll
+                for (int ct = 0; ct < VT; ++ct) {
+                    const int k = wcol + 16 * ct + 4 * g;
+                    const int64_t at = (((int64_t)(R.rev ? a.T - 1 - row : row) * a.B + b) * a.NH + h) * R.Db + col0 + k;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[it][ct][r] *= R.os;
+                    if (R.o_f32)
+                        store4((float *)R.o + at, o[it][ct], nc - k, (R.Db & 3) == 0);
+                    else
+                        store4((T *)R.o + at, o[it][ct], nc - k, (R.Db & 3) == 0);
                 }
             }
         }
-        // X <- a^n X + y^T (decayed z); the forward's final state takes one decay less
-        const bool last = row0 + C >= a.T;
+        // X <- a^m X + y^T (decayed z)
         if (STATE || row0 + C < row_hi || (last && R.fin)) {
-            const int m = n - (last && R.fin_less ? 1 : 0);
             const float f = power(m);
 #pragma unroll
-            for (int t = 0; t < DA / 16; ++t)
+            for (int ct = 0; ct < VT; ++ct)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) X[t][r] *= f;
+                for (int t = 0; t < DT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) X[ct][t][r] *= f;
 #pragma unroll
             for (int kb = 0; kb < RB; ++kb) {
-                float e[8];
-                unpack(e, zf[kb]);
+                const float4 wa = *(const float4 *)(wz + kb * 32 + 4 * g);
+                const float4 wb = *(const float4 *)(wz + kb * 32 + 16 + 4 * g);
+                const float ww[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+                Wide<T> zw[VT];
+                Frag<T> rest[VT];  // the third part of bf16 calls
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int j = kb * 32 + (i >> 2) * 16 + 4 * g + (i & 3);
-                    e[i] *= R.is * power(max(m - j, 0));  // rows past n are zero in z
+                for (int ct = 0; ct < VT; ++ct) {
+                    float e[8];
+                    unpack(e, zf[ct][kb]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) e[i] *= ww[i];
+                    zw[ct].set(e);
+                    if constexpr (sizeof(T) == 2) split8(rest[ct], e);
                 }
-                Wide<T> zw;
-                zw.set(e);
 #pragma unroll
-                for (int t = 0; t < DA / 16; ++t) {
+                for (int t = 0; t < DT; ++t) {
                     Frag<T> yf;
                     across(yf, ys, LD, 16 * t, kb, g, c);
-                    mma(X[t], yf, zw);
+#pragma unroll
+                    for (int ct = 0; ct < VT; ++ct) {
+                        mma(X[ct][t], yf, zw[ct]);
+                        if constexpr (sizeof(T) == 2)
+                            if (R.fin) mma(X[ct][t], yf, rest[ct]);
+                    }
                 }
             }
         }
@@ -408,25 +535,29 @@ __global__ __launch_bounds__(kThreads) void lin_kernel(LinArgs a) {
     if constexpr (STATE) {
         // this segment's own X, in the slot of the segment it is carried into
 #pragma unroll
-        for (int t = 0; t < DA / 16; ++t)
-            *(f32x4 *)(R.part + part_at<DA>(a, bh, slice, seg + 1, t)) = X[t];
+        for (int ct = 0; ct < VT; ++ct)
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+                *(f32x4 *)(R.part + part_at<DA, VT>(a, bh, slice, seg + 1, ct, t)) = X[ct][t];
     } else if (R.fin && seg == a.nseg - 1 && wave_on) {
         float *S = R.fin + (int64_t)bh * R.Da * R.Db;
 #pragma unroll
-        for (int t = 0; t < DA / 16; ++t)
+        for (int ct = 0; ct < VT; ++ct)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int d = 16 * t + 4 * g + r;
-                if (d < R.Da && col < R.Db) S[(int64_t)d * R.Db + col] = X[t][r];
-            }
+            for (int t = 0; t < DT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int d = 16 * t + 4 * g + r, col = col0 + wcol + 16 * ct + c;
+                    if (d < R.Da && col < R.Db) S[(int64_t)d * R.Db + col] = X[ct][t][r];
+                }
     }
 }
 
 // Carries X across segments in place: slot s holds segment s-1's own X and
-// gets sum_{s' < s} a^(L (s-1-s')) of them, L rows to a segment.
-template <int DA>
-__global__ __launch_bounds__(256) void lin_carry_kernel(LinArgs a) {
-    constexpr int E = DA * kCols;  // values of one workgroup's X
+// gets sum_{s' < s} a^(L (s-1-s')) of them, L rows to a segment.  E: values of
+// one workgroup's X.
+__global__ __launch_bounds__(256) void lin_carry_kernel(LinArgs a, int E) {
+    constexpr int kAhead = 8;  // segments loaded at a time
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t per = (int64_t)a.B * a.NH * a.slices * (E / 4);
     if (i >= per * a.nroles) return;
@@ -436,12 +567,18 @@ __global__ __launch_bounds__(256) void lin_carry_kernel(LinArgs a) {
     const float f = __builtin_amdgcn_exp2f(fmaxf(a.g[h] * kLog2e, -1e30f) * (float)a.seg_rows);
     f32x4 *p = (f32x4 *)R.part + wg * a.nseg * (E / 4) + j % (E / 4);
     f32x4 X{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 1; s < a.nseg; ++s) {
-        f32x4 &q = p[(int64_t)s * (E / 4)];
-        const f32x4 own = q;
+    for (int s = 1; s < a.nseg; s += kAhead) {
+        f32x4 own[kAhead];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) X[r] = f * X[r] + own[r];
-        q = X;
+        for (int u = 0; u < kAhead; ++u)
+            if (s + u < a.nseg) own[u] = p[(int64_t)(s + u) * (E / 4)];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (s + u < a.nseg) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) X[r] = f * X[r] + own[u][r];
+                p[(int64_t)(s + u) * (E / 4)] = X;
+            }
     }
 }
 
@@ -458,14 +595,16 @@ __global__ __launch_bounds__(256) void lin_share_kernel(const float *__restrict_
     out[i] = from_f32<T>(s);
 }
 
+constexpr int kStepCols = 64;
+
 // One token: S' = a S + k^T v, o = scale q S'.  A workgroup owns 64 columns of
 // a (row, head)'s state, 16 lanes of 4 columns by 16 groups of rows.
 template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void lin_step_kernel(LinDims d, LinSeq q, LinSeq k, LinSeq v,
                                                        const float *g, float scale, const float *S0,
                                                        T *o, float *S1, int slices) {
-    __shared__ float sum[16][kCols];
-    const int bh = blockIdx.x / slices, col0 = (blockIdx.x % slices) * kCols;
+    __shared__ float sum[16][kStepCols];
+    const int bh = blockIdx.x / slices, col0 = (blockIdx.x % slices) * kStepCols;
     const int b = bh / d.NH, h = bh % d.NH, hk = h / (d.NH / d.NKV);
     const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4;
     const T *qp = (const T *)q.p + (int64_t)b * q.sb + (int64_t)h * d.Dk;
@@ -512,7 +651,7 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinDims d, LinSeq q, LinS
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum[grp][4 * lane + e] = acc[e];
     __syncthreads();
-    if (threadIdx.x < kCols && col0 + (int)threadIdx.x < d.Dv) {
+    if (threadIdx.x < kStepCols && col0 + (int)threadIdx.x < d.Dv) {
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) s += sum[i][threadIdx.x];
@@ -523,7 +662,11 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinDims d, LinSeq q, LinS
 // ------------------------------------------------------------------- host
 size_t up(size_t v) { return (v + 255) & ~(size_t)255; }
 int pad_depth(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : d <= 128 ? 128 : 256; }
-int slices_of(int Db) { return (Db + kCols - 1) / kCols; }
+// Column tiles per wave: two where there are the columns for them, as x, y and
+// P are then read from LDS half as often; one at depth 256, whose X would not
+// fit the registers twice.
+int col_tiles(int DA, int Db) { return DA <= 128 && Db > 64 ? 2 : 1; }
+int slices_of(int Db, int VT) { return (Db + 64 * VT - 1) / (64 * VT); }
 
 // Segments: enough workgroups for the chip's 256 CUs several times over, at
 // least two chunks to a segment (each costs a pass over y and z and a state).
@@ -538,53 +681,54 @@ Cut cut(int T, int C, long wgs) {
     return {(chunks + per - 1) / per, per * C};
 }
 
-size_t part_bytes(const LinDims &d, int DA, int slices, int nseg) {
-    return nseg > 1 ? up(sizeof(float) * (size_t)d.B * d.NH * slices * nseg * DA * kCols) : 0;
+size_t part_bytes(const LinDims &d, int DA, int VT, int slices, int nseg) {
+    return nseg > 1 ? up(sizeof(float) * (size_t)d.B * d.NH * slices * nseg * DA * 64 * VT) : 0;
 }
 
-template <typename T, int DA, bool STATE>
+template <typename T, int DA, int VT, bool STATE>
 hipError_t lin_launch(const LinArgs &a, hipStream_t s) {
-    constexpr size_t lds = STATE ? lds_bytes<T, DA>() - sizeof(T) * Shape<T>::C * (DA + Shape<T>::pad)
-                                 : lds_bytes<T, DA>();
+    constexpr size_t lds = Lds<T, DA, VT, STATE>::bytes;
     static std::once_flag once;
     static hipError_t attr = hipSuccess;
     std::call_once(once, [] {
-        attr = hipFuncSetAttribute(reinterpret_cast<const void *>(&lin_kernel<T, DA, STATE>),
+        attr = hipFuncSetAttribute(reinterpret_cast<const void *>(&lin_kernel<T, DA, VT, STATE>),
                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     });
     if (attr != hipSuccess) return attr;
     const long groups = (long)a.nroles * a.B * a.NH * (STATE ? a.nseg - 1 : a.nseg);
     const long blocks = (groups + 7) / 8 * 8 * a.slices;
     if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((lin_kernel<T, DA, STATE>), dim3((unsigned)blocks), dim3(kThreads), lds, s, a);
+    hipLaunchKernelGGL((lin_kernel<T, DA, VT, STATE>), dim3((unsigned)blocks), dim3(kThreads), lds, s, a);
     return hipGetLastError();
 }
 
-template <typename T, int DA>
+template <typename T, int DA, int VT>
 hipError_t lin_run(const LinArgs &a, hipStream_t s) {
     if (a.nseg > 1) {
-        hipError_t e = lin_launch<T, DA, true>(a, s);
+        hipError_t e = lin_launch<T, DA, VT, true>(a, s);
         if (e != hipSuccess) return e;
-        const long n = (long)a.nroles * a.B * a.NH * a.slices * (DA * kCols / 4);
-        hipLaunchKernelGGL(lin_carry_kernel<DA>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a);
+        const int E = DA * 64 * VT;
+        const long n = (long)a.nroles * a.B * a.NH * a.slices * (E / 4);
+        hipLaunchKernelGGL(lin_carry_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, E);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    return lin_launch<T, DA, false>(a, s);
+    return lin_launch<T, DA, VT, false>(a, s);
 }
 
 template <typename T>
-hipError_t lin_run_depth(const LinArgs &a, int DA, hipStream_t s) {
+hipError_t lin_run_depth(const LinArgs &a, int DA, int VT, hipStream_t s) {
+    const bool two = VT == 2;
     switch (DA) {
-        case 32: return lin_run<T, 32>(a, s);
-        case 64: return lin_run<T, 64>(a, s);
-        case 128: return lin_run<T, 128>(a, s);
-        default: return lin_run<T, 256>(a, s);
+        case 32: return two ? lin_run<T, 32, 2>(a, s) : lin_run<T, 32, 1>(a, s);
+        case 64: return two ? lin_run<T, 64, 2>(a, s) : lin_run<T, 64, 1>(a, s);
+        case 128: return two ? lin_run<T, 128, 2>(a, s) : lin_run<T, 128, 1>(a, s);
+        default: return lin_run<T, 256, 1>(a, s);
     }
 }
 
-hipError_t lin_run_any(const LinArgs &a, bool bf16, int DA, hipStream_t s) {
-    return bf16 ? lin_run_depth<uint16_t>(a, DA, s) : lin_run_depth<float>(a, DA, s);
+hipError_t lin_run_any(const LinArgs &a, bool bf16, int DA, int VT, hipStream_t s) {
+    return bf16 ? lin_run_depth<uint16_t>(a, DA, VT, s) : lin_run_depth<float>(a, DA, VT, s);
 }
 
 int chunk_of(bool bf16) { return bf16 ? Shape<uint16_t>::C : Shape<float>::C; }
@@ -593,7 +737,7 @@ int chunk_of(bool bf16) { return bf16 ? Shape<uint16_t>::C : Shape<float>::C; }
 struct BwdPlan {
     int n;             // launches
     int roles[2];      // roles of each
-    int DA[2], slices[2];
+    int DA[2], VT[2], slices[2];
     Cut c[2];
     size_t part[2], shared_k, shared_v, total;
 };
@@ -604,23 +748,27 @@ BwdPlan bwd_plan(const LinDims &d, bool bf16) {
     const long bh = (long)d.B * d.NH;
     size_t off = 0;
     if (da == db) {
+        const int D = std::max(d.Dk, d.Dv);
         p.n = 1;
         p.roles[0] = 3;
         p.DA[0] = da;
-        p.slices[0] = std::max(slices_of(d.Dk), slices_of(d.Dv));
+        p.VT[0] = col_tiles(da, D);
+        p.slices[0] = slices_of(D, p.VT[0]);
     } else {
         p.n = 2;
         p.roles[0] = 2;
         p.DA[0] = da;
-        p.slices[0] = slices_of(d.Dk);
+        p.VT[0] = col_tiles(da, d.Dk);
+        p.slices[0] = slices_of(d.Dk, p.VT[0]);
         p.roles[1] = 1;
         p.DA[1] = db;
-        p.slices[1] = slices_of(d.Dv);
+        p.VT[1] = col_tiles(db, d.Dv);
+        p.slices[1] = slices_of(d.Dv, p.VT[1]);
     }
     for (int i = 0; i < p.n; ++i) {
         p.c[i] = cut(d.T, C, bh * p.slices[i] * p.roles[i]);
         p.part[i] = off;
-        off += p.roles[i] * part_bytes(d, p.DA[i], p.slices[i], p.c[i].nseg);
+        off += p.roles[i] * part_bytes(d, p.DA[i], p.VT[i], p.slices[i], p.c[i].nseg);
     }
     p.shared_k = p.shared_v = off;
     if (d.NH != d.NKV) {
@@ -642,9 +790,9 @@ hipError_t share(const float *in, void *out, int64_t n, int grp, int D, hipStrea
 }  // namespace
 
 size_t lin_fwd_bytes(const LinDims &d, bool bf16) {
-    const int DA = pad_depth(d.Dk), sl = slices_of(d.Dv);
+    const int DA = pad_depth(d.Dk), VT = col_tiles(DA, d.Dv), sl = slices_of(d.Dv, VT);
     const Cut c = cut(d.T, chunk_of(bf16), (long)d.B * d.NH * sl);
-    return part_bytes(d, DA, sl, c.nseg);
+    return part_bytes(d, DA, VT, sl, c.nseg);
 }
 
 size_t lin_bwd_bytes(const LinDims &d, bool bf16) { return bwd_plan(d, bf16).total; }
@@ -652,7 +800,7 @@ size_t lin_bwd_bytes(const LinDims &d, bool bf16) { return bwd_plan(d, bf16).tot
 hipError_t launch_lin_step(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSeq v,
                            const float *g, float scale, const float *S0, void *o, float *S1,
                            hipStream_t s) {
-    const int sl = slices_of(d.Dv);
+    const int sl = (d.Dv + kStepCols - 1) / kStepCols;
     const long blocks = (long)d.B * d.NH * sl;
     if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks), thr(256);
@@ -677,17 +825,17 @@ hipError_t launch_lin_fwd(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSe
                           void *ws, hipStream_t s) {
     if (d.T == 1) return launch_lin_step(d, bf16, q, k, v, g, scale, S0, o, ST, s);
     LinArgs a{};
-    const int grp = d.NH / d.NKV, DA = pad_depth(d.Dk);
+    const int grp = d.NH / d.NKV, DA = pad_depth(d.Dk), VT = col_tiles(DA, d.Dv);
     a.nroles = 1;
     a.T = d.T; a.B = d.B; a.NH = d.NH;
     a.g = g;
-    a.slices = slices_of(d.Dv);
+    a.slices = slices_of(d.Dv, VT);
     const Cut c = cut(d.T, chunk_of(bf16), (long)d.B * d.NH * a.slices);
     a.nseg = c.nseg;
     a.seg_rows = c.rows;
     a.role[0] = Role{q, k, v, 1, grp, grp, d.Dk, d.Dv, S0, 0, 1, ST, 1, 0, 1.0f, scale, o, 0,
                      (float *)ws};
-    return lin_run_any(a, bf16, DA, s);
+    return lin_run_any(a, bf16, DA, VT, s);
 }
 
 hipError_t launch_lin_bwd(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSeq v,
@@ -713,12 +861,12 @@ hipError_t launch_lin_bwd(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSe
         a.slices = p.slices[i];
         a.nseg = p.c[i].nseg;
         a.seg_rows = p.c[i].rows;
-        const size_t each = part_bytes(d, p.DA[i], p.slices[i], a.nseg);
+        const size_t each = part_bytes(d, p.DA[i], p.VT[i], p.slices[i], a.nseg);
         for (int j = 0; j < a.nroles; ++j) {
             a.role[j] = *order[next++];
             a.role[j].part = (float *)(base + p.part[i] + j * each);
         }
-        hipError_t e = lin_run_any(a, bf16, p.DA[i], s);
+        hipError_t e = lin_run_any(a, bf16, p.DA[i], p.VT[i], s);
         if (e != hipSuccess) return e;
     }
     if (grp > 1) {

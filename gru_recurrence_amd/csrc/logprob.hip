@@ -15,12 +15,13 @@
 // vocabulary then fill the chip, and small workgroups hide each other's
 // reductions.  All sums are float32.
 //
-// The K candidates of a chunk: the K-th largest of the 256 threads' maxima is
-// a bound that at least K entries reach, and few more do.  Those that reach
-// it are collected (any order) and ranked by counting over the unique keys
-// (value, index), so the result does not depend on the order.  Where ties or
-// a sorted row let more than kCand through, the K-th key is found exactly by
-// bisection over value and index instead.
+// The K candidates of a chunk: the K-th largest of the maxima of 64 groups of
+// four threads is a bound that at least K entries reach, and few more do.
+// Those that reach it are collected (any order) and ranked by counting over
+// the unique keys (value, index), so the result does not depend on the order.
+// Where ties or a sorted row let more than kCand through, the K-th key is
+// found exactly by bisection over value and index instead (the chunk is read
+// again for it: held on to, it cost the ordinary path its registers).
 #include "lm.h"
 
 namespace rnn355 {
@@ -122,6 +123,7 @@ __device__ __forceinline__ void rank_keys(const uint64_t *key, int n, int K, F o
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const uint64_t mine = key[i];
         int r = 0;
+#pragma unroll 8
         for (int j = 0; j < n; ++j) r += key[j] > mine;
         if (r < K) out(r, mine);
     }
@@ -137,14 +139,61 @@ __device__ __forceinline__ int block_count(int mine, int *tmp) {
     return tmp[0] + tmp[1] + tmp[2] + tmp[3];
 }
 
+// The K largest keys of a chunk, exactly, in `cand`; returns their number (K,
+// or the chunk's entries if those are fewer).
+template <typename T>
+__device__ __forceinline__ int exact_top(Row<T> r, int u0, int K, uint64_t *cand, int *ncand, int *tmp) {
+    constexpr int N = Row<T>::N, U = kPer / N;
+    const int tid = threadIdx.x;
+    // entries of this thread that satisfy a predicate on (value key, index)
+    auto count = [&](auto pred) {
+        int k = 0;
+#pragma unroll 1
+        for (int j = 0; j < U; ++j) {
+            const int u = u0 + j * kThreads + tid, i0 = u * N - r.off;
+            float x[N];
+            r.load(u, x);
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                k += i0 + e >= 0 && i0 + e < r.V && pred(order_key(x[e]), i0 + e);
+        }
+        return block_count(k, tmp);
+    };
+    // the largest value key that at least K entries reach
+    uint32_t vk = 0;
+#pragma unroll 1
+    for (int b = 31; b >= 0; --b) {
+        const uint32_t c = vk | (1u << b);
+        if (count([&](uint32_t k, int) { return k >= c; }) >= K) vk = c;
+    }
+    // and the lowest index bound that completes K among its equals
+    const int need = K - count([&](uint32_t k, int) { return k > vk; });
+    int lo = 0, hi = r.V - 1;
+#pragma unroll 1
+    while (lo < hi) {
+        const int mid = lo + (hi - lo) / 2;
+        if (count([&](uint32_t k, int i) { return k == vk && i <= mid; }) >= need)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    if (tid == 0) *ncand = 0;
+    __syncthreads();
+    count([&](uint32_t k, int i) {
+        if (k > vk || (k == vk && i <= lo)) cand[atomicAdd(ncand, 1)] = ((uint64_t)k << 32) | (uint32_t)~(uint32_t)i;
+        return false;
+    });
+    __syncthreads();
+    return *ncand;
+}
+
 template <typename T, bool TOP>
 __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
     constexpr int N = Row<T>::N, U = kPer / N;
     __shared__ float wm[4], ws[4], wt[4];
-    __shared__ __attribute__((aligned(16))) float tm[kThreads];
+    __shared__ __attribute__((aligned(16))) float tm[64];
     __shared__ uint64_t cand[TOP ? kCand : 1];
     __shared__ int ncand, tmp[4];
-    __shared__ float bound;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int row = blockIdx.x / nch, ch = blockIdx.x - row * nch;
     const Row<T> r((const T *)a.logits + (int64_t)row * a.ld, a.V);
@@ -152,13 +201,15 @@ __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
     float x[kPer];
 #pragma unroll
     for (int j = 0; j < U; ++j) r.load(u0 + j * kThreads + tid, x + j * N);
-    auto index = [&](int i) { return (u0 + (i / N) * kThreads + tid) * N + (i % N) - r.off; };
 
     float m = x[0];
 #pragma unroll
     for (int i = 1; i < kPer; ++i) m = fmaxf(m, x[i]);
     if constexpr (TOP) {
-        tm[tid] = m != m ? INFINITY : m;  // nothing but NaN: a bound all the same
+        const float q = m != m ? INFINITY : m;  // nothing but NaN: a bound all the same
+        const float h = fmaxf(q, __shfl_xor(q, 1));
+        const float f = fmaxf(h, __shfl_xor(h, 2));
+        if ((tid & 3) == 0) tm[tid >> 2] = f;
         if (tid == 0) ncand = 0;
     }
     m = wave_max(m);
@@ -178,87 +229,43 @@ __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
     t = wave_sum(t);
     if (lane == 0) ws[w] = s, wt[w] = t;
     if constexpr (TOP) {
-        // rank of this thread's maximum among all (ties by thread)
-        const float mine = tm[tid];
-        int above = 0;
+        // the K-th largest group maximum: the least of those with fewer than K above
+        const float mine = tm[lane];
         const float4 *q = (const float4 *)tm;
-        for (int j = 0; j < kThreads / 4; ++j) {
+        int above = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
             const float4 v = q[j];
-            above += (v.x > mine || (v.x == mine && 4 * j < tid));
-            above += (v.y > mine || (v.y == mine && 4 * j + 1 < tid));
-            above += (v.z > mine || (v.z == mine && 4 * j + 2 < tid));
-            above += (v.w > mine || (v.w == mine && 4 * j + 3 < tid));
+            above += v.x > mine;
+            above += v.y > mine;
+            above += v.z > mine;
+            above += v.w > mine;
         }
-        if (above == a.K - 1) bound = mine;
+        const float tau = -wave_max(above < a.K ? -mine : -INFINITY);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (!(x[i] < tau)) {
+                const int idx = (u0 + (i / N) * kThreads + tid) * N + (i % N) - r.off;
+                if (idx >= 0 && idx < a.V) {
+                    const int at = atomicAdd(&ncand, 1);
+                    if (at < kCand) cand[at] = pair_key(x[i], idx);
+                }
+            }
+        }
     }
     __syncthreads();
     s = ws[0] + ws[1] + ws[2] + ws[3];
     t = wt[0] + wt[1] + wt[2] + wt[3];
     const Final f = finish(m, s, t);
-    if (nch == 1) {
-        if (tid == 0) write_row<T>(a, row, f);
-    } else if (tid == 0) {
-        ((Part *)a.ws)[blockIdx.x] = Part{m, s, t, 0.0f};
+    if (tid == 0) {
+        if (nch == 1)
+            write_row<T>(a, row, f);
+        else
+            ((Part *)a.ws)[blockIdx.x] = Part{m, s, t, 0.0f};
     }
     if constexpr (TOP) {
-        const float tau = bound;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int idx = index(i);
-            if (!(x[i] < tau) && idx >= 0 && idx < a.V) {
-                const int at = atomicAdd(&ncand, 1);
-                if (at < kCand) cand[at] = pair_key(x[i], idx);
-            }
-        }
-        __syncthreads();
         int n = ncand;
-        if (n > kCand) {
-            // exact K-th: the largest value key that at least K entries reach
-            uint32_t vk = 0;
-            for (int b = 31; b >= 0; --b) {
-                const uint32_t c = vk | (1u << b);
-                int k = 0;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int idx = index(i);
-                    k += idx >= 0 && idx < a.V && order_key(x[i]) >= c;
-                }
-                if (block_count(k, tmp) >= a.K) vk = c;
-            }
-            // and the lowest index bound that completes K among its equals
-            int more = 0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int idx = index(i);
-                more += idx >= 0 && idx < a.V && order_key(x[i]) > vk;
-            }
-            const int need = a.K - block_count(more, tmp);
-            int lo = 0, hi = a.V - 1;
-            while (lo < hi) {
-                const int mid = lo + (hi - lo) / 2;
-                int k = 0;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int idx = index(i);
-                    k += idx >= 0 && idx <= mid && order_key(x[i]) == vk;
-                }
-                if (block_count(k, tmp) >= need)
-                    hi = mid;
-                else
-                    lo = mid + 1;
-            }
-            if (tid == 0) ncand = 0;
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int idx = index(i);
-                const uint32_t k = order_key(x[i]);
-                if (idx >= 0 && idx < a.V && (k > vk || (k == vk && idx <= lo)))
-                    cand[atomicAdd(&ncand, 1)] = pair_key(x[i], idx);
-            }
-            __syncthreads();
-            n = ncand;
-        }
+        if (n > kCand) n = exact_top<T>(r, u0, a.K, cand, &ncand, tmp);
         if (nch == 1) {
             rank_keys(cand, n, a.K, [&](int k, uint64_t key) {
                 a.top_id[(int64_t)row * a.K + k] = (int)~(uint32_t)key;
@@ -283,16 +290,23 @@ __global__ __launch_bounds__(kThreads) void logp_join_kernel(LogpArgs a, int nch
     const uint64_t *in = (const uint64_t *)((const Part *)a.ws + (int64_t)a.M * nch) +
                          (int64_t)row * nch * a.K;
     for (int i = tid; i < nch * a.K; i += kThreads) keys[i] = in[i];
-    float m = -INFINITY;
-    for (int c = 0; c < nch; ++c) m = fmaxf(m, p[c].m);
+    // a lane to a chunk, two where there are more than 64 (V <= 1000000: at most 123)
+    const int lane = tid & 63;
+    Part q[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        q[i] = i * 64 + lane < nch ? p[i * 64 + lane] : Part{-INFINITY, 0.0f, 0.0f, 0.0f};
+    const float m = wave_max(fmaxf(q[0].m, q[1].m));
     float s = 0.0f, t = 0.0f;
-    for (int c = 0; c < nch; ++c) {
-        const Part q = p[c];
-        if (q.m == -INFINITY && q.s == 0.0f) continue;  // nothing allowed in it
-        const float d = q.m - m, e = exp_fast(d);
-        s += q.s * e;
-        t += (q.t + q.s * fmaxf(d, kFloor)) * e;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (q[i].m == -INFINITY && q[i].s == 0.0f) continue;  // nothing allowed in it
+        const float d = q[i].m - m, e = exp_fast(d);
+        s += q[i].s * e;
+        t += (q[i].t + q[i].s * fmaxf(d, kFloor)) * e;
     }
+    s = wave_sum(s);
+    t = wave_sum(t);
     const Final f = finish(m, s, t);
     if (tid == 0) write_row<T>(a, row, f);
     __syncthreads();
