@@ -32,10 +32,10 @@
 // loads of gfx950.
 //
 // Arithmetic: x, y, z as given (bf16 or float32), all sums float32.  P, X and
-// the decayed z are operands of further products; in bf16 calls each is split
-// into a bf16 and the bf16 of what that leaves (2^-17 of it), so that outputs
-// carry one rounding, their own.  Where a float32 state is returned the decayed
-// z is split in three, which keeps the state to float32.  float32 calls use the
+// the decayed z are operands of further products; in bf16 calls P and X are
+// split into a bf16 and the bf16 of what that leaves (2^-17 of it), so that
+// outputs carry one rounding, their own; the decayed z, which X is made of, is
+// split in three and so keeps the states to float32.  float32 calls use the
 // float32 matrix instructions.
 //
 // Few (batch row, head) pairs leave the chip empty, so the rows are cut into
@@ -131,6 +131,21 @@ struct Wide<uint16_t> {
         split8(lo, x);
     }
 };
+// The same with nothing left out: a bf16 operand in three parts.
+template <typename T>
+struct Whole : Wide<T> {};
+template <>
+struct Whole<uint16_t> {
+    Frag<uint16_t> part[3];
+    __device__ void set(float *x) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) split8(part[i], x);
+    }
+};
+__device__ __forceinline__ void mma(f32x4 &d, const Frag<uint16_t> &a, const Whole<uint16_t> &b) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) mma(d, a, b.part[i]);
+}
 __device__ __forceinline__ void mma(f32x4 &d, const Frag<float> &a, const Wide<float> &b) { mma(d, a, b.f); }
 __device__ __forceinline__ void mma(f32x4 &d, const Wide<float> &a, const Frag<float> &b) { mma(d, a.f, b); }
 __device__ __forceinline__ void mma(f32x4 &d, const Frag<uint16_t> &a, const Wide<uint16_t> &b) {
@@ -206,34 +221,51 @@ __device__ __forceinline__ void unpack(float *x, const Frag<float> &f) {
     for (int e = 0; e < 8; ++e) x[e] = f.v[e];
 }
 
-// A [C][W] tile of a sequence operand on its way from memory to LDS: each
-// thread holds R pieces of 16 bytes.
+// A [C][W] tile of a sequence operand: rows row0.. of n (walking order, t =
+// rev ? T-1-row : row), columns [0, D) of `src`, zeros outside.  Where rows are
+// whole 16-byte pieces (`vec`) it waits in registers between fetch() and put():
+// R pieces per thread, loaded without a branch (pieces outside come from inside
+// and are dropped by put) so that all are in flight at once.  Otherwise put()
+// reads it value by value.
 template <typename T, int C, int W>
 struct Tile {
-    static constexpr int N = 16 / sizeof(T), PR = W / N, R = C * PR / kThreads;
-    static_assert(C * PR % kThreads == 0, "whole pieces per thread");
-    Unit<T, N> r[R];
-    // rows row0.. of n (walking order, t = rev ? T-1-row : row), columns [0, D) of `src`
-    __device__ void fetch(const T *src, int64_t st, int T_, int rev, int row0, int n, int D, bool vec) {
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int q = i * kThreads + threadIdx.x, row = q / PR, c = (q % PR) * N;
-            const int at = row0 + row;
-            const T *p = src + (int64_t)(rev ? T_ - 1 - at : at) * st + c;
-            if (row < n && vec && c + N <= D) {
-                r[i] = *(const Unit<T, N> *)p;
-            } else {
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                    r[i].v[e] = row < n && c + e < D ? p[e] : from_f32<T>(0.0f);
-            }
-        }
+    static constexpr int N = 16 / sizeof(T), PR = W / N, RS = kThreads / PR, R = C / RS;
+    static_assert(kThreads % PR == 0 && C % RS == 0, "a thread's pieces share their columns");
+    const T *src;
+    int64_t step;
+    int D, first_t;
+    bool vec;
+    uint4 r[R];
+    __device__ void init(const T *src_, int64_t st, int T_, int rev, int D_) {
+        src = src_;
+        step = rev ? -st : st;
+        first_t = rev ? T_ - 1 : 0;
+        D = D_;
+        vec = ((uintptr_t)src & 15) == 0 && st % N == 0 && D % N == 0;
+        src += first_t * st;
     }
-    __device__ void put(T *t, int ld) const {
+    __device__ void fetch(int row0, int n) {
+        if (!vec) return;
+        const int row = threadIdx.x / PR, c = (threadIdx.x % PR) * N;
+        const T *p = src + row0 * step + (c < D ? c : 0);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int q = i * kThreads + threadIdx.x;
-            *(Unit<T, N> *)(t + (q / PR) * ld + (q % PR) * N) = r[i];
+        for (int i = 0; i < R; ++i) r[i] = *(const uint4 *)(p + min(row + i * RS, n - 1) * step);
+    }
+    __device__ void put(T *t, int ld, int row0, int n) const {
+        const int row = threadIdx.x / PR, c = (threadIdx.x % PR) * N;
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const bool in = row + i * RS < n && c < D;
+                *(uint4 *)(t + (row + i * RS) * ld + c) =
+                    make_uint4(in ? r[i].x : 0, in ? r[i].y : 0, in ? r[i].z : 0, in ? r[i].w : 0);
+            }
+        } else {
+#pragma unroll 1
+            for (int q = threadIdx.x; q < C * W; q += kThreads) {
+                const int i = q / W, k = q % W;
+                t[i * ld + k] = i < n && k < D ? src[(row0 + i) * step + k] : from_f32<T>(0.0f);
+            }
         }
     }
 };
@@ -262,27 +294,26 @@ __device__ __forceinline__ void store4(uint16_t *p, const f32x4 &v, int left, bo
 }
 
 template <typename T>
-__device__ __forceinline__ bool rows_aligned(const T *p, int64_t st, int D) {
-    constexpr int N = 16 / sizeof(T);
-    return ((uintptr_t)p & 15) == 0 && st % N == 0 && D % N == 0;
-}
-
-template <typename T>
 struct Shape;
+// Rows of a chunk; values of padding to a row of an LDS tile.  A tile that is
+// read along its rows puts 16 rows 16 bytes apart over the 64 banks; the
+// transposing 16-bit reads take 32 bytes of 8 rows at a time, so theirs are 32
+// bytes apart.
 template <>
-struct Shape<uint16_t> { static constexpr int C = 64, pad = 16; };
+struct Shape<uint16_t> { static constexpr int C = 64, pad = 16, padx = 8; };
 template <>
-struct Shape<float> { static constexpr int C = 32, pad = 8; };
+struct Shape<float> { static constexpr int C = 32, pad = 4, padx = 4; };
 
 // Where each part of the workgroup's LDS starts.
 template <typename T, int DA, int VT, bool STATE>
 struct Lds {
     static constexpr int C = Shape<T>::C, RT = C / 16;
-    static constexpr int LD = DA + Shape<T>::pad, LDZ = 64 * VT + Shape<T>::pad;
+    static constexpr int LD = DA + Shape<T>::pad, LDZ = 64 * VT + Shape<T>::pad,
+                         LDX = DA + Shape<T>::padx;
     // operands of P: depth blocks up to each 16-row tile's own
     static constexpr int operands = (RT / 2) * (RT / 2 + 1);
     static constexpr size_t y = 0, z = y + sizeof(T) * C * LD, w = z + sizeof(T) * C * LDZ,
-                            x = w + sizeof(float) * C, p = x + sizeof(T) * C * LD,
+                            x = w + sizeof(float) * C, p = x + sizeof(T) * C * LDX,
                             bytes = STATE ? x : p + operands * kOperand;
 };
 
@@ -301,7 +332,7 @@ template <typename T, int DA, int VT, bool STATE>
 __global__ __launch_bounds__(kThreads, (2 * Lds<T, DA, VT, STATE>::bytes <= 160 * 1024 ? 2 : 1))
 void lin_kernel(LinArgs a) {
     using L = Lds<T, DA, VT, STATE>;
-    constexpr int C = L::C, LD = L::LD, LDZ = L::LDZ, COLS = 64 * VT;
+    constexpr int C = L::C, LD = L::LD, LDZ = L::LDZ, LDX = L::LDX, COLS = 64 * VT;
     constexpr int KB = DA / 32, RB = C / 32, RT = C / 16, DT = DA / 16;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     T *ys = (T *)(smem + L::y), *zs = (T *)(smem + L::z), *xs = (T *)(smem + L::x);
@@ -319,17 +350,18 @@ void lin_kernel(LinArgs a) {
     if (grp >= groups) return;
     const int seg = grp % nsegs, rest = grp / nsegs;
     const int bh = rest % (a.B * a.NH);
-    const Role &R = a.role[rest / (a.B * a.NH)];
+    const Role R = a.role[rest / (a.B * a.NH)];
     const int b = bh / a.NH, h = bh % a.NH;
     const int col0 = slice * COLS;
     if (col0 >= R.Db) return;
     const int nc = min(R.Db - col0, COLS);
 
-    const T *x = (const T *)R.x.p + (int64_t)b * R.x.sb + (int64_t)(h / R.gx) * R.Da;
-    const T *y = (const T *)R.y.p + (int64_t)b * R.y.sb + (int64_t)(h / R.gy) * R.Da;
-    const T *z = (const T *)R.z.p + (int64_t)b * R.z.sb + (int64_t)(h / R.gz) * R.Db + col0;
-    const bool vx = !STATE && rows_aligned(x, R.x.st, R.Da), vy = rows_aligned(y, R.y.st, R.Da);
-    const bool vz = rows_aligned(z, R.z.st, R.Db);
+    Tile<T, C, DA> tx, ty;
+    Tile<T, C, COLS> tz;
+    if constexpr (!STATE)
+        tx.init((const T *)R.x.p + (int64_t)b * R.x.sb + (int64_t)(h / R.gx) * R.Da, R.x.st, a.T, R.rev, R.Da);
+    ty.init((const T *)R.y.p + (int64_t)b * R.y.sb + (int64_t)(h / R.gy) * R.Da, R.y.st, a.T, R.rev, R.Da);
+    tz.init((const T *)R.z.p + (int64_t)b * R.z.sb + (int64_t)(h / R.gz) * R.Db + col0, R.z.st, a.T, R.rev, nc);
 
     // log2 of the decay; kept finite so that 0 times it is 0 (a = 0)
     const float g2 = fmaxf(a.g[h] * kLog2e, -1e30f);
@@ -356,30 +388,32 @@ void lin_kernel(LinArgs a) {
         if (R.init) {
             const float f = power(row_lo + (R.init_decay ? 1 : 0));
             const float *S = R.init + (int64_t)bh * R.Da * R.Db;
+            const int sd = R.init_t ? 1 : R.Db, sc = R.init_t ? R.Da : 1;
 #pragma unroll
-            for (int ct = 0; ct < VT; ++ct)
+            for (int ct = 0; ct < VT; ++ct) {
+                const int col = col0 + wcol + 16 * ct + c;
+                // loads without a branch, from inside the state
+                const float *Sc = S + min(col, R.Db - 1) * sc;
 #pragma unroll
                 for (int t = 0; t < DT; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int d = 16 * t + 4 * g + r, col = col0 + wcol + 16 * ct + c;
-                        if (d < R.Da && col < R.Db)
-                            X[ct][t][r] += f * (R.init_t ? S[(int64_t)col * R.Da + d]
-                                                         : S[(int64_t)d * R.Db + col]);
+                        const int d = 16 * t + 4 * g + r;
+                        const float v = Sc[min(d, R.Da - 1) * sd];
+                        X[ct][t][r] += d < R.Da && col < R.Db ? f * v : 0.0f;
                     }
+            }
         }
         // the tiles above the diagonal that share an operand with one on it
         for (int i = tid; i < L::operands * kOperand / 16; i += kThreads)
             ((uint4 *)ps)[i] = make_uint4(0, 0, 0, 0);
     }
 
-    Tile<T, C, DA> tx, ty;
-    Tile<T, C, COLS> tz;
     auto fetch = [&](int row0) {
         const int n = min(C, row_hi - row0);
-        ty.fetch(y, R.y.st, a.T, R.rev, row0, n, R.Da, vy);
-        tz.fetch(z, R.z.st, a.T, R.rev, row0, n, nc, vz);
-        if constexpr (!STATE) tx.fetch(x, R.x.st, a.T, R.rev, row0, n, R.Da, vx);
+        ty.fetch(row0, n);
+        tz.fetch(row0, n);
+        if constexpr (!STATE) tx.fetch(row0, n);
     };
     fetch(row_lo);
     for (int row0 = row_lo; row0 < row_hi; row0 += C) {
@@ -388,9 +422,9 @@ void lin_kernel(LinArgs a) {
         // rows that X moves on by; the forward's final state takes one decay less
         const int m = n - (last && R.fin_less ? 1 : 0);
         lds_barrier();
-        ty.put(ys, LD);
-        tz.put(zs, LDZ);
-        if constexpr (!STATE) tx.put(xs, LD);
+        ty.put(ys, LD, row0, n);
+        tz.put(zs, LDZ, row0, n);
+        if constexpr (!STATE) tx.put(xs, LDX, row0, n);
         if (tid < C) wz[tid] = R.is * power(max(m - tid, 0));  // rows past n are zero in z
         lds_barrier();
         if (row0 + C < row_hi) fetch(row0 + C);
@@ -408,7 +442,7 @@ void lin_kernel(LinArgs a) {
                 for (int kb = 0; kb < KB; ++kb) {
                     Frag<T> yf, xf;
                     along(yf, ys, LD, jt * 16 + c, kb, g);
-                    along(xf, xs, LD, it * 16 + c, kb, g);
+                    along(xf, xs, LDX, it * 16 + c, kb, g);
                     mma(d, yf, xf);
                 }
                 float e[4];
@@ -429,6 +463,7 @@ void lin_kernel(LinArgs a) {
             if (wave_on) {
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
+                    __builtin_amdgcn_sched_barrier(0);
                     Wide<T> Xw[VT];
 #pragma unroll
                     for (int ct = 0; ct < VT; ++ct) {
@@ -440,7 +475,7 @@ void lin_kernel(LinArgs a) {
 #pragma unroll
                     for (int it = 0; it < RT; ++it) {
                         Frag<T> xf;
-                        along(xf, xs, LD, it * 16 + c, kb, g);
+                        along(xf, xs, LDX, it * 16 + c, kb, g);
 #pragma unroll
                         for (int ct = 0; ct < VT; ++ct) mma(o[it][ct], Xw[ct], xf);
                     }
@@ -476,20 +511,23 @@ void lin_kernel(LinArgs a) {
                     for (int ct = 0; ct < VT; ++ct) mma(o[it][ct], zf[ct][jb], pw);
                 }
             // lane: row it*16 + c, columns wcol + 16 ct + 4 g ..+3
+            const int64_t ostep = (int64_t)a.B * a.NH * R.Db * (R.rev ? -1 : 1);
+            const int64_t at = ((int64_t)(R.rev ? a.T - 1 - row0 : row0) * a.B + b) * a.NH * R.Db +
+                               (int64_t)h * R.Db + col0 + wcol + 4 * g + c * ostep;
+            const bool ovec = (R.Db & 3) == 0;
 #pragma unroll
             for (int it = 0; it < RT; ++it) {
-                const int row = row0 + it * 16 + c;
                 if (it * 16 + c >= n) continue;
 #pragma unroll
                 for (int ct = 0; ct < VT; ++ct) {
-                    const int k = wcol + 16 * ct + 4 * g;
-                    const int64_t at = (((int64_t)(R.rev ? a.T - 1 - row : row) * a.B + b) * a.NH + h) * R.Db + col0 + k;
+                    const int left = nc - wcol - 16 * ct - 4 * g;
+                    const int64_t k = at + it * 16 * ostep + 16 * ct;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) o[it][ct][r] *= R.os;
                     if (R.o_f32)
-                        store4((float *)R.o + at, o[it][ct], nc - k, (R.Db & 3) == 0);
+                        store4((float *)R.o + k, o[it][ct], left, ovec);
                     else
-                        store4((T *)R.o + at, o[it][ct], nc - k, (R.Db & 3) == 0);
+                        store4((T *)R.o + k, o[it][ct], left, ovec);
                 }
             }
         }
@@ -504,11 +542,11 @@ void lin_kernel(LinArgs a) {
                     for (int r = 0; r < 4; ++r) X[ct][t][r] *= f;
 #pragma unroll
             for (int kb = 0; kb < RB; ++kb) {
+                __builtin_amdgcn_sched_barrier(0);
                 const float4 wa = *(const float4 *)(wz + kb * 32 + 4 * g);
                 const float4 wb = *(const float4 *)(wz + kb * 32 + 16 + 4 * g);
                 const float ww[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-                Wide<T> zw[VT];
-                Frag<T> rest[VT];  // the third part of bf16 calls
+                Whole<T> zw[VT];
 #pragma unroll
                 for (int ct = 0; ct < VT; ++ct) {
                     float e[8];
@@ -516,18 +554,13 @@ void lin_kernel(LinArgs a) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) e[i] *= ww[i];
                     zw[ct].set(e);
-                    if constexpr (sizeof(T) == 2) split8(rest[ct], e);
                 }
 #pragma unroll
                 for (int t = 0; t < DT; ++t) {
                     Frag<T> yf;
                     across(yf, ys, LD, 16 * t, kb, g, c);
 #pragma unroll
-                    for (int ct = 0; ct < VT; ++ct) {
-                        mma(X[ct][t], yf, zw[ct]);
-                        if constexpr (sizeof(T) == 2)
-                            if (R.fin) mma(X[ct][t], yf, rest[ct]);
-                    }
+                    for (int ct = 0; ct < VT; ++ct) mma(X[ct][t], yf, zw[ct]);
                 }
             }
         }
@@ -675,7 +708,7 @@ struct Cut {
 };
 Cut cut(int T, int C, long wgs) {
     const int chunks = (T + C - 1) / C;
-    long want = std::max(1L, 1024 / std::max(1L, wgs));
+    long want = std::max(1L, 512 / std::max(1L, wgs));
     want = std::min(want, (long)std::max(1, chunks / 2));
     const int per = (int)((chunks + want - 1) / want);
     return {(chunks + per - 1) / per, per * C};
