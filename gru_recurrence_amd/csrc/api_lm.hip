@@ -39,7 +39,11 @@ bool lin_dims_ok(const rnn_lin_dims *d) {
            d->NH % d->NKV == 0 && (long)d->T * d->B <= (1L << 30) && (long)d->B * d->NH <= (1L << 24);
 }
 
-bool lin_supported(const rnn_lin_dims *d) { return d->Dk <= 256 && d->Dv <= 256; }
+// 16 rows of a sequence stay within 32 bits of each other (4-byte values)
+bool lin_supported(const rnn_lin_dims *d) {
+    return d->Dk <= 256 && d->Dv <= 256 &&
+           (d->T == 1 || (long)d->B * d->NH * (d->Dk > d->Dv ? d->Dk : d->Dv) < (1L << 26));
+}
 
 lm::LinDims lin_dims(const rnn_lin_dims *d) {
     return lm::LinDims{d->T, d->B, d->NH, d->NKV, d->Dk, d->Dv};

@@ -20,14 +20,14 @@
 // P = (x y^T) o a^(r-j) is formed and applied to z; the rest goes through X.
 // Exponents are never negative, so no decay overflows, a = 0 included.
 //
-// Layout: a workgroup of four waves owns (batch row, head, 64 or 128 columns of
-// z, a segment of the rows); wave w owns 16 or 32 of the columns and the whole
-// X for them.  In the 16x16 matrix instructions a lane holds, for its column,
+// Layout: a workgroup of four or eight waves owns (batch row, head, 64 or 128
+// columns of z, a segment of the rows); a wave owns 16 of the columns and the
+// whole X for them.  In the 16x16 matrix instructions a lane holds, for its column,
 // four consecutive rows of a result; with the operand's depth numbered so that
 // a lane's eight depth elements are rows 4g..4g+3 of two neighbouring 16-row
 // tiles (g = lane / 16), a result is an operand as it stands: X never leaves
-// the registers, and P, which all four waves need, is formed once, a tile at a
-// time by one of them, and passed through LDS in operand order.  y and z are
+// the registers, and P, which all waves need, is formed once, a tile at a time
+// by one of them, and passed through LDS in operand order.  y and z are
 // needed along their rows too: LDS is read through the transposing 16-bit
 // loads of gfx950.
 //
@@ -51,7 +51,6 @@ namespace lm {
 
 namespace {
 
-constexpr int kThreads = 256;
 
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -184,7 +183,21 @@ __device__ __forceinline__ void get_operand(Wide<float> &w, const char *o) {
 }
 
 // Depth elements of row `row`, depths [32 kb, 32 kb + 32), from a row-major
-// LDS tile.
+// LDS tile.  Tiles that are only read this way (x) keep each lane's eight
+// together in bf16 calls: one 16-byte read, where two of 8 bytes would meet in
+// the same banks.
+__device__ __forceinline__ int x_col(int k, uint16_t) {
+    return (k & ~31) | ((k & 12) << 1) | ((k & 16) >> 2) | (k & 3);
+}
+__device__ __forceinline__ int x_col(int k, float) { return k; }
+__device__ __forceinline__ void put_x(uint16_t *t, int c, const uint4 &v) {
+    *(uint2 *)(t + x_col(c, uint16_t())) = make_uint2(v.x, v.y);
+    *(uint2 *)(t + x_col(c + 4, uint16_t())) = make_uint2(v.z, v.w);
+}
+__device__ __forceinline__ void put_x(float *t, int c, const uint4 &v) { *(uint4 *)(t + c) = v; }
+__device__ __forceinline__ void along_x(Frag<uint16_t> &f, const uint16_t *t, int ld, int row, int kb, int g) {
+    f.v = *(const bf16x8 *)(t + row * ld + kb * 32 + 8 * g);
+}
 __device__ __forceinline__ void along(Frag<uint16_t> &f, const uint16_t *t, int ld, int row, int kb, int g) {
     const uint2 a = *(const uint2 *)(t + row * ld + kb * 32 + 4 * g);
     const uint2 b = *(const uint2 *)(t + row * ld + kb * 32 + 16 + 4 * g);
@@ -196,6 +209,9 @@ __device__ __forceinline__ void along(Frag<float> &f, const float *t, int ld, in
     const float4 b = *(const float4 *)(t + row * ld + kb * 32 + 16 + 4 * g);
     f.v[0] = a.x; f.v[1] = a.y; f.v[2] = a.z; f.v[3] = a.w;
     f.v[4] = b.x; f.v[5] = b.y; f.v[6] = b.z; f.v[7] = b.w;
+}
+__device__ __forceinline__ void along_x(Frag<float> &f, const float *t, int ld, int row, int kb, int g) {
+    along(f, t, ld, row, kb, g);
 }
 // Depth runs over the tile's rows [32 kb, 32 kb + 32) at column col0 + lane % 16.
 __device__ __forceinline__ void across(Frag<uint16_t> &f, const uint16_t *t, int ld, int col0, int kb,
@@ -221,76 +237,86 @@ __device__ __forceinline__ void unpack(float *x, const Frag<float> &f) {
     for (int e = 0; e < 8; ++e) x[e] = f.v[e];
 }
 
+// Whether a sequence's rows are whole 16-byte pieces and a chunk of them lies
+// within 32 bits of its first.
+template <typename T>
+bool pieces_ok(const LinSeq &q, int D) {
+    constexpr int N = 16 / sizeof(T);
+    return ((uintptr_t)q.p & 15) == 0 && q.st % N == 0 && q.sb % N == 0 && D % N == 0 && q.st >= 0 &&
+           q.st < (1ll << 23);
+}
+
 // A [C][W] tile of a sequence operand: rows row0.. of n (walking order, t =
-// rev ? T-1-row : row), columns [0, D) of `src`, zeros outside.  Where rows are
-// whole 16-byte pieces (`vec`) it waits in registers between fetch() and put():
-// R pieces per thread, loaded without a branch (pieces outside come from inside
-// and are dropped by put) so that all are in flight at once.  Otherwise put()
-// reads it value by value.
-template <typename T, int C, int W>
+// rev ? T-1-row : row), columns [0, D) of `src`, zeros outside.  FAST (see
+// lin_kernel): 16-byte pieces wait in registers between fetch() and put(), R
+// per thread, loaded without a branch (rows outside come from inside and are
+// dropped by put) so that all are in flight at once.  Otherwise put() reads the
+// tile value by value.
+template <typename T, int C, int W, int THREADS, bool FAST>
 struct Tile {
-    static constexpr int N = 16 / sizeof(T), PR = W / N, RS = kThreads / PR, R = C / RS;
-    static_assert(kThreads % PR == 0 && C % RS == 0, "a thread's pieces share their columns");
+    static constexpr int N = 16 / sizeof(T), PR = W / N, RS = THREADS / PR, R = (C + RS - 1) / RS;
+    static_assert(THREADS % PR == 0 && (C % RS == 0 || RS > C), "a thread's pieces share their columns");
     const T *src;
-    int64_t step;
-    int D, first_t;
-    bool vec;
-    uint4 r[R];
-    __device__ void init(const T *src_, int64_t st, int T_, int rev, int D_) {
+    int64_t st;
+    int D, T_, rev;
+    uint4 r[FAST ? R : 1];
+    __device__ void init(const T *src_, int64_t st_, int Tn, int rev_, int D_) {
         src = src_;
-        step = rev ? -st : st;
-        first_t = rev ? T_ - 1 : 0;
+        st = st_;
+        T_ = Tn;
+        rev = rev_;
         D = D_;
-        vec = ((uintptr_t)src & 15) == 0 && st % N == 0 && D % N == 0;
-        src += first_t * st;
     }
     __device__ void fetch(int row0, int n) {
-        if (!vec) return;
-        const int row = threadIdx.x / PR, c = (threadIdx.x % PR) * N;
-        const T *p = src + row0 * step + (c < D ? c : 0);
-#pragma unroll
-        for (int i = 0; i < R; ++i) r[i] = *(const uint4 *)(p + min(row + i * RS, n - 1) * step);
-    }
-    __device__ void put(T *t, int ld, int row0, int n) const {
-        const int row = threadIdx.x / PR, c = (threadIdx.x % PR) * N;
-        if (vec) {
+        if constexpr (FAST) {
+            const int row = threadIdx.x / PR, c = (threadIdx.x % PR) * N;
+            const int64_t t0 = rev ? T_ - row0 - C : row0;  // lowest t of a whole chunk
+            const char *base = (const char *)(src + t0 * st);
+            const uint32_t pitch = (uint32_t)st * sizeof(T), at = (c < D ? c : 0) * sizeof(T);
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const bool in = row + i * RS < n && c < D;
-                *(uint4 *)(t + (row + i * RS) * ld + c) =
-                    make_uint4(in ? r[i].x : 0, in ? r[i].y : 0, in ? r[i].z : 0, in ? r[i].w : 0);
+                const int k = min(row + i * RS, n - 1);
+                r[i] = *(const uint4 *)(base + ((uint32_t)(rev ? C - 1 - k : k) * pitch + at));
+            }
+        }
+    }
+    template <bool X = false>
+    __device__ void put(T *t, int ld, int row0, int n) const {
+        if constexpr (FAST) {
+            const int row = threadIdx.x / PR, c = (threadIdx.x % PR) * N;
+            const bool all = n == C && D == W;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                if (RS > C && row >= C) break;  // more threads than pieces
+                uint4 v = r[i];
+                if (!all && !(row + i * RS < n && c < D)) v = make_uint4(0, 0, 0, 0);
+                T *at = t + (row + i * RS) * ld;
+                if constexpr (X)
+                    put_x(at, c, v);
+                else
+                    *(uint4 *)(at + c) = v;
             }
         } else {
 #pragma unroll 1
-            for (int q = threadIdx.x; q < C * W; q += kThreads) {
+            for (int q = threadIdx.x; q < C * W; q += THREADS) {
                 const int i = q / W, k = q % W;
-                t[i * ld + k] = i < n && k < D ? src[(row0 + i) * step + k] : from_f32<T>(0.0f);
+                t[i * ld + (X ? x_col(k, T()) : k)] =
+                    i < n && k < D ? src[(int64_t)(rev ? T_ - 1 - row0 - i : row0 + i) * st + k]
+                                   : from_f32<T>(0.0f);
             }
         }
     }
 };
 
-// Four neighbouring values, or the `left` of them that exist.
-__device__ __forceinline__ void store4(float *p, const f32x4 &v, int left, bool vec) {
-    if (vec && left >= 4) {
-        *(f32x4 *)p = v;
-    } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (r < left) p[r] = v[r];
-    }
+// Four neighbouring values at p[at], one base for all threads.
+__device__ __forceinline__ void store4(float *p, uint32_t at, const f32x4 &v) {
+    *(f32x4 *)((char *)p + at * 4u) = v;
 }
-__device__ __forceinline__ void store4(uint16_t *p, const f32x4 &v, int left, bool vec) {
-    if (vec && left >= 4) {
-        uint2 u;
-        u.x = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[0], v[1]}, bf16x2));
-        u.y = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2], v[3]}, bf16x2));
-        *(uint2 *)p = u;
-    } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (r < left) p[r] = f32_to_bf16_rne(v[r]);
-    }
+__device__ __forceinline__ void store4(uint16_t *p, uint32_t at, const f32x4 &v) {
+    uint2 u;
+    u.x = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[0], v[1]}, bf16x2));
+    u.y = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2], v[3]}, bf16x2));
+    *(uint2 *)((char *)p + at * 2u) = u;
 }
 
 template <typename T>
@@ -305,10 +331,10 @@ template <>
 struct Shape<float> { static constexpr int C = 32, pad = 4, padx = 4; };
 
 // Where each part of the workgroup's LDS starts.
-template <typename T, int DA, int VT, bool STATE>
+template <typename T, int DA, int NW, bool STATE>
 struct Lds {
     static constexpr int C = Shape<T>::C, RT = C / 16;
-    static constexpr int LD = DA + Shape<T>::pad, LDZ = 64 * VT + Shape<T>::pad,
+    static constexpr int LD = DA + Shape<T>::pad, LDZ = 16 * NW + Shape<T>::pad,
                          LDX = DA + Shape<T>::padx;
     // operands of P: depth blocks up to each 16-row tile's own
     static constexpr int operands = (RT / 2) * (RT / 2 + 1);
@@ -317,22 +343,25 @@ struct Lds {
                             bytes = STATE ? x : p + operands * kOperand;
 };
 
-// Fragment order of one workgroup's X: [wave][VT][DA/16 tiles][lane][4].
-template <int DA, int VT>
-__device__ __forceinline__ int64_t part_at(const LinArgs &a, int bh, int slice, int seg, int ct, int tile) {
+// Fragment order of one workgroup's X: [wave][DA/16 tiles][lane][4].
+template <int DA, int NW>
+__device__ __forceinline__ int64_t part_at(const LinArgs &a, int bh, int slice, int seg, int tile) {
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int64_t wg = ((int64_t)bh * a.slices + slice) * a.nseg + seg;
-    return ((((wg * 4 + w) * VT + ct) * (DA / 16) + tile) * 64 + lane) * 4;
+    return (((wg * NW + w) * (DA / 16) + tile) * 64 + lane) * 4;
 }
 
 // STATE: only the segment's own X, from nothing, into its slot of `part`.
 // Two workgroups to a CU where their LDS allows it: one's barriers and loads
 // then hide behind the other's products.
-template <typename T, int DA, int VT, bool STATE>
-__global__ __launch_bounds__(kThreads, (2 * Lds<T, DA, VT, STATE>::bytes <= 160 * 1024 ? 2 : 1))
+// FAST: every operand in whole 16-byte pieces, x and y as deep as DA and z in
+// whole 16-column tiles (the host's rule); the general form then stays out of
+// the registers of the ordinary one.
+template <typename T, int DA, int NW, bool STATE, bool FAST>
+__global__ __launch_bounds__(64 * NW, (DA <= 128 && 2 * Lds<T, DA, NW, STATE>::bytes <= 160 * 1024 ? 2 : 1) * NW / 4)
 void lin_kernel(LinArgs a) {
-    using L = Lds<T, DA, VT, STATE>;
-    constexpr int C = L::C, LD = L::LD, LDZ = L::LDZ, LDX = L::LDX, COLS = 64 * VT;
+    using L = Lds<T, DA, NW, STATE>;
+    constexpr int C = L::C, LD = L::LD, LDZ = L::LDZ, LDX = L::LDX, COLS = 16 * NW;
     constexpr int KB = DA / 32, RB = C / 32, RT = C / 16, DT = DA / 16;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     T *ys = (T *)(smem + L::y), *zs = (T *)(smem + L::z), *xs = (T *)(smem + L::x);
@@ -345,67 +374,69 @@ void lin_kernel(LinArgs a) {
     // go round the eight of them), where they share x and y in its L2
     const int nsegs = STATE ? a.nseg - 1 : a.nseg;
     const int groups = a.nroles * a.B * a.NH * nsegs;
-    const int slice = (blockIdx.x >> 3) % a.slices;
-    const int grp = ((blockIdx.x >> 3) / a.slices) * 8 + (blockIdx.x & 7);
+    // (quotients come from the vector units; all of this is the same for a wave)
+    auto div = [](int p, int q) { return __builtin_amdgcn_readfirstlane(p / q); };
+    const int outer = div(blockIdx.x >> 3, a.slices), slice = (blockIdx.x >> 3) - outer * a.slices;
+    const int grp = outer * 8 + (blockIdx.x & 7);
     if (grp >= groups) return;
-    const int seg = grp % nsegs, rest = grp / nsegs;
-    const int bh = rest % (a.B * a.NH);
-    const Role R = a.role[rest / (a.B * a.NH)];
-    const int b = bh / a.NH, h = bh % a.NH;
+    const int rest = div(grp, nsegs), seg = grp - rest * nsegs;
+    const int role = div(rest, a.B * a.NH), bh = rest - role * a.B * a.NH;
+    const Role R = a.role[role];
+    const int b = div(bh, a.NH), h = bh - b * a.NH;
     const int col0 = slice * COLS;
     if (col0 >= R.Db) return;
     const int nc = min(R.Db - col0, COLS);
 
-    Tile<T, C, DA> tx, ty;
-    Tile<T, C, COLS> tz;
+    Tile<T, C, DA, 64 * NW, FAST> tx, ty;
+    Tile<T, C, COLS, 64 * NW, FAST> tz;
     if constexpr (!STATE)
-        tx.init((const T *)R.x.p + (int64_t)b * R.x.sb + (int64_t)(h / R.gx) * R.Da, R.x.st, a.T, R.rev, R.Da);
-    ty.init((const T *)R.y.p + (int64_t)b * R.y.sb + (int64_t)(h / R.gy) * R.Da, R.y.st, a.T, R.rev, R.Da);
-    tz.init((const T *)R.z.p + (int64_t)b * R.z.sb + (int64_t)(h / R.gz) * R.Db + col0, R.z.st, a.T, R.rev, nc);
+        tx.init((const T *)R.x.p + (int64_t)b * R.x.sb + (int64_t)div(h, R.gx) * R.Da, R.x.st, a.T, R.rev, R.Da);
+    ty.init((const T *)R.y.p + (int64_t)b * R.y.sb + (int64_t)div(h, R.gy) * R.Da, R.y.st, a.T, R.rev, R.Da);
+    tz.init((const T *)R.z.p + (int64_t)b * R.z.sb + (int64_t)div(h, R.gz) * R.Db + col0, R.z.st, a.T, R.rev, nc);
 
     // log2 of the decay; kept finite so that 0 times it is 0 (a = 0)
     const float g2 = fmaxf(a.g[h] * kLog2e, -1e30f);
     auto power = [&](int n) { return __builtin_amdgcn_exp2f(g2 * (float)n); };
 
+    const float powc = power(c);
+
     const int row_lo = seg * a.seg_rows, row_hi = min(row_lo + a.seg_rows, a.T);
 
-    // element r of X[ct][t]: depth 16 t + 4 g + r, column wcol + 16 ct + c
-    f32x4 X[VT][DT];
-    const int wcol = 16 * VT * w;
+    // element r of X[t]: depth 16 t + 4 g + r, column wcol + c of the slice
+    f32x4 X[DT];
+    const int wcol = 16 * w;
     const bool wave_on = wcol < nc;
 #pragma unroll
-    for (int ct = 0; ct < VT; ++ct)
-#pragma unroll
-        for (int t = 0; t < DT; ++t) X[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < DT; ++t) X[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (!STATE) {
         if (seg > 0) {
 #pragma unroll
-            for (int ct = 0; ct < VT; ++ct)
+            for (int t = 0; t < DT; ++t) {
+                const f32x4 v = *(const f32x4 *)(R.part + part_at<DA, NW>(a, bh, slice, seg, t));
+                // added, not assigned: the loads are then waited for here, where a
+                // wait inside the loop would be for the next chunk's loads as well
 #pragma unroll
-                for (int t = 0; t < DT; ++t)
-                    X[ct][t] = *(const f32x4 *)(R.part + part_at<DA, VT>(a, bh, slice, seg, ct, t));
+                for (int r = 0; r < 4; ++r) X[t][r] += v[r];
+            }
         }
         if (R.init) {
             const float f = power(row_lo + (R.init_decay ? 1 : 0));
             const float *S = R.init + (int64_t)bh * R.Da * R.Db;
             const int sd = R.init_t ? 1 : R.Db, sc = R.init_t ? R.Da : 1;
+            const int col = col0 + wcol + c;
+            // loads without a branch, from inside the state
+            const float *Sc = S + min(col, R.Db - 1) * sc;
 #pragma unroll
-            for (int ct = 0; ct < VT; ++ct) {
-                const int col = col0 + wcol + 16 * ct + c;
-                // loads without a branch, from inside the state
-                const float *Sc = S + min(col, R.Db - 1) * sc;
+            for (int t = 0; t < DT; ++t)
 #pragma unroll
-                for (int t = 0; t < DT; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int d = 16 * t + 4 * g + r;
-                        const float v = Sc[min(d, R.Da - 1) * sd];
-                        X[ct][t][r] += d < R.Da && col < R.Db ? f * v : 0.0f;
-                    }
-            }
+                for (int r = 0; r < 4; ++r) {
+                    const int d = 16 * t + 4 * g + r;
+                    const float v = Sc[min(d, R.Da - 1) * sd];
+                    X[t][r] += d < R.Da && col < R.Db ? f * v : 0.0f;
+                }
         }
         // the tiles above the diagonal that share an operand with one on it
-        for (int i = tid; i < L::operands * kOperand / 16; i += kThreads)
+        for (int i = tid; i < L::operands * kOperand / 16; i += 64 * NW)
             ((uint4 *)ps)[i] = make_uint4(0, 0, 0, 0);
     }
 
@@ -424,26 +455,31 @@ void lin_kernel(LinArgs a) {
         lds_barrier();
         ty.put(ys, LD, row0, n);
         tz.put(zs, LDZ, row0, n);
-        if constexpr (!STATE) tx.put(xs, LDX, row0, n);
+        if constexpr (!STATE) tx.template put<true>(xs, LDX, row0, n);
         if (tid < C) wz[tid] = R.is * power(max(m - tid, 0));  // rows past n are zero in z
         lds_barrier();
-        if (row0 + C < row_hi) fetch(row0 + C);
 
-        f32x4 o[STATE ? 1 : RT][VT];
+        f32x4 o[STATE ? 1 : RT];
         if constexpr (!STATE) {
             // P^T, tile by tile: rows j of y, columns i of x
-            for (int p = w; p < RT * (RT + 1) / 2; p += 4) {
+            for (int p = w; p < RT * (RT + 1) / 2; p += NW) {
                 int it = 0;
                 while ((it + 1) * (it + 2) / 2 <= p) ++it;
                 const int jt = p - it * (it + 1) / 2;
                 if (it * 16 >= n) break;
                 f32x4 d{0.0f, 0.0f, 0.0f, 0.0f};
+                constexpr int PM = sizeof(T) == 2 ? 4 : 1, PB = KB < PM ? KB : PM;  // depth blocks read at a time
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    Frag<T> yf, xf;
-                    along(yf, ys, LD, jt * 16 + c, kb, g);
-                    along(xf, xs, LDX, it * 16 + c, kb, g);
-                    mma(d, yf, xf);
+                for (int k0 = 0; k0 < KB; k0 += PB) {
+                    Frag<T> yf[PB], xf[PB];
+#pragma unroll
+                    for (int kb = 0; kb < PB; ++kb) {
+                        along(yf[kb], ys, LD, jt * 16 + c, k0 + kb, g);
+                        along_x(xf[kb], xs, LDX, it * 16 + c, k0 + kb, g);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int kb = 0; kb < PB; ++kb) mma(d, yf[kb], xf[kb]);
                 }
                 float e[4];
 #pragma unroll
@@ -457,110 +493,120 @@ void lin_kernel(LinArgs a) {
             }
             // what the carried X gives
 #pragma unroll
-            for (int it = 0; it < RT; ++it)
-#pragma unroll
-                for (int ct = 0; ct < VT; ++ct) o[it][ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int it = 0; it < RT; ++it) o[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             if (wave_on) {
+                // reads of LDS run AX operands ahead of the products
+                constexpr int AX = 2, NX = KB * RT;
+                Frag<T> xf[AX + 1];
+                Wide<T> Xw;
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
+                for (int i = 0; i < AX; ++i) along_x(xf[i], xs, LDX, (i % RT) * 16 + c, i / RT, g);
+#pragma unroll
+                for (int i = 0; i < NX; ++i) {
+                    const int kb = i / RT, j = i + AX;
+                    if (j < NX) along_x(xf[j % (AX + 1)], xs, LDX, (j % RT) * 16 + c, j / RT, g);
                     __builtin_amdgcn_sched_barrier(0);
-                    Wide<T> Xw[VT];
-#pragma unroll
-                    for (int ct = 0; ct < VT; ++ct) {
+                    if (i % RT == 0) {
                         float e[8];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) e[r] = X[ct][2 * kb][r], e[4 + r] = X[ct][2 * kb + 1][r];
-                        Xw[ct].set(e);
+                        for (int r = 0; r < 4; ++r) e[r] = X[2 * kb][r], e[4 + r] = X[2 * kb + 1][r];
+                        Xw.set(e);
                     }
-#pragma unroll
-                    for (int it = 0; it < RT; ++it) {
-                        Frag<T> xf;
-                        along(xf, xs, LDX, it * 16 + c, kb, g);
-#pragma unroll
-                        for (int ct = 0; ct < VT; ++ct) mma(o[it][ct], Xw[ct], xf);
-                    }
+                    mma(o[i % RT], Xw, xf[i % (AX + 1)]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
                 for (int it = 0; it < RT; ++it) {
-                    const float f = power(it * 16 + c);
+                    const float f = power(it * 16) * powc;
 #pragma unroll
-                    for (int ct = 0; ct < VT; ++ct)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) o[it][ct][r] *= f;
+                    for (int r = 0; r < 4; ++r) o[it][r] *= f;
                 }
             }
             lds_barrier();
         }
+        if (STATE || !wave_on) { if (row0 + C < row_hi) fetch(row0 + C); }
         if (!wave_on) continue;
 
         // this wave's columns of z, depth along the chunk's rows
-        Frag<T> zf[VT][RB];
+        Frag<T> zf[RB];
 #pragma unroll
-        for (int ct = 0; ct < VT; ++ct)
-#pragma unroll
-            for (int kb = 0; kb < RB; ++kb) across(zf[ct][kb], zs, LDZ, wcol + 16 * ct, kb, g, c);
+        for (int kb = 0; kb < RB; ++kb) across(zf[kb], zs, LDZ, wcol, kb, g, c);
 
         if constexpr (!STATE) {
+            // operand q belongs to tile row its[q], depth block jbs[q]
+            constexpr int its[6] = {0, 1, 2, 2, 3, 3}, jbs[6] = {0, 0, 0, 1, 0, 1};
+            Wide<T> pw[2];
+            get_operand(pw[0], ps);
 #pragma unroll
-            for (int it = 0; it < RT; ++it)
-#pragma unroll
-                for (int jb = 0; jb <= it / 2; ++jb) {
-                    Wide<T> pw;
-                    get_operand(pw, ps + ((it / 2) * (it / 2 + 1) + (it & 1) * (it / 2 + 1) + jb) * kOperand);
-#pragma unroll
-                    for (int ct = 0; ct < VT; ++ct) mma(o[it][ct], zf[ct][jb], pw);
-                }
-            // lane: row it*16 + c, columns wcol + 16 ct + 4 g ..+3
-            const int64_t ostep = (int64_t)a.B * a.NH * R.Db * (R.rev ? -1 : 1);
-            const int64_t at = ((int64_t)(R.rev ? a.T - 1 - row0 : row0) * a.B + b) * a.NH * R.Db +
-                               (int64_t)h * R.Db + col0 + wcol + 4 * g + c * ostep;
-            const bool ovec = (R.Db & 3) == 0;
+            for (int q = 0; q < L::operands; ++q) {
+                if (q + 1 < L::operands) get_operand(pw[(q + 1) & 1], ps + (q + 1) * kOperand);
+                __builtin_amdgcn_sched_barrier(0);
+                mma(o[its[q]], zf[jbs[q]], pw[q & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            // lane: row it*16 + c, columns wcol + 4 g ..+3
+            // 16 rows lie within 32 bits of each other (the host's check)
+            const uint32_t pitch = (uint32_t)(a.B * a.NH * R.Db);
+            const uint32_t mine = (uint32_t)(R.rev ? 15 - c : c) * pitch + (uint32_t)(wcol + 4 * g);
+            const int64_t at = ((int64_t)b * a.NH + h) * R.Db + col0;
 #pragma unroll
             for (int it = 0; it < RT; ++it) {
                 if (it * 16 + c >= n) continue;
 #pragma unroll
-                for (int ct = 0; ct < VT; ++ct) {
-                    const int left = nc - wcol - 16 * ct - 4 * g;
-                    const int64_t k = at + it * 16 * ostep + 16 * ct;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) o[it][ct][r] *= R.os;
+                for (int r = 0; r < 4; ++r) o[it][r] *= R.os;
+                const int row = row0 + it * 16;
+                const int64_t base = at + (int64_t)(R.rev ? a.T - row - 16 : row) * pitch;
+                if constexpr (FAST) {
                     if (R.o_f32)
-                        store4((float *)R.o + k, o[it][ct], left, ovec);
+                        store4((float *)R.o + base, mine, o[it]);
                     else
-                        store4((T *)R.o + k, o[it][ct], left, ovec);
+                        store4((T *)R.o + base, mine, o[it]);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (wcol + 4 * g + r < nc) {
+                            if (R.o_f32)
+                                ((float *)R.o)[base + mine + r] = o[it][r];
+                            else
+                                ((T *)R.o)[base + mine + r] = from_f32<T>(o[it][r]);
+                        }
                 }
             }
         }
+        if (!STATE && row0 + C < row_hi) fetch(row0 + C);
         // X <- a^m X + y^T (decayed z)
         if (STATE || row0 + C < row_hi || (last && R.fin)) {
             const float f = power(m);
 #pragma unroll
-            for (int ct = 0; ct < VT; ++ct)
+            for (int t = 0; t < DT; ++t)
 #pragma unroll
-                for (int t = 0; t < DT; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) X[ct][t][r] *= f;
+                for (int r = 0; r < 4; ++r) X[t][r] *= f;
 #pragma unroll
             for (int kb = 0; kb < RB; ++kb) {
-                __builtin_amdgcn_sched_barrier(0);
                 const float4 wa = *(const float4 *)(wz + kb * 32 + 4 * g);
                 const float4 wb = *(const float4 *)(wz + kb * 32 + 16 + 4 * g);
                 const float ww[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-                Whole<T> zw[VT];
+                float e[8];
+                unpack(e, zf[kb]);
 #pragma unroll
-                for (int ct = 0; ct < VT; ++ct) {
-                    float e[8];
-                    unpack(e, zf[ct][kb]);
+                for (int i = 0; i < 8; ++i) e[i] *= ww[i];
+                Whole<T> zw;
+                zw.set(e);
+                // reads of LDS run a tile ahead of the products
+                constexpr int YA = 1;
+                Frag<T> yf[2][YA];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) e[i] *= ww[i];
-                    zw[ct].set(e);
-                }
+                for (int u = 0; u < YA; ++u) across(yf[0][u], ys, LD, 16 * u, kb, g, c);
 #pragma unroll
-                for (int t = 0; t < DT; ++t) {
-                    Frag<T> yf;
-                    across(yf, ys, LD, 16 * t, kb, g, c);
+                for (int t0 = 0; t0 < DT; t0 += YA) {
+                    if (t0 + YA < DT)
 #pragma unroll
-                    for (int ct = 0; ct < VT; ++ct) mma(X[ct][t], yf, zw[ct]);
+                        for (int u = 0; u < YA; ++u)
+                            across(yf[(t0 / YA + 1) & 1][u], ys, LD, 16 * (t0 + YA + u), kb, g, c);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int u = 0; u < YA; ++u) mma(X[t0 + u], yf[(t0 / YA) & 1][u], zw);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
@@ -568,21 +614,18 @@ void lin_kernel(LinArgs a) {
     if constexpr (STATE) {
         // this segment's own X, in the slot of the segment it is carried into
 #pragma unroll
-        for (int ct = 0; ct < VT; ++ct)
-#pragma unroll
-            for (int t = 0; t < DT; ++t)
-                *(f32x4 *)(R.part + part_at<DA, VT>(a, bh, slice, seg + 1, ct, t)) = X[ct][t];
+        for (int t = 0; t < DT; ++t)
+            *(f32x4 *)(R.part + part_at<DA, NW>(a, bh, slice, seg + 1, t)) = X[t];
     } else if (R.fin && seg == a.nseg - 1 && wave_on) {
         float *S = R.fin + (int64_t)bh * R.Da * R.Db;
+        const int col = col0 + wcol + c;
 #pragma unroll
-        for (int ct = 0; ct < VT; ++ct)
+        for (int t = 0; t < DT; ++t)
 #pragma unroll
-            for (int t = 0; t < DT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int d = 16 * t + 4 * g + r, col = col0 + wcol + 16 * ct + c;
-                    if (d < R.Da && col < R.Db) S[(int64_t)d * R.Db + col] = X[ct][t][r];
-                }
+            for (int r = 0; r < 4; ++r) {
+                const int d = 16 * t + 4 * g + r;
+                if (d < R.Da && col < R.Db) S[(int64_t)d * R.Db + col] = X[t][r];
+            }
     }
 }
 
@@ -695,11 +738,10 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinDims d, LinSeq q, LinS
 // ------------------------------------------------------------------- host
 size_t up(size_t v) { return (v + 255) & ~(size_t)255; }
 int pad_depth(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : d <= 128 ? 128 : 256; }
-// Column tiles per wave: two where there are the columns for them, as x, y and
-// P are then read from LDS half as often; one at depth 256, whose X would not
-// fit the registers twice.
-int col_tiles(int DA, int Db) { return DA <= 128 && Db > 64 ? 2 : 1; }
-int slices_of(int Db, int VT) { return (Db + 64 * VT - 1) / (64 * VT); }
+// Waves (of 16 columns) of a workgroup: eight where there are the columns, as
+// they share P and the staged x and y.
+int waves_of(int Db) { return Db > 64 ? 8 : 4; }
+int slices_of(int Db, int NW) { return (Db + 16 * NW - 1) / (16 * NW); }
 
 // Segments: enough workgroups for the chip's 256 CUs several times over, at
 // least two chunks to a segment (each costs a pass over y and z and a state).
@@ -714,54 +756,66 @@ Cut cut(int T, int C, long wgs) {
     return {(chunks + per - 1) / per, per * C};
 }
 
-size_t part_bytes(const LinDims &d, int DA, int VT, int slices, int nseg) {
-    return nseg > 1 ? up(sizeof(float) * (size_t)d.B * d.NH * slices * nseg * DA * 64 * VT) : 0;
+size_t part_bytes(const LinDims &d, int DA, int NW, int slices, int nseg) {
+    return nseg > 1 ? up(sizeof(float) * (size_t)d.B * d.NH * slices * nseg * DA * 16 * NW) : 0;
 }
 
-template <typename T, int DA, int VT, bool STATE>
+template <typename T, int DA, int NW, bool STATE, bool FAST>
 hipError_t lin_launch(const LinArgs &a, hipStream_t s) {
-    constexpr size_t lds = Lds<T, DA, VT, STATE>::bytes;
+    constexpr size_t lds = Lds<T, DA, NW, STATE>::bytes;
     static std::once_flag once;
     static hipError_t attr = hipSuccess;
     std::call_once(once, [] {
-        attr = hipFuncSetAttribute(reinterpret_cast<const void *>(&lin_kernel<T, DA, VT, STATE>),
+        attr = hipFuncSetAttribute(reinterpret_cast<const void *>(&lin_kernel<T, DA, NW, STATE, FAST>),
                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     });
     if (attr != hipSuccess) return attr;
     const long groups = (long)a.nroles * a.B * a.NH * (STATE ? a.nseg - 1 : a.nseg);
     const long blocks = (groups + 7) / 8 * 8 * a.slices;
     if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((lin_kernel<T, DA, VT, STATE>), dim3((unsigned)blocks), dim3(kThreads), lds, s, a);
+    hipLaunchKernelGGL((lin_kernel<T, DA, NW, STATE, FAST>), dim3((unsigned)blocks), dim3(64 * NW), lds, s,
+                       a);
     return hipGetLastError();
 }
 
-template <typename T, int DA, int VT>
+template <typename T, int DA, int NW, bool FAST>
 hipError_t lin_run(const LinArgs &a, hipStream_t s) {
     if (a.nseg > 1) {
-        hipError_t e = lin_launch<T, DA, VT, true>(a, s);
+        hipError_t e = lin_launch<T, DA, NW, true, FAST>(a, s);
         if (e != hipSuccess) return e;
-        const int E = DA * 64 * VT;
+        const int E = DA * 16 * NW;
         const long n = (long)a.nroles * a.B * a.NH * a.slices * (E / 4);
         hipLaunchKernelGGL(lin_carry_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, E);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    return lin_launch<T, DA, VT, false>(a, s);
+    return lin_launch<T, DA, NW, false, FAST>(a, s);
 }
 
-template <typename T>
-hipError_t lin_run_depth(const LinArgs &a, int DA, int VT, hipStream_t s) {
-    const bool two = VT == 2;
+template <typename T, int NW, bool FAST>
+hipError_t lin_run_depth(const LinArgs &a, int DA, hipStream_t s) {
     switch (DA) {
-        case 32: return two ? lin_run<T, 32, 2>(a, s) : lin_run<T, 32, 1>(a, s);
-        case 64: return two ? lin_run<T, 64, 2>(a, s) : lin_run<T, 64, 1>(a, s);
-        case 128: return two ? lin_run<T, 128, 2>(a, s) : lin_run<T, 128, 1>(a, s);
-        default: return lin_run<T, 256, 1>(a, s);
+        case 32: return lin_run<T, 32, NW, FAST>(a, s);
+        case 64: return lin_run<T, 64, NW, FAST>(a, s);
+        case 128: return lin_run<T, 128, NW, FAST>(a, s);
+        default: return lin_run<T, 256, NW, FAST>(a, s);
     }
 }
 
-hipError_t lin_run_any(const LinArgs &a, bool bf16, int DA, int VT, hipStream_t s) {
-    return bf16 ? lin_run_depth<uint16_t>(a, DA, VT, s) : lin_run_depth<float>(a, DA, VT, s);
+template <typename T>
+hipError_t lin_run_type(const LinArgs &a, int DA, int NW, hipStream_t s) {
+    bool fast = true;
+    for (int i = 0; i < a.nroles; ++i) {
+        const Role &r = a.role[i];
+        fast = fast && r.Da == DA && r.Db % 16 == 0 && pieces_ok<T>(r.x, r.Da) && pieces_ok<T>(r.y, r.Da) &&
+               pieces_ok<T>(r.z, r.Db);
+    }
+    if (NW == 8) return fast ? lin_run_depth<T, 8, true>(a, DA, s) : lin_run_depth<T, 8, false>(a, DA, s);
+    return fast ? lin_run_depth<T, 4, true>(a, DA, s) : lin_run_depth<T, 4, false>(a, DA, s);
+}
+
+hipError_t lin_run_any(const LinArgs &a, bool bf16, int DA, int NW, hipStream_t s) {
+    return bf16 ? lin_run_type<uint16_t>(a, DA, NW, s) : lin_run_type<float>(a, DA, NW, s);
 }
 
 int chunk_of(bool bf16) { return bf16 ? Shape<uint16_t>::C : Shape<float>::C; }
@@ -770,7 +824,7 @@ int chunk_of(bool bf16) { return bf16 ? Shape<uint16_t>::C : Shape<float>::C; }
 struct BwdPlan {
     int n;             // launches
     int roles[2];      // roles of each
-    int DA[2], VT[2], slices[2];
+    int DA[2], NW[2], slices[2];
     Cut c[2];
     size_t part[2], shared_k, shared_v, total;
 };
@@ -785,23 +839,23 @@ BwdPlan bwd_plan(const LinDims &d, bool bf16) {
         p.n = 1;
         p.roles[0] = 3;
         p.DA[0] = da;
-        p.VT[0] = col_tiles(da, D);
-        p.slices[0] = slices_of(D, p.VT[0]);
+        p.NW[0] = waves_of(D);
+        p.slices[0] = slices_of(D, p.NW[0]);
     } else {
         p.n = 2;
         p.roles[0] = 2;
         p.DA[0] = da;
-        p.VT[0] = col_tiles(da, d.Dk);
-        p.slices[0] = slices_of(d.Dk, p.VT[0]);
+        p.NW[0] = waves_of(d.Dk);
+        p.slices[0] = slices_of(d.Dk, p.NW[0]);
         p.roles[1] = 1;
         p.DA[1] = db;
-        p.VT[1] = col_tiles(db, d.Dv);
-        p.slices[1] = slices_of(d.Dv, p.VT[1]);
+        p.NW[1] = waves_of(d.Dv);
+        p.slices[1] = slices_of(d.Dv, p.NW[1]);
     }
     for (int i = 0; i < p.n; ++i) {
         p.c[i] = cut(d.T, C, bh * p.slices[i] * p.roles[i]);
         p.part[i] = off;
-        off += p.roles[i] * part_bytes(d, p.DA[i], p.VT[i], p.slices[i], p.c[i].nseg);
+        off += p.roles[i] * part_bytes(d, p.DA[i], p.NW[i], p.slices[i], p.c[i].nseg);
     }
     p.shared_k = p.shared_v = off;
     if (d.NH != d.NKV) {
@@ -823,9 +877,9 @@ hipError_t share(const float *in, void *out, int64_t n, int grp, int D, hipStrea
 }  // namespace
 
 size_t lin_fwd_bytes(const LinDims &d, bool bf16) {
-    const int DA = pad_depth(d.Dk), VT = col_tiles(DA, d.Dv), sl = slices_of(d.Dv, VT);
+    const int DA = pad_depth(d.Dk), NW = waves_of(d.Dv), sl = slices_of(d.Dv, NW);
     const Cut c = cut(d.T, chunk_of(bf16), (long)d.B * d.NH * sl);
-    return part_bytes(d, DA, VT, sl, c.nseg);
+    return part_bytes(d, DA, NW, sl, c.nseg);
 }
 
 size_t lin_bwd_bytes(const LinDims &d, bool bf16) { return bwd_plan(d, bf16).total; }
@@ -858,17 +912,17 @@ hipError_t launch_lin_fwd(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSe
                           void *ws, hipStream_t s) {
     if (d.T == 1) return launch_lin_step(d, bf16, q, k, v, g, scale, S0, o, ST, s);
     LinArgs a{};
-    const int grp = d.NH / d.NKV, DA = pad_depth(d.Dk), VT = col_tiles(DA, d.Dv);
+    const int grp = d.NH / d.NKV, DA = pad_depth(d.Dk), NW = waves_of(d.Dv);
     a.nroles = 1;
     a.T = d.T; a.B = d.B; a.NH = d.NH;
     a.g = g;
-    a.slices = slices_of(d.Dv, VT);
+    a.slices = slices_of(d.Dv, NW);
     const Cut c = cut(d.T, chunk_of(bf16), (long)d.B * d.NH * a.slices);
     a.nseg = c.nseg;
     a.seg_rows = c.rows;
     a.role[0] = Role{q, k, v, 1, grp, grp, d.Dk, d.Dv, S0, 0, 1, ST, 1, 0, 1.0f, scale, o, 0,
                      (float *)ws};
-    return lin_run_any(a, bf16, DA, VT, s);
+    return lin_run_any(a, bf16, DA, NW, s);
 }
 
 hipError_t launch_lin_bwd(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSeq v,
@@ -894,12 +948,12 @@ hipError_t launch_lin_bwd(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSe
         a.slices = p.slices[i];
         a.nseg = p.c[i].nseg;
         a.seg_rows = p.c[i].rows;
-        const size_t each = part_bytes(d, p.DA[i], p.VT[i], p.slices[i], a.nseg);
+        const size_t each = part_bytes(d, p.DA[i], p.NW[i], p.slices[i], a.nseg);
         for (int j = 0; j < a.nroles; ++j) {
             a.role[j] = *order[next++];
             a.role[j].part = (float *)(base + p.part[i] + j * each);
         }
-        hipError_t e = lin_run_any(a, bf16, p.DA[i], p.VT[i], s);
+        hipError_t e = lin_run_any(a, bf16, p.DA[i], p.NW[i], s);
         if (e != hipSuccess) return e;
     }
     if (grp > 1) {
