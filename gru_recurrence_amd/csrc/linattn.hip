@@ -351,6 +351,10 @@ __device__ __forceinline__ int64_t part_at(const LinArgs &a, int bh, int slice, 
     return (((wg * NW + w) * (DA / 16) + tile) * 64 + lane) * 4;
 }
 
+// Up to this many segments a workgroup adds up the earlier ones' X itself; past
+// it their reading costs more than a launch.
+constexpr int kFold = 4;
+
 // STATE: only the segment's own X, from nothing, into its slot of `part`.
 // Two workgroups to a CU where their LDS allows it: one's barriers and loads
 // then hide behind the other's products.
@@ -409,15 +413,18 @@ void lin_kernel(LinArgs a) {
 #pragma unroll
     for (int t = 0; t < DT; ++t) X[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (!STATE) {
-        if (seg > 0) {
+        // the earlier segments' X: carried by a launch of its own, or added up here
+        const float fs = power(a.seg_rows);
+        for (int from = a.nseg <= kFold ? 1 : seg; from <= seg && from > 0; ++from) {
+            f32x4 v[DT];
 #pragma unroll
-            for (int t = 0; t < DT; ++t) {
-                const f32x4 v = *(const f32x4 *)(R.part + part_at<DA, NW>(a, bh, slice, seg, t));
-                // added, not assigned: the loads are then waited for here, where a
-                // wait inside the loop would be for the next chunk's loads as well
+            for (int t = 0; t < DT; ++t) v[t] = *(const f32x4 *)(R.part + part_at<DA, NW>(a, bh, slice, from, t));
+            // X is no plain copy of loads: those are then waited for here, where a
+            // wait inside the loop would be for the next chunk's loads as well
 #pragma unroll
-                for (int r = 0; r < 4; ++r) X[t][r] += v[r];
-            }
+            for (int t = 0; t < DT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) X[t][r] = fs * X[t][r] + v[t][r];
         }
         if (R.init) {
             const float f = power(row_lo + (R.init_decay ? 1 : 0));
@@ -481,6 +488,7 @@ void lin_kernel(LinArgs a) {
 #pragma unroll
                     for (int kb = 0; kb < PB; ++kb) mma(d, yf[kb], xf[kb]);
                 }
+                mfma_chain_end();
                 float e[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -515,6 +523,7 @@ void lin_kernel(LinArgs a) {
                     mma(o[i % RT], Xw, xf[i % (AX + 1)]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
+                mfma_chain_end();
 #pragma unroll
                 for (int it = 0; it < RT; ++it) {
                     const float f = power(it * 16) * powc;
@@ -533,17 +542,17 @@ void lin_kernel(LinArgs a) {
         for (int kb = 0; kb < RB; ++kb) across(zf[kb], zs, LDZ, wcol, kb, g, c);
 
         if constexpr (!STATE) {
-            // operand q belongs to tile row its[q], depth block jbs[q]
-            constexpr int its[6] = {0, 1, 2, 2, 3, 3}, jbs[6] = {0, 0, 0, 1, 0, 1};
+            // operand q belongs to tile row (0, 1, 2, 2, 3, 3)[q], depth block (0, 0, 0, 1, 0, 1)[q]
             Wide<T> pw[2];
             get_operand(pw[0], ps);
 #pragma unroll
             for (int q = 0; q < L::operands; ++q) {
                 if (q + 1 < L::operands) get_operand(pw[(q + 1) & 1], ps + (q + 1) * kOperand);
                 __builtin_amdgcn_sched_barrier(0);
-                mma(o[its[q]], zf[jbs[q]], pw[q & 1]);
+                mma(o[q < 2 ? q : 1 + q / 2], zf[q < 2 ? 0 : q & 1], pw[q & 1]);
                 __builtin_amdgcn_sched_barrier(0);
             }
+            mfma_chain_end();
             // lane: row it*16 + c, columns wcol + 4 g ..+3
             // 16 rows lie within 32 bits of each other (the host's check)
             const uint32_t pitch = (uint32_t)(a.B * a.NH * R.Db);
@@ -609,6 +618,7 @@ void lin_kernel(LinArgs a) {
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
+            mfma_chain_end();
         }
     }
     if constexpr (STATE) {
@@ -633,42 +643,52 @@ void lin_kernel(LinArgs a) {
 // gets sum_{s' < s} a^(L (s-1-s')) of them, L rows to a segment.  E: values of
 // one workgroup's X.
 __global__ __launch_bounds__(256) void lin_carry_kernel(LinArgs a, int E) {
-    constexpr int kAhead = 8;  // segments loaded at a time
+    constexpr int kAhead = 16;  // segments loaded at a time
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t per = (int64_t)a.B * a.NH * a.slices * (E / 4);
+    const int64_t per = (int64_t)a.B * a.NH * a.slices * E;
     if (i >= per * a.nroles) return;
     const Role &R = a.role[i / per];
-    const int64_t j = i % per, wg = j / (E / 4);
+    const int64_t j = i % per, wg = j / E;
     const int h = (int)(wg / a.slices % a.NH);
     const float f = __builtin_amdgcn_exp2f(fmaxf(a.g[h] * kLog2e, -1e30f) * (float)a.seg_rows);
-    f32x4 *p = (f32x4 *)R.part + wg * a.nseg * (E / 4) + j % (E / 4);
-    f32x4 X{0.0f, 0.0f, 0.0f, 0.0f};
+    float *p = R.part + wg * a.nseg * E + j % E;
+    float X = 0.0f;
     for (int s = 1; s < a.nseg; s += kAhead) {
-        f32x4 own[kAhead];
+        float own[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) own[u] = p[(int64_t)min(s + u, a.nseg - 1) * E];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-            if (s + u < a.nseg) own[u] = p[(int64_t)(s + u) * (E / 4)];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (s + u < a.nseg) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) X[r] = f * X[r] + own[u][r];
-                p[(int64_t)(s + u) * (E / 4)] = X;
-            }
+            if (s + u < a.nseg) p[(int64_t)(s + u) * E] = X = f * X + own[u];
     }
 }
 
-// Gradients of a shared head: the sum over its `grp` heads, in order.
-template <typename T>
-__global__ __launch_bounds__(256) void lin_share_kernel(const float *__restrict__ in, T *__restrict__ out,
-                                                        int64_t n, int grp, int D) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    const int64_t head = i / D;
-    const float *p = in + head * grp * D + i % D;
-    float s = 0.0f;
-    for (int j = 0; j < grp; ++j) s += p[(int64_t)j * D];
-    out[i] = from_f32<T>(s);
+// Gradients of a shared head: the sum over its `grp` heads, in order; V values
+// of one head to a thread, dk in the first workgroups and dv in the rest.
+struct ShareArgs {
+    const float *in[2];
+    void *out[2];
+    int64_t n[2];  // outputs / V
+    int D[2], grp;
+};
+template <typename T, int V>
+__global__ __launch_bounds__(256) void lin_share_kernel(ShareArgs a, unsigned blocks0) {
+    const int which = blockIdx.x >= blocks0;
+    const int64_t i = (int64_t)(blockIdx.x - (which ? blocks0 : 0)) * 256 + threadIdx.x;
+    if (i >= a.n[which]) return;
+    const int per = a.D[which] / V;
+    const int64_t head = i / per;
+    const Unit<float, V> *p = (const Unit<float, V> *)a.in[which] + head * a.grp * per + i % per;
+    Unit<float, V> s = p[0];
+    for (int j = 1; j < a.grp; ++j) {
+        const Unit<float, V> x = p[(int64_t)j * per];
+#pragma unroll
+        for (int e = 0; e < V; ++e) s.v[e] += x.v[e];
+    }
+    Unit<T, V> o;
+#pragma unroll
+    for (int e = 0; e < V; ++e) o.v[e] = from_f32<T>(s.v[e]);
+    ((Unit<T, V> *)a.out[which])[i] = o;
 }
 
 constexpr int kStepCols = 64;
@@ -783,11 +803,13 @@ hipError_t lin_run(const LinArgs &a, hipStream_t s) {
     if (a.nseg > 1) {
         hipError_t e = lin_launch<T, DA, NW, true, FAST>(a, s);
         if (e != hipSuccess) return e;
-        const int E = DA * 16 * NW;
-        const long n = (long)a.nroles * a.B * a.NH * a.slices * (E / 4);
-        hipLaunchKernelGGL(lin_carry_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, E);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        if (a.nseg > kFold) {
+            const int E = DA * 16 * NW;
+            const long n = (long)a.nroles * a.B * a.NH * a.slices * E;
+            hipLaunchKernelGGL(lin_carry_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, E);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
     }
     return lin_launch<T, DA, NW, false, FAST>(a, s);
 }
@@ -867,10 +889,11 @@ BwdPlan bwd_plan(const LinDims &d, bool bf16) {
     return p;
 }
 
-template <typename T>
-hipError_t share(const float *in, void *out, int64_t n, int grp, int D, hipStream_t s) {
-    hipLaunchKernelGGL(lin_share_kernel<T>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, in,
-                       (T *)out, n, grp, D);
+template <typename T, int V>
+hipError_t share(ShareArgs a, hipStream_t s) {
+    for (int i = 0; i < 2; ++i) a.n[i] /= V;
+    const unsigned b0 = (unsigned)((a.n[0] + 255) / 256), b1 = (unsigned)((a.n[1] + 255) / 256);
+    hipLaunchKernelGGL((lin_share_kernel<T, V>), dim3(b0 + b1), dim3(256), 0, s, a, b0);
     return hipGetLastError();
 }
 
@@ -958,11 +981,10 @@ hipError_t launch_lin_bwd(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSe
     }
     if (grp > 1) {
         const int64_t n = (int64_t)d.T * d.B * d.NKV;
-        hipError_t e = bf16 ? share<uint16_t>(pk, dk, n * d.Dk, grp, d.Dk, s)
-                            : share<float>(pk, dk, n * d.Dk, grp, d.Dk, s);
-        if (e != hipSuccess) return e;
-        return bf16 ? share<uint16_t>(pv, dv, n * d.Dv, grp, d.Dv, s)
-                    : share<float>(pv, dv, n * d.Dv, grp, d.Dv, s);
+        const ShareArgs a{{pk, pv}, {dk, dv}, {n * d.Dk, n * d.Dv}, {d.Dk, d.Dv}, grp};
+        if (d.Dk % 4 == 0 && d.Dv % 4 == 0)
+            return bf16 ? share<uint16_t, 4>(a, s) : share<float, 4>(a, s);
+        return bf16 ? share<uint16_t, 1>(a, s) : share<float, 1>(a, s);
     }
     return hipSuccess;
 }

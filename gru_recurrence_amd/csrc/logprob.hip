@@ -116,16 +116,28 @@ __device__ __forceinline__ void write_row(const LogpArgs &a, int row, const Fina
     if (a.lse) a.lse[row] = f.lse;
 }
 
-// Ranks n unique keys (LDS) by counting and hands (rank, key) of the K
-// largest to out.
+// Ranks n unique keys (LDS, 16-byte aligned, room for an even number) by
+// counting and hands (rank, key) of the K largest to out.  Four threads share
+// a key's comparisons.
 template <typename F>
-__device__ __forceinline__ void rank_keys(const uint64_t *key, int n, int K, F out) {
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+__device__ __forceinline__ void rank_keys(uint64_t *key, int n, int K, F out) {
+    const int part = threadIdx.x & 3;
+    if (n & 1) {
+        if (threadIdx.x == 0) key[n] = 0;  // below every key
+        __syncthreads();
+    }
+    for (int i = threadIdx.x >> 2; i < n; i += kThreads / 4) {
         const uint64_t mine = key[i];
+        const ulonglong2 *pair = (const ulonglong2 *)key;
         int r = 0;
-#pragma unroll 8
-        for (int j = 0; j < n; ++j) r += key[j] > mine;
-        if (r < K) out(r, mine);
+#pragma unroll 4
+        for (int j = part; j < (n + 1) / 2; j += 4) {
+            const ulonglong2 q = pair[j];
+            r += (q.x > mine) + (q.y > mine);
+        }
+        r += __shfl_xor(r, 1);
+        r += __shfl_xor(r, 2);
+        if (part == 0 && r < K) out(r, mine);
     }
 }
 
@@ -192,7 +204,7 @@ __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
     constexpr int N = Row<T>::N, U = kPer / N;
     __shared__ float wm[4], ws[4], wt[4];
     __shared__ __attribute__((aligned(16))) float tm[64];
-    __shared__ uint64_t cand[TOP ? kCand : 1];
+    __shared__ __attribute__((aligned(16))) uint64_t cand[TOP ? kCand + 2 : 2];
     __shared__ int ncand, tmp[4];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int row = blockIdx.x / nch, ch = blockIdx.x - row * nch;
@@ -309,14 +321,31 @@ __global__ __launch_bounds__(kThreads) void logp_join_kernel(LogpArgs a, int nch
     t = wave_sum(t);
     const Final f = finish(m, s, t);
     if (tid == 0) write_row<T>(a, row, f);
+    if (a.K == 0) return;
+    // a chunk whose last key is the largest of the last keys has K of them at or
+    // above that bound: only keys that reach it can be among the row's K
+    __shared__ __attribute__((aligned(16))) uint64_t kept[kCand + 2];
+    __shared__ int nkept;
+    if (tid == 0) nkept = 0;
     __syncthreads();
-    if (a.K)
-        rank_keys(keys, nch * a.K, a.K, [&](int k, uint64_t key) {
-            if (key == 0) return;
-            a.top_id[(int64_t)row * a.K + k] = (int)~(uint32_t)key;
-            a.top_logp[(int64_t)row * a.K + k] =
-                minus_lse(key_value((uint32_t)(key >> 32)), f.lse);
-        });
+    uint64_t bound = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (i * 64 + lane < nch) bound = max(bound, keys[(i * 64 + lane) * a.K + a.K - 1]);
+#pragma unroll
+    for (int o = 32; o; o >>= 1) bound = max(bound, (uint64_t)__shfl_xor((unsigned long long)bound, o));
+    for (int i = tid; i < nch * a.K; i += kThreads)
+        if (keys[i] >= bound) {
+            const int at = atomicAdd(&nkept, 1);
+            if (at < kCand) kept[at] = keys[i];
+        }
+    __syncthreads();
+    const int n = nkept;
+    rank_keys(n <= kCand ? kept : keys, n <= kCand ? n : nch * a.K, a.K, [&](int k, uint64_t key) {
+        if (key == 0) return;
+        a.top_id[(int64_t)row * a.K + k] = (int)~(uint32_t)key;
+        a.top_logp[(int64_t)row * a.K + k] = minus_lse(key_value((uint32_t)(key >> 32)), f.lse);
+    });
 }
 
 // dl for 4 units of 256 threads each.
@@ -376,7 +405,7 @@ hipError_t logp_t(const LogpArgs &a, hipStream_t s) {
         hipLaunchKernelGGL((logp_kernel<T, false>), grid, dim3(kThreads), 0, s, a, nch);
     if (nch > 1)
         hipLaunchKernelGGL(logp_join_kernel<T>, dim3((unsigned)a.M), dim3(kThreads),
-                           (size_t)nch * a.K * 8, s, a, nch);
+                           ((size_t)nch * a.K + 2) * 8, s, a, nch);
     return hipGetLastError();
 }
 
