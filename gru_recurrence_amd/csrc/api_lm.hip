@@ -97,9 +97,10 @@ rnn_status rnn_token_logprobs(int M, int V, rnn_dtype dt, const void *logits, in
     if (!view_ok(logits, elt(dt)) || !view_ok(tok, it == RNN_I64 ? 8 : 4) || !logp)
         return RNN_ERR_INVALID_ARG;
     if (K > 0 && (!top_logp || !top_id)) return RNN_ERR_INVALID_ARG;
-    const void *ps[] = {logp, entropy, lse, top_logp, top_id, ws};
+    const void *ps[] = {logp, entropy, lse, top_logp, top_id};
     for (const void *p : ps)
-        if (!aligned16(p)) return RNN_ERR_INVALID_ARG;
+        if (p && !view_ok(p, 4)) return RNN_ERR_INVALID_ARG;
+    if (!aligned16(ws)) return RNN_ERR_INVALID_ARG;
     if (V > kMaxVocab || K > lm::kMaxTop || !lm::logp_grid_ok(M, V)) return RNN_ERR_UNSUPPORTED;
     const size_t need = lm::logp_bytes(M, V, K);
     if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;
@@ -119,7 +120,7 @@ rnn_status rnn_token_logprobs_bwd(int M, int V, rnn_dtype dt, const void *logits
         return RNN_ERR_INVALID_ARG;
     const void *ps[] = {lse, entropy, dlogp, dentropy};
     for (const void *p : ps)
-        if (!aligned16(p)) return RNN_ERR_INVALID_ARG;
+        if (p && !view_ok(p, 4)) return RNN_ERR_INVALID_ARG;
     if (V > kMaxVocab || !lm::logp_grid_ok(M, V)) return RNN_ERR_UNSUPPORTED;
     lm::LogpBwdArgs a{M, V, logits, ld, tok, it == RNN_I64, lse, entropy, dlogp, dentropy, dlogits, ldd};
     return done(lm::launch_logp_bwd(a, dt == RNN_BF16, stream));

@@ -20,6 +20,8 @@
 //     carry;
 //  3. the carries of each run of pieces with the same open row are added to
 //     that row, in order.
+#include <algorithm>
+
 #include "common.h"
 #include "lm.h"
 
@@ -129,6 +131,21 @@ __device__ __forceinline__ void rank_items(const uint32_t *key, int nmine, int s
     }
 }
 
+// A digit's counts in the waves (at cnt, `ND` apart) -> `from` plus those of
+// earlier waves; returns their total.
+__device__ __forceinline__ int add_waves(int *cnt, int ND, int from) {
+    int c[kSortWaves];
+#pragma unroll
+    for (int i = 0; i < kSortWaves; ++i) c[i] = cnt[i * ND];
+    int s = from;
+#pragma unroll
+    for (int i = 0; i < kSortWaves; ++i) {
+        cnt[i * ND] = s;
+        s += c[i];
+    }
+    return s - from;
+}
+
 // Exclusive prefix sum over the first ND entries of tot (LDS), in place.
 __device__ __forceinline__ void scan_digits(int *tot, int ND, int *tmp) {
     const int tid = threadIdx.x;
@@ -142,7 +159,8 @@ __device__ __forceinline__ void scan_digits(int *tot, int ND, int *tmp) {
     if (lane == 63) tmp[w] = x;
     __syncthreads();
     int base = 0;
-    for (int i = 0; i < w; ++i) base += tmp[i];
+#pragma unroll
+    for (int i = 0; i < kSortWaves; ++i) base += i < w ? tmp[i] : 0;
     if (tid < ND) tot[tid] = base + x - v;
     __syncthreads();
 }
@@ -171,16 +189,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(Ids ids, int V, 
         __syncthreads();
         rank_items<R>(key, nmine, p * rb, rb, cnt + w * ND, rank);
         __syncthreads();
-        if (tid < ND) {  // counts of earlier waves, total
-            int s = 0;
-#pragma unroll
-            for (int i = 0; i < kSortWaves; ++i) {
-                const int c = cnt[i * ND + tid];
-                cnt[i * ND + tid] = s;
-                s += c;
-            }
-            tot[tid] = s;
-        }
+        if (tid < ND) tot[tid] = add_waves(cnt + tid, ND, 0);
         __syncthreads();
         scan_digits(tot, ND, tmp);
 #pragma unroll
@@ -225,7 +234,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(Ids ids, int V
 }
 
 // The same pass's scatter: a block's place for a digit is the count of all
-// smaller digits plus that of the digit in earlier blocks.
+// smaller digits plus that of the digit in earlier blocks.  (A launch apart
+// from the count: where each of 16 blocks counted all 16384 items itself, a
+// pass took 13-18 us instead of 3.3 + 5.3.)
 template <int R>
 __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
     Ids ids, int V, int shift, int rb, const uint32_t *ikey, const uint32_t *ipos, const int *hist,
@@ -262,15 +273,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
     __syncthreads();
     rank_items<R>(key, nmine, shift, rb, cnt + w * ND, rank);
     scan_digits(tot, ND, tmp);  // its barriers also order cnt
-    if (tid < ND) {
-        int s = tot[tid] + mine;
-#pragma unroll
-        for (int i = 0; i < kSortWaves; ++i) {
-            const int c = cnt[i * ND + tid];
-            cnt[i * ND + tid] = s;
-            s += c;
-        }
-    }
+    if (tid < ND) add_waves(cnt + tid, ND, tot[tid] + mine);
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -285,7 +288,11 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
 // A wave sums columns [tile*64*N, ...) of its piece: VEC lanes hold N
 // neighbouring columns, otherwise N columns 64 apart (any width, any
 // alignment).
-constexpr int kPiece = 32;   // items (positions and row ends) of one piece
+// Items (positions and row ends) of one piece: 32, fewer (down to 8) where
+// that would leave less than about 4096 waves.
+int piece_items(long M, long V, int tiles) {
+    return (int)std::min(32L, std::max(8L, (M + V + 1) * tiles / 4096));
+}
 constexpr int kInFlight = 8; // rows a wave has in flight
 
 template <typename T, int N, bool VEC>
@@ -347,7 +354,7 @@ __device__ __forceinline__ int merge_cut(const uint32_t *key, int M, int V, long
 }
 
 template <typename T, int N, bool VEC>
-__global__ __launch_bounds__(256) void embed_sum_kernel(int M, int V, int D, int pieces,
+__global__ __launch_bounds__(256) void embed_sum_kernel(int M, int V, int D, int pieces, int piece,
                                                         const uint32_t *__restrict__ key,
                                                         const uint32_t *__restrict__ pos,
                                                         const T *__restrict__ dx, float scale,
@@ -358,7 +365,7 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(int M, int V, int D, int
     const int w = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
     if (w >= pieces) return;
     const long items = (long)M + V + 1;
-    const long d0 = (long)w * kPiece, d1 = min(d0 + kPiece, items);
+    const long d0 = (long)w * piece, d1 = min(d0 + piece, items);
     const int cut = merge_cut(key, M, V, lane < 32 ? d0 : d1);
     const int p0 = __builtin_amdgcn_readlane(cut, 0), p1 = __builtin_amdgcn_readlane(cut, 32);
     int v = (int)(d0 - p0);
@@ -443,7 +450,13 @@ __global__ __launch_bounds__(256) void embed_carry_kernel(int V, int D, int piec
 }
 
 size_t up(size_t v) { return (v + 255) & ~(size_t)255; }
-long pieces_of(long M, long V) { return (M + V + 1 + kPiece - 1) / kPiece; }
+// Columns per lane: as many neighbours as fill one wave.
+int cols_per_lane(int D) { return D > 128 ? 4 : D > 64 ? 2 : 1; }
+int col_tiles(int D) { return (D + 64 * cols_per_lane(D) - 1) / (64 * cols_per_lane(D)); }
+long pieces_of(long M, long V, int D) {
+    const int piece = piece_items(M, V, col_tiles(D));
+    return (M + V + 1 + piece - 1) / piece;
+}
 
 // Items per thread of the blocked sort: few blocks' counts to add up, and yet
 // many blocks.
@@ -466,8 +479,8 @@ BwdWs bwd_ws(int M, int V, int D) {
         const int per = kSortThreads * sort_rounds(M);
         w.hist = off; off += up(sizeof(int) * (size_t)((M + per - 1) / per) * kMaxDigits);
     }
-    w.crow = off; off += up(sizeof(int) * (size_t)pieces_of(M, V));
-    w.carry = off; off += up(sizeof(float) * (size_t)pieces_of(M, V) * D);
+    w.crow = off; off += up(sizeof(int) * (size_t)pieces_of(M, V, D));
+    w.carry = off; off += up(sizeof(float) * (size_t)pieces_of(M, V, D) * D);
     w.total = off;
     return w;
 }
@@ -475,10 +488,10 @@ BwdWs bwd_ws(int M, int V, int D) {
 template <typename T, int N, bool VEC>
 hipError_t sums(int M, int V, int D, const uint32_t *key, const uint32_t *pos, const T *dx,
                 float scale, float *dtable, float *carry, int *crow, hipStream_t s) {
-    const int pieces = (int)pieces_of(M, V), tiles = (D + 64 * N - 1) / (64 * N);
+    const int tiles = col_tiles(D), pieces = (int)pieces_of(M, V, D);
     const dim3 grid((pieces + 3) / 4, tiles);
-    hipLaunchKernelGGL((embed_sum_kernel<T, N, VEC>), grid, dim3(256), 0, s, M, V, D, pieces, key,
-                       pos, dx, scale, dtable, carry, crow);
+    hipLaunchKernelGGL((embed_sum_kernel<T, N, VEC>), grid, dim3(256), 0, s, M, V, D, pieces,
+                       piece_items(M, V, tiles), key, pos, dx, scale, dtable, carry, crow);
     hipLaunchKernelGGL((embed_carry_kernel<N, VEC>), grid, dim3(256), 0, s, V, D, pieces, scale,
                        dtable, carry, crow);
     return hipGetLastError();
@@ -487,11 +500,10 @@ hipError_t sums(int M, int V, int D, const uint32_t *key, const uint32_t *pos, c
 template <typename T>
 hipError_t sums_t(int M, int V, int D, const uint32_t *key, const uint32_t *pos, const T *dx,
                   float scale, float *dtable, float *carry, int *crow, hipStream_t s) {
-    // as many neighbouring columns per lane as fill one wave
-    if (D > 128)
+    if (cols_per_lane(D) == 4)
         return D % 4 == 0 ? sums<T, 4, true>(M, V, D, key, pos, dx, scale, dtable, carry, crow, s)
                           : sums<T, 4, false>(M, V, D, key, pos, dx, scale, dtable, carry, crow, s);
-    if (D > 64)
+    if (cols_per_lane(D) == 2)
         return D % 2 == 0 ? sums<T, 2, true>(M, V, D, key, pos, dx, scale, dtable, carry, crow, s)
                           : sums<T, 2, false>(M, V, D, key, pos, dx, scale, dtable, carry, crow, s);
     return sums<T, 1, true>(M, V, D, key, pos, dx, scale, dtable, carry, crow, s);
@@ -527,8 +539,8 @@ hipError_t launch_embed_bwd(const Ids &ids, int V, int D, bool bf16, const void 
         hipLaunchKernelGGL(sort_one_kernel<4>, dim3(1), dim3(kSortThreads), 0, s, ids, V, rb, passes,
                            key[0], pos[0]);
     } else {
-        int *hist = (int *)(base + w.hist);
         const int R = sort_rounds(M), per = kSortThreads * R;
+        int *hist = (int *)(base + w.hist);
         const dim3 grid((M + per - 1) / per), thr(kSortThreads);
         for (int p = 0; p < passes; ++p) {
             const uint32_t *ik = p ? key[(p - 1) & 1] : nullptr, *ip = p ? pos[(p - 1) & 1] : nullptr;

@@ -8,20 +8,24 @@
 // and backward, p_v = e^(l_v - lse):
 //   dl_v = dlogp ([v = y] - p_v) - dH p_v (l_v - lse + H)
 //
-// The forward reads every logit once: a workgroup holds a chunk of 8192 of a
-// row in registers, takes the chunk's maximum, sums and K candidates from
-// there, and a second launch joins a row's chunks (only where V needs more
-// than one).  Chunks rather than whole rows: a few rows with a long
-// vocabulary then fill the chip, and small workgroups hide each other's
-// reductions.  All sums are float32.
+// The forward reads every logit once: a workgroup holds a chunk of a row in
+// registers, 32 values to a thread, takes the chunk's maximum, sums and K
+// candidates from there, and a second launch joins a row's chunks (only where
+// V needs more than one).  Chunks of 8192 values rather than whole rows: a few
+// rows with a long vocabulary then fill the chip, and small workgroups hide
+// each other's reductions (4096 rows of 32000 float32: 92 us and 7 for the
+// join; chunks of 32768 with 1024 threads, no join: 122).  All sums are
+// float32.
 //
 // The K candidates of a chunk: the K-th largest of the maxima of 64 groups of
-// four threads is a bound that at least K entries reach, and few more do.
+// threads is a bound that at least K entries reach, and few more do.
 // Those that reach it are collected (any order) and ranked by counting over
 // the unique keys (value, index), so the result does not depend on the order.
 // Where ties or a sorted row let more than kCand through, the K-th key is
 // found exactly by bisection over value and index instead (the chunk is read
 // again for it: held on to, it cost the ordinary path its registers).
+#include <algorithm>
+
 #include "lm.h"
 
 namespace rnn355 {
@@ -119,14 +123,14 @@ __device__ __forceinline__ void write_row(const LogpArgs &a, int row, const Fina
 // Ranks n unique keys (LDS, 16-byte aligned, room for an even number) by
 // counting and hands (rank, key) of the K largest to out.  Four threads share
 // a key's comparisons.
-template <typename F>
+template <int NT, typename F>
 __device__ __forceinline__ void rank_keys(uint64_t *key, int n, int K, F out) {
     const int part = threadIdx.x & 3;
     if (n & 1) {
         if (threadIdx.x == 0) key[n] = 0;  // below every key
         __syncthreads();
     }
-    for (int i = threadIdx.x >> 2; i < n; i += kThreads / 4) {
+    for (int i = threadIdx.x >> 2; i < n; i += NT / 4) {
         const uint64_t mine = key[i];
         const ulonglong2 *pair = (const ulonglong2 *)key;
         int r = 0;
@@ -142,18 +146,22 @@ __device__ __forceinline__ void rank_keys(uint64_t *key, int n, int K, F out) {
 }
 
 // Number of threads' entries that satisfy a predicate, over the workgroup.
+template <int NT>
 __device__ __forceinline__ int block_count(int mine, int *tmp) {
 #pragma unroll
     for (int o = 32; o; o >>= 1) mine += __shfl_xor(mine, o);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = mine;
     __syncthreads();
-    return tmp[0] + tmp[1] + tmp[2] + tmp[3];
+    int all = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) all += tmp[i];
+    return all;
 }
 
 // The K largest keys of a chunk, exactly, in `cand`; returns their number (K,
 // or the chunk's entries if those are fewer).
-template <typename T>
+template <typename T, int NT>
 __device__ __forceinline__ int exact_top(Row<T> r, int u0, int K, uint64_t *cand, int *ncand, int *tmp) {
     constexpr int N = Row<T>::N, U = kPer / N;
     const int tid = threadIdx.x;
@@ -162,14 +170,14 @@ __device__ __forceinline__ int exact_top(Row<T> r, int u0, int K, uint64_t *cand
         int k = 0;
 #pragma unroll 1
         for (int j = 0; j < U; ++j) {
-            const int u = u0 + j * kThreads + tid, i0 = u * N - r.off;
+            const int u = u0 + j * NT + tid, i0 = u * N - r.off;
             float x[N];
             r.load(u, x);
 #pragma unroll
             for (int e = 0; e < N; ++e)
                 k += i0 + e >= 0 && i0 + e < r.V && pred(order_key(x[e]), i0 + e);
         }
-        return block_count(k, tmp);
+        return block_count<NT>(k, tmp);
     };
     // the largest value key that at least K entries reach
     uint32_t vk = 0;
@@ -201,33 +209,35 @@ __device__ __forceinline__ int exact_top(Row<T> r, int u0, int K, uint64_t *cand
 
 template <typename T, bool TOP>
 __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
-    constexpr int N = Row<T>::N, U = kPer / N;
-    __shared__ float wm[4], ws[4], wt[4];
+    constexpr int NT = kThreads, N = Row<T>::N, U = kPer / N, W = NT / 64, GROUP = NT / 64;
+    __shared__ float wm[W], ws[W], wt[W];
     __shared__ __attribute__((aligned(16))) float tm[64];
     __shared__ __attribute__((aligned(16))) uint64_t cand[TOP ? kCand + 2 : 2];
-    __shared__ int ncand, tmp[4];
+    __shared__ int ncand, tmp[W];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int row = blockIdx.x / nch, ch = blockIdx.x - row * nch;
     const Row<T> r((const T *)a.logits + (int64_t)row * a.ld, a.V);
-    const int u0 = ch * (kChunk / N);
+    const int u0 = ch * (NT * kPer / N);
     float x[kPer];
 #pragma unroll
-    for (int j = 0; j < U; ++j) r.load(u0 + j * kThreads + tid, x + j * N);
+    for (int j = 0; j < U; ++j) r.load(u0 + j * NT + tid, x + j * N);
 
     float m = x[0];
 #pragma unroll
     for (int i = 1; i < kPer; ++i) m = fmaxf(m, x[i]);
     if constexpr (TOP) {
-        const float q = m != m ? INFINITY : m;  // nothing but NaN: a bound all the same
-        const float h = fmaxf(q, __shfl_xor(q, 1));
-        const float f = fmaxf(h, __shfl_xor(h, 2));
-        if ((tid & 3) == 0) tm[tid >> 2] = f;
+        float q = m != m ? INFINITY : m;  // nothing but NaN: a bound all the same
+#pragma unroll
+        for (int o = 1; o < GROUP; o <<= 1) q = fmaxf(q, __shfl_xor(q, o));
+        if (tid % GROUP == 0) tm[tid / GROUP] = q;
         if (tid == 0) ncand = 0;
     }
     m = wave_max(m);
     if (lane == 0) wm[w] = m;
     __syncthreads();
-    m = fmaxf(fmaxf(wm[0], wm[1]), fmaxf(wm[2], wm[3]));
+    m = wm[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) m = fmaxf(m, wm[i]);
     // a chunk of nothing but -inf: weights e^(-inf - 0) = 0
     const float ref = m == -INFINITY ? 0.0f : m;
     float s = 0.0f, t = 0.0f;
@@ -257,7 +267,7 @@ __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             if (!(x[i] < tau)) {
-                const int idx = (u0 + (i / N) * kThreads + tid) * N + (i % N) - r.off;
+                const int idx = (u0 + (i / N) * NT + tid) * N + (i % N) - r.off;
                 if (idx >= 0 && idx < a.V) {
                     const int at = atomicAdd(&ncand, 1);
                     if (at < kCand) cand[at] = pair_key(x[i], idx);
@@ -266,8 +276,9 @@ __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
         }
     }
     __syncthreads();
-    s = ws[0] + ws[1] + ws[2] + ws[3];
-    t = wt[0] + wt[1] + wt[2] + wt[3];
+    s = t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) s += ws[i], t += wt[i];
     const Final f = finish(m, s, t);
     if (tid == 0) {
         if (nch == 1)
@@ -277,9 +288,9 @@ __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
     }
     if constexpr (TOP) {
         int n = ncand;
-        if (n > kCand) n = exact_top<T>(r, u0, a.K, cand, &ncand, tmp);
+        if (n > kCand) n = exact_top<T, NT>(r, u0, a.K, cand, &ncand, tmp);
         if (nch == 1) {
-            rank_keys(cand, n, a.K, [&](int k, uint64_t key) {
+            rank_keys<NT>(cand, n, a.K, [&](int k, uint64_t key) {
                 a.top_id[(int64_t)row * a.K + k] = (int)~(uint32_t)key;
                 a.top_logp[(int64_t)row * a.K + k] =
                     minus_lse(key_value((uint32_t)(key >> 32)), f.lse);
@@ -287,21 +298,22 @@ __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
         } else {
             uint64_t *out = (uint64_t *)((Part *)a.ws + (int64_t)a.M * nch) + (int64_t)blockIdx.x * a.K;
             // a chunk with fewer than K entries leaves the lowest key for the rest
-            for (int k = n + tid; k < a.K; k += kThreads) out[k] = 0;
-            rank_keys(cand, n, a.K, [&](int k, uint64_t key) { out[k] = key; });
+            for (int k = n + tid; k < a.K; k += NT) out[k] = 0;
+            rank_keys<NT>(cand, n, a.K, [&](int k, uint64_t key) { out[k] = key; });
         }
     }
 }
 
 // Joins the chunks of a row.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void logp_join_kernel(LogpArgs a, int nch) {
+template <typename T, int NT>
+__global__ __launch_bounds__(NT) void logp_join_kernel(LogpArgs a, int nch) {
+    constexpr int CAP = NT == 64 ? 256 : kCand;
     extern __shared__ __attribute__((aligned(16))) uint64_t keys[];
     const int row = blockIdx.x, tid = threadIdx.x;
     const Part *p = (const Part *)a.ws + (int64_t)row * nch;
     const uint64_t *in = (const uint64_t *)((const Part *)a.ws + (int64_t)a.M * nch) +
                          (int64_t)row * nch * a.K;
-    for (int i = tid; i < nch * a.K; i += kThreads) keys[i] = in[i];
+    for (int i = tid; i < nch * a.K; i += NT) keys[i] = in[i];
     // a lane to a chunk, two where there are more than 64 (V <= 1000000: at most 123)
     const int lane = tid & 63;
     Part q[2];
@@ -324,7 +336,7 @@ __global__ __launch_bounds__(kThreads) void logp_join_kernel(LogpArgs a, int nch
     if (a.K == 0) return;
     // a chunk whose last key is the largest of the last keys has K of them at or
     // above that bound: only keys that reach it can be among the row's K
-    __shared__ __attribute__((aligned(16))) uint64_t kept[kCand + 2];
+    __shared__ __attribute__((aligned(16))) uint64_t kept[CAP + 2];
     __shared__ int nkept;
     if (tid == 0) nkept = 0;
     __syncthreads();
@@ -334,14 +346,14 @@ __global__ __launch_bounds__(kThreads) void logp_join_kernel(LogpArgs a, int nch
         if (i * 64 + lane < nch) bound = max(bound, keys[(i * 64 + lane) * a.K + a.K - 1]);
 #pragma unroll
     for (int o = 32; o; o >>= 1) bound = max(bound, (uint64_t)__shfl_xor((unsigned long long)bound, o));
-    for (int i = tid; i < nch * a.K; i += kThreads)
+    for (int i = tid; i < nch * a.K; i += NT)
         if (keys[i] >= bound) {
             const int at = atomicAdd(&nkept, 1);
-            if (at < kCand) kept[at] = keys[i];
+            if (at < CAP) kept[at] = keys[i];
         }
     __syncthreads();
     const int n = nkept;
-    rank_keys(n <= kCand ? kept : keys, n <= kCand ? n : nch * a.K, a.K, [&](int k, uint64_t key) {
+    rank_keys<NT>(n <= CAP ? kept : keys, n <= CAP ? n : nch * a.K, a.K, [&](int k, uint64_t key) {
         if (key == 0) return;
         a.top_id[(int64_t)row * a.K + k] = (int)~(uint32_t)key;
         a.top_logp[(int64_t)row * a.K + k] = minus_lse(key_value((uint32_t)(key >> 32)), f.lse);
@@ -398,14 +410,19 @@ int chunks(int V, int per, size_t elt) {
 template <typename T>
 hipError_t logp_t(const LogpArgs &a, hipStream_t s) {
     const int nch = chunks(a.V, kChunk, sizeof(T));
-    const dim3 grid((unsigned)((long)a.M * nch));
+    const dim3 grid((unsigned)((long)a.M * nch)), thr(kThreads);
     if (a.K)
-        hipLaunchKernelGGL((logp_kernel<T, true>), grid, dim3(kThreads), 0, s, a, nch);
+        hipLaunchKernelGGL((logp_kernel<T, true>), grid, thr, 0, s, a, nch);
     else
-        hipLaunchKernelGGL((logp_kernel<T, false>), grid, dim3(kThreads), 0, s, a, nch);
-    if (nch > 1)
-        hipLaunchKernelGGL(logp_join_kernel<T>, dim3((unsigned)a.M), dim3(kThreads),
-                           ((size_t)nch * a.K + 2) * 8, s, a, nch);
+        hipLaunchKernelGGL((logp_kernel<T, false>), grid, thr, 0, s, a, nch);
+    if (nch > 1) {
+        // a wave joins a row where its keys are few: more rows are then in flight
+        const size_t lds = ((size_t)nch * a.K + 2) * 8;
+        if (nch * a.K <= 256)
+            hipLaunchKernelGGL((logp_join_kernel<T, 64>), dim3((unsigned)a.M), dim3(64), lds, s, a, nch);
+        else
+            hipLaunchKernelGGL((logp_join_kernel<T, 256>), dim3((unsigned)a.M), dim3(256), lds, s, a, nch);
+    }
     return hipGetLastError();
 }
 

@@ -242,8 +242,12 @@ def token_logprobs(logits, tokens, top: int = 0, *, ws=None, out=None):
     M, V = rows.shape
     lead = logits.shape[:-1]
     tp = _dense(tokens, "tokens", tokens.dtype, lead, dev)
-    out = out or {}
-    r = {k: _new(out.get(k), k, torch.float32, lead, dev) for k in ("logp", "entropy", "lse")}
+    names = ("logp", "entropy", "lse")
+    if out:
+        r = {k: _new(out.get(k), k, torch.float32, lead, dev) for k in names}
+    else:  # one allocation for the three
+        out = {}
+        r = dict(zip(names, torch.empty((3, *lead), dtype=torch.float32, device=dev).unbind()))
     kp = ki = None
     if top:
         r["top_logp"] = _new(out.get("top_logp"), "top_logp", torch.float32, (*lead, top), dev)

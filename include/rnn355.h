@@ -415,8 +415,9 @@ rnn_status rnn_workspace_status(const void *ws, size_t ws_bytes, hipStream_t str
  * above (caller-owned device memory, everything checked on the host before
  * anything is enqueued, stream order, no allocation, no synchronisation).
  * Views (ids, tables, logits, the sequences of linear attention) may start at
- * any element and have any strides, given in elements; dense arrays (outputs,
- * states, workspaces) are 16-byte aligned.
+ * any element and have any strides, given in elements; so may the arrays with
+ * one value or K values for each row of logits start anywhere.  Other arrays
+ * (outputs, states, workspaces) are 16-byte aligned.
  */
 typedef enum { RNN_I32 = 0, RNN_I64 = 1 } rnn_itype;  /* type of token ids */
 

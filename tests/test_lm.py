@@ -56,8 +56,8 @@ def test_logprobs_refusals():
         return lib.rnn_token_logprobs(*{**ok, **kw}.values(), None)
     for kw in (dict(M=0), dict(V=0), dict(dt=3), dict(x=None), dict(x=FAKE + 2), dict(ld=19999),
                dict(tok=None), dict(tok=FAKE + 4), dict(it=2), dict(K=-1), dict(K=20001),
-               dict(logp=None), dict(tl=None), dict(ti=None), dict(lse=FAKE + 4),
-               dict(ent=FAKE + 4), dict(ws=FAKE + 4)):
+               dict(logp=None), dict(tl=None), dict(ti=None), dict(lse=FAKE + 2),
+               dict(ent=FAKE + 1), dict(ws=FAKE + 4)):
         assert fwd(**kw) == INV, kw
     assert fwd(K=65) == UNS and fwd(V=1000001, ld=1000001) == UNS
     assert fwd(M=1 << 30, V=999999, ld=1000000) == UNS  # more workgroups than a grid has
@@ -71,7 +71,7 @@ def test_logprobs_refusals():
         return lib.rnn_token_logprobs_bwd(*{**ok, **kw}.values(), None)
     for kw in (dict(M=0), dict(V=0), dict(dt=3), dict(x=None), dict(x=FAKE + 1), dict(ld=99),
                dict(tok=None), dict(tok=FAKE + 2), dict(it=9), dict(lse=None), dict(ent=None),
-               dict(lse=FAKE + 4), dict(dl=FAKE + 4), dict(out=None), dict(ldd=99)):
+               dict(lse=FAKE + 2), dict(dl=FAKE + 1), dict(out=None), dict(ldd=99)):
         assert bwd(**kw) == INV, kw
     assert bwd(V=1000001, ld=1000001, ldd=1000001) == UNS
 
