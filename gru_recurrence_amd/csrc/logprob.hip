@@ -17,9 +17,9 @@
 // join; chunks of 32768 with 1024 threads, no join: 122).  All sums are
 // float32.
 //
-// The K candidates of a chunk: the K-th largest of the maxima of 64 groups of
-// threads is a bound that at least K entries reach, and few more do.
-// Those that reach it are collected (any order) and ranked by counting over
+// The K candidates of a chunk: the K-th largest of the maxima of 16, 32 or 64
+// groups of threads (at least twice K, or 64) is a bound that at least K
+// entries reach, and few more do.  Those that reach it are collected (any order) and ranked by counting over
 // the unique keys (value, index), so the result does not depend on the order.
 // Where ties or a sorted row let more than kCand through, the K-th key is
 // found exactly by bisection over value and index instead (the chunk is read
@@ -74,6 +74,29 @@ struct Row {
     __device__ Row(const T *row, int V_) : V(V_) {
         off = (int)(((uintptr_t)row & 15) / sizeof(T));
         base = row - off;
+    }
+    // Units u, u + step, ... (n of them).  Whole units load without a branch, the
+    // row's nearest whole unit in the place of others, so that all loads are in
+    // flight at once; the few units across the row's ends are then read again.
+    template <int n>
+    __device__ void load_all(int u, int step, float *x) const {
+        const int first = (off + N - 1) / N, last = (V + off) / N - 1;
+        if (last < first) {  // no whole unit
+#pragma unroll
+            for (int j = 0; j < n; ++j) load(u + j * step, x + j * N);
+            return;
+        }
+        Unit<T, N> q[n];
+#pragma unroll
+        for (int j = 0; j < n; ++j)
+            q[j] = *(const Unit<T, N> *)(base + (int64_t)min(max(u + j * step, first), last) * N);
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[j * N + e] = to_f32<T>(q[j].v[e]);
+            const int v = u + j * step;
+            if (v < first || v > last) load(v, x + j * N);
+        }
     }
     // N values of unit u; entries outside the row are -inf
     __device__ void load(int u, float *x) const {
@@ -209,9 +232,9 @@ __device__ __forceinline__ int exact_top(Row<T> r, int u0, int K, uint64_t *cand
 
 template <typename T, bool TOP>
 __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
-    constexpr int NT = kThreads, N = Row<T>::N, U = kPer / N, W = NT / 64, GROUP = NT / 64;
+    constexpr int NT = kThreads, N = Row<T>::N, U = kPer / N, W = NT / 64;
     __shared__ float wm[W], ws[W], wt[W];
-    __shared__ __attribute__((aligned(16))) float tm[64];
+    __shared__ float tm[W][64];
     __shared__ __attribute__((aligned(16))) uint64_t cand[TOP ? kCand + 2 : 2];
     __shared__ int ncand, tmp[W];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
@@ -219,17 +242,15 @@ __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
     const Row<T> r((const T *)a.logits + (int64_t)row * a.ld, a.V);
     const int u0 = ch * (NT * kPer / N);
     float x[kPer];
-#pragma unroll
-    for (int j = 0; j < U; ++j) r.load(u0 + j * NT + tid, x + j * N);
+    r.template load_all<U>(u0 + tid, NT, x);
 
     float m = x[0];
 #pragma unroll
     for (int i = 1; i < kPer; ++i) m = fmaxf(m, x[i]);
+    const int groups = a.K <= 8 ? 16 : a.K <= 16 ? 32 : 64;
     if constexpr (TOP) {
         float q = m != m ? INFINITY : m;  // nothing but NaN: a bound all the same
-#pragma unroll
-        for (int o = 1; o < GROUP; o <<= 1) q = fmaxf(q, __shfl_xor(q, o));
-        if (tid % GROUP == 0) tm[tid / GROUP] = q;
+        tm[w][lane] = q;
         if (tid == 0) ncand = 0;
     }
     m = wave_max(m);
@@ -252,17 +273,14 @@ __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
     if (lane == 0) ws[w] = s, wt[w] = t;
     if constexpr (TOP) {
         // the K-th largest group maximum: the least of those with fewer than K above
-        const float mine = tm[lane];
-        const float4 *q = (const float4 *)tm;
+        // (groups by lane, so that a chunk that is hardly filled still fills them)
+        float mine = fmaxf(fmaxf(tm[0][lane], tm[1][lane]), fmaxf(tm[2][lane], tm[3][lane]));
+        if (groups <= 32) mine = fmaxf(mine, __shfl_xor(mine, 32));
+        if (groups <= 16) mine = fmaxf(mine, __shfl_xor(mine, 16));
         int above = 0;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float4 v = q[j];
-            above += v.x > mine;
-            above += v.y > mine;
-            above += v.z > mine;
-            above += v.w > mine;
-        }
+#pragma unroll 8
+        for (int j = 0; j < groups; ++j)
+            above += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), j)) > mine;
         const float tau = -wave_max(above < a.K ? -mine : -INFINITY);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -377,8 +395,7 @@ __global__ __launch_bounds__(kThreads) void logp_bwd_kernel(LogpBwdArgs a, int n
     const bool none = lse == -INFINITY;  // nothing allowed: no gradient
     float x[4][N];
     const int u0 = ch * 4 * kThreads + threadIdx.x;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r.load(u0 + j * kThreads, x[j]);
+    r.template load_all<4>(u0, kThreads, &x[0][0]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int u = u0 + j * kThreads, i0 = u * N - r.off;
