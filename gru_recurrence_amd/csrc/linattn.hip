@@ -39,8 +39,10 @@
 // float32 matrix instructions.
 //
 // Few (batch row, head) pairs leave the chip empty, so the rows are cut into
-// segments: a first launch forms each segment's own X from nothing, a second
-// carries X across segments, and the main launch runs all segments at once.
+// segments: a first launch forms the segments' own X from nothing (in pieces of
+// a segment where that fills the chip), a second carries X across them (where
+// they are few the main launch adds them up itself), and the main launch runs
+// all segments at once.
 #include <algorithm>
 #include <mutex>
 
@@ -75,7 +77,8 @@ struct LinArgs {
     Role role[3];
     int nroles, T, B, NH;
     const float *g;
-    int nseg, seg_rows, slices;  // segments of seg_rows rows; slices of the columns of z
+    int nseg, subs, sub_rows;  // segments of `subs` pieces of sub_rows rows
+    int slices;                // of the columns of z
 };
 
 // ---- element types
@@ -347,15 +350,15 @@ struct Lds {
 template <int DA, int NW>
 __device__ __forceinline__ int64_t part_at(const LinArgs &a, int bh, int slice, int seg, int tile) {
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t wg = ((int64_t)bh * a.slices + slice) * a.nseg + seg;
+    const int64_t wg = ((int64_t)bh * a.slices + slice) * a.nseg * a.subs + seg;
     return (((wg * NW + w) * (DA / 16) + tile) * 64 + lane) * 4;
 }
 
-// Up to this many segments a workgroup adds up the earlier ones' X itself; past
-// it their reading costs more than a launch.
-constexpr int kFold = 4;
+// Up to three pieces before the last segment, a workgroup adds up the earlier
+// ones' X itself; past that their reading costs more than a launch.
+__host__ __device__ __forceinline__ bool folds(const LinArgs &a) { return (a.nseg - 1) * a.subs <= 3; }
 
-// STATE: only the segment's own X, from nothing, into its slot of `part`.
+// STATE: only the piece's own X, from nothing, into its slot of `part`.
 // Two workgroups to a CU where their LDS allows it: one's barriers and loads
 // then hide behind the other's products.
 // FAST: every operand in whole 16-byte pieces, x and y as deep as DA and z in
@@ -376,7 +379,7 @@ void lin_kernel(LinArgs a) {
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     // slices of one (role, row, head, segment) go to the same XCD (workgroups
     // go round the eight of them), where they share x and y in its L2
-    const int nsegs = STATE ? a.nseg - 1 : a.nseg;
+    const int nsegs = STATE ? (a.nseg - 1) * a.subs : a.nseg;
     const int groups = a.nroles * a.B * a.NH * nsegs;
     // (quotients come from the vector units; all of this is the same for a wave)
     auto div = [](int p, int q) { return __builtin_amdgcn_readfirstlane(p / q); };
@@ -404,7 +407,8 @@ void lin_kernel(LinArgs a) {
 
     const float powc = power(c);
 
-    const int row_lo = seg * a.seg_rows, row_hi = min(row_lo + a.seg_rows, a.T);
+    const int rows = STATE ? a.sub_rows : a.subs * a.sub_rows;
+    const int row_lo = seg * rows, row_hi = min(row_lo + rows, a.T);
 
     // element r of X[t]: depth 16 t + 4 g + r, column wcol + c of the slice
     f32x4 X[DT];
@@ -413,9 +417,10 @@ void lin_kernel(LinArgs a) {
 #pragma unroll
     for (int t = 0; t < DT; ++t) X[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (!STATE) {
-        // the earlier segments' X: carried by a launch of its own, or added up here
-        const float fs = power(a.seg_rows);
-        for (int from = a.nseg <= kFold ? 1 : seg; from <= seg && from > 0; ++from) {
+        // the earlier pieces' X: carried by a launch of its own, or added up here
+        const float fs = power(a.sub_rows);
+        const int before = seg * a.subs;
+        for (int from = folds(a) ? 1 : before; from <= before && from > 0; ++from) {
             f32x4 v[DT];
 #pragma unroll
             for (int t = 0; t < DT; ++t) v[t] = *(const f32x4 *)(R.part + part_at<DA, NW>(a, bh, slice, from, t));
@@ -622,7 +627,7 @@ void lin_kernel(LinArgs a) {
         }
     }
     if constexpr (STATE) {
-        // this segment's own X, in the slot of the segment it is carried into
+        // this piece's own X, in the slot of the piece it is carried into
 #pragma unroll
         for (int t = 0; t < DT; ++t)
             *(f32x4 *)(R.part + part_at<DA, NW>(a, bh, slice, seg + 1, t)) = X[t];
@@ -639,27 +644,28 @@ void lin_kernel(LinArgs a) {
     }
 }
 
-// Carries X across segments in place: slot s holds segment s-1's own X and
-// gets sum_{s' < s} a^(L (s-1-s')) of them, L rows to a segment.  E: values of
-// one workgroup's X.
+// Carries X across pieces in place: slot s holds piece s-1's own X and gets
+// sum_{s' < s} a^(L (s-1-s')) of them, L rows to a piece.  E: values of one
+// workgroup's X.
 __global__ __launch_bounds__(256) void lin_carry_kernel(LinArgs a, int E) {
-    constexpr int kAhead = 16;  // segments loaded at a time
+    constexpr int kAhead = 16;  // pieces loaded at a time
+    const int slots = a.nseg * a.subs, last = (a.nseg - 1) * a.subs;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t per = (int64_t)a.B * a.NH * a.slices * E;
     if (i >= per * a.nroles) return;
     const Role &R = a.role[i / per];
     const int64_t j = i % per, wg = j / E;
     const int h = (int)(wg / a.slices % a.NH);
-    const float f = __builtin_amdgcn_exp2f(fmaxf(a.g[h] * kLog2e, -1e30f) * (float)a.seg_rows);
-    float *p = R.part + wg * a.nseg * E + j % E;
+    const float f = __builtin_amdgcn_exp2f(fmaxf(a.g[h] * kLog2e, -1e30f) * (float)a.sub_rows);
+    float *p = R.part + wg * slots * E + j % E;
     float X = 0.0f;
-    for (int s = 1; s < a.nseg; s += kAhead) {
+    for (int s = 1; s <= last; s += kAhead) {
         float own[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) own[u] = p[(int64_t)min(s + u, a.nseg - 1) * E];
+        for (int u = 0; u < kAhead; ++u) own[u] = p[(int64_t)min(s + u, last) * E];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-            if (s + u < a.nseg) p[(int64_t)(s + u) * E] = X = f * X + own[u];
+            if (s + u <= last) p[(int64_t)(s + u) * E] = X = f * X + own[u];
     }
 }
 
@@ -763,21 +769,33 @@ int pad_depth(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : d <= 128 ? 128 : 256
 int waves_of(int Db) { return Db > 64 ? 8 : 4; }
 int slices_of(int Db, int NW) { return (Db + 16 * NW - 1) / (16 * NW); }
 
-// Segments: enough workgroups for the chip's 256 CUs several times over, at
-// least two chunks to a segment (each costs a pass over y and z and a state).
+// Segments: enough workgroups for the chip's 256 CUs, one of eight waves or
+// three of four to a CU (t1024 b16 nh6 d128, two segments: 51 us against 69
+// with four; 8191 rows of 12 heads of 64 in float32: 57 against 63 with 256
+// workgroups), and at least two chunks to a segment, which costs another pass
+// over y and z and a state.  That pass cuts a segment into pieces where there
+// are few of them.
 struct Cut {
-    int nseg, rows;
+    int nseg, subs, rows;  // rows of a piece
 };
-Cut cut(int T, int C, long wgs) {
+Cut cut(int T, int C, long wgs, int NW) {
     const int chunks = (T + C - 1) / C;
-    long want = std::max(1L, 512 / std::max(1L, wgs));
+    const long target = NW == 8 ? 256 : 768;
+    long want = std::max(1L, target / std::max(1L, wgs));
     want = std::min(want, (long)std::max(1, chunks / 2));
     const int per = (int)((chunks + want - 1) / want);
-    return {(chunks + per - 1) / per, per * C};
+    const int nseg = (chunks + per - 1) / per;
+    if (nseg == 1) return {1, 1, per * C};
+    long subs = std::max(1L, target / (wgs * (nseg - 1)));
+    subs = std::min(subs, (long)per);
+    const int rows = (int)((per + subs - 1) / subs);
+    subs = (per + rows - 1) / rows;
+    const int whole = (int)subs * rows;  // chunks of a segment, rounded up to its pieces
+    return {(chunks + whole - 1) / whole, (int)subs, rows * C};
 }
 
-size_t part_bytes(const LinDims &d, int DA, int NW, int slices, int nseg) {
-    return nseg > 1 ? up(sizeof(float) * (size_t)d.B * d.NH * slices * nseg * DA * 16 * NW) : 0;
+size_t part_bytes(const LinDims &d, int DA, int NW, int slices, const Cut &c) {
+    return c.nseg > 1 ? up(sizeof(float) * (size_t)d.B * d.NH * slices * c.nseg * c.subs * DA * 16 * NW) : 0;
 }
 
 template <typename T, int DA, int NW, bool STATE, bool FAST>
@@ -790,7 +808,7 @@ hipError_t lin_launch(const LinArgs &a, hipStream_t s) {
                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     });
     if (attr != hipSuccess) return attr;
-    const long groups = (long)a.nroles * a.B * a.NH * (STATE ? a.nseg - 1 : a.nseg);
+    const long groups = (long)a.nroles * a.B * a.NH * (STATE ? (a.nseg - 1) * a.subs : a.nseg);
     const long blocks = (groups + 7) / 8 * 8 * a.slices;
     if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
     hipLaunchKernelGGL((lin_kernel<T, DA, NW, STATE, FAST>), dim3((unsigned)blocks), dim3(64 * NW), lds, s,
@@ -803,7 +821,7 @@ hipError_t lin_run(const LinArgs &a, hipStream_t s) {
     if (a.nseg > 1) {
         hipError_t e = lin_launch<T, DA, NW, true, FAST>(a, s);
         if (e != hipSuccess) return e;
-        if (a.nseg > kFold) {
+        if (!folds(a)) {
             const int E = DA * 16 * NW;
             const long n = (long)a.nroles * a.B * a.NH * a.slices * E;
             hipLaunchKernelGGL(lin_carry_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, E);
@@ -875,9 +893,9 @@ BwdPlan bwd_plan(const LinDims &d, bool bf16) {
         p.slices[1] = slices_of(d.Dv, p.NW[1]);
     }
     for (int i = 0; i < p.n; ++i) {
-        p.c[i] = cut(d.T, C, bh * p.slices[i] * p.roles[i]);
+        p.c[i] = cut(d.T, C, bh * p.slices[i] * p.roles[i], p.NW[i]);
         p.part[i] = off;
-        off += p.roles[i] * part_bytes(d, p.DA[i], p.NW[i], p.slices[i], p.c[i].nseg);
+        off += p.roles[i] * part_bytes(d, p.DA[i], p.NW[i], p.slices[i], p.c[i]);
     }
     p.shared_k = p.shared_v = off;
     if (d.NH != d.NKV) {
@@ -901,8 +919,7 @@ hipError_t share(ShareArgs a, hipStream_t s) {
 
 size_t lin_fwd_bytes(const LinDims &d, bool bf16) {
     const int DA = pad_depth(d.Dk), NW = waves_of(d.Dv), sl = slices_of(d.Dv, NW);
-    const Cut c = cut(d.T, chunk_of(bf16), (long)d.B * d.NH * sl);
-    return part_bytes(d, DA, NW, sl, c.nseg);
+    return part_bytes(d, DA, NW, sl, cut(d.T, chunk_of(bf16), (long)d.B * d.NH * sl, NW));
 }
 
 size_t lin_bwd_bytes(const LinDims &d, bool bf16) { return bwd_plan(d, bf16).total; }
@@ -940,9 +957,10 @@ hipError_t launch_lin_fwd(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSe
     a.T = d.T; a.B = d.B; a.NH = d.NH;
     a.g = g;
     a.slices = slices_of(d.Dv, NW);
-    const Cut c = cut(d.T, chunk_of(bf16), (long)d.B * d.NH * a.slices);
+    const Cut c = cut(d.T, chunk_of(bf16), (long)d.B * d.NH * a.slices, NW);
     a.nseg = c.nseg;
-    a.seg_rows = c.rows;
+    a.subs = c.subs;
+    a.sub_rows = c.rows;
     a.role[0] = Role{q, k, v, 1, grp, grp, d.Dk, d.Dv, S0, 0, 1, ST, 1, 0, 1.0f, scale, o, 0,
                      (float *)ws};
     return lin_run_any(a, bf16, DA, NW, s);
@@ -970,8 +988,9 @@ hipError_t launch_lin_bwd(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSe
         a.g = g;
         a.slices = p.slices[i];
         a.nseg = p.c[i].nseg;
-        a.seg_rows = p.c[i].rows;
-        const size_t each = part_bytes(d, p.DA[i], p.NW[i], p.slices[i], a.nseg);
+        a.subs = p.c[i].subs;
+        a.sub_rows = p.c[i].rows;
+        const size_t each = part_bytes(d, p.DA[i], p.NW[i], p.slices[i], p.c[i]);
         for (int j = 0; j < a.nroles; ++j) {
             a.role[j] = *order[next++];
             a.role[j].part = (float *)(base + p.part[i] + j * each);
