@@ -358,7 +358,8 @@ __device__ __forceinline__ int64_t part_at(const LinArgs &a, int bh, int slice, 
 // ones' X itself; past that their reading costs more than a launch.
 __host__ __device__ __forceinline__ bool folds(const LinArgs &a) { return (a.nseg - 1) * a.subs <= 3; }
 
-// STATE: only the piece's own X, from nothing, into its slot of `part`.
+// STATE: only the piece's own X, from nothing (the first: from the initial
+// state), into its slot of `part`.
 // Two workgroups to a CU where their LDS allows it: one's barriers and loads
 // then hide behind the other's products.
 // FAST: every operand in whole 16-byte pieces and z in whole 16-column tiles
@@ -417,11 +418,38 @@ void lin_kernel(LinArgs a) {
     const bool wave_on = wcol < nc;
 #pragma unroll
     for (int t = 0; t < DT; ++t) X[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // The initial state: from where the caller has it by the one workgroup that
+    // starts there.  With several segments that is the first piece's, in the
+    // launch before; it also leaves a copy in slot 0 for the main launch, whose
+    // last segment may be writing the final state over the initial one by then.
+    if (R.init && seg == 0 && STATE == (a.nseg > 1)) {
+        const float f = R.init_decay ? power(1) : 1.0f;
+        const float *S = R.init + (int64_t)bh * R.Da * R.Db;
+        const int sd = R.init_t ? 1 : R.Db, sc = R.init_t ? R.Da : 1;
+        const int col = col0 + wcol + c;
+        // loads without a branch, from inside the state
+        const float *Sc = S + min(col, R.Db - 1) * sc;
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int d = 16 * t + 4 * g + r;
+                const float v = Sc[min(d, R.Da - 1) * sd];
+                X[t][r] = d < R.Da && col < R.Db ? f * v : 0.0f;
+            }
+        if constexpr (STATE) {
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+                *(f32x4 *)(R.part + part_at<DA, NW>(a, bh, slice, 0, t)) = X[t];
+        }
+    }
     if constexpr (!STATE) {
-        // the earlier pieces' X: carried by a launch of its own, or added up here
+        // what comes before: the initial state for the first segment; for others
+        // the earlier pieces' X, carried by a launch of its own or added up here
         const float fs = power(a.sub_rows);
         const int before = seg * a.subs;
-        for (int from = folds(a) ? 1 : before; from <= before && from > 0; ++from) {
+        const int from0 = a.nseg == 1 || (seg == 0 && !R.init) ? before + 1 : seg == 0 ? 0 : folds(a) ? 1 : before;
+        for (int from = from0; from <= before; ++from) {
             f32x4 v[DT];
 #pragma unroll
             for (int t = 0; t < DT; ++t) v[t] = *(const f32x4 *)(R.part + part_at<DA, NW>(a, bh, slice, from, t));
@@ -431,22 +459,6 @@ void lin_kernel(LinArgs a) {
             for (int t = 0; t < DT; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) X[t][r] = fs * X[t][r] + v[t][r];
-        }
-        if (R.init) {
-            const float f = power(row_lo + (R.init_decay ? 1 : 0));
-            const float *S = R.init + (int64_t)bh * R.Da * R.Db;
-            const int sd = R.init_t ? 1 : R.Db, sc = R.init_t ? R.Da : 1;
-            const int col = col0 + wcol + c;
-            // loads without a branch, from inside the state
-            const float *Sc = S + min(col, R.Db - 1) * sc;
-#pragma unroll
-            for (int t = 0; t < DT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int d = 16 * t + 4 * g + r;
-                    const float v = Sc[min(d, R.Da - 1) * sd];
-                    X[t][r] += d < R.Da && col < R.Db ? f * v : 0.0f;
-                }
         }
         // the tiles above the diagonal that share an operand with one on it
         for (int i = tid; i < L::operands * kOperand / 16; i += 64 * NW)
@@ -646,8 +658,9 @@ void lin_kernel(LinArgs a) {
     }
 }
 
-// Carries X across pieces in place: slot s holds piece s-1's own X and gets
-// sum_{s' < s} a^(L (s-1-s')) of them, L rows to a piece.  E: values of one
+// Carries X across pieces in place: slot s holds piece s-1's own X (the first
+// with the initial state in it) and gets sum_{s' < s} a^(L (s-1-s')) of them, L
+// rows to a piece.  E: values of one
 // workgroup's X.
 __global__ __launch_bounds__(256) void lin_carry_kernel(LinArgs a, int E) {
     constexpr int kAhead = 16;  // pieces loaded at a time

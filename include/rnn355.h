@@ -497,8 +497,9 @@ rnn_status rnn_token_logprobs_bwd(int M, int V, rnn_dtype dt, const void *logits
  * they are.  g [NH] float32 (log decay, <= 0; -inf forgets everything; a
  * constant, no gradient).  States [B][NH][Dk][Dv] float32.  Outputs are dense
  * [T][B][heads][D] in dtype dt.  Dk, Dv <= 256 (else RNN_ERR_UNSUPPORTED).
- * bf16 calls accumulate in float32 and keep every intermediate to about 17
- * bits; the outputs' rounding is the only one to bf16.  Inputs are finite; a
+ * Outputs overlap no input but where a call says so.
+ * bf16 calls accumulate in float32 and keep every intermediate to 2^-17 of
+ * itself, states to float32; the outputs' rounding is the only one to bf16.  Inputs are finite; a
  * value that is not may reach every output of its batch row and head.
  */
 typedef struct {

@@ -427,6 +427,22 @@ def test_linattn_prompt_then_steps_and_state_in_place():
     assert (S1 - S).norm() <= 1e-5 * S.norm()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,B,NH,Dk,Dv", [(200, 1, 2, 64, 64), (1100, 1, 2, 64, 48), (1500, 2, 3, 128, 128),
+                                          (700, 1, 1, 33, 70)])
+def test_linattn_state_in_place_over_segments(T, B, NH, Dk, Dv, dt):
+    """The final state over the initial one, where the sequence runs in
+    segments at once: the same bits as into another tensor."""
+    _, q, k, v, gd, S0 = _lin_case(T, T, B, NH, NH, Dk, Dv, dt)
+    assert g.workspace_size_linattn(g.OP_LIN_FWD, g.LinDims(T, B, NH, NH, Dk, Dv),
+                                    g.RNN_BF16 if dt == "bf16" else g.RNN_F32) > 0
+    o, S = g.linattn_fwd(q, k, v, gd, S0)
+    for _ in range(3):
+        S1 = S0.clone()
+        o1, S2 = g.linattn_fwd(q, k, v, gd, S1, out={"S": S1})
+        assert S2 is S1 and torch.equal(S1, S) and torch.equal(o1, o)
+
+
 def test_linattn_strides_past_32_bits():
     _, q, k, v, gd, S0 = _lin_case(6, 3, 1, 2, 2, 32, 32, "bf16")
     far = torch.empty((3, 1, 1 << 30, 1), dtype=torch.bfloat16, device="cuda")
