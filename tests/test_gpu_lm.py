@@ -507,3 +507,39 @@ def test_another_stream():
         torch.cuda.current_stream().wait_stream(side)
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_captured_in_a_graph():
+    """Calls with their outputs and workspaces given, captured and replayed
+    over changing inputs with eager work between the replays."""
+    rng = np.random.default_rng(12)
+    ids = torch.from_numpy(rng.integers(-1, 3000, (600, 9))).cuda()
+    dx = _rand(rng, (600, 9, 64), "f32")
+    x, tok = _rand(rng, (6, 20001), "bf16", 3.0), torch.from_numpy(rng.integers(0, 20001, 6)).cuda()
+    _, q, k, v, gd, S0 = _lin_case(4, 900, 1, 2, 1, 64, 64, "bf16")
+    do = _rand(rng, (900, 1, 2, 64), "bf16")
+    u8 = lambda n: torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")  # noqa: E731
+    d = g.LinDims(900, 1, 2, 1, 64, 64)
+    w = [u8(g.workspace_size_embed_bwd(600, 9, 3000, 64)), u8(g.workspace_size_logprobs(6, 20001, 7)),
+         u8(g.workspace_size_linattn(g.OP_LIN_FWD, d, 1)), u8(g.workspace_size_linattn(g.OP_LIN_BWD, d, 1))]
+
+    def calls():
+        r = g.token_logprobs(x, tok, top=7, ws=w[1])
+        b = g.linattn_bwd(q, k, v, gd, do, S0, ws=w[3])
+        return [g.embed_bwd(ids, dx, 3000, ws=w[0]), *r.values(),
+                *g.linattn_fwd(q, k, v, gd, S0, ws=w[2]), *b.values()]
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = calls()
+    for i in range(4):
+        dx.mul_(1.0 + i)
+        ids.copy_(ids.roll(i, 0))
+        x.copy_(x.roll(i, 1))
+        q.copy_(q.flip(0))
+        graph.replay()
+        got = [t.clone() for t in out]
+        for a, b in zip(got, calls()):
+            assert torch.equal(a, b), i
+        torch.cuda.synchronize()
