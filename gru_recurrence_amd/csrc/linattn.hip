@@ -43,6 +43,12 @@
 // a segment where that fills the chip), a second carries X across them (where
 // they are few the main launch adds them up itself), and the main launch runs
 // all segments at once.
+//
+// Measured: T1024 B16 NH6 D128 bf16 12.6 us for the states and 47 for the main
+// launch (114 MB from memory, matrix units 18% busy): bound by the latency of a
+// chunk's phases, 12-13 thousand cycles for 2800 of products.  T8191 NH12 D64
+// float32 15 + 8 + 33 us, matrix units 47% busy.  A token for B64 NH12 D64
+// 7.0 us (3.6 TB/s).
 #include <algorithm>
 #include <mutex>
 
@@ -52,7 +58,6 @@ namespace rnn355 {
 namespace lm {
 
 namespace {
-
 
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
