@@ -117,6 +117,24 @@ def test_embed_bwd(T, B, V, D, skew, dt):
     assert torch.equal(out, g.embed_bwd(ids.t().contiguous().t(), dx, V, 0.3))
 
 
+@pytest.mark.parametrize("M,V,D", [(70001, 1000, 8), (300007, 50000, 4), (300007, 3, 5), (5000, 300000, 4),
+                                   (1000, 600000, 1)])
+def test_embed_bwd_many_ids(M, V, D):
+    """The blocked sort's larger blocks and its third pass, against sums in
+    64 bits on the device."""
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    ids = torch.randint(-1, V + 1, (M,), generator=gen, device="cuda")
+    ids[::3] = V // 2
+    dx = torch.randn((M, D), generator=gen, device="cuda")
+    out = g.embed_bwd(ids, dx, V, 0.5)
+    ok = (ids >= 0) & (ids < V)
+    ref, mag = (torch.zeros((V, D), dtype=torch.float64, device="cuda").index_add_(
+        0, ids[ok], t[ok].double() * 0.5) for t in (dx, dx.abs()))
+    cnt = torch.bincount(ids[ok], minlength=V)[:, None]
+    assert ((out - ref).abs() <= (cnt + 2) * U * mag).all()
+    assert torch.equal(out, g.embed_bwd(ids, dx, V, 0.5))
+
+
 def test_embed_bwd_all_padding():
     out = torch.full((11, 5), float("nan"), device="cuda")
     g.embed_bwd(torch.full((3, 4), -1, device="cuda"), torch.ones((3, 4, 5), device="cuda"), 11,
