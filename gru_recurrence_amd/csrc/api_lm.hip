@@ -39,11 +39,16 @@ bool lin_dims_ok(const rnn_lin_dims *d) {
            d->NH % d->NKV == 0 && (long)d->T * d->B <= (1L << 30) && (long)d->B * d->NH <= (1L << 24);
 }
 
-// 16 rows of a sequence stay within 32 bits of each other (4-byte values)
-bool lin_supported(const rnn_lin_dims *d) {
-    return d->Dk <= 256 && d->Dv <= 256 &&
-           (d->T == 1 || (long)d->B * d->NH * (d->Dk > d->Dv ? d->Dk : d->Dv) < (1L << 26));
+bool lin_depths_ok(const rnn_lin_dims *d) { return d->Dk <= 256 && d->Dv <= 256; }
+
+// Calls that walk the rows, the backward of one token among them: 16 rows of a
+// sequence stay within 32 bits of each other (4-byte values).
+bool lin_rows_ok(const rnn_lin_dims *d) {
+    return lin_depths_ok(d) && (long)d->B * d->NH * (d->Dk > d->Dv ? d->Dk : d->Dv) < (1L << 26);
 }
+
+// The forward of one token runs as a step, which has no such distances.
+bool lin_fwd_ok(const rnn_lin_dims *d) { return d->T == 1 ? lin_depths_ok(d) : lin_rows_ok(d); }
 
 lm::LinDims lin_dims(const rnn_lin_dims *d) {
     return lm::LinDims{d->T, d->B, d->NH, d->NKV, d->Dk, d->Dv};
@@ -127,9 +132,9 @@ rnn_status rnn_token_logprobs_bwd(int M, int V, rnn_dtype dt, const void *logits
 }
 
 size_t rnn_workspace_size_linattn(rnn_lin_op op, const rnn_lin_dims *d, rnn_dtype dt) {
-    if (!lin_dims_ok(d) || !lin_supported(d) || !dtype_ok(dt)) return 0;
-    if (op == RNN_OP_LIN_FWD) return lm::lin_fwd_bytes(lin_dims(d), dt == RNN_BF16);
-    if (op == RNN_OP_LIN_BWD) return lm::lin_bwd_bytes(lin_dims(d), dt == RNN_BF16);
+    if (!lin_dims_ok(d) || !dtype_ok(dt)) return 0;
+    if (op == RNN_OP_LIN_FWD && lin_fwd_ok(d)) return lm::lin_fwd_bytes(lin_dims(d), dt == RNN_BF16);
+    if (op == RNN_OP_LIN_BWD && lin_rows_ok(d)) return lm::lin_bwd_bytes(lin_dims(d), dt == RNN_BF16);
     return 0;
 }
 
@@ -142,7 +147,7 @@ rnn_status rnn_linattn_fwd(const rnn_lin_dims *d, rnn_dtype dt, const rnn_seq *q
     const void *ps[] = {g, S0, o, ST, ws};
     for (const void *p : ps)
         if (!aligned16(p)) return RNN_ERR_INVALID_ARG;
-    if (!lin_supported(d)) return RNN_ERR_UNSUPPORTED;
+    if (!lin_fwd_ok(d)) return RNN_ERR_UNSUPPORTED;
     const lm::LinDims n = lin_dims(d);
     const size_t need = lm::lin_fwd_bytes(n, dt == RNN_BF16);
     if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;
@@ -159,7 +164,7 @@ rnn_status rnn_linattn_step(const rnn_lin_dims *d, rnn_dtype dt, const rnn_seq *
     const void *ps[] = {g, S, o, S_out};
     for (const void *p : ps)
         if (!aligned16(p)) return RNN_ERR_INVALID_ARG;
-    if (!lin_supported(d)) return RNN_ERR_UNSUPPORTED;
+    if (!lin_depths_ok(d)) return RNN_ERR_UNSUPPORTED;
     return done(lm::launch_lin_step(lin_dims(d), dt == RNN_BF16, seq_of(q), seq_of(k), seq_of(v), g,
                                     scale, S, o, S_out, stream));
 }
@@ -176,7 +181,7 @@ rnn_status rnn_linattn_bwd(const rnn_lin_dims *d, rnn_dtype dt, const rnn_seq *q
     const void *ps[] = {g, S0, dST, dq, dk, dv, dS0, ws};
     for (const void *p : ps)
         if (!aligned16(p)) return RNN_ERR_INVALID_ARG;
-    if (!lin_supported(d)) return RNN_ERR_UNSUPPORTED;
+    if (!lin_rows_ok(d)) return RNN_ERR_UNSUPPORTED;
     const lm::LinDims n = lin_dims(d);
     const size_t need = lm::lin_bwd_bytes(n, dt == RNN_BF16);
     if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;

@@ -496,7 +496,8 @@ rnn_status rnn_token_logprobs_bwd(int M, int V, rnn_dtype dt, const void *logits
  * dtype dt, so slices of a fused projection and batch-first arrays are read as
  * they are.  g [NH] float32 (log decay, <= 0; -inf forgets everything; a
  * constant, no gradient).  States [B][NH][Dk][Dv] float32.  Outputs are dense
- * [T][B][heads][D] in dtype dt.  Dk, Dv <= 256 (else RNN_ERR_UNSUPPORTED).
+ * [T][B][heads][D] in dtype dt.  Dk, Dv <= 256, and B * NH * max(Dk, Dv) < 2^26
+ * but for the forward of one token (else RNN_ERR_UNSUPPORTED).
  * Outputs overlap no input but where a call says so.
  * bf16 calls accumulate in float32 and keep every intermediate to 2^-17 of
  * itself, states to float32; the outputs' rounding is the only one to bf16.  Inputs are finite; a
