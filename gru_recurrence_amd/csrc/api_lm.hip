@@ -69,6 +69,7 @@ rnn_status rnn_embed_fwd(int T, int B, int V, int D, rnn_dtype dt, const rnn_ids
                          hipStream_t stream) {
     if (!embed_dims_ok(T, B, V, D) || !dtype_ok(dt) || !ids_ok(ids)) return RNN_ERR_INVALID_ARG;
     if (!view_ok(table, elt(dt)) || ld < D || !x || !aligned16(x)) return RNN_ERR_INVALID_ARG;
+    if (!lm::embed_fwd_grid_ok(T * B, D, dt == RNN_BF16, table, ld)) return RNN_ERR_UNSUPPORTED;
     return done(lm::launch_embed_fwd(ids_of(ids, T, B), V, D, dt == RNN_BF16, table, ld, scale, x,
                                      stream));
 }
@@ -83,6 +84,7 @@ rnn_status rnn_embed_bwd(int T, int B, int V, int D, rnn_dtype dt, const rnn_ids
     if (!embed_dims_ok(T, B, V, D) || !dtype_ok(dt) || !ids_ok(ids)) return RNN_ERR_INVALID_ARG;
     if (!dx || !dtable || !aligned16(dx) || !aligned16(dtable) || !aligned16(ws))
         return RNN_ERR_INVALID_ARG;
+    if (!lm::embed_bwd_grid_ok(T * B, V, D)) return RNN_ERR_UNSUPPORTED;
     if (!ws || ws_bytes < lm::embed_bwd_bytes(T * B, V, D)) return RNN_ERR_WORKSPACE;
     return done(lm::launch_embed_bwd(ids_of(ids, T, B), V, D, dt == RNN_BF16, dx, scale, dtable, ws,
                                      stream));
@@ -106,7 +108,8 @@ rnn_status rnn_token_logprobs(int M, int V, rnn_dtype dt, const void *logits, in
     for (const void *p : ps)
         if (p && !view_ok(p, 4)) return RNN_ERR_INVALID_ARG;
     if (!aligned16(ws)) return RNN_ERR_INVALID_ARG;
-    if (V > kMaxVocab || K > lm::kMaxTop || !lm::logp_grid_ok(M, V)) return RNN_ERR_UNSUPPORTED;
+    if (V > kMaxVocab || K > lm::kMaxTop || !lm::logp_grid_ok(M, V, dt == RNN_BF16))
+        return RNN_ERR_UNSUPPORTED;
     const size_t need = lm::logp_bytes(M, V, K);
     if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;
     lm::LogpArgs a{M, V, K, logits, ld, tok, it == RNN_I64, logp, entropy, lse, top_logp, top_id, ws};
@@ -126,7 +129,7 @@ rnn_status rnn_token_logprobs_bwd(int M, int V, rnn_dtype dt, const void *logits
     const void *ps[] = {lse, entropy, dlogp, dentropy};
     for (const void *p : ps)
         if (p && !view_ok(p, 4)) return RNN_ERR_INVALID_ARG;
-    if (V > kMaxVocab || !lm::logp_grid_ok(M, V)) return RNN_ERR_UNSUPPORTED;
+    if (V > kMaxVocab || !lm::logp_bwd_grid_ok(M, V, dt == RNN_BF16)) return RNN_ERR_UNSUPPORTED;
     lm::LogpBwdArgs a{M, V, logits, ld, tok, it == RNN_I64, lse, entropy, dlogp, dentropy, dlogits, ldd};
     return done(lm::launch_logp_bwd(a, dt == RNN_BF16, stream));
 }
@@ -147,8 +150,8 @@ rnn_status rnn_linattn_fwd(const rnn_lin_dims *d, rnn_dtype dt, const rnn_seq *q
     const void *ps[] = {g, S0, o, ST, ws};
     for (const void *p : ps)
         if (!aligned16(p)) return RNN_ERR_INVALID_ARG;
-    if (!lin_fwd_ok(d)) return RNN_ERR_UNSUPPORTED;
     const lm::LinDims n = lin_dims(d);
+    if (!lin_fwd_ok(d) || !lm::lin_fwd_grid_ok(n, dt == RNN_BF16)) return RNN_ERR_UNSUPPORTED;
     const size_t need = lm::lin_fwd_bytes(n, dt == RNN_BF16);
     if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;
     return done(lm::launch_lin_fwd(n, dt == RNN_BF16, seq_of(q), seq_of(k), seq_of(v), g, scale, S0,
@@ -164,7 +167,7 @@ rnn_status rnn_linattn_step(const rnn_lin_dims *d, rnn_dtype dt, const rnn_seq *
     const void *ps[] = {g, S, o, S_out};
     for (const void *p : ps)
         if (!aligned16(p)) return RNN_ERR_INVALID_ARG;
-    if (!lin_depths_ok(d)) return RNN_ERR_UNSUPPORTED;
+    if (!lin_depths_ok(d) || !lm::lin_step_grid_ok(lin_dims(d))) return RNN_ERR_UNSUPPORTED;
     return done(lm::launch_lin_step(lin_dims(d), dt == RNN_BF16, seq_of(q), seq_of(k), seq_of(v), g,
                                     scale, S, o, S_out, stream));
 }
@@ -181,8 +184,8 @@ rnn_status rnn_linattn_bwd(const rnn_lin_dims *d, rnn_dtype dt, const rnn_seq *q
     const void *ps[] = {g, S0, dST, dq, dk, dv, dS0, ws};
     for (const void *p : ps)
         if (!aligned16(p)) return RNN_ERR_INVALID_ARG;
-    if (!lin_rows_ok(d)) return RNN_ERR_UNSUPPORTED;
     const lm::LinDims n = lin_dims(d);
+    if (!lin_rows_ok(d) || !lm::lin_bwd_grid_ok(n, dt == RNN_BF16)) return RNN_ERR_UNSUPPORTED;
     const size_t need = lm::lin_bwd_bytes(n, dt == RNN_BF16);
     if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;
     return done(lm::launch_lin_bwd(n, dt == RNN_BF16, seq_of(q), seq_of(k), seq_of(v), g, scale, S0,

@@ -65,34 +65,48 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(Ids ids, int V, int upr,
     }
 }
 
-template <typename T, int N>
-hipError_t embed_fwd_n(const Ids &ids, int V, int D, const T *table, int64_t ld, float scale, T *x,
-                       hipStream_t s) {
-    const int upr = D / N;
-    // lanes per row: the power of two that wastes the fewest in the last round
+// Lanes per row (their log2): the power of two that wastes the fewest in the
+// last round.
+int lane_shift(int upr) {
     int best = 6;
     long waste = -1;
     for (int g = 6; g >= 3; --g) {
         const long w = ((long)(upr + (1 << g) - 1) >> g << g) - upr;
         if (waste < 0 || w < waste) waste = w, best = g;
     }
-    const long M = (long)ids.T * ids.B, rows = 256 >> best;
-    hipLaunchKernelGGL((embed_fwd_kernel<T, N>), dim3((unsigned)((M + rows - 1) / rows)), dim3(256),
-                       0, s, ids, V, upr, best, table, ld, scale, x);
+    return best;
+}
+long row_blocks(long M, int upr) {
+    const long rows = 256 >> lane_shift(upr);
+    return (M + rows - 1) / rows;
+}
+
+// Values of the widest unit that divides a row and keeps every row aligned.
+int row_unit(int D, size_t elt, const void *table, int64_t ld) {
+    for (int n = 16 / (int)elt; n > 1; n = n > 2 ? 2 : 1)
+        if (D % n == 0 && ld % n == 0 && (uintptr_t)table % (n * elt) == 0) return n;
+    return 1;
+}
+
+template <typename T, int N>
+hipError_t embed_fwd_n(const Ids &ids, int V, int D, const T *table, int64_t ld, float scale, T *x,
+                       hipStream_t s) {
+    const int upr = D / N;
+    const long blocks = row_blocks((long)ids.T * ids.B, upr);
+    hipLaunchKernelGGL((embed_fwd_kernel<T, N>), dim3((unsigned)blocks), dim3(256), 0, s, ids, V, upr,
+                       lane_shift(upr), table, ld, scale, x);
     return hipGetLastError();
 }
 
 template <typename T>
 hipError_t embed_fwd_t(const Ids &ids, int V, int D, const T *table, int64_t ld, float scale, T *x,
                        hipStream_t s) {
-    // widest unit that divides a row and keeps every row aligned
     constexpr int W = 16 / sizeof(T);
-    auto fits = [&](int n) {
-        return D % n == 0 && ld % n == 0 && (uintptr_t)table % (n * sizeof(T)) == 0;
-    };
-    if (fits(W)) return embed_fwd_n<T, W>(ids, V, D, table, ld, scale, x, s);
-    if (fits(2)) return embed_fwd_n<T, 2>(ids, V, D, table, ld, scale, x, s);
-    return embed_fwd_n<T, 1>(ids, V, D, table, ld, scale, x, s);
+    switch (row_unit(D, sizeof(T), table, ld)) {
+        case W: return embed_fwd_n<T, W>(ids, V, D, table, ld, scale, x, s);
+        case 2: return embed_fwd_n<T, 2>(ids, V, D, table, ld, scale, x, s);
+        default: return embed_fwd_n<T, 1>(ids, V, D, table, ld, scale, x, s);
+    }
 }
 
 // -------------------------------------------------------------------- sort
@@ -514,6 +528,13 @@ hipError_t sums_t(int M, int V, int D, const uint32_t *key, const uint32_t *pos,
 }
 
 }  // namespace
+
+bool embed_fwd_grid_ok(int M, int D, bool bf16, const void *table, int64_t ld) {
+    return grid_ok(row_blocks(M, D / row_unit(D, bf16 ? 2 : 4, table, ld)), 256);
+}
+
+// The sort's launches have at most one thread for each id.
+bool embed_bwd_grid_ok(int M, int V, int D) { return grid_ok((pieces_of(M, V, D) + 3) / 4, 256); }
 
 hipError_t launch_embed_fwd(const Ids &ids, int V, int D, bool bf16, const void *table,
                             int64_t ld, float scale, void *x, hipStream_t s) {

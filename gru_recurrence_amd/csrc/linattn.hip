@@ -818,6 +818,12 @@ size_t part_bytes(const LinDims &d, int DA, int NW, int slices, const Cut &c) {
     return c.nseg > 1 ? up(sizeof(float) * (size_t)d.B * d.NH * slices * c.nseg * c.subs * DA * 16 * NW) : 0;
 }
 
+// Workgroups of a launch over `segs` segments: the slices of eight (role, row,
+// head, segment) go together.
+long lin_blocks(int nroles, int B, int NH, int segs, int slices) {
+    return ((long)nroles * B * NH * segs + 7) / 8 * 8 * slices;
+}
+
 template <typename T, int DA, int NW, bool STATE, bool FAST>
 hipError_t lin_launch(const LinArgs &a, hipStream_t s) {
     constexpr size_t lds = Lds<T, DA, NW, STATE>::bytes;
@@ -828,9 +834,8 @@ hipError_t lin_launch(const LinArgs &a, hipStream_t s) {
                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     });
     if (attr != hipSuccess) return attr;
-    const long groups = (long)a.nroles * a.B * a.NH * (STATE ? (a.nseg - 1) * a.subs : a.nseg);
-    const long blocks = (groups + 7) / 8 * 8 * a.slices;
-    if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
+    const long blocks =
+        lin_blocks(a.nroles, a.B, a.NH, STATE ? (a.nseg - 1) * a.subs : a.nseg, a.slices);
     hipLaunchKernelGGL((lin_kernel<T, DA, NW, STATE, FAST>), dim3((unsigned)blocks), dim3(64 * NW), lds, s,
                        a);
     return hipGetLastError();
@@ -927,15 +932,42 @@ BwdPlan bwd_plan(const LinDims &d, bool bf16) {
     return p;
 }
 
+// Values of a head to a thread, and the workgroups of one array's n outputs.
+int share_unit(const LinDims &d) { return d.Dk % 4 == 0 && d.Dv % 4 == 0 ? 4 : 1; }
+long share_blocks(int64_t n, int V) { return (long)((n / V + 255) / 256); }
+
 template <typename T, int V>
 hipError_t share(ShareArgs a, hipStream_t s) {
+    const long b0 = share_blocks(a.n[0], V), b1 = share_blocks(a.n[1], V);
     for (int i = 0; i < 2; ++i) a.n[i] /= V;
-    const unsigned b0 = (unsigned)((a.n[0] + 255) / 256), b1 = (unsigned)((a.n[1] + 255) / 256);
-    hipLaunchKernelGGL((lin_share_kernel<T, V>), dim3(b0 + b1), dim3(256), 0, s, a, b0);
+    hipLaunchKernelGGL((lin_share_kernel<T, V>), dim3((unsigned)(b0 + b1)), dim3(256), 0, s, a, (unsigned)b0);
     return hipGetLastError();
 }
 
+int step_slices(const LinDims &d) { return (d.Dv + kStepCols - 1) / kStepCols; }
+
 }  // namespace
+
+bool lin_step_grid_ok(const LinDims &d) { return grid_ok((long)d.B * d.NH * step_slices(d), 256); }
+
+// The main launches only: those of the states have at most the 768 workgroups
+// that cut() aims at for each segment, the carries a thread for a value of
+// their X.
+bool lin_fwd_grid_ok(const LinDims &d, bool bf16) {
+    if (d.T == 1) return lin_step_grid_ok(d);
+    const int NW = waves_of(d.Dv), sl = slices_of(d.Dv, NW);
+    const Cut c = cut(d.T, chunk_of(bf16), (long)d.B * d.NH * sl, NW);
+    return grid_ok(lin_blocks(1, d.B, d.NH, c.nseg, sl), 64 * NW);
+}
+
+bool lin_bwd_grid_ok(const LinDims &d, bool bf16) {
+    const BwdPlan p = bwd_plan(d, bf16);
+    for (int i = 0; i < p.n; ++i)
+        if (!grid_ok(lin_blocks(p.roles[i], d.B, d.NH, p.c[i].nseg, p.slices[i]), 64 * p.NW[i])) return false;
+    const int64_t n = (int64_t)d.T * d.B * d.NKV;
+    const int V = share_unit(d);
+    return d.NH == d.NKV || grid_ok(share_blocks(n * d.Dk, V) + share_blocks(n * d.Dv, V), 256);
+}
 
 size_t lin_fwd_bytes(const LinDims &d, bool bf16) {
     const int DA = pad_depth(d.Dk), NW = waves_of(d.Dv), sl = slices_of(d.Dv, NW);
@@ -947,10 +979,8 @@ size_t lin_bwd_bytes(const LinDims &d, bool bf16) { return bwd_plan(d, bf16).tot
 hipError_t launch_lin_step(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSeq v,
                            const float *g, float scale, const float *S0, void *o, float *S1,
                            hipStream_t s) {
-    const int sl = (d.Dv + kStepCols - 1) / kStepCols;
-    const long blocks = (long)d.B * d.NH * sl;
-    if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks), thr(256);
+    const int sl = step_slices(d);
+    const dim3 grid((unsigned)((long)d.B * d.NH * sl)), thr(256);
     const bool vec = d.Dv % 4 == 0;
     if (bf16 && vec)
         hipLaunchKernelGGL((lin_step_kernel<uint16_t, true>), grid, thr, 0, s, d, q, k, v, g, scale,
@@ -1021,7 +1051,7 @@ hipError_t launch_lin_bwd(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSe
     if (grp > 1) {
         const int64_t n = (int64_t)d.T * d.B * d.NKV;
         const ShareArgs a{{pk, pv}, {dk, dv}, {n * d.Dk, n * d.Dv}, {d.Dk, d.Dv}, grp};
-        if (d.Dk % 4 == 0 && d.Dv % 4 == 0)
+        if (share_unit(d) == 4)
             return bf16 ? share<uint16_t, 4>(a, s) : share<float, 4>(a, s);
         return bf16 ? share<uint16_t, 1>(a, s) : share<float, 1>(a, s);
     }

@@ -49,7 +49,13 @@ __device__ __forceinline__ int load_id(const Ids &t, int m, int V) {
     return id < 0 || id >= V ? V : (int)id;
 }
 
+// A launch has fewer than 2^32 threads in a dimension.  Each operator's
+// *_grid_ok says whether all launches of a call do.
+inline bool grid_ok(int64_t blocks, int threads) { return blocks * threads < ((int64_t)1 << 32); }
+
 // ---- embedding (embed.hip)
+bool embed_fwd_grid_ok(int M, int D, bool bf16, const void *table, int64_t ld);
+bool embed_bwd_grid_ok(int M, int V, int D);
 hipError_t launch_embed_fwd(const Ids &ids, int V, int D, bool bf16, const void *table,
                             int64_t ld, float scale, void *x, hipStream_t s);
 size_t embed_bwd_bytes(int M, int V, int D);
@@ -70,7 +76,8 @@ struct LogpArgs {
     void *ws;
 };
 size_t logp_bytes(int M, int V, int K);
-bool logp_grid_ok(int M, int V);  // workgroups of a launch fit its grid
+bool logp_grid_ok(int M, int V, bool bf16);
+bool logp_bwd_grid_ok(int M, int V, bool bf16);
 hipError_t launch_logp(const LogpArgs &a, bool bf16, hipStream_t s);
 struct LogpBwdArgs {
     int M, V;
@@ -94,6 +101,9 @@ struct LinSeq {
 struct LinDims {
     int T, B, NH, NKV, Dk, Dv;
 };
+bool lin_fwd_grid_ok(const LinDims &d, bool bf16);
+bool lin_step_grid_ok(const LinDims &d);
+bool lin_bwd_grid_ok(const LinDims &d, bool bf16);
 size_t lin_fwd_bytes(const LinDims &d, bool bf16);
 size_t lin_bwd_bytes(const LinDims &d, bool bf16);
 hipError_t launch_lin_fwd(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSeq v,

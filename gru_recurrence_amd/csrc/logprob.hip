@@ -463,8 +463,14 @@ size_t logp_bytes(int M, int V, int K) {
     return nch > 1 ? (size_t)M * nch * (sizeof(Part) + 8 * (size_t)K) : 0;
 }
 
-bool logp_grid_ok(int M, int V) {
-    return (long)M * chunks(V, 4 * kThreads * Row<float>::N, 2) <= 0x7fffffffL;
+// The join has at most as many workgroups as the rows have chunks.
+bool logp_grid_ok(int M, int V, bool bf16) {
+    return grid_ok((long)M * chunks(V, kChunk, bf16 ? 2 : 4), kThreads);
+}
+
+bool logp_bwd_grid_ok(int M, int V, bool bf16) {
+    const int per = 4 * kThreads * (bf16 ? Row<uint16_t>::N : Row<float>::N);
+    return grid_ok((long)M * chunks(V, per, bf16 ? 2 : 4), kThreads);
 }
 
 hipError_t launch_logp(const LogpArgs &a, bool bf16, hipStream_t s) {

@@ -417,7 +417,10 @@ rnn_status rnn_workspace_status(const void *ws, size_t ws_bytes, hipStream_t str
  * Views (ids, tables, logits, the sequences of linear attention) may start at
  * any element and have any strides, given in elements; so may the arrays with
  * one value or K values for each row of logits start anywhere.  Other arrays
- * (outputs, states, workspaces) are 16-byte aligned.
+ * (outputs, states, workspaces) are 16-byte aligned.  Dimensions are at least 1
+ * (T * B at most 2^30).  A call that would need a launch of 2^32 threads or more
+ * is RNN_ERR_UNSUPPORTED: a row of logits takes at least 256, so 2^24 rows are
+ * too many for one call.
  */
 typedef enum { RNN_I32 = 0, RNN_I64 = 1 } rnn_itype;  /* type of token ids */
 
