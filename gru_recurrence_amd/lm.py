@@ -72,17 +72,22 @@ def load():
 
 def _on_stream(fn):
     """Run with `stream`, and the first operand's device, current."""
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
         if stream is not None:
             with torch.cuda.stream(stream):
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
+        if not args and name not in kw:
+            raise TypeError("%s() missing operand %r" % (fn.__name__, name))
+        first = args[0] if args else kw[name]
         if not first.is_cuda:
             raise ValueError("operands must be device tensors")
         if first.get_device() != torch.cuda.current_device():
             with torch.cuda.device(first.device):
-                return fn(first, *args, **kw)
-        return fn(first, *args, **kw)
+                return fn(*args, **kw)
+        return fn(*args, **kw)
     return call
 
 
