@@ -76,14 +76,16 @@ def _on_stream(fn):
 
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        if stream is not None:
-            with torch.cuda.stream(stream):
-                return fn(*args, **kw)
         if not args and name not in kw:
             raise TypeError("%s() missing operand %r" % (fn.__name__, name))
         first = args[0] if args else kw[name]
         if not first.is_cuda:
             raise ValueError("operands must be device tensors")
+        if stream is not None:
+            if stream.device != first.device:
+                raise ValueError("stream is on %s, the operands on %s" % (stream.device, first.device))
+            with torch.cuda.stream(stream):
+                return fn(*args, **kw)
         if first.get_device() != torch.cuda.current_device():
             with torch.cuda.device(first.device):
                 return fn(*args, **kw)

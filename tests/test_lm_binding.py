@@ -42,3 +42,17 @@ def test_signature_and_missing_operands(op):
     assert names[:len(_args(op))] == list(_args(op))
     with pytest.raises(TypeError, match=names[0]):
         getattr(g, op)()
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_stream_of_another_device(op):
+    """A stream that is not the operands' device's is refused: the work would
+    go to the other device's current stream, unordered with the caller's."""
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    class Operand:
+        device, is_cuda = torch.device("cuda", 0), True
+    rest = list(_args(op).values())[1:]
+    with pytest.raises(ValueError, match="stream"):
+        getattr(g, op)(Operand(), *rest, stream=Stream())
