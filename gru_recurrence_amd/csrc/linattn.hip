@@ -359,6 +359,13 @@ __device__ __forceinline__ int64_t part_at(const LinArgs &a, int bh, int slice, 
     return (((wg * NW + w) * (DA / 16) + tile) * 64 + lane) * 4;
 }
 
+// log2 of the decay e^g; kept finite, so that 0 times it is 0 (a = 0).  NaN
+// stays (fmaxf would make it a decay of 0).
+__device__ __forceinline__ float log2_decay(float g) {
+    const float g2 = g * kLog2e;
+    return g2 < -1e30f ? -1e30f : g2;
+}
+
 // Up to three pieces before the last segment, a workgroup adds up the earlier
 // ones' X itself; past that their reading costs more than a launch.
 __host__ __device__ __forceinline__ bool folds(const LinArgs &a) { return (a.nseg - 1) * a.subs <= 3; }
@@ -408,8 +415,7 @@ void lin_kernel(LinArgs a) {
     ty.init((const T *)R.y.p + (int64_t)b * R.y.sb + (int64_t)div(h, R.gy) * R.Da, R.y.st, a.T, R.rev, R.Da);
     tz.init((const T *)R.z.p + (int64_t)b * R.z.sb + (int64_t)div(h, R.gz) * R.Db + col0, R.z.st, a.T, R.rev, nc);
 
-    // log2 of the decay; kept finite so that 0 times it is 0 (a = 0)
-    const float g2 = fmaxf(a.g[h] * kLog2e, -1e30f);
+    const float g2 = log2_decay(a.g[h]);
     auto power = [&](int n) { return __builtin_amdgcn_exp2f(g2 * (float)n); };
 
     const float powc = power(c);
@@ -676,7 +682,7 @@ __global__ __launch_bounds__(256) void lin_carry_kernel(LinArgs a, int E) {
     const Role &R = a.role[i / per];
     const int64_t j = i % per, wg = j / E;
     const int h = (int)(wg / a.slices % a.NH);
-    const float f = __builtin_amdgcn_exp2f(fmaxf(a.g[h] * kLog2e, -1e30f) * (float)a.sub_rows);
+    const float f = __builtin_amdgcn_exp2f(log2_decay(a.g[h]) * (float)a.sub_rows);
     float *p = R.part + wg * slots * E + j % E;
     float X = 0.0f;
     for (int s = 1; s <= last; s += kAhead) {
