@@ -32,11 +32,12 @@
 // loads of gfx950.
 //
 // Arithmetic: x, y, z as given (bf16 or float32), all sums float32.  P, X and
-// the decayed z are operands of further products; in bf16 calls P and X are
-// split into a bf16 and the bf16 of what that leaves (2^-17 of it), so that
-// outputs carry one rounding, their own; the decayed z, which X is made of, is
-// split in three and so keeps the states to float32.  float32 calls use the
-// float32 matrix instructions.
+// the decayed z are operands of further products; in bf16 calls they are split
+// in three bf16 parts (8 + 8 + 8 bits, so nothing is left out), and outputs
+// carry one rounding, their own.  Two parts for P and X (2^-17 of them left out)
+// took 62 us for 66 (T1024 B16 NH6 D128) and 96 for 104 (backward T1000 B8
+// NH8:4 D128), but left outputs 1e-4 from a float32 evaluation rounded once,
+// for 3e-5.  float32 calls use the float32 matrix instructions.
 //
 // Few (batch row, head) pairs leave the chip empty, so the rows are cut into
 // segments: a first launch forms the segments' own X from nothing (in pieces of
@@ -108,7 +109,8 @@ typedef __attribute__((ext_vector_type(2))) float f32x2;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
-// A float32 operand: as it is, or as a bf16 and the bf16 of what that leaves.
+// A float32 operand: as it is, or as a bf16, the bf16 of what that leaves, and
+// the bf16 of what is left then (nothing beyond: 8 + 8 + 8 bits).
 template <typename T>
 struct Wide;
 template <>
@@ -132,62 +134,50 @@ __device__ __forceinline__ void split8(Frag<uint16_t> &f, float *x) {
 }
 template <>
 struct Wide<uint16_t> {
-    Frag<uint16_t> hi, lo;
-    __device__ void set(float *x) {
-        split8(hi, x);
-        split8(lo, x);
-    }
-};
-// The same with nothing left out: a bf16 operand in three parts.
-template <typename T>
-struct Whole : Wide<T> {};
-template <>
-struct Whole<uint16_t> {
     Frag<uint16_t> part[3];
     __device__ void set(float *x) {
 #pragma unroll
         for (int i = 0; i < 3; ++i) split8(part[i], x);
     }
 };
-__device__ __forceinline__ void mma(f32x4 &d, const Frag<uint16_t> &a, const Whole<uint16_t> &b) {
-#pragma unroll
-    for (int i = 0; i < 3; ++i) mma(d, a, b.part[i]);
-}
 __device__ __forceinline__ void mma(f32x4 &d, const Frag<float> &a, const Wide<float> &b) { mma(d, a, b.f); }
 __device__ __forceinline__ void mma(f32x4 &d, const Wide<float> &a, const Frag<float> &b) { mma(d, a.f, b); }
 __device__ __forceinline__ void mma(f32x4 &d, const Frag<uint16_t> &a, const Wide<uint16_t> &b) {
-    mma(d, a, b.hi);
-    mma(d, a, b.lo);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) mma(d, a, b.part[i]);
 }
 __device__ __forceinline__ void mma(f32x4 &d, const Wide<uint16_t> &a, const Frag<uint16_t> &b) {
-    mma(d, a.hi, b);
-    mma(d, a.lo, b);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) mma(d, a.part[i], b);
 }
 
 // P^T in LDS: operands of depth 32 (pairs of tiles), each in lane order.  A
 // tile is half an operand: four of a lane's eight elements.
-constexpr int kOperand = 64 * 32;  // bytes of one, of either type
+template <typename T>
+constexpr int kOperand = sizeof(T) == 2 ? 3 * 64 * 16 : 2 * 64 * 16;  // bytes of one
 __device__ __forceinline__ void put_half(char *o, int half, float *x, uint16_t) {
     const int lane = threadIdx.x & 63;
-    uint2 h, l;
-    h.x = split2(x), h.y = split2(x + 2);
-    l.x = split2(x), l.y = split2(x + 2);
-    *(uint2 *)(o + lane * 16 + half * 8) = h;
-    *(uint2 *)(o + 1024 + lane * 16 + half * 8) = l;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        uint2 w;
+        w.x = split2(x), w.y = split2(x + 2);
+        *(uint2 *)(o + i * 1024 + lane * 16 + half * 8) = w;
+    }
 }
 __device__ __forceinline__ void put_half(char *o, int half, float *x, float) {
     *(float4 *)(o + half * 1024 + (threadIdx.x & 63) * 16) = make_float4(x[0], x[1], x[2], x[3]);
 }
-__device__ __forceinline__ void get_operand(Wide<uint16_t> &w, const char *o) {
-    const int lane = threadIdx.x & 63;
-    w.hi.v = *(const bf16x8 *)(o + lane * 16);
-    w.lo.v = *(const bf16x8 *)(o + 1024 + lane * 16);
+// One of its parts: products take them one after another.
+template <typename T>
+constexpr int kParts = sizeof(T) == 2 ? 3 : 1;
+__device__ __forceinline__ void get_part(Frag<uint16_t> &f, const char *o, int i) {
+    f.v = *(const bf16x8 *)(o + i * 1024 + (threadIdx.x & 63) * 16);
 }
-__device__ __forceinline__ void get_operand(Wide<float> &w, const char *o) {
+__device__ __forceinline__ void get_part(Frag<float> &f, const char *o, int) {
     const int lane = threadIdx.x & 63;
     const float4 a = *(const float4 *)(o + lane * 16), b = *(const float4 *)(o + 1024 + lane * 16);
-    w.f.v[0] = a.x; w.f.v[1] = a.y; w.f.v[2] = a.z; w.f.v[3] = a.w;
-    w.f.v[4] = b.x; w.f.v[5] = b.y; w.f.v[6] = b.z; w.f.v[7] = b.w;
+    f.v[0] = a.x; f.v[1] = a.y; f.v[2] = a.z; f.v[3] = a.w;
+    f.v[4] = b.x; f.v[5] = b.y; f.v[6] = b.z; f.v[7] = b.w;
 }
 
 // Depth elements of row `row`, depths [32 kb, 32 kb + 32), from a row-major
@@ -348,7 +338,7 @@ struct Lds {
     static constexpr int operands = (RT / 2) * (RT / 2 + 1);
     static constexpr size_t y = 0, z = y + sizeof(T) * C * LD, w = z + sizeof(T) * C * LDZ,
                             x = w + sizeof(float) * C, p = x + sizeof(T) * C * LDX,
-                            bytes = STATE ? x : p + operands * kOperand;
+                            bytes = STATE ? x : p + operands * kOperand<T>;
 };
 
 // Fragment order of one workgroup's X: [wave][DA/16 tiles][lane][4].
@@ -472,7 +462,7 @@ void lin_kernel(LinArgs a) {
                 for (int r = 0; r < 4; ++r) X[t][r] = fs * X[t][r] + v[t][r];
         }
         // the tiles above the diagonal that share an operand with one on it
-        for (int i = tid; i < L::operands * kOperand / 16; i += 64 * NW)
+        for (int i = tid; i < L::operands * kOperand<T> / 16; i += 64 * NW)
             ((uint4 *)ps)[i] = make_uint4(0, 0, 0, 0);
     }
 
@@ -528,7 +518,7 @@ void lin_kernel(LinArgs a) {
                     e[r] = lag >= 0 ? d[r] * (R.is * power(max(lag, 0))) : 0.0f;
                 }
                 // operands before this tile row's: 1, 1, 2, 2, ... each
-                put_half(ps + ((it / 2) * (it / 2 + 1) + (it & 1) * (it / 2 + 1) + jt / 2) * kOperand,
+                put_half(ps + ((it / 2) * (it / 2 + 1) + (it & 1) * (it / 2 + 1) + jt / 2) * kOperand<T>,
                          jt & 1, e, T());
             }
             // what the carried X gives
@@ -574,13 +564,16 @@ void lin_kernel(LinArgs a) {
 
         if constexpr (!STATE) {
             // operand q belongs to tile row (0, 1, 2, 2, 3, 3)[q], depth block (0, 0, 0, 1, 0, 1)[q]
-            Wide<T> pw[2];
-            get_operand(pw[0], ps);
+            constexpr int NP = L::operands * kParts<T>;
+            Frag<T> pf[3];
+            get_part(pf[0], ps, 0);
+            if (NP > 1) get_part(pf[1], ps + 1 / kParts<T> * kOperand<T>, 1 % kParts<T>);
 #pragma unroll
-            for (int q = 0; q < L::operands; ++q) {
-                if (q + 1 < L::operands) get_operand(pw[(q + 1) & 1], ps + (q + 1) * kOperand);
+            for (int i = 0; i < NP; ++i) {
+                const int q = i / kParts<T>, j = i + 2;
+                if (j < NP) get_part(pf[j % 3], ps + j / kParts<T> * kOperand<T>, j % kParts<T>);
                 __builtin_amdgcn_sched_barrier(0);
-                mma(o[q < 2 ? q : 1 + q / 2], zf[q < 2 ? 0 : q & 1], pw[q & 1]);
+                mma(o[q < 2 ? q : 1 + q / 2], zf[q < 2 ? 0 : q & 1], pf[i % 3]);
                 __builtin_amdgcn_sched_barrier(0);
             }
             mfma_chain_end();
@@ -629,7 +622,7 @@ void lin_kernel(LinArgs a) {
                 unpack(e, zf[kb]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) e[i] *= ww[i];
-                Whole<T> zw;
+                Wide<T> zw;
                 zw.set(e);
                 // reads of LDS run a tile ahead of the products
                 constexpr int YA = 1;

@@ -502,9 +502,9 @@ rnn_status rnn_token_logprobs_bwd(int M, int V, rnn_dtype dt, const void *logits
  * [T][B][heads][D] in dtype dt.  Dk, Dv <= 256, and B * NH * max(Dk, Dv) < 2^26
  * but for the forward of one token (else RNN_ERR_UNSUPPORTED).
  * Outputs overlap no input but where a call says so.
- * bf16 calls accumulate in float32 and keep every intermediate to 2^-17 of
- * itself, states to float32; the outputs' rounding is the only one to bf16.  Inputs are finite; a
- * value that is not may reach every output of its batch row and head.
+ * bf16 calls keep every sum, state and intermediate to float32; the outputs'
+ * rounding is the only one to bf16.  Inputs are finite; a value that is not may
+ * reach every output of its batch row and head.
  */
 typedef struct {
     int T, B, NH, NKV, Dk, Dv;

@@ -65,3 +65,67 @@ def test_linattn_states_are_float32(T, dt):
         assert (err <= c * np.abs(want)).all(), (name, float((err / (c * np.abs(want) + 1e-300)).max()))
     near("S", g.linattn_fwd(zero, first, firstv, gd)[1], T - 1)
     near("dS0", g.linattn_bwd(last, zero, zero, gd, lastv, scale=1.0)["dS0"], T)
+
+
+def _pairs(rng, n, D):
+    """n rows of whole numbers up to 255 in neighbours that differ in one place
+    by one: products with any row are large, their differences small."""
+    x = rng.integers(-255, 256, (n, D))
+    x[1::2] = x[0::2]
+    x[1::2, rng.integers(0, D)] += 1
+    return np.clip(x, -256, 255)
+
+
+def _differences(n, D):
+    """Column c takes row 2c less row 2c + 1."""
+    z = np.zeros((n, D), np.int64)
+    for c in range(min(D, n // 2)):
+        z[2 * c, c], z[2 * c + 1, c] = 1, -1
+    return z
+
+
+@TYPES
+@pytest.mark.parametrize("T,D", [(40, 16), (64, 32), (64, 128), (150, 64)])
+def test_linattn_products_of_rows_keep_every_bit(T, D, dt):
+    """Without decay and with whole numbers every product and sum is exact in
+    float32, so the outputs are the exact ones, rounded once: x . y reaches 2^23
+    and its odd last bits are all that is left of z's differences."""
+    rng = np.random.default_rng(T + D)
+    x, y, z = rng.integers(-255, 256, (T, D)), _pairs(rng, T, D), _differences(T, D)
+    low = np.tril(np.ones((T, T), np.int64))
+    want = _bf(((x @ y.T) * low) @ z, dt)                         # row i: sum over j <= i
+    assert np.abs((x @ y.T)).max() < 2 ** 24
+    rev = lambda t: t[::-1]  # noqa: E731
+    X, Y, Z = (_dev(t.reshape(T, 1, 1, D), dt) for t in (x, y, z))
+    Xr, Yr, Zr = (_dev(rev(t).reshape(T, 1, 1, D), dt) for t in (x, y, z))
+    gd = torch.zeros(1, device="cuda")
+    o, _ = g.linattn_fwd(X, Y, Z, gd, scale=1.0)
+    got = {"o": o, "dq": g.linattn_bwd(Y, Z, Y, gd, X, scale=1.0)["dq"],   # x, y, z = do, v, k
+           "dk": g.linattn_bwd(Zr, Zr, Xr, gd, Yr, scale=1.0)["dk"].flip(0),  # v, do, q
+           "dv": g.linattn_bwd(Yr, Xr, Yr, gd, Zr, scale=1.0)["dv"].flip(0)}  # k, q, do
+    for name, t in got.items():
+        assert np.array_equal(t.double().cpu().numpy()[:, 0, 0], want), name
+
+
+@TYPES
+@pytest.mark.parametrize("T,D", [(3, 16), (70, 64), (64, 128), (1500, 128)])
+def test_linattn_outputs_see_every_bit_of_the_state(T, D, dt):
+    """The state's share of an output is the difference of two of its rows, of
+    24 bits each."""
+    rng = np.random.default_rng(T * D)
+    S = rng.integers(2 ** 22, 2 ** 23, (D, D))
+    S[1::2] = S[0::2] - rng.integers(-255, 256, (D // 2, D))
+    x = np.zeros((T, D), np.int64)
+    m = rng.integers(0, D // 2, T)
+    x[np.arange(T), 2 * m], x[np.arange(T), 2 * m + 1] = 1, -1
+    want = (x @ S).astype(np.float64)                             # at most 255: exact in bf16
+    z = torch.zeros((T, 1, 1, D), dtype=DT[dt], device="cuda")
+    X, gd = _dev(x.reshape(T, 1, 1, D), dt), torch.zeros(1, device="cuda")
+    St, Sr = _dev(S.reshape(1, 1, D, D), "f32"), _dev(S.T.reshape(1, 1, D, D), "f32")
+    o, ST = g.linattn_fwd(X, z, z, gd, St, scale=1.0)
+    got = {"o": o, "dq": g.linattn_bwd(z, z, z, gd, X, Sr, scale=1.0)["dq"],
+           "dk": g.linattn_bwd(z, z, X, gd, z, None, Sr, scale=1.0)["dk"],
+           "dv": g.linattn_bwd(z, X, z, gd, z, None, St, scale=1.0)["dv"]}
+    for name, t in got.items():
+        assert np.array_equal(t.double().cpu().numpy()[:, 0, 0], want), name
+    assert torch.equal(ST, St)
