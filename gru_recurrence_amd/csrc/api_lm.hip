@@ -30,8 +30,6 @@ lm::Ids ids_of(const rnn_ids *i, int T, int B) {
     return lm::Ids{i->data, i->stride_t, i->stride_b, T, B, i->type == RNN_I64};
 }
 
-constexpr int kMaxVocab = 1000000;
-
 bool logp_dims_ok(int M, int V) { return M > 0 && V > 0; }
 
 bool lin_dims_ok(const rnn_lin_dims *d) {
@@ -91,7 +89,7 @@ rnn_status rnn_embed_bwd(int T, int B, int V, int D, rnn_dtype dt, const rnn_ids
 }
 
 size_t rnn_workspace_size_logprobs(int M, int V, int K) {
-    if (!logp_dims_ok(M, V) || V > kMaxVocab || K < 0 || K > V || K > lm::kMaxTop) return 0;
+    if (!logp_dims_ok(M, V) || V > lm::kMaxVocab || K < 0 || K > V || K > lm::kMaxTop) return 0;
     return lm::logp_bytes(M, V, K);
 }
 
@@ -108,7 +106,7 @@ rnn_status rnn_token_logprobs(int M, int V, rnn_dtype dt, const void *logits, in
     for (const void *p : ps)
         if (p && !view_ok(p, 4)) return RNN_ERR_INVALID_ARG;
     if (!aligned16(ws)) return RNN_ERR_INVALID_ARG;
-    if (V > kMaxVocab || K > lm::kMaxTop || !lm::logp_grid_ok(M, V, dt == RNN_BF16))
+    if (V > lm::kMaxVocab || K > lm::kMaxTop || !lm::logp_grid_ok(M, V, dt == RNN_BF16))
         return RNN_ERR_UNSUPPORTED;
     const size_t need = lm::logp_bytes(M, V, K);
     if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;
@@ -129,7 +127,7 @@ rnn_status rnn_token_logprobs_bwd(int M, int V, rnn_dtype dt, const void *logits
     const void *ps[] = {lse, entropy, dlogp, dentropy};
     for (const void *p : ps)
         if (p && !view_ok(p, 4)) return RNN_ERR_INVALID_ARG;
-    if (V > kMaxVocab || !lm::logp_bwd_grid_ok(M, V, dt == RNN_BF16)) return RNN_ERR_UNSUPPORTED;
+    if (V > lm::kMaxVocab || !lm::logp_bwd_grid_ok(M, V, dt == RNN_BF16)) return RNN_ERR_UNSUPPORTED;
     lm::LogpBwdArgs a{M, V, logits, ld, tok, it == RNN_I64, lse, entropy, dlogp, dentropy, dlogits, ldd};
     return done(lm::launch_logp_bwd(a, dt == RNN_BF16, stream));
 }

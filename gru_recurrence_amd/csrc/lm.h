@@ -63,7 +63,7 @@ hipError_t launch_embed_bwd(const Ids &ids, int V, int D, bool bf16, const void 
                             float *dtable, void *ws, hipStream_t s);
 
 // ---- token log probabilities (logprob.hip)
-constexpr int kMaxTop = 64;
+constexpr int kMaxTop = 64, kMaxVocab = 1000000;
 struct LogpArgs {
     int M, V, K;
     const void *logits;

@@ -25,6 +25,7 @@
 // found exactly by bisection over value and index instead (the chunk is read
 // again for it: held on to, it cost the ordinary path its registers).
 #include <algorithm>
+#include <mutex>
 
 #include "lm.h"
 
@@ -439,10 +440,23 @@ hipError_t logp_t(const LogpArgs &a, hipStream_t s) {
     if (nch > 1) {
         // a wave joins a row where its keys are few: more rows are then in flight
         const size_t lds = ((size_t)nch * a.K + 2) * 8;
-        if (nch * a.K <= 256)
+        if (nch * a.K <= 256) {
             hipLaunchKernelGGL((logp_join_kernel<T, 64>), dim3((unsigned)a.M), dim3(64), lds, s, a, nch);
-        else
+        } else {
+            hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            // with its kept keys this passes 64 KiB from V of about 909000 at K = 64
+            // on, which must be allowed once per kernel
+            static std::once_flag once;
+            static hipError_t attr = hipSuccess;
+            std::call_once(once, [] {
+                attr = hipFuncSetAttribute(reinterpret_cast<const void *>(&logp_join_kernel<T, 256>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)((chunks(kMaxVocab, kChunk, sizeof(T)) * kMaxTop + 2) * 8));
+            });
+            if (attr != hipSuccess) return attr;
             hipLaunchKernelGGL((logp_join_kernel<T, 256>), dim3((unsigned)a.M), dim3(256), lds, s, a, nch);
+        }
     }
     return hipGetLastError();
 }
