@@ -19,11 +19,15 @@
 //
 // The K candidates of a chunk: the K-th largest of the maxima of 16, 32 or 64
 // groups of threads (at least twice K, or 64) is a bound that at least K
-// entries reach, and few more do.  Those that reach it are collected (any order) and ranked by counting over
-// the unique keys (value, index), so the result does not depend on the order.
-// Where ties or a sorted row let more than kCand through, the K-th key is
-// found exactly by bisection over value and index instead (the chunk is read
-// again for it: held on to, it cost the ordinary path its registers).
+// entries reach, and few more do.  Those that reach it are collected (any
+// order) and ranked by counting over the unique keys (value, index), so the
+// result does not depend on the order.  Where ties at the bound let more than kCand through (a mask rules out the
+// chunk, or all but fewer than K of its groups), those above it are collected
+// and the lowest indices of those that equal it added (4096 rows of 32000
+// float32, one block of 8192 ids ruled out: 161 us for 100 without; the search
+// below took 2490).  Where more than kCand lie above it (in fewer than K
+// groups), the K-th key is found by bisection over value and index.  (The chunk is read again for either: held on to, it cost the
+// ordinary path its registers.)
 #include <algorithm>
 #include <mutex>
 
@@ -231,6 +235,69 @@ __device__ __forceinline__ int exact_top(Row<T> r, int u0, int K, uint64_t *cand
     return *ncand;
 }
 
+// The same where `tau`, which more than kCand entries of the chunk reach, lets
+// at most that many above it: those, and of the entries that equal it the lowest
+// indices.  (Masks are such ties: a chunk that -inf or the type's lowest value
+// rules out but for fewer than K of its groups has that value for its bound.)
+// Reads the chunk once more, and again as far as the equal entries are needed.
+template <typename T, int NT>
+__device__ __forceinline__ int tied_top(Row<T> r, int u0, int K, float tau, uint64_t *cand, int *ncand,
+                                        int *tmp) {
+    constexpr int N = Row<T>::N, U = kPer / N;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    __syncthreads();
+    if (tid == 0) *ncand = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int j = 0; j < U; ++j) {
+        const int u = u0 + j * NT + tid, i0 = u * N - r.off;
+        float x[N];
+        r.load(u, x);
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (!(x[e] <= tau) && i0 + e >= 0 && i0 + e < r.V) {
+                const int at = atomicAdd(ncand, 1);
+                if (at < kCand) cand[at] = pair_key(x[e], i0 + e);
+            }
+    }
+    __syncthreads();
+    int n = *ncand;
+    if (n > kCand) return exact_top<T, NT>(r, u0, K, cand, ncand, tmp);
+#pragma unroll 1
+    for (int j = 0; j < U && n < K; ++j) {  // indices grow with j, the thread, e
+        const int u = u0 + j * NT + tid, i0 = u * N - r.off;
+        float x[N];
+        r.load(u, x);
+        int mine = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) mine += x[e] == tau && i0 + e >= 0 && i0 + e < r.V;
+        int at = mine;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int y = __shfl_up(at, o);
+            if (lane >= o) at += y;
+        }
+        if (lane == 63) tmp[w] = at;
+        __syncthreads();
+        at += n - mine;
+        int all = 0;
+#pragma unroll
+        for (int i = 0; i < NT / 64; ++i) {
+            at += i < w ? tmp[i] : 0;
+            all += tmp[i];
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (x[e] == tau && i0 + e >= 0 && i0 + e < r.V) {
+                if (at < K) cand[at] = pair_key(x[e], i0 + e);
+                ++at;
+            }
+        n = min(n + all, K);
+        __syncthreads();
+    }
+    return n;
+}
+
 template <typename T, bool TOP>
 __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
     constexpr int NT = kThreads, N = Row<T>::N, U = kPer / N, W = NT / 64;
@@ -272,6 +339,7 @@ __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
     s = wave_sum(s);
     t = wave_sum(t);
     if (lane == 0) ws[w] = s, wt[w] = t;
+    float tau = 0.0f;
     if constexpr (TOP) {
         // the K-th largest group maximum: the least of those with fewer than K above
         // (groups by lane, so that a chunk that is hardly filled still fills them)
@@ -282,7 +350,8 @@ __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
 #pragma unroll 8
         for (int j = 0; j < groups; ++j)
             above += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), j)) > mine;
-        const float tau = -wave_max(above < a.K ? -mine : -INFINITY);
+        tau = __uint_as_float(
+            __builtin_amdgcn_readfirstlane(__float_as_uint(-wave_max(above < a.K ? -mine : -INFINITY))));
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             if (!(x[i] < tau)) {
@@ -307,7 +376,7 @@ __global__ __launch_bounds__(kThreads) void logp_kernel(LogpArgs a, int nch) {
     }
     if constexpr (TOP) {
         int n = ncand;
-        if (n > kCand) n = exact_top<T, NT>(r, u0, a.K, cand, &ncand, tmp);
+        if (n > kCand) n = tied_top<T, NT>(r, u0, a.K, tau, cand, &ncand, tmp);
         if (nch == 1) {
             rank_keys<NT>(cand, n, a.K, [&](int k, uint64_t key) {
                 a.top_id[(int64_t)row * a.K + k] = (int)~(uint32_t)key;

@@ -465,7 +465,9 @@ rnn_status rnn_embed_bwd(int T, int B, int V, int D, rnn_dtype dt, const rnn_ids
  * everything out has lse and every log probability -inf and entropy 0.  A row
  * with a NaN or +inf gives NaN.  entropy, lse may be NULL; top_id, top_logp
  * are required where K > 0.  0 <= K <= min(V, 64), V <= 1000000 (else
- * RNN_ERR_UNSUPPORTED).  Float32 throughout, each logit read once.
+ * RNN_ERR_UNSUPPORTED).  Float32 throughout.  Each logit is read once; for the
+ * alternatives again where over a thousand of a chunk of 8192 reach what bounds
+ * them, as in a chunk that a mask rules out.
  */
 size_t rnn_workspace_size_logprobs(int M, int V, int K);
 rnn_status rnn_token_logprobs(int M, int V, rnn_dtype dt, const void *logits, int64_t ld,
