@@ -73,6 +73,12 @@ def load(path: Optional[str] = None):
     if not os.path.exists(p):
         raise ImportError("librnn355.so not built at %s: run "
                           "`python -m gru_recurrence_amd.build`" % p)
+    try:
+        # torch brings a HIP runtime of its own, which the library then uses too; the
+        # other way round the process would hold two, and crash at the first launch
+        import torch  # noqa: F401
+    except ImportError:
+        pass
     lib = ctypes.CDLL(p)
     P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
     D = ctypes.POINTER(Dims)
