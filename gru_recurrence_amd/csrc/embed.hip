@@ -16,10 +16,13 @@
 //     pieces, one for each wave (the merge-path split: a binary search along
 //     each cut's diagonal).  A piece reads its positions' rows and writes the
 //     rows that end in it, zeros included, so neither a frequent id nor an
-//     absent one unbalances it.  The open row at a piece's end goes to a
+//     absent one unbalances this step.  The open row at a piece's end goes to a
 //     carry;
 //  3. the carries of each run of pieces with the same open row are added to
-//     that row, in order.
+//     that row, in order, by one wave for each tile of columns: a sum in turn
+//     over a 32nd of an id's occurrences.  So here a dominant id does cost:
+//     16384 ids of 32000 x 768 float32 44 us with the skew of text, 62 with half
+//     of them the same, 82 with all; 262144 ids 297, 685 and 1130.
 //
 // Measured: lookup of 16384 rows of 768 bf16 8.4 us (4.1 TB/s); gradient of
 // 16384 ids of 32000 x 768 float32 31 us for the sums (4.8 TB/s), 17 for the

@@ -45,10 +45,10 @@
 // they are few the main launch adds them up itself), and the main launch runs
 // all segments at once.
 //
-// Measured: T1024 B16 NH6 D128 bf16 12.6 us for the states and 47 for the main
-// launch (114 MB from memory, matrix units 18% busy): bound by the latency of a
-// chunk's phases, 12-13 thousand cycles for 2800 of products.  T8191 NH12 D64
-// float32 15 + 8 + 33 us, matrix units 47% busy.  A token for B64 NH12 D64
+// Measured: T1024 B16 NH6 D128 bf16 13.6 us for the states and 52 for the main
+// launch (114 MB from memory, matrix units 20% busy): bound by the latency of a
+// chunk's phases, 13-14 thousand cycles for 3500 of products.  T8191 NH12 D64
+// float32 16 + 8 + 33 us, matrix units 47% busy.  A token for B64 NH12 D64
 // 7.0 us (3.6 TB/s).
 #include <algorithm>
 #include <mutex>
@@ -362,8 +362,10 @@ __host__ __device__ __forceinline__ bool folds(const LinArgs &a) { return (a.nse
 
 // STATE: only the piece's own X, from nothing (the first: from the initial
 // state), into its slot of `part`.
-// Two workgroups to a CU where their LDS allows it: one's barriers and loads
-// then hide behind the other's products.
+// Registers for two workgroups to a CU where their LDS allows it: in a grid of
+// many, one's barriers and loads then hide behind the other's products (B64 NH8
+// T1024 D128 175 us against 190 with the registers of one; backward B16 NH6 129
+// against 156).  A grid of one to a CU gains nothing (T1024 B16 NH6 66 for 65).
 // FAST: every operand in whole 16-byte pieces and z in whole 16-column tiles
 // (the host's rule); the general form, which reads value by value, then stays
 // out of the registers of the ordinary one (7 rows of 1968 tokens, 6 heads of
@@ -485,8 +487,8 @@ void lin_kernel(LinArgs a) {
         if (tid < C) wz[tid] = R.is * power(max(m - tid, 0));  // rows past n are zero in z
         lds_barrier();
 
-        // the next chunk's loads have this chunk's whole time (issued after P.z only:
-        // t1024 b16 nh6 64 us for 60, b64 nh8 171 for 154)
+        // the next chunk's loads have this chunk's whole time (T1024 B16 NH6 D128 66 us
+        // against 71 issued after P.z, B64 NH8 175 against 183)
         if (row0 + C < row_hi) fetch(row0 + C);
         f32x4 o[STATE ? 1 : RT];
         if constexpr (!STATE) {
@@ -789,11 +791,19 @@ int waves_of(int Db) { return Db > 64 ? 8 : 4; }
 int slices_of(int Db, int NW) { return (Db + 16 * NW - 1) / (16 * NW); }
 
 // Segments: enough workgroups for the chip's 256 CUs, one of eight waves or
-// three of four to a CU (t1024 b16 nh6 d128, two segments: 51 us against 69
-// with four; 8191 rows of 12 heads of 64 in float32: 57 against 63 with 256
-// workgroups), and at least two chunks to a segment, which costs another pass
-// over y and z and a state.  That pass cuts a segment into pieces where there
-// are few of them.
+// three of four to a CU, and at least two chunks to a segment, which costs
+// another pass over y and z and a state.  That pass cuts a segment into pieces
+// where there are few of them.  Measured, us, for the workgroups aimed at:
+//   eight waves, bf16 D128                 256    512
+//     T1024 B16 NH6                         66     70
+//     T4096 B2 NH8                          54     63
+//     backward T1000 B8 NH8:4              104    118
+//   four waves, D64                        256    512    768   1024
+//     bf16 T8191 B1 NH12                  45.5   40.2   39.1   38.5
+//     bf16 T4096 B2 NH4                   27.6   28.9   28.9   28.7
+//     bf16 backward T8191 B1 NH12         94.9   70.2   67.3   73.3
+//     float32 T8191 B1 NH12               59.5   56.3   55.0   54.9
+//     float32 T1024 B16 NH12              84.8   91.1   82.5   93.7
 struct Cut {
     int nseg, subs, rows;  // rows of a piece
 };
