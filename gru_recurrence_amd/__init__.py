@@ -33,7 +33,9 @@ EXPORTS = ("rnn_status_str", "rnn_workspace_size", "rnn_plan_describe", "rnn_inp
            "rnn_embed_fwd", "rnn_workspace_size_embed_bwd", "rnn_embed_bwd",
            "rnn_workspace_size_logprobs", "rnn_token_logprobs", "rnn_token_logprobs_bwd",
            "rnn_workspace_size_linattn", "rnn_linattn_fwd", "rnn_linattn_step",
-           "rnn_linattn_bwd")
+           "rnn_linattn_bwd", "rnn_workspace_size_gated", "rnn_gated_fwd", "rnn_gated_step",
+           "rnn_gated_bwd", "rnn_workspace_size_clip", "rnn_grad_norm", "rnn_clip_grads",
+           "rnn_workspace_size_verify", "rnn_verify_drafts")
 
 
 class Dims(ctypes.Structure):
@@ -670,7 +672,10 @@ def workspace_status(ws, stream=None) -> int:
 # loaded with their first use.
 _LM = ("embed_fwd", "embed_bwd", "token_logprobs", "token_logprobs_bwd", "linattn_fwd",
        "linattn_step", "linattn_bwd", "LinDims", "workspace_size_embed_bwd",
-       "workspace_size_logprobs", "workspace_size_linattn", "OP_LIN_FWD", "OP_LIN_BWD")
+       "workspace_size_logprobs", "workspace_size_linattn", "OP_LIN_FWD", "OP_LIN_BWD",
+       "gated_fwd", "gated_step", "gated_bwd", "GatedDims", "workspace_size_gated", "OP_GATED_FWD",
+       "OP_GATED_BWD", "grad_norm", "clip_grads", "GradList", "workspace_size_clip",
+       "verify_drafts", "workspace_size_verify")
 
 
 def __getattr__(name):

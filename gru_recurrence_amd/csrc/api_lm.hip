@@ -1,6 +1,7 @@
 // api_lm.hip -- C ABI of the operators around the recurrence (embedding,
-// token log probabilities, linear attention): argument checks, workspace
-// sizes and the launches (lm.h).
+// token log probabilities, linear attention, gated linear recurrence, gradient
+// clipping, draft verification): argument checks, workspace sizes and the
+// launches (lm.h).
 #include "../../include/rnn355.h"
 #include "host.h"
 #include "lm.h"
@@ -55,6 +56,52 @@ lm::LinDims lin_dims(const rnn_lin_dims *d) {
 lm::LinSeq seq_of(const rnn_seq *s) { return lm::LinSeq{s->data, s->stride_t, s->stride_b}; }
 
 bool seq_ok(const rnn_seq *s, rnn_dtype dt) { return s && view_ok(s->data, elt(dt)); }
+
+bool out_ok(const rnn_seq_out *s, rnn_dtype dt) { return s && view_ok(s->data, elt(dt)); }
+
+lm::SeqOut out_of(const rnn_seq_out *s) {
+    return s ? lm::SeqOut{s->data, s->stride_t, s->stride_b} : lm::SeqOut{nullptr, 0, 0};
+}
+
+lm::LinSeq seq_or_none(const rnn_seq *s) { return s ? seq_of(s) : lm::LinSeq{nullptr, 0, 0}; }
+
+bool gated_dims_ok(const rnn_gated_dims *d) {
+    return d && d->T > 0 && d->B > 0 && d->D > 0 && (long)d->T * d->B <= (1L << 30);
+}
+
+bool gate_ok(rnn_gate g) { return g == RNN_GATE_LOGIT || g == RNN_GATE_DECAY; }
+
+bool gated_width_ok(const rnn_gated_dims *d) { return (long)d->B * d->D <= (1L << 30); }
+
+lm::GatedDims gated_dims(const rnn_gated_dims *d, rnn_gate g) {
+    return lm::GatedDims{d->T, d->B, d->D, g == RNN_GATE_LOGIT};
+}
+
+bool clip_list_ok(int count, const rnn_grad *list) {
+    if (count < 1 || !list) return false;
+    int64_t all = 0;
+    for (int i = 0; i < count; ++i) {
+        const rnn_grad &t = list[i];
+        if (!dtype_ok(t.dtype) || t.n < 0 || t.n > ((int64_t)1 << 40)) return false;
+        if ((all += t.n) > ((int64_t)1 << 40)) return false;
+        if (t.n > 0 && (!view_ok(t.data, elt(t.dtype)) || (uintptr_t)t.out % elt(t.dtype)))
+            return false;
+    }
+    return true;
+}
+
+// max_norm < 0: the norm alone
+rnn_status clip(int count, const rnn_grad *list, float max_norm, float *norm, void *ws,
+                size_t ws_bytes, hipStream_t stream) {
+    if (!clip_list_ok(count, list) || !norm || !view_ok(norm, 4) || !aligned16(ws))
+        return RNN_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < lm::clip_bytes()) return RNN_ERR_WORKSPACE;
+    return lm::launch_clip(count, list, max_norm, norm, ws, stream) == hipSuccess ? RNN_OK : RNN_ERR_HIP;
+}
+
+bool verify_dims_ok(int K, int B, int V) {
+    return K >= 0 && B > 0 && V > 0 && (long)(K + 1) * B <= (1L << 30);
+}
 
 rnn_status done(hipError_t e) { return e == hipSuccess ? RNN_OK : RNN_ERR_HIP; }
 
@@ -188,6 +235,104 @@ rnn_status rnn_linattn_bwd(const rnn_lin_dims *d, rnn_dtype dt, const rnn_seq *q
     if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;
     return done(lm::launch_lin_bwd(n, dt == RNN_BF16, seq_of(q), seq_of(k), seq_of(v), g, scale, S0,
                                    seq_of(dO), dST, dq, dk, dv, dS0, ws, stream));
+}
+
+size_t rnn_workspace_size_gated(rnn_gated_op op, const rnn_gated_dims *d, rnn_dtype dt) {
+    if (!gated_dims_ok(d) || !dtype_ok(dt) || !gated_width_ok(d)) return 0;
+    if (op != RNN_OP_GATED_FWD && op != RNN_OP_GATED_BWD) return 0;
+    return lm::gated_bytes(gated_dims(d, RNN_GATE_LOGIT), dt == RNN_BF16, op == RNN_OP_GATED_BWD);
+}
+
+rnn_status rnn_gated_fwd(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, const rnn_seq *f,
+                         const rnn_seq *x, const float *h0, const int *lens, const rnn_seq_out *h,
+                         float *hT, void *ws, size_t ws_bytes, hipStream_t stream) {
+    if (!gated_dims_ok(d) || !dtype_ok(dt) || !gate_ok(gate)) return RNN_ERR_INVALID_ARG;
+    if (!seq_ok(f, dt) || !seq_ok(x, dt) || !out_ok(h, dt) || (uintptr_t)lens % 4)
+        return RNN_ERR_INVALID_ARG;
+    const void *ps[] = {h0, hT, ws};
+    for (const void *p : ps)
+        if (!aligned16(p)) return RNN_ERR_INVALID_ARG;
+    const lm::GatedDims n = gated_dims(d, gate);
+    if (!gated_width_ok(d) || !lm::gated_grid_ok(n, dt == RNN_BF16, false)) return RNN_ERR_UNSUPPORTED;
+    const size_t need = lm::gated_bytes(n, dt == RNN_BF16, false);
+    if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;
+    return done(lm::launch_gated_fwd(n, dt == RNN_BF16, seq_of(f), seq_of(x), h0, lens, out_of(h), hT,
+                                     ws, stream));
+}
+
+rnn_status rnn_gated_step(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, const rnn_seq *f,
+                          const rnn_seq *x, const float *h, const rnn_seq_out *y, float *h_out,
+                          hipStream_t stream) {
+    if (!gated_dims_ok(d) || d->T != 1 || !dtype_ok(dt) || !gate_ok(gate)) return RNN_ERR_INVALID_ARG;
+    if (!seq_ok(f, dt) || !seq_ok(x, dt) || (y && !out_ok(y, dt)) || !h || !h_out || !aligned16(h) ||
+        !aligned16(h_out))
+        return RNN_ERR_INVALID_ARG;
+    const lm::GatedDims n = gated_dims(d, gate);
+    if (!gated_width_ok(d) || !lm::gated_step_grid_ok(n)) return RNN_ERR_UNSUPPORTED;
+    return done(lm::launch_gated_step(n, dt == RNN_BF16, seq_of(f), seq_of(x), h, out_of(y), h_out,
+                                      stream));
+}
+
+rnn_status rnn_gated_bwd(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, const rnn_seq *f,
+                         const rnn_seq *x, const rnn_seq *h, const rnn_seq *dh, const float *h0,
+                         const float *dhT, const int *lens, const rnn_seq_out *df,
+                         const rnn_seq_out *dx, float *dh0, void *ws, size_t ws_bytes,
+                         hipStream_t stream) {
+    if (!gated_dims_ok(d) || !dtype_ok(dt) || !gate_ok(gate)) return RNN_ERR_INVALID_ARG;
+    if (!seq_ok(f, dt) || !seq_ok(h, dt) || !seq_ok(dh, dt) || !out_ok(df, dt) || !out_ok(dx, dt) ||
+        (uintptr_t)lens % 4)
+        return RNN_ERR_INVALID_ARG;
+    if (gate == RNN_GATE_LOGIT ? !seq_ok(x, dt) : x && (uintptr_t)x->data % elt(dt))
+        return RNN_ERR_INVALID_ARG;
+    const void *ps[] = {h0, dhT, dh0, ws};
+    for (const void *p : ps)
+        if (!aligned16(p)) return RNN_ERR_INVALID_ARG;
+    const lm::GatedDims n = gated_dims(d, gate);
+    if (!gated_width_ok(d) || !lm::gated_grid_ok(n, dt == RNN_BF16, true)) return RNN_ERR_UNSUPPORTED;
+    const size_t need = lm::gated_bytes(n, dt == RNN_BF16, true);
+    if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;
+    return done(lm::launch_gated_bwd(n, dt == RNN_BF16, seq_of(f), seq_or_none(x), seq_of(h), seq_of(dh),
+                                     h0, dhT, lens, out_of(df), out_of(dx), dh0, ws, stream));
+}
+
+size_t rnn_workspace_size_clip(int count, const rnn_grad *list) {
+    return clip_list_ok(count, list) ? lm::clip_bytes() : 0;
+}
+
+rnn_status rnn_grad_norm(int count, const rnn_grad *list, float *norm, void *ws, size_t ws_bytes,
+                         hipStream_t stream) {
+    return clip(count, list, -1.0f, norm, ws, ws_bytes, stream);
+}
+
+rnn_status rnn_clip_grads(int count, const rnn_grad *list, float max_norm, float *norm, void *ws,
+                          size_t ws_bytes, hipStream_t stream) {
+    if (!(max_norm >= 0.0f)) return RNN_ERR_INVALID_ARG;
+    return clip(count, list, max_norm, norm, ws, ws_bytes, stream);
+}
+
+size_t rnn_workspace_size_verify(int K, int B, int V) {
+    if (!verify_dims_ok(K, B, V) || K > lm::kMaxDrafts || V > lm::kMaxVocab) return 0;
+    return lm::verify_bytes(K, B, V);
+}
+
+rnn_status rnn_verify_drafts(int K, int B, int V, rnn_dtype dt, const rnn_seq *logits,
+                             const rnn_ids *drafts, const rnn_seq *draft_logits, const float *u,
+                             const float *temperature, const int *n_drafts, int *tokens,
+                             int *accepted, void *ws, size_t ws_bytes, hipStream_t stream) {
+    if (!verify_dims_ok(K, B, V) || !dtype_ok(dt) || !seq_ok(logits, dt)) return RNN_ERR_INVALID_ARG;
+    if (K > 0 && !ids_ok(drafts)) return RNN_ERR_INVALID_ARG;
+    if (K > 0 && draft_logits && !seq_ok(draft_logits, dt)) return RNN_ERR_INVALID_ARG;
+    if (!u || !tokens || !accepted || !aligned16(ws)) return RNN_ERR_INVALID_ARG;
+    const void *ps[] = {u, temperature, n_drafts, tokens, accepted};
+    for (const void *p : ps)
+        if ((uintptr_t)p % 4) return RNN_ERR_INVALID_ARG;
+    if (K > lm::kMaxDrafts || V > lm::kMaxVocab || !lm::verify_grid_ok(K, B, V))
+        return RNN_ERR_UNSUPPORTED;
+    if (!ws || ws_bytes < lm::verify_bytes(K, B, V)) return RNN_ERR_WORKSPACE;
+    lm::VerifyArgs a{K, B, V, seq_of(logits), K > 0 ? seq_or_none(draft_logits) : lm::LinSeq{nullptr, 0, 0},
+                     K > 0 ? ids_of(drafts, K, B) : lm::Ids{nullptr, 0, 0, 1, 1, 0}, u, temperature,
+                     n_drafts, tokens, accepted, ws};
+    return done(lm::launch_verify(a, dt == RNN_BF16, stream));
 }
 
 }  // extern "C"

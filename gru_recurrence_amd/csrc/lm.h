@@ -1,14 +1,16 @@
 // lm.h -- launch interface of the operators around the recurrence of a
 // language model: embedding lookup and its gradient (embed.hip), token log
 // probabilities and their gradient (logprob.hip), linear attention with a
-// decay for each head (linattn.hip).  api_lm.hip checks the arguments and
-// calls these.
+// decay for each head (linattn.hip), the gated linear recurrence (gated.hip),
+// the gradient norm and clipping (clip.hip), verification of drafted tokens
+// (verify.hip).  api_lm.hip checks the arguments and calls these.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/rnn355.h"
 #include "common.h"
 
 namespace rnn355 {
@@ -116,6 +118,48 @@ hipError_t launch_lin_bwd(const LinDims &d, bool bf16, LinSeq q, LinSeq k, LinSe
                           const float *g, float scale, const float *S0, LinSeq dO,
                           const float *dST, void *dq, void *dk, void *dv, float *dS0, void *ws,
                           hipStream_t s);
+
+// ---- gated linear recurrence (gated.hip)
+struct GatedDims {
+    int T, B, D;
+    bool logit;  // gates given by their logits
+};
+// A sequence that is written: like LinSeq, D contiguous values a row.
+struct SeqOut {
+    void *p;
+    int64_t st, sb;
+};
+bool gated_grid_ok(const GatedDims &d, bool bf16, bool bwd);
+bool gated_step_grid_ok(const GatedDims &d);
+size_t gated_bytes(const GatedDims &d, bool bf16, bool bwd);
+hipError_t launch_gated_fwd(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, const float *h0,
+                            const int *lens, SeqOut h, float *hT, void *ws, hipStream_t s);
+hipError_t launch_gated_step(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, const float *h,
+                             SeqOut y, float *h_out, hipStream_t s);
+hipError_t launch_gated_bwd(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, LinSeq h, LinSeq dh,
+                            const float *h0, const float *dhT, const int *lens, SeqOut df,
+                            SeqOut dx, float *dh0, void *ws, hipStream_t s);
+
+// ---- gradient norm and clipping (clip.hip)
+size_t clip_bytes();
+// max_norm < 0: the norm alone
+hipError_t launch_clip(int count, const rnn_grad *list, float max_norm, float *norm, void *ws,
+                       hipStream_t s);
+
+// ---- verification of drafted tokens (verify.hip)
+constexpr int kMaxDrafts = 63;
+struct VerifyArgs {
+    int K, B, V;
+    LinSeq logits, q;  // q.p null: drafts without probabilities
+    Ids drafts;
+    const float *u, *temp;  // temp may be null
+    const int *n;           // may be null
+    int *tokens, *accepted;
+    void *ws;
+};
+size_t verify_bytes(int K, int B, int V);
+bool verify_grid_ok(int K, int B, int V);
+hipError_t launch_verify(const VerifyArgs &a, bool bf16, hipStream_t s);
 
 }  // namespace lm
 }  // namespace rnn355

@@ -1,6 +1,8 @@
 """Binding of the operators around the recurrence of a language model:
 embedding lookup and gradient, token log probabilities and gradient, linear
-attention with a decay for each head (include/rnn355.h has their formulas).
+attention with a decay for each head, gated linear recurrence, gradient norm
+and clipping, verification of drafted tokens (include/rnn355.h has their
+formulas).
 
 As in the rest of the package this is argument marshalling only.  Work and
 allocations of a call go to `stream` (default: the current stream of the
@@ -19,9 +21,14 @@ from . import RNN_BF16, RNN_F32, RNN_OK, RnnError, load as _load
 
 __all__ = ["embed_fwd", "embed_bwd", "token_logprobs", "token_logprobs_bwd", "linattn_fwd",
            "linattn_step", "linattn_bwd", "LinDims", "workspace_size_embed_bwd",
-           "workspace_size_logprobs", "workspace_size_linattn", "OP_LIN_FWD", "OP_LIN_BWD"]
+           "workspace_size_logprobs", "workspace_size_linattn", "OP_LIN_FWD", "OP_LIN_BWD",
+           "gated_fwd", "gated_step", "gated_bwd", "GatedDims", "workspace_size_gated",
+           "OP_GATED_FWD", "OP_GATED_BWD", "grad_norm", "clip_grads", "GradList",
+           "workspace_size_clip", "verify_drafts", "workspace_size_verify"]
 
 OP_LIN_FWD, OP_LIN_BWD = 0, 1
+OP_GATED_FWD, OP_GATED_BWD = 0, 1
+_GATES = {"logit": 0, "decay": 1}
 _DT = {torch.bfloat16: RNN_BF16, torch.float32: RNN_F32}
 _IT = {torch.int32: 0, torch.int64: 1}
 
@@ -41,6 +48,16 @@ class LinDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("T", "B", "NH", "NKV", "Dk", "Dv")]
 
 
+class GatedDims(ctypes.Structure):
+    """Dimensions of the gated linear recurrence (rnn_gated_dims)."""
+    _fields_ = [(n, ctypes.c_int) for n in ("T", "B", "D")]
+
+
+class _Grad(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int)]
+
+
 _declared = None
 
 
@@ -53,6 +70,7 @@ def load():
     P, I, S, L, F = (ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64,
                      ctypes.c_float)
     ids, seq, dims = ctypes.POINTER(_Ids), ctypes.POINTER(_Seq), ctypes.POINTER(LinDims)
+    gated, grads = ctypes.POINTER(GatedDims), ctypes.POINTER(_Grad)
     for name, res, args in (
             ("rnn_embed_fwd", I, [I, I, I, I, I, ids, P, L, F, P, P]),
             ("rnn_workspace_size_embed_bwd", S, [I] * 4),
@@ -63,7 +81,16 @@ def load():
             ("rnn_workspace_size_linattn", S, [I, dims, I]),
             ("rnn_linattn_fwd", I, [dims, I, seq, seq, seq, P, F, P, P, P, P, S, P]),
             ("rnn_linattn_step", I, [dims, I, seq, seq, seq, P, F, P, P, P, P]),
-            ("rnn_linattn_bwd", I, [dims, I, seq, seq, seq, P, F, P, seq, P, P, P, P, P, P, S, P])):
+            ("rnn_linattn_bwd", I, [dims, I, seq, seq, seq, P, F, P, seq, P, P, P, P, P, P, S, P]),
+            ("rnn_workspace_size_gated", S, [I, gated, I]),
+            ("rnn_gated_fwd", I, [gated, I, I, seq, seq, P, P, seq, P, P, S, P]),
+            ("rnn_gated_step", I, [gated, I, I, seq, seq, P, seq, P, P]),
+            ("rnn_gated_bwd", I, [gated, I, I, seq, seq, seq, seq, P, P, P, seq, seq, P, P, S, P]),
+            ("rnn_workspace_size_clip", S, [I, grads]),
+            ("rnn_grad_norm", I, [I, grads, P, P, S, P]),
+            ("rnn_clip_grads", I, [I, grads, F, P, P, S, P]),
+            ("rnn_workspace_size_verify", S, [I] * 3),
+            ("rnn_verify_drafts", I, [I, I, I, I, seq, ids, seq, P, P, P, P, P, P, S, P])):
         f = getattr(lib, name)
         f.restype, f.argtypes = res, args
     _declared = lib
@@ -392,3 +419,244 @@ def linattn_bwd(q, k, v, g, do, S0=None, dST=None, *, scale: Optional[float] = N
                                sdo, pT, *[r[n].data_ptr() for n in ("dq", "dk", "dv", "dS0")], wp,
                                wn, _current(dev)), "rnn_linattn_bwd")
     return r
+
+
+# ------------------------------------------------- gated linear recurrence
+def _gate(gate):
+    c = _GATES.get(gate)
+    if c is None:
+        raise ValueError("gate must be 'logit' or 'decay', got %r" % (gate,))
+    return c
+
+
+def _row(t, name, dtype, shape, dev):
+    """[T,B,D] with contiguous rows, any other strides."""
+    if t.device != dev:
+        _dev(t, name, dev)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    st, sb, sd = t.stride()
+    if sd != 1 and shape[2] > 1:
+        raise ValueError("%s needs contiguous rows of D values" % name)
+    return _Seq(t.data_ptr(), st, sb)
+
+
+def _row_out(t, name, dtype, shape, dev):
+    """An output sequence: (tensor, view); a view given must not overlap itself."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t, _Seq(t.data_ptr(), shape[1] * shape[2], shape[2])
+    v = _row(t, name, dtype, shape, dev)
+    need = shape[2]
+    for step, n in sorted(((v.stride_t, shape[0]), (v.stride_b, shape[1]))):
+        if n > 1:
+            if step < need:
+                raise ValueError("rows of %s overlap" % name)
+            need += step * (n - 1)
+    return t, v
+
+
+def _gated(f, x, gate, lens):
+    dev = f.device
+    dt = _dt(f, "f")
+    if f.dim() != 3:
+        raise ValueError("f must be [T, B, D], got %s" % (tuple(f.shape),))
+    shape = f.shape
+    sf = _row(f, "f", f.dtype, shape, dev)
+    sx = None if x is None else _row(x, "x", f.dtype, shape, dev)
+    d = GatedDims(*shape)
+    lp = _dense(lens, "lens", torch.int32, torch.Size((d.B,)), dev)
+    return d, dt, _gate(gate), sf, sx, lp, shape, dev
+
+
+def workspace_size_gated(op: int, dims: GatedDims, dtype_code: int) -> int:
+    return int(load().rnn_workspace_size_gated(op, dims, dtype_code))
+
+
+@_on_stream
+def gated_fwd(f, x, h0=None, *, gate: str = "logit", lens=None, ws=None, out=None):
+    """Gated linear recurrence over T tokens, elementwise in [T,B,D] views with
+    contiguous rows: gate "logit" h_t = a h_{t-1} + (1 - a) x_t with a =
+    sigmoid(f_t), gate "decay" h_t = f_t h_{t-1} + x_t.  h0 [B,D] float32 or None
+    (zeros); lens [B] int32: tokens of each row that count (h is 0 behind them).
+    Returns (h [T,B,D] in f's type, h_T [B,D] float32, the state behind the last
+    token that counts); `out` is a dict with "h" (any view) and "hT" (may be h0)."""
+    if x is None:
+        raise ValueError("x is required")
+    d, dt, gt, sf, sx, lp, shape, dev = _gated(f, x, gate, lens)
+    state = torch.Size((d.B, d.D))
+    out = out or {}
+    p0 = _dense(h0, "h0", torch.float32, state, dev)
+    h, sh = _row_out(out.get("h"), "h", f.dtype, shape, dev)
+    hT = _new(out.get("hT"), "hT", torch.float32, state, dev)
+    ws, wp, wn = _space(ws, workspace_size_gated(OP_GATED_FWD, d, dt), dev)
+    _ok(load().rnn_gated_fwd(d, dt, gt, sf, sx, p0, lp, sh, hT.data_ptr(), wp, wn, _current(dev)),
+        "rnn_gated_fwd")
+    return h, hT
+
+
+@_on_stream
+def gated_step(f, x, h, *, gate: str = "logit", h_out=None, out=None):
+    """One token (T = 1) for each batch row.  The state h [B,D] float32 is updated
+    in place unless `h_out` is given.  Returns (its rounding [1,B,D] in f's type,
+    the new state)."""
+    if x is None or h is None:
+        raise ValueError("x and h are required")
+    d, dt, gt, sf, sx, _, shape, dev = _gated(f, x, gate, None)
+    if d.T != 1:
+        raise ValueError("gated_step takes one token, got T = %d" % d.T)
+    h_out = h if h_out is None else h_out
+    state = torch.Size((d.B, d.D))
+    p0 = _dense(h, "h", torch.float32, state, dev)
+    p1 = _dense(h_out, "h_out", torch.float32, state, dev)
+    y, sy = _row_out(out, "out", f.dtype, shape, dev)
+    _ok(load().rnn_gated_step(d, dt, gt, sf, sx, p0, sy, p1, _current(dev)), "rnn_gated_step")
+    return y, h_out
+
+
+@_on_stream
+def gated_bwd(f, x, h, dh, h0=None, dhT=None, *, gate: str = "logit", lens=None, ws=None, out=None):
+    """Gradients of sum(dh * h) + sum(dhT * h_T), given gated_fwd's h: dict df, dx
+    (in f's type) and dh0 float32.  x may be None with gate "decay"; `out` is a
+    dict with "df", "dx" (any views) and "dh0" (may be dhT)."""
+    d, dt, gt, sf, sx, lp, shape, dev = _gated(f, x, gate, lens)
+    if x is None and gt == 0:
+        raise ValueError("x is required with gate 'logit'")
+    sh, sdh = _row(h, "h", f.dtype, shape, dev), _row(dh, "dh", f.dtype, shape, dev)
+    state = torch.Size((d.B, d.D))
+    p0 = _dense(h0, "h0", torch.float32, state, dev)
+    pT = _dense(dhT, "dhT", torch.float32, state, dev)
+    out = out or {}
+    df, sdf = _row_out(out.get("df"), "df", f.dtype, shape, dev)
+    dx, sdx = _row_out(out.get("dx"), "dx", f.dtype, shape, dev)
+    dh0 = _new(out.get("dh0"), "dh0", torch.float32, state, dev)
+    ws, wp, wn = _space(ws, workspace_size_gated(OP_GATED_BWD, d, dt), dev)
+    _ok(load().rnn_gated_bwd(d, dt, gt, sf, sx, sh, sdh, p0, pT, lp, sdf, sdx, dh0.data_ptr(), wp,
+                             wn, _current(dev)), "rnn_gated_bwd")
+    return {"df": df, "dx": dx, "dh0": dh0}
+
+
+# ------------------------------------------------ gradient norm, clipping
+class GradList:
+    """Gradients checked once, for programs whose gradient buffers stay where they
+    are: `grads` are contiguous bfloat16 or float32 tensors of one device, `out`
+    (None: in place) tensors of the same types and shapes."""
+
+    def __init__(self, grads, out=None):
+        grads = list(grads)
+        if not grads:
+            raise ValueError("an empty list of gradients")
+        self.device = dev = grads[0].device
+        self.is_cuda = grads[0].is_cuda
+        if not self.is_cuda:
+            raise ValueError("operands must be device tensors")
+        outs = grads if out is None else list(out)
+        if len(outs) != len(grads):
+            raise ValueError("%d outputs for %d gradients" % (len(outs), len(grads)))
+        rows, seen = [], set()
+        for t, o in zip(grads, outs):
+            code, n, at = _DT.get(t.dtype), t.numel(), o.data_ptr()
+            if code is None:
+                raise TypeError("gradients must be bfloat16 or float32, got %s" % t.dtype)
+            if t.device != dev or not t.is_contiguous():
+                raise ValueError("gradients must be contiguous tensors of one device")
+            if o is not t and (o.dtype != t.dtype or o.shape != t.shape or o.device != dev
+                               or not o.is_contiguous()):
+                raise ValueError("outputs must match their gradients")
+            if n and at in seen:
+                raise ValueError("the same output more than once")
+            seen.add(at)
+            rows.append((t.data_ptr(), at, n, code))
+        self.grads, self.out = grads, outs
+        self.count, self.array = len(rows), (_Grad * len(rows))(*rows)
+
+    def get_device(self):
+        return self.device.index
+
+
+def workspace_size_clip(grads) -> int:
+    g = grads if isinstance(grads, GradList) else GradList(grads)
+    return int(load().rnn_workspace_size_clip(g.count, g.array))
+
+
+@_on_stream
+def _clip(g, max_norm, norm, ws):
+    dev, lib = g.device, load()
+    norm = _new(norm, "norm", torch.float32, (), dev)
+    ws, wp, wn = _space(ws, int(lib.rnn_workspace_size_clip(g.count, g.array)), dev)
+    if max_norm is None:
+        _ok(lib.rnn_grad_norm(g.count, g.array, norm.data_ptr(), wp, wn, _current(dev)),
+            "rnn_grad_norm")
+    else:
+        _ok(lib.rnn_clip_grads(g.count, g.array, max_norm, norm.data_ptr(), wp, wn, _current(dev)),
+            "rnn_clip_grads")
+    return norm
+
+
+def grad_norm(grads, *, norm=None, ws=None, stream=None):
+    """Global 2-norm of a list of gradients (or a GradList): a float32 scalar on
+    their device, written to `norm` where given."""
+    g = grads if isinstance(grads, GradList) else GradList(grads)
+    return _clip(g, None, norm, ws, stream=stream)
+
+
+def clip_grads(grads, max_norm: float, *, out=None, norm=None, ws=None, stream=None):
+    """Scale gradients by max_norm / norm where their global 2-norm exceeds
+    max_norm, in place or into the tensors of `out` (a GradList brings its own).
+    Returns the norm before that, a float32 scalar on the device; where it is not
+    finite the gradients stay as they are."""
+    if isinstance(grads, GradList):
+        if out is not None:
+            raise ValueError("a GradList brings its own outputs")
+        g = grads
+    else:
+        g = GradList(grads, out)
+    if not max_norm >= 0:
+        raise ValueError("max_norm must be 0 or more, got %r" % (max_norm,))
+    return _clip(g, float(max_norm), norm, ws, stream=stream)
+
+
+# ------------------------------------------- verification of drafted tokens
+def workspace_size_verify(K: int, B: int, V: int) -> int:
+    return int(load().rnn_workspace_size_verify(K, B, V))
+
+
+@_on_stream
+def verify_drafts(logits, drafts, u, draft_logits=None, *, temperature=None, n_drafts=None, ws=None,
+                  out=None):
+    """Verify drafted tokens against the target's logits, so that what comes out is
+    distributed as the target's own.  logits [K+1,B,V] (rows contiguous), drafts
+    [K,B] int32 or int64 (any strides), u [K+1,B] float32 uniform numbers: u[k]
+    tests draft k, u[K] draws the token behind the accepted ones.  draft_logits
+    [K,B,V] the logits the drafts were drawn from (None: found some other way);
+    temperature [B] float32 (0 or less: greedy), n_drafts [B] int32 (None: K).
+    Returns (tokens [K+1,B] int32: accepted drafts, the drawn token, then -1;
+    accepted [B] int32); `out` is a dict with "tokens" and "accepted"."""
+    dev = logits.device
+    _dev(logits, "logits", dev)
+    dt = _dt(logits, "logits")
+    if logits.dim() != 3 or 0 in logits.shape:
+        raise ValueError("logits must be [K+1, B, V], got %s" % (tuple(logits.shape),))
+    K, B, V = logits.shape[0] - 1, logits.shape[1], logits.shape[2]
+    sl = _row(logits, "logits", logits.dtype, logits.shape, dev)
+    view = sq = None
+    if K:
+        if drafts is None or tuple(drafts.shape) != (K, B):
+            raise ValueError("drafts must be [K, B] = [%d, %d]" % (K, B))
+        view = _ids(drafts, dev)[2]
+        if draft_logits is not None:
+            sq = _row(draft_logits, "draft_logits", logits.dtype, torch.Size((K, B, V)), dev)
+    if u is None:
+        raise ValueError("u is required")
+    up = _dense(u, "u", torch.float32, torch.Size((K + 1, B)), dev)
+    tp = _dense(temperature, "temperature", torch.float32, torch.Size((B,)), dev)
+    np_ = _dense(n_drafts, "n_drafts", torch.int32, torch.Size((B,)), dev)
+    out = out or {}
+    tokens = _new(out.get("tokens"), "tokens", torch.int32, (K + 1, B), dev)
+    accepted = _new(out.get("accepted"), "accepted", torch.int32, (B,), dev)
+    ws, wp, wn = _space(ws, workspace_size_verify(K, B, V), dev)
+    _ok(load().rnn_verify_drafts(K, B, V, dt, sl, view, sq, up, tp, np_, tokens.data_ptr(),
+                                 accepted.data_ptr(), wp, wn, _current(dev)), "rnn_verify_drafts")
+    return tokens, accepted

@@ -541,6 +541,128 @@ rnn_status rnn_linattn_bwd(const rnn_lin_dims *d, rnn_dtype dt, const rnn_seq *q
                            void *dk, void *dv, float *dS0, void *ws, size_t ws_bytes,
                            hipStream_t stream);
 
+/*
+ * Gated linear recurrence: the member of the family whose gates come from the
+ * input alone, so that it runs over segments of the time axis at once.  For
+ * every batch row and channel, with an elementwise state (float32):
+ *   RNN_GATE_LOGIT  a_t = sigmoid(f_t):  h_t = a_t h_{t-1} + (1 - a_t) x_t
+ *   RNN_GATE_DECAY  a_t = f_t:           h_t = a_t h_{t-1} + x_t
+ * f, x, h and the gradients are sequences of D contiguous values for each
+ * (t, b) in dtype dt: views at any strides (rnn_seq; rnn_seq_out for outputs),
+ * so the halves of one projection and batch-first arrays are read and written
+ * as they are.  Rows of an output must not overlap.  States [B][D] float32.
+ * lens (may be NULL: T for all) [B]: only the first lens[b] tokens of row b, at
+ * least 0 and at most T, count (other values are taken as the nearest of these).
+ * Behind them the state stays as it is, h and the gradients df, dx are 0, and
+ * nothing is read from f, x, h or dh.
+ * Sums and states are float32 in an order that the dimensions set, so results
+ * repeat bit for bit; outputs are rounded once.  Decays are of magnitude 1 at
+ * most: the products of up to 256 consecutive ones are formed, which larger
+ * ones may carry past float32.  A value that is not finite may reach every
+ * later output of its batch row and channel (backward: every earlier one).
+ * B * D at most 2^30, else RNN_ERR_UNSUPPORTED.
+ */
+typedef enum { RNN_GATE_LOGIT = 0, RNN_GATE_DECAY = 1 } rnn_gate;
+typedef struct {
+    int T, B, D;
+} rnn_gated_dims;
+typedef struct {
+    void *data;
+    int64_t stride_t, stride_b;
+} rnn_seq_out;
+
+typedef enum { RNN_OP_GATED_FWD = 0, RNN_OP_GATED_BWD = 1 } rnn_gated_op;
+/* 0 where none is needed (then ws may be NULL) or the dims are invalid. */
+size_t rnn_workspace_size_gated(rnn_gated_op op, const rnn_gated_dims *d, rnn_dtype dt);
+
+/* Forward over T tokens.  h0 may be NULL (zeros); hT (the state behind the last
+ * token that counts) may be NULL, or be h0. */
+rnn_status rnn_gated_fwd(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, const rnn_seq *f,
+                         const rnn_seq *x, const float *h0, const int *lens, const rnn_seq_out *h,
+                         float *hT, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* One token (d->T == 1) for each batch row: reads the state h, writes h_out,
+ * which may be h itself, and its rounding y (dtype dt; may be NULL). */
+rnn_status rnn_gated_step(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, const rnn_seq *f,
+                          const rnn_seq *x, const float *h, const rnn_seq_out *y, float *h_out,
+                          hipStream_t stream);
+
+/* Gradients for the loss sum(dh * h) + sum(dhT * hT), given the forward's h:
+ *   g_t = dh_t + a_{t+1} g_{t+1} (behind the last token: dhT), dh0 = a_0 g_0
+ *   LOGIT  df_t = g_t (h_{t-1} - x_t) a_t (1 - a_t),  dx_t = (1 - a_t) g_t
+ *   DECAY  df_t = g_t h_{t-1},                        dx_t = g_t
+ * x may be NULL with RNN_GATE_DECAY, which does not need it.  h0, dhT may be
+ * NULL (zeros), dh0 may be NULL, or be dhT. */
+rnn_status rnn_gated_bwd(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, const rnn_seq *f,
+                         const rnn_seq *x, const rnn_seq *h, const rnn_seq *dh, const float *h0,
+                         const float *dhT, const int *lens, const rnn_seq_out *df,
+                         const rnn_seq_out *dx, float *dh0, void *ws, size_t ws_bytes,
+                         hipStream_t stream);
+
+/*
+ * Global norm of a list of gradients, and clipping by it:
+ *   norm = sqrt(sum over all tensors and values of g^2)
+ *   out = g * max_norm / norm if norm > max_norm, else g
+ * `list` (host memory, read during the call) holds `count` tensors of n >= 0
+ * contiguous values each, in their own dtype, starting at any element; out is
+ * of the tensor's dtype, NULL or `data` itself for clipping in place.  In place
+ * nothing is written where norm <= max_norm.  A norm that is not finite leaves
+ * the values as they are (a program drops such a step).  norm: one float.
+ * Squares are summed in 64 bits, in an order that the list sets, so results
+ * repeat bit for bit and finite gradients always have a finite sum; a norm past
+ * float32 is written as +inf, and clips all the same.  max_norm >= 0.  Tensors
+ * may overlap none of the outputs but their own.  count >= 1; the values of all
+ * tensors at most 2^40.
+ */
+typedef struct {
+    const void *data;
+    void *out;
+    int64_t n;
+    rnn_dtype dtype;
+} rnn_grad;
+size_t rnn_workspace_size_clip(int count, const rnn_grad *list);
+rnn_status rnn_grad_norm(int count, const rnn_grad *list, float *norm, void *ws, size_t ws_bytes,
+                         hipStream_t stream);
+rnn_status rnn_clip_grads(int count, const rnn_grad *list, float max_norm, float *norm, void *ws,
+                          size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Verification of drafted tokens.  For each of B sequences a draft of up to K
+ * tokens and the target model's logits of the K + 1 positions that they lead
+ * through; with p_k = softmax(logits_k / temperature), and q_k the same of the
+ * draft's logits:
+ *   draft k is accepted if u_k q_k(x_k) < p_k(x_k), the first that is not ends it;
+ *   the token behind the accepted ones is drawn from max(p_k - q_k, 0), where
+ *   draft k was refused, or from p_k, where none is left: the lowest index whose
+ *   cumulated weight exceeds u_K times their sum.
+ * So the tokens are distributed as the target's own.  Without draft logits
+ * (drafts found some other way) q_k is 1 at the draft and 0 elsewhere.
+ * logits (t, b) rows [K+1][B] of V contiguous values in dtype dt, draft_logits
+ * [K][B] (may be NULL), as views; drafts [K][B] (may be NULL where K = 0: plain
+ * sampling); u [K+1][B] float32 in [0, 1), dense; temperature [B] float32 (NULL:
+ * 1), where 0 or less puts all of p on the largest logit, the lowest index among
+ * equals; n_drafts [B] (NULL: K): only the first n_drafts[b], at least 0 and at
+ * most K (other values are taken as the nearest of these), are tested, and rows
+ * behind them are not read.
+ * tokens [K+1][B] int32: the accepted drafts, the drawn token, then -1;
+ * accepted [B] int32.
+ * -inf rules a token out.  A draft outside [0, V) is refused.  Where no weight is
+ * left in max(p - q, 0), p is drawn from.  A row that rules everything out, or
+ * holds a NaN or +inf, accepts nothing and draws -1 (as draft: takes nothing
+ * from p if it rules everything out, draws -1 otherwise).  u outside [0, 1] is
+ * taken as the nearer end, a NaN as 0; at the very end of the sum the last entry
+ * with any weight is drawn.
+ * Weights and sums are 64-bit: 32 bits would move the borders of a long
+ * vocabulary's cumulated sum by more than they are apart.
+ * K <= 63, V <= 1000000, B * (2 K + 1) chunks of 4096 values in one launch, else
+ * RNN_ERR_UNSUPPORTED.
+ */
+size_t rnn_workspace_size_verify(int K, int B, int V);
+rnn_status rnn_verify_drafts(int K, int B, int V, rnn_dtype dt, const rnn_seq *logits,
+                             const rnn_ids *drafts, const rnn_seq *draft_logits, const float *u,
+                             const float *temperature, const int *n_drafts, int *tokens,
+                             int *accepted, void *ws, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
