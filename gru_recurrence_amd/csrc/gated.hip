@@ -2,8 +2,28 @@
 //
 //   h_t = a_t h_{t-1} + b_t,  elementwise;  a, b from the gate's form:
 //   logit  a = sigmoid(f), b = (1 - a) x:  h + u (x - h) with u = sigmoid(-f), so
-//          that neither a gate near 1 nor one near 0 loses its small side
+//          that a gate near 1 does not lose its small side: a constant x is a
+//          fixed point, and the memory 1 / (1 - a) is right to float32
 //   decay  a = f, b = x
+// Steps compose: (A1, B1) then (A2, B2) is (A2 A1, A2 B1 + B2).  Backward is the same
+// kind of recurrence from the end: e_t = a_t (dh_t + e_{t+1}).
+//
+// Every operand is read once and every output written once; memory bounds it.  A
+// workgroup takes a tile of kWaves S steps (a wave S of them) by 64 lanes of VEC
+// channels, all of it in registers.  Each thread composes its S steps; a segment's
+// total goes to memory, the carry into it is composed from the totals of the
+// segments before it, and the steps run again from the carry, still in registers.
+//
+// Segments wait for each other inside one launch: a workgroup draws its place from a
+// counter, time first, so that whatever it waits for belongs to workgroups that
+// run already and wait for earlier places only; the first waits for none.  A total
+// is one 64-bit word for each channel, which says by being other than 0 that it is
+// there (written and read whole, so nothing else needs an order).  Past
+// kGroup segments the last of a group of about sqrt(segments) publishes the group's
+// total, so that a segment reads no more than twice that many words.  The order of
+// all products is the dimensions' alone.
+#include <algorithm>
+
 #include "lm.h"
 
 namespace rnn355 {
@@ -11,118 +31,493 @@ namespace lm {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512, kWaves = kThreads / 64;
+constexpr int kGroup = 16;
+constexpr int kHead = 64;            // bytes: status word, counter
+constexpr unsigned kSpins = 1u << 22;  // polls of a wait before it is given up (seconds)
+
+// How a call is cut, and the words that its segments exchange.
+struct Cut {
+    int T, D, C;      // steps, channels of a row, channels of all rows
+    int nseg, ntile;  // segments of time, tiles of channels
+    int G;            // segments of a group
+    unsigned *flag, *ticket;
+    uint64_t *word, *gword;  // [segment][channel], [group][channel]
+};
+
+__device__ __forceinline__ uint64_t pack(float A, float B) {
+    const uint64_t w = ((uint64_t)__float_as_uint(A) << 32) | __float_as_uint(B);
+    return w ? w : (uint64_t)0x80000000u << 32;  // (-0, 0) for (0, 0)
+}
+__device__ __forceinline__ void publish(uint64_t *p, float A, float B) {
+    __hip_atomic_store(p, pack(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// A h + B; a state of 0 takes no part, whatever the product of the decays is.
+__device__ __forceinline__ float apply(float A, float B, float h) { return h == 0.0f ? B : fmaf(A, h, B); }
 
 // 1 - sigmoid(f)
 __device__ __forceinline__ float shut(float f) { return rcp_fast(1.0f + exp_fast(f)); }
 
-template <bool LOGIT>
-__device__ __forceinline__ float advance(float f, float x, float h) {
-    return LOGIT ? fmaf(shut(f), x - h, h) : fmaf(f, h, x);
-}
-
-template <typename T, bool LOGIT>
-__global__ __launch_bounds__(kThreads) void gated_fwd_kernel(GatedDims d, LinSeq f, LinSeq x,
-                                                             const float *h0, const int *lens,
-                                                             SeqOut out, float *hT) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= (int64_t)d.B * d.D) return;
-    const int b = (int)(c / d.D), i = (int)(c - (int64_t)b * d.D);
-    const int len = lens ? min(max(lens[b], 0), d.T) : d.T;
-    float h = h0 ? h0[c] : 0.0f;
-    for (int t = 0; t < d.T; ++t) {
-        if (t < len)
-            h = advance<LOGIT>(to_f32<T>(((const T *)f.p)[t * f.st + b * f.sb + i]),
-                               to_f32<T>(((const T *)x.p)[t * x.st + b * x.sb + i]), h);
-        ((T *)out.p)[t * out.st + b * out.sb + i] = from_f32<T>(t < len ? h : 0.0f);
+// This workgroup's segment and tile of channels.
+__device__ __forceinline__ void place(const Cut &k, int &seg, int &tile) {
+    __shared__ unsigned drawn;
+    unsigned at = blockIdx.x;
+    if (k.nseg > 1) {
+        if (threadIdx.x == 0)
+            drawn = __hip_atomic_fetch_add(k.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        at = __builtin_amdgcn_readfirstlane(drawn);
     }
-    if (hT) hT[c] = h;
+    seg = at / k.ntile;
+    tile = at - seg * k.ntile;
+}
+
+// From the threads' own (A, B) to the state that each begins with.  agg, car: LDS,
+// [kWaves][64 VEC].  Returns the state before the thread's first step in h.
+// start: the recurrence's initial state, in the first wave of segment 0.  Nobody
+// else reads that, and all that follows waits for what this wave makes of it, so
+// the last state may be written over the first.
+template <int VEC>
+__device__ __forceinline__ void join(const Cut &k, int seg, int c0, const float *A, const float *B,
+                                     const float *start, float2 (*agg)[64 * VEC],
+                                     float2 (*car)[64 * VEC], float *h) {
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, at = lane * VEC;
+    const bool first = seg == 0 && w == 0;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v)
+        agg[w][at + v] = first ? make_float2(0.0f, apply(A[v], B[v], start[v])) : make_float2(A[v], B[v]);
+    __syncthreads();
+    // the steps of this workgroup before this wave
+    float pA[VEC], pB[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) pA[v] = 1.0f, pB[v] = first ? start[v] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWaves - 1; ++i) {
+        if (i >= w) break;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float2 q = agg[i][at + v];
+            pB[v] = apply(q.x, q.y, pB[v]);
+            pA[v] *= q.x;
+        }
+    }
+    const bool last = seg == k.nseg - 1;
+    float tA[VEC], tB[VEC];  // the whole segment, in the last wave
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        tA[v] = seg == 0 ? 0.0f : pA[v] * A[v];
+        tB[v] = apply(A[v], B[v], pB[v]);
+        if (w == kWaves - 1 && !last && c0 + v < k.C) publish(k.word + (int64_t)seg * k.C + c0 + v, tA[v], tB[v]);
+    }
+    if (seg == 0) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) h[v] = pB[v];
+        return;
+    }
+    // the segments before: whole groups by the first half of the waves, those of the
+    // own group by the second (by all waves where there is no group before)
+    const int group = seg / k.G, inside = seg - group * k.G;
+    const int half = group ? kWaves / 2 : 0;
+    const bool mine = w >= half;
+    const int n = mine ? inside : group, parts = mine ? kWaves - half : half, part = mine ? w - half : w;
+    const uint64_t *words = mine ? k.word + (int64_t)(seg - inside) * k.C : k.gword;
+    const int lo = (int)((int64_t)n * part / parts), hi = (int)((int64_t)n * (part + 1) / parts);
+    float cA[VEC], cB[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) cA[v] = 1.0f, cB[v] = 0.0f;
+    const int c = min(c0, k.C - VEC);
+    for (int j = lo; j < hi; j += 4) {
+        uint64_t q[4][VEC];
+        unsigned spins = 0;
+        while (true) {
+            bool there = true;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    q[i][v] = __hip_atomic_load(words + (int64_t)min(j + i, hi - 1) * k.C + c + v,
+                                                __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    there &= q[i][v] != 0;
+                }
+            if (__all(there)) break;
+            if (++spins >= kSpins) {
+                __hip_atomic_store(k.flag, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                break;
+            }
+            __builtin_amdgcn_s_sleep(1);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (j + i < hi) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float a = __uint_as_float((uint32_t)(q[i][v] >> 32));
+                    cB[v] = apply(a, __uint_as_float((uint32_t)q[i][v]), cB[v]);
+                    cA[v] *= a;
+                }
+            }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) car[w][at + v] = make_float2(cA[v], cB[v]);
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) h[v] = 0.0f, cA[v] = 1.0f, cB[v] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float2 q = car[i][at + v];
+            h[v] = apply(q.x, q.y, h[v]);
+            if (i >= half) {
+                cB[v] = apply(q.x, q.y, cB[v]);
+                cA[v] *= q.x;
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        if (w == kWaves - 1 && !last && inside == k.G - 1 && c0 + v < k.C)
+            publish(k.gword + (int64_t)group * k.C + c0 + v, group ? tA[v] * cA[v] : 0.0f, apply(tA[v], tB[v], cB[v]));
+        h[v] = apply(pA[v], pB[v], h[v]);
+    }
+}
+
+struct FwdArgs {
+    Cut k;
+    LinSeq f, x;
+    const float *h0;
+    const int *lens;
+    SeqOut h;
+    float *hT;
+};
+
+template <typename T, bool LOGIT, int VEC, int S>
+__global__ __launch_bounds__(kThreads) void gated_fwd_kernel(FwdArgs a) {
+    typedef Unit<T, VEC> V;
+    __shared__ float2 agg[kWaves][64 * VEC], car[kWaves][64 * VEC];
+    const Cut &k = a.k;
+    int seg, tile;
+    place(k, seg, tile);
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int c0 = (tile * 64 + lane) * VEC, c = min(c0, k.C - VEC);
+    const int b = c / k.D, i = c - b * k.D;
+    const int len = a.lens ? min(max(a.lens[b], 0), k.T) : k.T;
+    const int t0 = (seg * kWaves + w) * S;  // the grid's limit keeps this in 31 bits
+    // what a step keeps: u (logit) or a (decay), and x
+    float g[S][VEC], x[S][VEC];
+    if (__any(t0 < len)) {
+        const T *fp = (const T *)a.f.p + (int64_t)b * a.f.sb + i, *xp = (const T *)a.x.p + (int64_t)b * a.x.sb + i;
+        V fr[S], xr[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int64_t t = min(t0 + s, k.T - 1);
+            fr[s] = *(const V *)(fp + t * a.f.st);
+            xr[s] = *(const V *)(xp + t * a.x.st);
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float fv = to_f32<T>(fr[s].v[v]);
+                g[s][v] = LOGIT ? shut(fv) : fv;
+                x[s][v] = to_f32<T>(xr[s].v[v]);
+            }
+    }
+    const bool full = __all(t0 + S <= len);
+    if (!full) {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+                if (t0 + s >= len) g[s][v] = LOGIT ? 0.0f : 1.0f, x[s][v] = 0.0f;
+    }
+    float A[VEC], h[VEC], start[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        A[v] = 1.0f, h[v] = 0.0f;
+        start[v] = seg == 0 && w == 0 && a.h0 ? a.h0[c + v] : 0.0f;
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            h[v] = LOGIT ? fmaf(g[s][v], x[s][v] - h[v], h[v]) : fmaf(g[s][v], h[v], x[s][v]);
+            A[v] = LOGIT ? fmaf(-g[s][v], A[v], A[v]) : A[v] * g[s][v];
+        }
+    float B[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) B[v] = h[v];
+    join<VEC>(k, seg, c0, A, B, start, agg, car, h);
+    T *out = (T *)a.h.p + (int64_t)b * a.h.sb + i;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        V o;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            h[v] = LOGIT ? fmaf(g[s][v], x[s][v] - h[v], h[v]) : fmaf(g[s][v], h[v], x[s][v]);
+            o.v[v] = from_f32<T>(full || t0 + s < len ? h[v] : 0.0f);
+        }
+        if (t0 + s < k.T && c0 < k.C) *(V *)(out + (int64_t)(t0 + s) * a.h.st) = o;
+    }
+    if (a.hT && seg == k.nseg - 1 && w == kWaves - 1 && c0 < k.C) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) a.hT[c + v] = h[v];
+    }
 }
 
 template <typename T, bool LOGIT>
-__global__ __launch_bounds__(kThreads) void gated_step_kernel(GatedDims d, LinSeq f, LinSeq x,
-                                                              const float *h, SeqOut y, float *h_out) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+__global__ __launch_bounds__(256) void gated_step_kernel(GatedDims d, LinSeq f, LinSeq x, const float *h,
+                                                         SeqOut y, float *h_out) {
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (c >= (int64_t)d.B * d.D) return;
     const int b = (int)(c / d.D), i = (int)(c - (int64_t)b * d.D);
-    const float n = advance<LOGIT>(to_f32<T>(((const T *)f.p)[b * f.sb + i]),
-                                   to_f32<T>(((const T *)x.p)[b * x.sb + i]), h[c]);
+    const float fv = to_f32<T>(((const T *)f.p)[b * f.sb + i]), xv = to_f32<T>(((const T *)x.p)[b * x.sb + i]);
+    const float n = LOGIT ? fmaf(shut(fv), xv - h[c], h[c]) : fmaf(fv, h[c], xv);
     h_out[c] = n;
     if (y.p) ((T *)y.p)[b * y.sb + i] = from_f32<T>(n);
 }
 
-template <typename T, bool LOGIT>
-__global__ __launch_bounds__(kThreads) void gated_bwd_kernel(GatedDims d, LinSeq f, LinSeq x, LinSeq h,
-                                                             LinSeq dh, const float *h0,
-                                                             const float *dhT, const int *lens,
-                                                             SeqOut df, SeqOut dx, float *dh0) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= (int64_t)d.B * d.D) return;
-    const int b = (int)(c / d.D), i = (int)(c - (int64_t)b * d.D);
-    const int len = lens ? min(max(lens[b], 0), d.T) : d.T;
-    float e = dhT ? dhT[c] : 0.0f;  // a_{t+1} g_{t+1}
-    for (int t = d.T - 1; t >= 0; --t) {
-        float of = 0.0f, ox = 0.0f;
-        if (t < len) {
-            const float g = e + to_f32<T>(((const T *)dh.p)[t * dh.st + b * dh.sb + i]);
-            const float before = t ? to_f32<T>(((const T *)h.p)[(t - 1) * h.st + b * h.sb + i])
-                                   : h0 ? h0[c] : 0.0f;
-            const float fv = to_f32<T>(((const T *)f.p)[t * f.st + b * f.sb + i]);
-            if (LOGIT) {
-                const float u = shut(fv), a = shut(-fv);
-                const float xv = to_f32<T>(((const T *)x.p)[t * x.st + b * x.sb + i]);
-                ox = u * g;
-                e = a * g;
-                of = e * u * (before - xv);
-            } else {
-                ox = g;
-                of = g * before;
-                e = fv * g;
-            }
+struct BwdArgs {
+    Cut k;
+    LinSeq f, x, h, dh;
+    const float *h0, *dhT;
+    const int *lens;
+    SeqOut df, dx;
+    float *dh0;
+};
+
+// Backwards in time: step s of a thread is t = T - 1 - (first + s).  The state is
+// e = a_{t+1} g_{t+1}; g_t = dh_t + e, e' = a_t g_t.
+template <typename T, bool LOGIT, int VEC, int S>
+__global__ __launch_bounds__(kThreads) void gated_bwd_kernel(BwdArgs a) {
+    typedef Unit<T, VEC> V;
+    __shared__ float2 agg[kWaves][64 * VEC], car[kWaves][64 * VEC];
+    const Cut &k = a.k;
+    int seg, tile;
+    place(k, seg, tile);
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int c0 = (tile * 64 + lane) * VEC, c = min(c0, k.C - VEC);
+    const int b = c / k.D, i = c - b * k.D;
+    const int len = a.lens ? min(max(a.lens[b], 0), k.T) : k.T;
+    const int t0 = k.T - 1 - (seg * kWaves + w) * S;  // the thread's last step in time; may be below 0
+    // u (logit) or a (decay), a u (logit), dh
+    float g[S][VEC], au[LOGIT ? S : 1][VEC], dh[S][VEC];
+    V xr[S], hr[S];
+    const bool any = __any(t0 - (S - 1) < len && t0 >= 0);
+    if (any) {
+        const T *fp = (const T *)a.f.p + (int64_t)b * a.f.sb + i, *dp = (const T *)a.dh.p + (int64_t)b * a.dh.sb + i;
+        const T *xp = (const T *)a.x.p + (int64_t)b * a.x.sb + i, *hp = (const T *)a.h.p + (int64_t)b * a.h.sb + i;
+        V fr[S], dr[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int64_t t = max(t0 - s, 0);
+            fr[s] = *(const V *)(fp + t * a.f.st);
+            dr[s] = *(const V *)(dp + t * a.dh.st);
         }
-        ((T *)df.p)[t * df.st + b * df.sb + i] = from_f32<T>(of);
-        ((T *)dx.p)[t * dx.st + b * dx.sb + i] = from_f32<T>(ox);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int64_t t = max(t0 - s, 0);
+            if (LOGIT) xr[s] = *(const V *)(xp + t * a.x.st);
+            hr[s] = *(const V *)(hp + max(t - 1, (int64_t)0) * a.h.st);
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float fv = to_f32<T>(fr[s].v[v]);
+                if (LOGIT) {
+                    const float ex = exp_fast(fv), u = rcp_fast(1.0f + ex);
+                    g[s][v] = u;
+                    au[s][v] = fminf(ex, 3e38f) * u * u;
+                } else {
+                    g[s][v] = fv;
+                }
+                dh[s][v] = to_f32<T>(dr[s].v[v]);
+            }
     }
-    if (dh0) dh0[c] = e;
+    // steps that do not count: outside the sequence, or before its start
+    const bool full = __all(t0 < len && t0 - (S - 1) >= 0);
+    if (!full) {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+                if (t0 - s >= len || t0 - s < 0) {
+                    g[s][v] = LOGIT ? 0.0f : 1.0f, dh[s][v] = 0.0f;
+                    if (LOGIT) au[s][v] = 0.0f;
+                }
+    }
+    float A[VEC], B[VEC], start[VEC], e[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        A[v] = 1.0f, B[v] = 0.0f;
+        start[v] = seg == 0 && w == 0 && a.dhT ? a.dhT[c + v] : 0.0f;
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float q = B[v] + dh[s][v];
+            B[v] = LOGIT ? fmaf(-g[s][v], q, q) : g[s][v] * q;
+            A[v] = LOGIT ? fmaf(-g[s][v], A[v], A[v]) : A[v] * g[s][v];
+        }
+    join<VEC>(k, seg, c0, A, B, start, agg, car, e);
+    T *of = (T *)a.df.p + (int64_t)b * a.df.sb + i, *ox = (T *)a.dx.p + (int64_t)b * a.dx.sb + i;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int t = t0 - s;
+        V vf, vx;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float q = e[v] + dh[s][v];
+            float before = to_f32<T>(hr[s].v[v]);
+            if (t == 0) before = a.h0 ? a.h0[c + v] : 0.0f;
+            float df, dx;
+            if (LOGIT) {
+                dx = g[s][v] * q;
+                df = au[s][v] * q * (before - to_f32<T>(xr[s].v[v]));
+                e[v] = fmaf(-g[s][v], q, q);
+            } else {
+                dx = q;
+                df = q * before;
+                e[v] = g[s][v] * q;
+            }
+            const bool live = full || t < len;
+            vf.v[v] = from_f32<T>(live ? df : 0.0f);
+            vx.v[v] = from_f32<T>(live ? dx : 0.0f);
+        }
+        if (t >= 0 && c0 < k.C) {
+            *(V *)(of + (int64_t)t * a.df.st) = vf;
+            *(V *)(ox + (int64_t)t * a.dx.st) = vx;
+        }
+    }
+    if (a.dh0 && seg == k.nseg - 1 && w == kWaves - 1 && c0 < k.C) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) a.dh0[c + v] = e[v];
+    }
 }
 
-unsigned blocks(const GatedDims &d) { return (unsigned)(((int64_t)d.B * d.D + kThreads - 1) / kThreads); }
+__global__ __launch_bounds__(256) void gated_clear_kernel(uint4 *p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        p[i] = make_uint4(0, 0, 0, 0);
+}
+
+// Steps of a thread, backward and forward.
+constexpr int kSteps = 8, kStepsBwd = 8;
+
+int64_t segments(int T, bool bwd) {
+    const int tile = kWaves * (bwd ? kStepsBwd : kSteps);
+    return ((int64_t)T + tile - 1) / tile;
+}
+int64_t group_of(int64_t nseg) {
+    if (nseg <= kGroup) return nseg;
+    int64_t g = kGroup;
+    while (g * g < nseg) ++g;
+    return g;
+}
+
+// vec: channels of a lane
+Cut cut(const GatedDims &d, bool bwd, int vec, void *ws) {
+    Cut k{};
+    k.T = d.T, k.D = d.D, k.C = d.B * d.D;
+    k.nseg = (int)segments(d.T, bwd);
+    k.G = (int)group_of(k.nseg);
+    k.ntile = (k.C + 64 * vec - 1) / (64 * vec);
+    k.flag = (unsigned *)ws;
+    k.ticket = k.flag + 1;
+    k.word = (uint64_t *)((char *)ws + kHead);
+    k.gword = k.word + (int64_t)k.nseg * k.C;
+    return k;
+}
+
+hipError_t clear(const Cut &k, size_t bytes, hipStream_t s) {
+    if (k.nseg == 1) return hipSuccess;
+    const int64_t n = (int64_t)(bytes / 16);
+    const unsigned grid = (unsigned)std::min<int64_t>((n + 255) / 256, 2048);
+    hipLaunchKernelGGL(gated_clear_kernel, dim3(grid), dim3(256), 0, s, (uint4 *)k.flag, n);
+    return hipGetLastError();
+}
+
+// Whether two channels of every row stand together at a multiple of their size.
+bool pairs(int D, size_t e, std::initializer_list<LinSeq> seqs) {
+    if (D % 2) return false;
+    for (const LinSeq &s : seqs)
+        if ((uintptr_t)s.p % (2 * e) || s.st % 2 || s.sb % 2) return false;
+    return true;
+}
+LinSeq in(const SeqOut &o) { return LinSeq{o.p, o.st, o.sb}; }
 
 }  // namespace
 
-// B * D <= 2^30: one thread to a channel is always a legal launch.
-bool gated_grid_ok(const GatedDims &, bool, bool) { return true; }
-bool gated_step_grid_ok(const GatedDims &) { return true; }
-size_t gated_bytes(const GatedDims &, bool, bool) { return 0; }
+size_t gated_bytes(const GatedDims &d, bool, bool bwd) {
+    const int64_t n = segments(d.T, bwd);
+    if (n == 1) return 0;
+    const int64_t words = n + (n + group_of(n) - 1) / group_of(n);
+    // rnn_workspace_status takes no less than 4 KiB
+    return (size_t)std::max<int64_t>(4096, kHead + (words * d.B * d.D * 8 + 15) / 16 * 16);
+}
 
-#define GATED_LAUNCH(kernel, ...)                                                                       \
-    do {                                                                                                \
-        const dim3 grid(blocks(d)), thr(kThreads);                                                      \
-        if (bf16) {                                                                                     \
-            if (d.logit) hipLaunchKernelGGL((kernel<uint16_t, true>), grid, thr, 0, s, __VA_ARGS__);    \
-            else hipLaunchKernelGGL((kernel<uint16_t, false>), grid, thr, 0, s, __VA_ARGS__);           \
-        } else {                                                                                        \
-            if (d.logit) hipLaunchKernelGGL((kernel<float, true>), grid, thr, 0, s, __VA_ARGS__);       \
-            else hipLaunchKernelGGL((kernel<float, false>), grid, thr, 0, s, __VA_ARGS__);              \
-        }                                                                                               \
-    } while (0)
+// With one channel to a lane; two need fewer.
+bool gated_grid_ok(const GatedDims &d, bool, bool bwd) {
+    return grid_ok(segments(d.T, bwd) * (((int64_t)d.B * d.D + 63) / 64), kThreads);
+}
+bool gated_step_grid_ok(const GatedDims &d) { return grid_ok(((int64_t)d.B * d.D + 255) / 256, 256); }
 
 hipError_t launch_gated_fwd(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, const float *h0,
-                            const int *lens, SeqOut h, float *hT, void *, hipStream_t s) {
-    GATED_LAUNCH(gated_fwd_kernel, d, f, x, h0, lens, h, hT);
+                            const int *lens, SeqOut h, float *hT, void *ws, hipStream_t s) {
+    const int vec = bf16 && pairs(d.D, 2, {f, x, in(h)}) ? 2 : 1;
+    const FwdArgs a{cut(d, false, vec, ws), f, x, h0, lens, h, hT};
+    const hipError_t e = clear(a.k, gated_bytes(d, bf16, false), s);
+    if (e != hipSuccess) return e;
+    const dim3 grid((unsigned)((int64_t)a.k.nseg * a.k.ntile)), thr(kThreads);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, thr, 0, s, a); };
+    if (!bf16) {
+        if (d.logit) go(gated_fwd_kernel<float, true, 1, kSteps>);
+        else go(gated_fwd_kernel<float, false, 1, kSteps>);
+    } else if (vec == 2) {
+        if (d.logit) go(gated_fwd_kernel<uint16_t, true, 2, kSteps>);
+        else go(gated_fwd_kernel<uint16_t, false, 2, kSteps>);
+    } else {
+        if (d.logit) go(gated_fwd_kernel<uint16_t, true, 1, kSteps>);
+        else go(gated_fwd_kernel<uint16_t, false, 1, kSteps>);
+    }
     return hipGetLastError();
 }
 
 hipError_t launch_gated_step(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, const float *h,
                              SeqOut y, float *h_out, hipStream_t s) {
-    GATED_LAUNCH(gated_step_kernel, d, f, x, h, y, h_out);
+    const dim3 grid((unsigned)(((int64_t)d.B * d.D + 255) / 256)), thr(256);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, thr, 0, s, d, f, x, h, y, h_out); };
+    if (bf16) {
+        if (d.logit) go(gated_step_kernel<uint16_t, true>);
+        else go(gated_step_kernel<uint16_t, false>);
+    } else {
+        if (d.logit) go(gated_step_kernel<float, true>);
+        else go(gated_step_kernel<float, false>);
+    }
     return hipGetLastError();
 }
 
 hipError_t launch_gated_bwd(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, LinSeq h, LinSeq dh,
                             const float *h0, const float *dhT, const int *lens, SeqOut df, SeqOut dx,
-                            float *dh0, void *, hipStream_t s) {
-    GATED_LAUNCH(gated_bwd_kernel, d, f, x, h, dh, h0, dhT, lens, df, dx, dh0);
+                            float *dh0, void *ws, hipStream_t s) {
+    if (!d.logit) x = f;  // not read
+    const int vec = bf16 && pairs(d.D, 2, {f, x, h, dh, in(df), in(dx)}) ? 2 : 1;
+    const BwdArgs a{cut(d, true, vec, ws), f, x, h, dh, h0, dhT, lens, df, dx, dh0};
+    const hipError_t e = clear(a.k, gated_bytes(d, bf16, true), s);
+    if (e != hipSuccess) return e;
+    const dim3 grid((unsigned)((int64_t)a.k.nseg * a.k.ntile)), thr(kThreads);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, thr, 0, s, a); };
+    if (!bf16) {
+        if (d.logit) go(gated_bwd_kernel<float, true, 1, kStepsBwd>);
+        else go(gated_bwd_kernel<float, false, 1, kStepsBwd>);
+    } else if (vec == 2) {
+        if (d.logit) go(gated_bwd_kernel<uint16_t, true, 2, kStepsBwd>);
+        else go(gated_bwd_kernel<uint16_t, false, 2, kStepsBwd>);
+    } else {
+        if (d.logit) go(gated_bwd_kernel<uint16_t, true, 1, kStepsBwd>);
+        else go(gated_bwd_kernel<uint16_t, false, 1, kStepsBwd>);
+    }
     return hipGetLastError();
 }
 
