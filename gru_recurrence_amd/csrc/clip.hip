@@ -4,9 +4,15 @@
 //
 // Two passes, as the factor needs every value: the first leaves one sum of
 // squares for each workgroup, the second adds those up (every workgroup for
-// itself, in the same order) and scales.  The list travels in the kernels'
-// arguments, kGroup tensors a launch: nothing of it has to be in device memory
-// or outlive the call, so that a captured call replays what it was given.
+// itself, in the same order) and scales.  A list that one workgroup reads in a
+// microsecond takes one launch.  The list travels in the kernels' arguments,
+// kGroup tensors a launch: nothing of it has to be in device memory or outlive
+// the call, so that a captured call replays what it was given.
+//
+// Memory bounds it: a workgroup takes an equal share of the list, in pieces of a
+// 16-byte unit to a thread, kAhead of them in flight.  The second pass walks each
+// share backwards: what the first read last is then still in the last-level cache.
+// It stores past the caches.
 //
 // Squares are summed in 64 bits: the largest float32 squared is far inside
 // them, so only a value that is not finite gives such a sum, and there is
@@ -20,21 +26,24 @@ namespace lm {
 
 namespace {
 
-constexpr int kThreads = 256, kUnits = 4;  // 16-byte units of a thread in a chunk
-constexpr int kChunkBytes = kThreads * kUnits * 16;
-constexpr int kGroup = 96;   // tensors of one launch
-constexpr int kSlots = 2048; // sums kept: the first pass has at most that many workgroups
+constexpr int kThreads = 256, kAhead = 8;
+constexpr int kPiece = kThreads * 16;  // bytes
+constexpr int kGroup = 96;    // tensors of one launch
+constexpr int kSlots = 2048;  // sums kept: the first pass has at most that many workgroups
+constexpr int kOne = 1024;    // threads of a single workgroup that does it all
+constexpr int kOnePieces = 32;
 
 struct Group {
     const void *p[kGroup];
     void *out[kGroup];
     int64_t n[kGroup];
-    int32_t first[kGroup + 1];  // chunk at which a tensor starts
+    int32_t first[kGroup + 1];  // piece at which a tensor starts
     uint8_t bf16[kGroup];
     int count;
 };
 
 // Workgroup sum of 64-bit values, the same in every thread.
+template <int NT>
 __device__ __forceinline__ double block_sum(double v, double *tmp) {
 #pragma unroll
     for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
@@ -42,16 +51,16 @@ __device__ __forceinline__ double block_sum(double v, double *tmp) {
     __syncthreads();
     double all = 0.0;
 #pragma unroll
-    for (int i = 0; i < kThreads / 64; ++i) all += tmp[i];
+    for (int i = 0; i < NT / 64; ++i) all += tmp[i];
     return all;
 }
 
-// Tensor of a chunk.
-__device__ __forceinline__ int find(const Group &g, int chunk) {
+// Tensor of a piece.
+__device__ __forceinline__ int find(const Group &g, int piece) {
     int lo = 0, hi = g.count - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (g.first[mid] <= chunk)
+        if (g.first[mid] <= piece)
             lo = mid;
         else
             hi = mid - 1;
@@ -59,50 +68,178 @@ __device__ __forceinline__ int find(const Group &g, int chunk) {
     return lo;
 }
 
+// A tensor as units from the aligned address at or before its start.
 template <typename T>
-__device__ __forceinline__ double chunk_squares(const T *p, int64_t n, int ch) {
-    constexpr int N = 16 / sizeof(T);
-    const int off = (int)(((uintptr_t)p & 15) / sizeof(T));
-    const T *base = p - off;
-    double s = 0.0;
+struct Units {
+    static constexpr int N = 16 / sizeof(T);
+    const T *base;
+    int64_t n;
+    int off;
+    __device__ __forceinline__ Units(const void *p, int64_t n_) : n(n_) {
+        off = (int)(((uintptr_t)p & 15) / sizeof(T));
+        base = (const T *)p - off;
+    }
+    // whether piece i (of NT units) holds nothing but whole units
+    __device__ __forceinline__ bool whole(int64_t lo, int64_t hi) const { return lo * N >= off && hi * N - off <= n; }
+};
+
+template <typename T>
+__device__ __forceinline__ double unit_squares(const Unit<T, 16 / sizeof(T)> &q, double s) {
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-        const int64_t u = ((int64_t)ch * kUnits + j) * kThreads + threadIdx.x, i0 = u * N - off;
-        if (i0 >= 0 && i0 + N <= n) {
-            const Unit<T, N> q = *(const Unit<T, N> *)(base + u * N);
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const double v = to_f32<T>(q.v[e]);
-                s = fma(v, v, s);
-            }
-        } else if (i0 < n) {
-            for (int e = 0; e < N; ++e)
-                if (i0 + e >= 0 && i0 + e < n) {
-                    const double v = to_f32<T>(p[i0 + e]);
-                    s = fma(v, v, s);
-                }
-        }
+    for (int e = 0; e < (int)(16 / sizeof(T)); ++e) {
+        const double v = to_f32<T>(q.v[e]);
+        s = fma(v, v, s);
     }
     return s;
 }
 
+// Sum of squares of units [lo, hi) of a tensor, NT threads.
+template <typename T, int NT>
+__device__ __forceinline__ double squares(const void *p, int64_t n, int64_t lo, int64_t hi) {
+    constexpr int N = Units<T>::N;
+    const Units<T> t(p, n);
+    double s = 0.0;
+    for (int64_t at = lo; at < hi;) {
+        if (at + NT * kAhead <= hi && t.whole(at, at + NT * kAhead)) {
+            Unit<T, N> q[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) q[j] = *(const Unit<T, N> *)(t.base + (at + j * NT + threadIdx.x) * N);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) s = unit_squares<T>(q[j], s);
+            at += NT * kAhead;
+            continue;
+        }
+        const int64_t u = at + threadIdx.x, i0 = u * N - t.off;
+        if (u < hi && i0 >= 0 && i0 + N <= n) {
+            s = unit_squares<T>(*(const Unit<T, N> *)(t.base + u * N), s);
+        } else if (u < hi) {
+            for (int e = 0; e < N; ++e)
+                if (i0 + e >= 0 && i0 + e < n) {
+                    const double v = to_f32<T>(t.base[u * N + e]);
+                    s = fma(v, v, s);
+                }
+        }
+        at += NT;
+    }
+    return s;
+}
+
+template <typename T>
+__device__ __forceinline__ void store(T *out, Unit<T, 16 / sizeof(T)> q, float c, bool whole) {
+    constexpr int N = 16 / sizeof(T);
+#pragma unroll
+    for (int e = 0; e < N; ++e) q.v[e] = from_f32<T>(to_f32<T>(q.v[e]) * c);
+    if (whole) {
+        typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+        __builtin_nontemporal_store(__builtin_bit_cast(u4, q), (u4 *)out);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) out[e] = q.v[e];
+    }
+}
+
+// out = c p over units [lo, hi), from the end.
+template <typename T, int NT>
+__device__ __forceinline__ void scale(const void *p, void *out_, int64_t n, int64_t lo, int64_t hi, float c) {
+    constexpr int N = Units<T>::N;
+    const Units<T> t(p, n);
+    T *out = (T *)out_ - t.off;
+    const bool same = ((uintptr_t)out & 15) == 0;  // at the same place of its 16 bytes
+    for (int64_t end = hi; end > lo;) {
+        if (end - NT * kAhead >= lo && t.whole(end - NT * kAhead, end)) {
+            end -= NT * kAhead;
+            Unit<T, N> q[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) q[j] = *(const Unit<T, N> *)(t.base + (end + j * NT + threadIdx.x) * N);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) store<T>(out + (end + j * NT + threadIdx.x) * N, q[j], c, same);
+            continue;
+        }
+        // to a multiple of NT from lo, so that what is left is whole pieces
+        const int64_t at = lo + (end - lo - 1) / NT * NT;
+        const int64_t u = at + threadIdx.x, i0 = u * N - t.off;
+        if (u < end && i0 >= 0 && i0 + N <= n) {
+            store<T>(out + u * N, *(const Unit<T, N> *)(t.base + u * N), c, same);
+        } else if (u < end) {
+            for (int e = 0; e < N; ++e)
+                if (i0 + e >= 0 && i0 + e < n) out[u * N + e] = from_f32<T>(to_f32<T>(t.base[u * N + e]) * c);
+        }
+        end = at;
+    }
+}
+
+// Pieces [lo, hi) of the list, tensor by tensor, forwards or from the end:
+// f(tensor, first unit, unit behind the last).
+template <bool BACK, typename F>
+__device__ __forceinline__ void each(const Group &g, int lo, int hi, F f) {
+    if (lo >= hi) return;
+    int t = find(g, BACK ? hi - 1 : lo);
+    while (lo < hi) {
+        const int from = max(g.first[t], lo), to = min(g.first[t + 1], hi);
+        f(t, (int64_t)(from - g.first[t]) * kThreads, (int64_t)(to - g.first[t]) * kThreads);
+        if (BACK) {
+            hi = from;
+            --t;
+        } else {
+            lo = to;
+            ++t;
+        }
+    }
+}
+
+// A workgroup's share of the pieces.
+__device__ __forceinline__ void share(int all, int &lo, int &hi) {
+    lo = (int)((int64_t)all * blockIdx.x / gridDim.x);
+    hi = (int)((int64_t)all * (blockIdx.x + 1) / gridDim.x);
+}
+
+template <int NT>
+__device__ __forceinline__ double share_squares(const Group &g, int lo, int hi) {
+    double s = 0.0;
+    each<false>(g, lo, hi, [&](int t, int64_t a, int64_t b) {
+        s += g.bf16[t] ? squares<uint16_t, NT>(g.p[t], g.n[t], a, b) : squares<float, NT>(g.p[t], g.n[t], a, b);
+    });
+    return s;
+}
+
+// The factor of a sum of squares, and whether the values change.
+__device__ __forceinline__ bool factor(double s, float max_norm, float &c) {
+    const double n = sqrt(s);
+    const bool over = n > (double)max_norm && n < (double)INFINITY;
+    c = over ? (float)((double)max_norm / n) : 1.0f;
+    return over;
+}
+
+template <int NT>
+__device__ __forceinline__ void share_scale(const Group &g, int lo, int hi, bool over, float c) {
+    each<true>(g, lo, hi, [&](int t, int64_t a, int64_t b) {
+        if (!over && !g.out[t]) return;  // in place, as it is
+        void *out = g.out[t] ? g.out[t] : const_cast<void *>(g.p[t]);
+        if (g.bf16[t])
+            scale<uint16_t, NT>(g.p[t], out, g.n[t], a, b, c);
+        else
+            scale<float, NT>(g.p[t], out, g.n[t], a, b, c);
+    });
+}
+
 __global__ __launch_bounds__(kThreads) void norm_kernel(Group g, double *slot, int add) {
     __shared__ double tmp[kThreads / 64];
-    const int all = g.first[g.count];
-    double s = 0.0;
-    for (int ch = blockIdx.x; ch < all; ch += gridDim.x) {
-        const int t = find(g, ch);
-        s += g.bf16[t] ? chunk_squares((const uint16_t *)g.p[t], g.n[t], ch - g.first[t])
-                       : chunk_squares((const float *)g.p[t], g.n[t], ch - g.first[t]);
-    }
-    s = block_sum(s, tmp);
+    int lo, hi;
+    share(g.first[g.count], lo, hi);
+    const double s = block_sum<kThreads>(share_squares<kThreads>(g, lo, hi), tmp);
     if (threadIdx.x == 0) slot[blockIdx.x] = add ? slot[blockIdx.x] + s : s;
 }
 
 __device__ __forceinline__ double total(const double *slot, int slots, double *tmp) {
-    double s = 0.0;
-    for (int i = threadIdx.x; i < slots; i += kThreads) s += slot[i];
-    return block_sum(s, tmp);
+    double v[kSlots / kThreads], s = 0.0;
+#pragma unroll
+    for (int j = 0; j < kSlots / kThreads; ++j) {
+        const int i = j * kThreads + (int)threadIdx.x;
+        v[j] = i < slots ? slot[i] : 0.0;
+    }
+#pragma unroll
+    for (int j = 0; j < kSlots / kThreads; ++j) s += v[j];
+    return block_sum<kThreads>(s, tmp);
 }
 
 __global__ __launch_bounds__(kThreads) void norm_only_kernel(const double *slot, int slots, float *norm) {
@@ -111,61 +248,40 @@ __global__ __launch_bounds__(kThreads) void norm_only_kernel(const double *slot,
     if (threadIdx.x == 0) norm[0] = (float)sqrt(s);
 }
 
-template <typename T>
-__device__ __forceinline__ void chunk_scale(const T *p, T *out, int64_t n, int ch, float c) {
-    constexpr int N = 16 / sizeof(T);
-    const int off = (int)(((uintptr_t)p & 15) / sizeof(T));
-    const bool whole = (int)(((uintptr_t)out & 15) / sizeof(T)) == off;
-    const T *base = p - off;
-#pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-        const int64_t u = ((int64_t)ch * kUnits + j) * kThreads + threadIdx.x, i0 = u * N - off;
-        if (i0 >= 0 && i0 + N <= n) {
-            Unit<T, N> q = *(const Unit<T, N> *)(base + u * N);
-#pragma unroll
-            for (int e = 0; e < N; ++e) q.v[e] = from_f32<T>(to_f32<T>(q.v[e]) * c);
-            if (whole) {
-                *(Unit<T, N> *)(out + i0) = q;
-            } else {
-#pragma unroll
-                for (int e = 0; e < N; ++e) out[i0 + e] = q.v[e];
-            }
-        } else if (i0 < n) {
-            for (int e = 0; e < N; ++e)
-                if (i0 + e >= 0 && i0 + e < n) out[i0 + e] = from_f32<T>(to_f32<T>(p[i0 + e]) * c);
-        }
-    }
-}
-
 __global__ __launch_bounds__(kThreads) void scale_kernel(Group g, const double *slot, int slots,
                                                          float max_norm, float *norm) {
     __shared__ double tmp[kThreads / 64];
-    const double s = total(slot, slots, tmp), n = sqrt(s);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = (float)n;
-    const bool over = n > (double)max_norm && n < (double)INFINITY;
-    const float c = over ? (float)((double)max_norm / n) : 1.0f;
-    const int all = g.first[g.count];
-    for (int ch = blockIdx.x; ch < all; ch += gridDim.x) {
-        const int t = find(g, ch);
-        if (!over && !g.out[t]) continue;  // in place, as it is
-        void *out = g.out[t] ? g.out[t] : const_cast<void *>(g.p[t]);
-        if (g.bf16[t])
-            chunk_scale((const uint16_t *)g.p[t], (uint16_t *)out, g.n[t], ch - g.first[t], c);
-        else
-            chunk_scale((const float *)g.p[t], (float *)out, g.n[t], ch - g.first[t], c);
-    }
+    const double s = total(slot, slots, tmp);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = (float)sqrt(s);
+    float c;
+    const bool over = factor(s, max_norm, c);
+    int lo, hi;
+    share(g.first[g.count], lo, hi);
+    share_scale<kThreads>(g, lo, hi, over, c);
 }
 
-// Chunks of a tensor, wherever it starts in its 16 bytes.
-int64_t tensor_chunks(const rnn_grad &t) {
+// A list of few pieces.  max_norm < 0: the norm alone.
+__global__ __launch_bounds__(kOne) void one_kernel(Group g, float max_norm, float *norm) {
+    __shared__ double tmp[kOne / 64];
+    const int all = g.first[g.count];
+    const double s = block_sum<kOne>(share_squares<kOne>(g, 0, all), tmp);
+    if (threadIdx.x == 0) norm[0] = (float)sqrt(s);
+    if (max_norm < 0.0f) return;
+    float c;
+    const bool over = factor(s, max_norm, c);
+    share_scale<kOne>(g, 0, all, over, c);
+}
+
+// Pieces of a tensor, wherever it starts in its 16 bytes.
+int64_t pieces(const rnn_grad &t) {
     const int64_t e = t.dtype == RNN_BF16 ? 2 : 4;
-    return t.n ? (t.n * e + (int64_t)((uintptr_t)t.data & 15) + kChunkBytes - 1) / kChunkBytes : 0;
+    return t.n ? (t.n * e + (int64_t)((uintptr_t)t.data & 15) + kPiece - 1) / kPiece : 0;
 }
 
 // The next tensors of the list, from `at` on: as many as a group takes.
 int fill(Group *g, int count, const rnn_grad *list, int at) {
     g->count = 0;
-    int64_t chunks = 0;
+    int64_t n = 0;
     while (at < count && g->count < kGroup) {
         const rnn_grad &t = list[at++];
         if (t.n == 0) continue;
@@ -174,11 +290,18 @@ int fill(Group *g, int count, const rnn_grad *list, int at) {
         g->out[i] = t.out == t.data ? nullptr : t.out;
         g->n[i] = t.n;
         g->bf16[i] = t.dtype == RNN_BF16;
-        g->first[i] = (int32_t)chunks;
-        chunks += tensor_chunks(t);
+        g->first[i] = (int32_t)n;
+        n += pieces(t);
     }
-    g->first[g->count] = (int32_t)chunks;
+    g->first[g->count] = (int32_t)n;
     return at;
+}
+
+// Workgroups of a launch over a group: a share is no less than kAhead pieces where the
+// list is short.
+int grid_of(const Group &g, int most) {
+    const int n = g.first[g.count];
+    return std::max(1, std::min(most, n < kSlots ? n : std::max(n / kAhead, kSlots / 2)));
 }
 
 }  // namespace
@@ -189,28 +312,28 @@ hipError_t launch_clip(int count, const rnn_grad *list, float max_norm, float *n
                        hipStream_t s) {
     double *slot = (double *)ws;
     Group g;
-    int64_t most = 0;  // chunks of the largest group
-    int groups = 0;
+    int groups = 0, slots = 1;
     for (int at = 0; at < count || !groups; ++groups) {
         at = fill(&g, count, list, at);
-        most = std::max<int64_t>(most, g.first[g.count]);
+        slots = std::max(slots, grid_of(g, kSlots));
+    }
+    if (groups == 1 && g.first[g.count] <= kOnePieces) {
+        hipLaunchKernelGGL(one_kernel, dim3(1), dim3(kOne), 0, s, g, max_norm, norm);
+        return hipGetLastError();
     }
     // the first launch writes all sums that a later one adds to
-    const int slots = (int)std::min<int64_t>(kSlots, std::max<int64_t>(1, most));
     for (int at = 0, i = 0; i < groups; ++i) {
-        at = fill(&g, count, list, at);
-        const int grid = i ? std::min(slots, std::max(1, g.first[g.count])) : slots;
-        hipLaunchKernelGGL(norm_kernel, dim3(grid), dim3(kThreads), 0, s, g, slot, i > 0);
+        if (groups > 1) at = fill(&g, count, list, at);
+        hipLaunchKernelGGL(norm_kernel, dim3(i ? grid_of(g, slots) : slots), dim3(kThreads), 0, s, g, slot, i > 0);
     }
     if (max_norm < 0.0f) {
         hipLaunchKernelGGL(norm_only_kernel, dim3(1), dim3(kThreads), 0, s, slot, slots, norm);
         return hipGetLastError();
     }
     for (int at = 0, i = 0; i < groups; ++i) {
-        at = fill(&g, count, list, at);
-        const int grid = std::min(slots, std::max(1, g.first[g.count]));
-        hipLaunchKernelGGL(scale_kernel, dim3(grid), dim3(kThreads), 0, s, g, slot, slots, max_norm,
-                           i ? nullptr : norm);
+        if (groups > 1) at = fill(&g, count, list, at);
+        hipLaunchKernelGGL(scale_kernel, dim3(i ? grid_of(g, slots) : slots), dim3(kThreads), 0, s, g, slot, slots,
+                           max_norm, i ? nullptr : norm);
     }
     return hipGetLastError();
 }

@@ -14,14 +14,15 @@
 // total goes to memory, the carry into it is composed from the totals of the
 // segments before it, and the steps run again from the carry, still in registers.
 //
-// Segments wait for each other inside one launch: a workgroup draws its place from a
-// counter, time first, so that whatever it waits for belongs to workgroups that
-// run already and wait for earlier places only; the first waits for none.  A total
+// Segments wait for each other inside one launch: a workgroup draws its segment from
+// its tile's counter, so that whatever it waits for belongs to workgroups that run
+// already and wait for earlier segments only; the first waits for none.  (One counter
+// for all serves a workgroup every 13 ns: 6144 workgroups then took 94 us.)  A total
 // is one 64-bit word for each channel, which says by being other than 0 that it is
-// there (written and read whole, so nothing else needs an order).  Past
-// kGroup segments the last of a group of about sqrt(segments) publishes the group's
-// total, so that a segment reads no more than twice that many words.  The order of
-// all products is the dimensions' alone.
+// there (written and read whole, so nothing else needs an order).  Past kGroup
+// segments the last of a group of about sqrt(segments) publishes the group's total,
+// so that a segment reads no more than twice that many words.  The order of all
+// products is the dimensions' alone.
 #include <algorithm>
 
 #include "lm.h"
@@ -33,7 +34,7 @@ namespace {
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;
 constexpr int kGroup = 16;
-constexpr int kHead = 64;            // bytes: status word, counter
+constexpr int kHead = 128;           // bytes before the counters: the status word
 constexpr unsigned kSpins = 1u << 22;  // polls of a wait before it is given up (seconds)
 
 // How a call is cut, and the words that its segments exchange.
@@ -41,7 +42,8 @@ struct Cut {
     int T, D, C;      // steps, channels of a row, channels of all rows
     int nseg, ntile;  // segments of time, tiles of channels
     int G;            // segments of a group
-    unsigned *flag, *ticket;
+    int pitch;        // words between the tiles' counters
+    unsigned *flag, *counter;
     uint64_t *word, *gword;  // [segment][channel], [group][channel]
 };
 
@@ -61,15 +63,15 @@ __device__ __forceinline__ float shut(float f) { return rcp_fast(1.0f + exp_fast
 // This workgroup's segment and tile of channels.
 __device__ __forceinline__ void place(const Cut &k, int &seg, int &tile) {
     __shared__ unsigned drawn;
-    unsigned at = blockIdx.x;
+    seg = 0;
+    tile = blockIdx.x % k.ntile;
     if (k.nseg > 1) {
         if (threadIdx.x == 0)
-            drawn = __hip_atomic_fetch_add(k.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            drawn = __hip_atomic_fetch_add(k.counter + (int64_t)tile * k.pitch, 1u, __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
-        at = __builtin_amdgcn_readfirstlane(drawn);
+        seg = __builtin_amdgcn_readfirstlane(drawn);
     }
-    seg = at / k.ntile;
-    tile = at - seg * k.ntile;
 }
 
 // From the threads' own (A, B) to the state that each begins with.  agg, car: LDS,
@@ -81,12 +83,12 @@ template <int VEC>
 __device__ __forceinline__ void join(const Cut &k, int seg, int c0, const float *A, const float *B,
                                      const float *start, float2 (*agg)[64 * VEC],
                                      float2 (*car)[64 * VEC], float *h) {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, at = lane * VEC;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), at = lane * VEC;
     const bool first = seg == 0 && w == 0;
 #pragma unroll
     for (int v = 0; v < VEC; ++v)
         agg[w][at + v] = first ? make_float2(0.0f, apply(A[v], B[v], start[v])) : make_float2(A[v], B[v]);
-    __syncthreads();
+    lds_barrier();
     // the steps of this workgroup before this wave
     float pA[VEC], pB[VEC];
 #pragma unroll
@@ -128,18 +130,25 @@ __device__ __forceinline__ void join(const Cut &k, int seg, int c0, const float 
     const int c = min(c0, k.C - VEC);
     for (int j = lo; j < hi; j += 4) {
         uint64_t q[4][VEC];
-        unsigned spins = 0;
+        unsigned spins = 0, left = (1u << min(hi - j, 4)) - 1;  // words still to come
         while (true) {
-            bool there = true;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
+                if (left & (1u << i)) {
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    q[i][v] = __hip_atomic_load(words + (int64_t)min(j + i, hi - 1) * k.C + c + v,
-                                                __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                    there &= q[i][v] != 0;
+                    for (int v = 0; v < VEC; ++v)
+                        q[i][v] = __hip_atomic_load(words + (int64_t)(j + i) * k.C + c + v, __ATOMIC_RELAXED,
+                                                    __HIP_MEMORY_SCOPE_AGENT);
                 }
-            if (__all(there)) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (left & (1u << i)) {
+                    bool there = true;
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) there &= q[i][v] != 0;
+                    if (__all(there)) left &= ~(1u << i);
+                }
+            if (!left) break;
             if (++spins >= kSpins) {
                 __hip_atomic_store(k.flag, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
                 break;
@@ -159,7 +168,7 @@ __device__ __forceinline__ void join(const Cut &k, int seg, int c0, const float 
     }
 #pragma unroll
     for (int v = 0; v < VEC; ++v) car[w][at + v] = make_float2(cA[v], cB[v]);
-    __syncthreads();
+    lds_barrier();
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h[v] = 0.0f, cA[v] = 1.0f, cB[v] = 0.0f;
 #pragma unroll
@@ -191,6 +200,21 @@ struct FwdArgs {
     float *hT;
 };
 
+// Makes the compiler take a register's value as new, so that what was computed from it
+// is computed again where it is needed again, in place of being kept.
+template <typename V>
+__device__ __forceinline__ void forget(V &q) {
+    if constexpr (sizeof(V) == 2) {
+        uint32_t r = __builtin_bit_cast(uint16_t, q);
+        asm volatile("" : "+v"(r));
+        q = __builtin_bit_cast(V, (uint16_t)r);
+    } else {
+        uint32_t r = __builtin_bit_cast(uint32_t, q);
+        asm volatile("" : "+v"(r));
+        q = __builtin_bit_cast(V, r);
+    }
+}
+
 template <typename T, bool LOGIT, int VEC, int S>
 __global__ __launch_bounds__(kThreads) void gated_fwd_kernel(FwdArgs a) {
     typedef Unit<T, VEC> V;
@@ -198,64 +222,55 @@ __global__ __launch_bounds__(kThreads) void gated_fwd_kernel(FwdArgs a) {
     const Cut &k = a.k;
     int seg, tile;
     place(k, seg, tile);
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c0 = (tile * 64 + lane) * VEC, c = min(c0, k.C - VEC);
     const int b = c / k.D, i = c - b * k.D;
     const int len = a.lens ? min(max(a.lens[b], 0), k.T) : k.T;
     const int t0 = (seg * kWaves + w) * S;  // the grid's limit keeps this in 31 bits
-    // what a step keeps: u (logit) or a (decay), and x
-    float g[S][VEC], x[S][VEC];
+    V fr[S], xr[S];
     if (__any(t0 < len)) {
         const T *fp = (const T *)a.f.p + (int64_t)b * a.f.sb + i, *xp = (const T *)a.x.p + (int64_t)b * a.x.sb + i;
-        V fr[S], xr[S];
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int64_t t = min(t0 + s, k.T - 1);
             fr[s] = *(const V *)(fp + t * a.f.st);
             xr[s] = *(const V *)(xp + t * a.x.st);
         }
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float fv = to_f32<T>(fr[s].v[v]);
-                g[s][v] = LOGIT ? shut(fv) : fv;
-                x[s][v] = to_f32<T>(xr[s].v[v]);
-            }
     }
     const bool full = __all(t0 + S <= len);
-    if (!full) {
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v)
-                if (t0 + s >= len) g[s][v] = LOGIT ? 0.0f : 1.0f, x[s][v] = 0.0f;
-    }
-    float A[VEC], h[VEC], start[VEC];
+    float A[VEC], B[VEC], h[VEC], start[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-        A[v] = 1.0f, h[v] = 0.0f;
+        A[v] = 1.0f, B[v] = 0.0f;
         start[v] = seg == 0 && w == 0 && a.h0 ? a.h0[c + v] : 0.0f;
     }
 #pragma unroll
     for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-            h[v] = LOGIT ? fmaf(g[s][v], x[s][v] - h[v], h[v]) : fmaf(g[s][v], h[v], x[s][v]);
-            A[v] = LOGIT ? fmaf(-g[s][v], A[v], A[v]) : A[v] * g[s][v];
+            const bool on = full || t0 + s < len;
+            const float fv = to_f32<T>(fr[s].v[v]), xv = to_f32<T>(xr[s].v[v]);
+            const float g = LOGIT ? shut(fv) : fv;
+            const float hn = LOGIT ? fmaf(g, xv - B[v], B[v]) : fmaf(g, B[v], xv);
+            const float an = LOGIT ? fmaf(-g, A[v], A[v]) : A[v] * g;
+            B[v] = on ? hn : B[v];
+            A[v] = on ? an : A[v];
         }
-    float B[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) B[v] = h[v];
+    for (int s = 0; s < S; ++s) forget(fr[s]), forget(xr[s]);
     join<VEC>(k, seg, c0, A, B, start, agg, car, h);
     T *out = (T *)a.h.p + (int64_t)b * a.h.sb + i;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
+        const bool on = full || t0 + s < len;
         V o;
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-            h[v] = LOGIT ? fmaf(g[s][v], x[s][v] - h[v], h[v]) : fmaf(g[s][v], h[v], x[s][v]);
-            o.v[v] = from_f32<T>(full || t0 + s < len ? h[v] : 0.0f);
+            const float fv = to_f32<T>(fr[s].v[v]), xv = to_f32<T>(xr[s].v[v]);
+            const float g = LOGIT ? shut(fv) : fv;
+            const float hn = LOGIT ? fmaf(g, xv - h[v], h[v]) : fmaf(g, h[v], xv);
+            h[v] = on ? hn : h[v];
+            o.v[v] = from_f32<T>(on ? hn : 0.0f);
         }
         if (t0 + s < k.T && c0 < k.C) *(V *)(out + (int64_t)(t0 + s) * a.h.st) = o;
     }
@@ -295,19 +310,15 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_kernel(BwdArgs a) {
     const Cut &k = a.k;
     int seg, tile;
     place(k, seg, tile);
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c0 = (tile * 64 + lane) * VEC, c = min(c0, k.C - VEC);
     const int b = c / k.D, i = c - b * k.D;
     const int len = a.lens ? min(max(a.lens[b], 0), k.T) : k.T;
     const int t0 = k.T - 1 - (seg * kWaves + w) * S;  // the thread's last step in time; may be below 0
-    // u (logit) or a (decay), a u (logit), dh
-    float g[S][VEC], au[LOGIT ? S : 1][VEC], dh[S][VEC];
-    V xr[S], hr[S];
-    const bool any = __any(t0 - (S - 1) < len && t0 >= 0);
-    if (any) {
+    V fr[S], dr[S], xr[S], hr[S];
+    if (__any(t0 - (S - 1) < len && t0 >= 0)) {
         const T *fp = (const T *)a.f.p + (int64_t)b * a.f.sb + i, *dp = (const T *)a.dh.p + (int64_t)b * a.dh.sb + i;
         const T *xp = (const T *)a.x.p + (int64_t)b * a.x.sb + i, *hp = (const T *)a.h.p + (int64_t)b * a.h.sb + i;
-        V fr[S], dr[S];
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int64_t t = max(t0 - s, 0);
@@ -320,33 +331,9 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_kernel(BwdArgs a) {
             if (LOGIT) xr[s] = *(const V *)(xp + t * a.x.st);
             hr[s] = *(const V *)(hp + max(t - 1, (int64_t)0) * a.h.st);
         }
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float fv = to_f32<T>(fr[s].v[v]);
-                if (LOGIT) {
-                    const float ex = exp_fast(fv), u = rcp_fast(1.0f + ex);
-                    g[s][v] = u;
-                    au[s][v] = fminf(ex, 3e38f) * u * u;
-                } else {
-                    g[s][v] = fv;
-                }
-                dh[s][v] = to_f32<T>(dr[s].v[v]);
-            }
     }
-    // steps that do not count: outside the sequence, or before its start
+    // steps outside the sequence, or before its start, do not count
     const bool full = __all(t0 < len && t0 - (S - 1) >= 0);
-    if (!full) {
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v)
-                if (t0 - s >= len || t0 - s < 0) {
-                    g[s][v] = LOGIT ? 0.0f : 1.0f, dh[s][v] = 0.0f;
-                    if (LOGIT) au[s][v] = 0.0f;
-                }
-    }
     float A[VEC], B[VEC], start[VEC], e[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
@@ -357,34 +344,41 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_kernel(BwdArgs a) {
     for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-            const float q = B[v] + dh[s][v];
-            B[v] = LOGIT ? fmaf(-g[s][v], q, q) : g[s][v] * q;
-            A[v] = LOGIT ? fmaf(-g[s][v], A[v], A[v]) : A[v] * g[s][v];
+            const bool on = full || (t0 - s < len && t0 - s >= 0);
+            const float fv = to_f32<T>(fr[s].v[v]), g = LOGIT ? shut(fv) : fv;
+            const float q = B[v] + to_f32<T>(dr[s].v[v]);
+            const float bn = LOGIT ? fmaf(-g, q, q) : g * q, an = LOGIT ? fmaf(-g, A[v], A[v]) : A[v] * g;
+            B[v] = on ? bn : B[v];
+            A[v] = on ? an : A[v];
         }
+#pragma unroll
+    for (int s = 0; s < S; ++s) forget(fr[s]), forget(dr[s]);
     join<VEC>(k, seg, c0, A, B, start, agg, car, e);
     T *of = (T *)a.df.p + (int64_t)b * a.df.sb + i, *ox = (T *)a.dx.p + (int64_t)b * a.dx.sb + i;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         const int t = t0 - s;
+        const bool on = full || (t < len && t >= 0);
         V vf, vx;
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-            const float q = e[v] + dh[s][v];
+            const float fv = to_f32<T>(fr[s].v[v]), q = e[v] + to_f32<T>(dr[s].v[v]);
             float before = to_f32<T>(hr[s].v[v]);
             if (t == 0) before = a.h0 ? a.h0[c + v] : 0.0f;
-            float df, dx;
+            float df, dx, en;
             if (LOGIT) {
-                dx = g[s][v] * q;
-                df = au[s][v] * q * (before - to_f32<T>(xr[s].v[v]));
-                e[v] = fmaf(-g[s][v], q, q);
+                const float ex = exp_fast(fv), u = rcp_fast(1.0f + ex);
+                dx = u * q;
+                df = fminf(ex, 3e38f) * u * dx * (before - to_f32<T>(xr[s].v[v]));
+                en = fmaf(-u, q, q);
             } else {
                 dx = q;
                 df = q * before;
-                e[v] = g[s][v] * q;
+                en = fv * q;
             }
-            const bool live = full || t < len;
-            vf.v[v] = from_f32<T>(live ? df : 0.0f);
-            vx.v[v] = from_f32<T>(live ? dx : 0.0f);
+            e[v] = on ? en : e[v];
+            vf.v[v] = from_f32<T>(on ? df : 0.0f);
+            vx.v[v] = from_f32<T>(on ? dx : 0.0f);
         }
         if (t >= 0 && c0 < k.C) {
             *(V *)(of + (int64_t)t * a.df.st) = vf;
@@ -402,11 +396,13 @@ __global__ __launch_bounds__(256) void gated_clear_kernel(uint4 *p, int64_t n) {
         p[i] = make_uint4(0, 0, 0, 0);
 }
 
-// Steps of a thread, backward and forward.
-constexpr int kSteps = 8, kStepsBwd = 8;
+// Steps of a thread: with two channels to a lane 8, with one 16.  Longer segments have
+// fewer words to exchange (32768 x 768 float32: 79 us with 8 steps, 70 with 16) until
+// their registers leave too few waves to hide a join.
+constexpr int steps(int vec) { return vec == 2 ? 8 : 16; }
 
-int64_t segments(int T, bool bwd) {
-    const int tile = kWaves * (bwd ? kStepsBwd : kSteps);
+int64_t segments(int T, int vec) {
+    const int tile = kWaves * steps(vec);
     return ((int64_t)T + tile - 1) / tile;
 }
 int64_t group_of(int64_t nseg) {
@@ -416,23 +412,35 @@ int64_t group_of(int64_t nseg) {
     return g;
 }
 
+// Counters a cache line apart while they are few; many tiles share the lines' work anyway.
+int pitch(int64_t ntile) { return ntile <= 1024 ? 32 : 1; }
+int64_t counter_words(int64_t ntile) { return (ntile * pitch(ntile) + 31) / 32 * 32; }
+
 // vec: channels of a lane
-Cut cut(const GatedDims &d, bool bwd, int vec, void *ws) {
+Cut cut(const GatedDims &d, int vec, void *ws) {
     Cut k{};
     k.T = d.T, k.D = d.D, k.C = d.B * d.D;
-    k.nseg = (int)segments(d.T, bwd);
+    k.nseg = (int)segments(d.T, vec);
     k.G = (int)group_of(k.nseg);
     k.ntile = (k.C + 64 * vec - 1) / (64 * vec);
+    k.pitch = pitch(k.ntile);
     k.flag = (unsigned *)ws;
-    k.ticket = k.flag + 1;
-    k.word = (uint64_t *)((char *)ws + kHead);
+    k.counter = (unsigned *)((char *)ws + kHead);
+    k.word = (uint64_t *)(k.counter + counter_words(k.ntile));
     k.gword = k.word + (int64_t)k.nseg * k.C;
     return k;
 }
 
-hipError_t clear(const Cut &k, size_t bytes, hipStream_t s) {
+// Bytes of the workspace, a multiple of 16; rnn_workspace_status takes no less than 4 KiB.
+int64_t space(const Cut &k) {
+    if (k.nseg == 1) return 0;
+    const int64_t words = ((int64_t)k.nseg + (k.nseg + k.G - 1) / k.G) * k.C;
+    return std::max<int64_t>(4096, kHead + 4 * counter_words(k.ntile) + (words * 8 + 15) / 16 * 16);
+}
+
+hipError_t clear(const Cut &k, hipStream_t s) {
     if (k.nseg == 1) return hipSuccess;
-    const int64_t n = (int64_t)(bytes / 16);
+    const int64_t n = space(k) / 16;
     const unsigned grid = (unsigned)std::min<int64_t>((n + 255) / 256, 2048);
     hipLaunchKernelGGL(gated_clear_kernel, dim3(grid), dim3(256), 0, s, (uint4 *)k.flag, n);
     return hipGetLastError();
@@ -449,37 +457,37 @@ LinSeq in(const SeqOut &o) { return LinSeq{o.p, o.st, o.sb}; }
 
 }  // namespace
 
-size_t gated_bytes(const GatedDims &d, bool, bool bwd) {
-    const int64_t n = segments(d.T, bwd);
-    if (n == 1) return 0;
-    const int64_t words = n + (n + group_of(n) - 1) / group_of(n);
-    // rnn_workspace_status takes no less than 4 KiB
-    return (size_t)std::max<int64_t>(4096, kHead + (words * d.B * d.D * 8 + 15) / 16 * 16);
+size_t gated_bytes(const GatedDims &d, bool bf16) {
+    // a bf16 call may have either number of channels to a lane
+    int64_t n = 0;
+    for (int vec = 1; vec <= (bf16 ? 2 : 1); ++vec) n = std::max(n, space(cut(d, vec, nullptr)));
+    return (size_t)n;
 }
 
-// With one channel to a lane; two need fewer.
-bool gated_grid_ok(const GatedDims &d, bool, bool bwd) {
-    return grid_ok(segments(d.T, bwd) * (((int64_t)d.B * d.D + 63) / 64), kThreads);
+bool gated_grid_ok(const GatedDims &d, bool bf16) {
+    for (int vec = 1; vec <= (bf16 ? 2 : 1); ++vec)
+        if (!grid_ok(segments(d.T, vec) * (((int64_t)d.B * d.D + 64 * vec - 1) / (64 * vec)), kThreads)) return false;
+    return true;
 }
 bool gated_step_grid_ok(const GatedDims &d) { return grid_ok(((int64_t)d.B * d.D + 255) / 256, 256); }
 
 hipError_t launch_gated_fwd(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, const float *h0,
                             const int *lens, SeqOut h, float *hT, void *ws, hipStream_t s) {
     const int vec = bf16 && pairs(d.D, 2, {f, x, in(h)}) ? 2 : 1;
-    const FwdArgs a{cut(d, false, vec, ws), f, x, h0, lens, h, hT};
-    const hipError_t e = clear(a.k, gated_bytes(d, bf16, false), s);
+    const FwdArgs a{cut(d, vec, ws), f, x, h0, lens, h, hT};
+    const hipError_t e = clear(a.k, s);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)((int64_t)a.k.nseg * a.k.ntile)), thr(kThreads);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, thr, 0, s, a); };
     if (!bf16) {
-        if (d.logit) go(gated_fwd_kernel<float, true, 1, kSteps>);
-        else go(gated_fwd_kernel<float, false, 1, kSteps>);
+        if (d.logit) go(gated_fwd_kernel<float, true, 1, steps(1)>);
+        else go(gated_fwd_kernel<float, false, 1, steps(1)>);
     } else if (vec == 2) {
-        if (d.logit) go(gated_fwd_kernel<uint16_t, true, 2, kSteps>);
-        else go(gated_fwd_kernel<uint16_t, false, 2, kSteps>);
+        if (d.logit) go(gated_fwd_kernel<uint16_t, true, 2, steps(2)>);
+        else go(gated_fwd_kernel<uint16_t, false, 2, steps(2)>);
     } else {
-        if (d.logit) go(gated_fwd_kernel<uint16_t, true, 1, kSteps>);
-        else go(gated_fwd_kernel<uint16_t, false, 1, kSteps>);
+        if (d.logit) go(gated_fwd_kernel<uint16_t, true, 1, steps(1)>);
+        else go(gated_fwd_kernel<uint16_t, false, 1, steps(1)>);
     }
     return hipGetLastError();
 }
@@ -503,20 +511,20 @@ hipError_t launch_gated_bwd(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, L
                             float *dh0, void *ws, hipStream_t s) {
     if (!d.logit) x = f;  // not read
     const int vec = bf16 && pairs(d.D, 2, {f, x, h, dh, in(df), in(dx)}) ? 2 : 1;
-    const BwdArgs a{cut(d, true, vec, ws), f, x, h, dh, h0, dhT, lens, df, dx, dh0};
-    const hipError_t e = clear(a.k, gated_bytes(d, bf16, true), s);
+    const BwdArgs a{cut(d, vec, ws), f, x, h, dh, h0, dhT, lens, df, dx, dh0};
+    const hipError_t e = clear(a.k, s);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)((int64_t)a.k.nseg * a.k.ntile)), thr(kThreads);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, thr, 0, s, a); };
     if (!bf16) {
-        if (d.logit) go(gated_bwd_kernel<float, true, 1, kStepsBwd>);
-        else go(gated_bwd_kernel<float, false, 1, kStepsBwd>);
+        if (d.logit) go(gated_bwd_kernel<float, true, 1, steps(1)>);
+        else go(gated_bwd_kernel<float, false, 1, steps(1)>);
     } else if (vec == 2) {
-        if (d.logit) go(gated_bwd_kernel<uint16_t, true, 2, kStepsBwd>);
-        else go(gated_bwd_kernel<uint16_t, false, 2, kStepsBwd>);
+        if (d.logit) go(gated_bwd_kernel<uint16_t, true, 2, steps(2)>);
+        else go(gated_bwd_kernel<uint16_t, false, 2, steps(2)>);
     } else {
-        if (d.logit) go(gated_bwd_kernel<uint16_t, true, 1, kStepsBwd>);
-        else go(gated_bwd_kernel<uint16_t, false, 1, kStepsBwd>);
+        if (d.logit) go(gated_bwd_kernel<uint16_t, true, 1, steps(1)>);
+        else go(gated_bwd_kernel<uint16_t, false, 1, steps(1)>);
     }
     return hipGetLastError();
 }
