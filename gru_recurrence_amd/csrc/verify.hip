@@ -10,12 +10,14 @@
 // many drafts stand (each workgroup of a sequence for itself) and sums w over the
 // chunks of the row to draw from; the sequence's last workgroup to finish finds the
 // chunk in which the sum passes u, and the entry in it.  Sums are added in the order of
-// the chunks, so nothing depends on which workgroup that is.
+// the chunks, so nothing depends on which workgroup that is.  A sum is one 64-bit word
+// that says by its value that it is there; an ordered counter in its place would write
+// back and empty the caches of every workgroup (70 us for 58 at 32 x 5 x 128000).
 //
 // Weights and sums are 64-bit.  The borders between a vocabulary's V entries lie
 // 1/V of the sum apart on average; a sum of 32-bit terms is off by 1e-7 of it, so
 // that about one draw in a hundred at V = 128000 would depend on how it was added
-// up.  With 64 bits (weights to 2e-14, below) that is one in 10^8.
+// up.  With 64 bits (weights to 1e-12, below) that is less than one in 10^6.
 #include <algorithm>
 
 #include "row.h"
@@ -25,31 +27,33 @@ namespace lm {
 
 namespace {
 
-constexpr int kThreads = 256, kPer = 16, kChunk = kThreads * kPer, kWaves = kThreads / 64;
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr unsigned kSpins = 1u << 20;  // polls of a word that is on its way
+constexpr uint64_t kNone = ~0ull;      // no sum yet (no sum is this NaN)
 constexpr double kLog2eD = 1.4426950408889634;
 
-// 2^t for t <= 0 to a relative 1.6e-14, exactly 1 at 0, 0 below -1020 (and for a NaN).
-// t = n + r with n the nearest whole number, 2^r = 1 + r q(r) with q of degree 8 fitted
-// on Chebyshev nodes of [-1/2, 1/2] by least squares on the relative error, reweighted
-// towards equal ripple; n goes into the exponent's bits.
-__device__ __forceinline__ double pow2(double t) {
+// 2^(d k) for d <= 0 < k to a relative 1e-12, exactly 1 at d = 0, with low = -1100 / k; 0
+// below -1075 (and for a NaN).  d k = n + r with n the nearest whole number, 2^r = 1 + r q(r)
+// with q of degree 7 fitted on Chebyshev nodes of [-1/2, 1/2] by least squares on the
+// relative error, reweighted towards equal ripple (8e-13).  With the conversion and the
+// sum 16 64-bit instructions, whose issue bounds the sums: one takes a wave 5.3 to 5.9
+// cycles, and 37 million weights 25 us.
+__device__ __forceinline__ double pow2(double d, double k, double low) {
+    d = fmax(d, low);
     const double big = 6755399441055744.0;  // 1.5 * 2^52: its lowest bits then hold n
-    const double s = t + big;
-    const double r = t - (s - big);
-    double q = 0x1.b3de036db3bd6p-24;
-    q = fma(q, r, 0x1.63e698d29c93cp-20);
-    q = fma(q, r, 0x1.ffce2ff794fdcp-17);
-    q = fma(q, r, 0x1.430897f0af9dbp-13);
-    q = fma(q, r, 0x1.5d87fd93724e7p-10);
-    q = fma(q, r, 0x1.3b2ab72413c05p-7);
-    q = fma(q, r, 0x1.c6b08d70c88e9p-5);
-    q = fma(q, r, 0x1.ebfbdff81bdf2p-3);
-    q = fma(q, r, 0x1.62e42fefa37d1p-1);
-    const uint64_t p = (uint64_t)__double_as_longlong(fma(q, r, 1.0));
-    const uint32_t n = (uint32_t)__double_as_longlong(s);
-    const uint64_t v = p + ((uint64_t)(n << 20) << 32);
-    return t >= -1020.0 ? __longlong_as_double((long long)v) : 0.0;
+    const double s = fma(d, k, big);
+    const double r = fma(d, k, big - s);
+    double q = 0x1.61c51b381035fp-20;
+    q = fma(q, r, 0x1.00d858d17751cp-16);
+    q = fma(q, r, 0x1.430aa865450adp-13);
+    q = fma(q, r, 0x1.5d874cfcc70f3p-10);
+    q = fma(q, r, 0x1.3b2ab5ed76007p-7);
+    q = fma(q, r, 0x1.c6b08dcede4ffp-5);
+    q = fma(q, r, 0x1.ebfbdff8edf23p-3);
+    q = fma(q, r, 0x1.62e42fef89cbbp-1);
+    return __builtin_amdgcn_ldexp(fma(q, r, 1.0), (int)(uint32_t)__double_as_longlong(s));
 }
+__device__ __forceinline__ double lowest(double k) { return -1100.0 / k; }
 
 // What a chunk of a row leaves: its maximum, the lowest index of that (only where
 // the sequence is greedy) and sum of 2^((x - m) scale), NaN where the chunk holds a
@@ -62,20 +66,52 @@ struct Part {
 
 // How to draw the token behind the accepted ones.
 struct Pick {
-    double scale, mp, ip, mq, iq;  // weight p = 2^((x - mp) scale) ip, q the same
+    double scale, low, mp, ip, mq, iq;  // weight p = 2^((x - mp) scale) ip, q the same
     int acc, drop, token;          // accepted, so also the row to draw from; draft without q to
                                    // leave out (or -1); token >= -1: already known
 };
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+// A lane's value moved along the wave (a row is 16 lanes): kShr + n by n lanes within
+// its row, kLast15 and kLast31 from lane 15 of a row to the next and from lane 31 to
+// rows 2 and 3, in the rows of `rows`; 0 where nothing comes.
+constexpr int kShr = 0x110, kLast15 = 0x142, kLast31 = 0x143;
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ double moved(double v) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+// Sum over the lanes up to one's own.
+__device__ __forceinline__ double scan(double v) {
+    v += moved<kShr + 1>(v);
+    v += moved<kShr + 2>(v);
+    v += moved<kShr + 4>(v);
+    v += moved<kShr + 8>(v);
+    v += moved<kLast15, 0xA>(v);
+    v += moved<kLast31, 0xC>(v);
     return v;
 }
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+__device__ __forceinline__ double from_lane(double v, int lane) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+__device__ __forceinline__ double wave_sum(double v) { return from_lane(scan(v), 63); }
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float larger(float v) {
+    const int low = (int)0xFF800000u;  // -inf
+    return fmaxf(v, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(low, (int)__float_as_uint(v), CTRL, ROWS, 0xF, false)));
+}
+__device__ __forceinline__ float wave_max(float v) {
+    v = larger<kShr + 1>(v);
+    v = larger<kShr + 2>(v);
+    v = larger<kShr + 4>(v);
+    v = larger<kShr + 8>(v);
+    v = larger<kLast15, 0xA>(v);
+    v = larger<kLast31, 0xC>(v);
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 __device__ __forceinline__ int wave_min(int v) {
 #pragma unroll
@@ -106,68 +142,68 @@ __device__ __forceinline__ unsigned *counter(const VerifyArgs &a, int nch, int r
 }
 
 // Rows of a sequence: 0 .. K the target's, K + 1 .. 2 K the draft's.
-template <typename T>
+// Each wave takes its own maximum for reference, so that it waits for the others once.
+template <typename T, int PER>
 __global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs a, int nch, int rows) {
-    constexpr int N = Row<T>::N, U = kPer / N;
-    __shared__ float wm[kWaves];
-    __shared__ double ws[kWaves];
-    __shared__ int wi[kWaves], wbad[kWaves];
+    constexpr int N = Row<T>::N, U = PER / N;
+    __shared__ Part waves[kWaves];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const int64_t at = blockIdx.x;
-    const int64_t rb = at / nch;
-    const int ch = (int)(at - rb * nch), r = (int)(rb / a.B), b = (int)(rb - (int64_t)r * a.B);
+    const unsigned rb = blockIdx.x / (unsigned)nch;  // fewer than 2^24 workgroups
+    const int ch = (int)(blockIdx.x - rb * nch), r = (int)(rb / (unsigned)a.B), b = (int)(rb - (unsigned)r * a.B);
     const int n = drafts_of(a, b);
-    const double scale = scale_of(a, b);
-    const bool draft = r > a.K;
-    if (r == 0 && ch == 0 && tid == 0) counter(a, nch, rows)[b] = 0;
-    if (draft ? r - a.K - 1 >= n || scale == 0.0 : r > n) return;  // a row that nothing asks for
+    const double scale = scale_of(a, b), low = lowest(scale);
+    const bool draft = r > a.K, greedy = scale == 0.0;
+    if (r == 0 && tid == 0) {
+        ((uint64_t *)chunk_sums(a, nch, rows))[(int64_t)b * nch + ch] = kNone;
+        if (ch == 0) counter(a, nch, rows)[b] = 0;
+    }
+    if (draft ? r - a.K - 1 >= n || greedy : r > n) return;  // a row that nothing asks for
     const Row<T> row(draft ? row_of<T>(a.q, r - a.K - 1, b) : row_of<T>(a.logits, r, b), a.V);
-    const int u0 = ch * (kChunk / N);
-    float x[kPer];
+    const int u0 = ch * (kThreads * U);
+    float x[PER];
     row.template load_all<U>(u0 + tid, kThreads, x);
     float m = -INFINITY;
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         m = fmaxf(m, x[i]);
         bad |= x[i] != x[i];
     }
     m = wave_max(m);
-    if (lane == 0) wm[w] = m;
-    bad = __any(bad);
-    if (lane == 0) wbad[w] = bad;
-    __syncthreads();
-    m = wm[0], bad = wbad[0];
+    bad = __any(bad) || m == INFINITY;
+    double s = 0.0;
+    int first = 0x7FFFFFFF;
+    if (greedy) {
 #pragma unroll
-    for (int i = 1; i < kWaves; ++i) m = fmaxf(m, wm[i]), bad |= wbad[i] != 0;
-    bad |= m == INFINITY;
-    Part *out = (Part *)a.ws + at;
-    if (scale == 0.0) {
-        int first = 0x7FFFFFFF;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
+        for (int i = 0; i < PER; ++i) {
             const int idx = (u0 + (i / N) * kThreads + tid) * N + (i % N) - row.off;
             if (x[i] == m && idx >= 0 && idx < a.V) first = min(first, idx);
         }
         first = wave_min(first);
-        if (lane == 0) wi[w] = first;
-        __syncthreads();
+        s = m == -INFINITY ? 0.0 : 1.0;
+    } else {
+        const double ref = m == -INFINITY ? 0.0 : (double)m;
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i) first = min(first, wi[i]);
-        if (tid == 0) *out = Part{bad ? NAN : m == -INFINITY ? 0.0 : 1.0, m, first};
-        return;
+        for (int i = 0; i < PER; ++i) s += pow2((double)x[i] - ref, scale, low);
+        s = wave_sum(s);
     }
-    const double ref = m == -INFINITY ? 0.0 : (double)m;
-    double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) s += pow2(((double)x[i] - ref) * scale);
-    s = wave_sum(s);
-    if (lane == 0) ws[w] = s;
+    if (lane == 0) waves[w] = Part{bad ? NAN : s, m, first};
     __syncthreads();
-    s = 0.0;
+    if (tid == 0) {
+        m = waves[0].m;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) s += ws[i];
-    if (tid == 0) *out = Part{bad ? NAN : s, m, 0};
+        for (int i = 1; i < kWaves; ++i) m = fmaxf(m, waves[i].m);
+        s = 0.0, first = 0x7FFFFFFF;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            const Part q = waves[i];
+            if (q.s != q.s) s = q.s;
+            if (q.m == -INFINITY) continue;
+            s += greedy ? q.s : q.s * pow2((double)q.m - (double)m, scale, low);
+            if (q.m == m) first = min(first, q.at);
+        }
+        ((Part *)a.ws)[blockIdx.x] = Part{s, m, first};
+    }
 }
 
 // A row's parts joined: maximum and sum (greedy: lowest index of the maximum in `at`).
@@ -180,7 +216,7 @@ struct Joined {
 // two of at least the chunks, or 64) to a row.
 constexpr int kMaxParts = 4;  // of a lane: V <= 1000000 has at most 246 chunks
 template <typename F>
-__device__ __forceinline__ void join(int live, int nch, int across, double scale, Joined *all, F part) {
+__device__ __forceinline__ void join(int live, int nch, int across, double scale, double low, Joined *all, F part) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int each = 64 / across, sub = lane / across, l = lane - sub * across;
     for (int base = w * each; base < live; base += kWaves * each) {
@@ -202,7 +238,7 @@ __device__ __forceinline__ void join(int live, int nch, int across, double scale
         for (int j = 0; j < kMaxParts; ++j) {
             if (q[j].s != q[j].s) s = q[j].s;  // a NaN somewhere
             if (q[j].m == -INFINITY) continue; // nothing allowed in it
-            s += scale == 0.0 ? q[j].s : q[j].s * pow2(((double)q[j].m - ref) * scale);
+            s += scale == 0.0 ? q[j].s : q[j].s * pow2((double)q[j].m - ref, scale, low);
             if (q[j].m == m) at = min(at, q[j].at);
         }
         for (int o = across >> 1; o; o >>= 1) {
@@ -215,17 +251,17 @@ __device__ __forceinline__ void join(int live, int nch, int across, double scale
 
 // Weight of entry i of the row to draw from, of value x, y (draft's).
 __device__ __forceinline__ double weight(const Pick &p, float x, float y, int i, bool q) {
-    const double w = pow2(((double)x - p.mp) * p.scale);
-    if (q) return fmax(w * p.ip - pow2(((double)y - p.mq) * p.scale) * p.iq, 0.0);
+    const double w = pow2((double)x - p.mp, p.scale, p.low);
+    if (q) return fmax(w * p.ip - pow2((double)y - p.mq, p.scale, p.low) * p.iq, 0.0);
     return i == p.drop ? 0.0 : w;
 }
 
 // Values of a chunk of the row to draw from (and of the draft's): unit u0 + j step + tid
 // of the target's aligned start for j = 0, 1, ...; the first is entry i0.
-template <typename T>
+template <typename T, int PER>
 __device__ __forceinline__ void load_pair(const VerifyArgs &a, const Pick &p, int b, int u, int step, bool q,
                                           float *x, float *y, int &i0) {
-    constexpr int N = Row<T>::N, U = kPer / N;
+    constexpr int N = Row<T>::N, U = PER / N;
     const Row<T> row(row_of<T>(a.logits, p.acc, b), a.V);
     row.template load_all<U>(u, step, x);
     i0 = u * N - row.off;
@@ -235,33 +271,23 @@ __device__ __forceinline__ void load_pair(const VerifyArgs &a, const Pick &p, in
         Row<T>(qr, a.V).template load_all<U>(u, step, y);
     } else {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
+        for (int i = 0; i < PER; ++i) {
             const int at = i0 + (i / N) * step * N + i % N;
             y[i] = at >= 0 && at < a.V ? to_f32<T>(qr[at]) : -INFINITY;
         }
     }
 }
 
-// Inclusive sum over the lanes up to one's own.
-__device__ __forceinline__ double scan(double v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const double up = __shfl_up(v, o);
-        if (lane >= o) v += up;
-    }
-    return v;
-}
-
 // The chunk in which the sum of v (lane's chunks j 64 + lane) passes u times the whole,
 // and the sum before it; at the very end the last with any weight; -1: no weight at all.
-__device__ __forceinline__ int find_chunk(const double *v, float u, double &before, double &goal) {
-    const int lane = threadIdx.x & 63;
+__device__ __forceinline__ int find_chunk(const double *v, int nch, float u, double &before, double &goal) {
     double incl[kMaxParts], run = 0.0;
 #pragma unroll
     for (int j = 0; j < kMaxParts; ++j) {
+        incl[j] = run;
+        if (j * 64 >= nch) continue;
         incl[j] = run + scan(v[j]);
-        run = __shfl(incl[j], 63);
+        run = from_lane(incl[j], 63);
     }
     goal = (double)u * run;
     int ch = -1, last = -1;
@@ -273,21 +299,20 @@ __device__ __forceinline__ int find_chunk(const double *v, float u, double &befo
     }
     if (ch < 0) ch = last;
     before = 0.0;
+    if (ch > 0) {
+        const int c = ch - 1;
 #pragma unroll
-    for (int j = 0; j < kMaxParts; ++j) {
-        double up = __shfl_up(incl[j], 1);
-        if (lane == 0) up = j ? __shfl(incl[j ? j - 1 : 0], 63) : 0.0;
-        const double at = __shfl(up, ch & 63);
-        if (ch >= 0 && j == ch >> 6) before = at;
+        for (int j = 0; j < kMaxParts; ++j)
+            if (j == c >> 6) before = from_lane(incl[j], c & 63);
     }
     return ch;
 }
 
 // One workgroup: the token drawn from the row that p names.
-template <typename T>
-__device__ __forceinline__ int draw(const VerifyArgs &a, Pick p, int b, int nch, bool q, const double *sums,
+template <typename T, int PER>
+__device__ __forceinline__ int draw(const VerifyArgs &a, Pick p, int b, int nch, bool q, const uint64_t *sums,
                                     const Part *parts) {
-    constexpr int U = kPer / Row<T>::N;
+    constexpr int U = PER / Row<T>::N;
     __shared__ double total[kWaves];
     __shared__ int found, last;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
@@ -295,29 +320,34 @@ __device__ __forceinline__ int draw(const VerifyArgs &a, Pick p, int b, int nch,
     const float u = fminf(fmaxf(a.u[(int64_t)a.K * a.B + b], 0.0f), 1.0f);
     double v[kMaxParts], before, goal;
 #pragma unroll
-    for (int j = 0; j < kMaxParts; ++j)
-        v[j] = j * 64 + lane < nch
-                   ? __hip_atomic_load(sums + j * 64 + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
-                   : 0.0;
-    int ch = find_chunk(v, u, before, goal);
+    for (int j = 0; j < kMaxParts; ++j) {
+        uint64_t word = 0;
+        // counted already, so stored already: on its way at most
+        for (unsigned spins = 0; j * 64 + lane < nch && spins < kSpins; ++spins) {
+            word = __hip_atomic_load(sums + j * 64 + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (word != kNone) break;
+        }
+        v[j] = __longlong_as_double((long long)word);
+    }
+    int ch = find_chunk(v, nch, u, before, goal);
     if (ch < 0) {  // nothing of p - q is left: p itself
         p.drop = -1;
         q = false;
 #pragma unroll
         for (int j = 0; j < kMaxParts; ++j) {
             const Part c = j * 64 + lane < nch ? parts[j * 64 + lane] : Part{0.0, -INFINITY, 0};
-            v[j] = c.m == -INFINITY ? 0.0 : c.s * pow2(((double)c.m - p.mp) * p.scale);
+            v[j] = c.m == -INFINITY ? 0.0 : c.s * pow2((double)c.m - p.mp, p.scale, p.low);
         }
-        ch = find_chunk(v, u, before, goal);
+        ch = find_chunk(v, nch, u, before, goal);
     }
     if (ch < 0) return -1;
     // a thread takes neighbouring entries: indices grow with the thread
-    float x[kPer], y[kPer];
-    double wt[kPer], s = 0.0;
+    float x[PER], y[PER];
+    double wt[PER], s = 0.0;
     int i0;
-    load_pair<T>(a, p, b, (ch * kThreads + tid) * U, 1, q, x, y, i0);
+    load_pair<T, PER>(a, p, b, (ch * kThreads + tid) * U, 1, q, x, y, i0);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         wt[i] = weight(p, x[i], y[i], i0 + i, q);
         s += wt[i];
     }
@@ -328,7 +358,7 @@ __device__ __forceinline__ int draw(const VerifyArgs &a, Pick p, int b, int nch,
     for (int i = 0; i < w; ++i) at += total[i];
     int mine = 0x7FFFFFFF, end = -1;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         at += wt[i];
         if (wt[i] > 0.0) {
             end = i0 + i;
@@ -345,7 +375,7 @@ __device__ __forceinline__ int draw(const VerifyArgs &a, Pick p, int b, int nch,
     return found != 0x7FFFFFFF ? found : last;
 }
 
-template <typename T>
+template <typename T, int PER>
 __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int nch, int rows, int across) {
     constexpr int N = Row<T>::N;
     __shared__ Joined all[2 * kMaxDrafts + 1];
@@ -355,7 +385,7 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int b = blockIdx.x / nch, ch = blockIdx.x - b * nch;
     const int n = drafts_of(a, b);
-    const double scale = scale_of(a, b);
+    const double scale = scale_of(a, b), low = lowest(scale);
     const Part *part = (const Part *)a.ws;
     const bool greedy = scale == 0.0, has_q = a.q.p != nullptr && !greedy;
     // the drafts' own logits, on their way while the rows are joined
@@ -369,7 +399,7 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int
             if (has_q) yd = to_f32<T>(row_of<T>(a.q, lane, b)[id]);
         }
     }
-    join(n + 1 + (has_q ? n : 0), nch, across, scale, all,
+    join(n + 1 + (has_q ? n : 0), nch, across, scale, low, all,
          [&](int i) { return part + ((int64_t)(i <= n ? i : a.K + (i - n)) * a.B + b) * nch; });
     __syncthreads();
     if (w == 0) {
@@ -379,11 +409,11 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int
             if (greedy) {
                 ok = p.s > 0.0 && id == p.at;
             } else if (p.s > 0.0) {
-                const double px = pow2(((double)xd - p.m) * scale) / p.s;
+                const double px = pow2((double)xd - p.m, scale, low) / p.s;
                 double qx = 1.0;
                 if (has_q) {
                     const Joined q = all[n + 1 + lane];
-                    qx = q.s == 0.0 ? 0.0 : pow2(((double)yd - q.m) * scale) / q.s;  // NaN: refuses
+                    qx = q.s == 0.0 ? 0.0 : pow2((double)yd - q.m, scale, low) / q.s;  // NaN: refuses
                 }
                 ok = (double)ud * qx < px;
             }
@@ -392,7 +422,7 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int
         const int acc = __ffsll((unsigned long long)~stood) - 1;  // n <= 63: bit 63 is never set
         if (lane == 0) {
             const Joined p = all[acc];
-            Pick k{scale, p.m, 1.0 / p.s, 0.0, 0.0, acc, -1, -2};
+            Pick k{scale, low, p.m, 1.0 / p.s, 0.0, 0.0, acc, -1, -2};
             if (!(p.s > 0.0)) {
                 k.token = -1;
             } else if (greedy) {
@@ -413,28 +443,28 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int
     int token = p.token;
     if (token == -2) {
         const bool q = has_q && p.acc < n;
-        float x[kPer], y[kPer];
+        float x[PER], y[PER];
         int i0;
-        load_pair<T>(a, p, b, ch * (kChunk / N) + tid, kThreads, q, x, y, i0);
+        load_pair<T, PER>(a, p, b, ch * (kThreads * PER / N) + tid, kThreads, q, x, y, i0);
         double s = 0.0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) s += weight(p, x[i], y[i], i0 + (i / N) * kThreads * N + i % N, q);
+        for (int i = 0; i < PER; ++i) s += weight(p, x[i], y[i], i0 + (i / N) * kThreads * N + i % N, q);
         s = wave_sum(s);
         if (lane == 0) tmp[w] = s;
         __syncthreads();
-        double *sums = chunk_sums(a, nch, rows) + (int64_t)b * nch;
+        uint64_t *sums = (uint64_t *)chunk_sums(a, nch, rows) + (int64_t)b * nch;
         if (tid == 0) {
             s = 0.0;
 #pragma unroll
             for (int i = 0; i < kWaves; ++i) s += tmp[i];
-            __hip_atomic_store(sums + ch, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            // this sum is there before the count, all others before the last count
-            done = __hip_atomic_fetch_add(counter(a, nch, rows) + b, 1u, __ATOMIC_ACQ_REL,
+            __hip_atomic_store(sums + ch, (uint64_t)__double_as_longlong(s), __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+            done = __hip_atomic_fetch_add(counter(a, nch, rows) + b, 1u, __ATOMIC_RELAXED,
                                           __HIP_MEMORY_SCOPE_AGENT) == (unsigned)nch - 1;
         }
         __syncthreads();
         if (!done) return;
-        token = draw<T>(a, p, b, nch, q, sums, part + ((int64_t)p.acc * a.B + b) * nch);
+        token = draw<T, PER>(a, p, b, nch, q, sums, part + ((int64_t)p.acc * a.B + b) * nch);
     } else if (ch != 0) {
         return;
     }
@@ -449,31 +479,43 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int
     }
 }
 
-template <typename T>
+// Values of a thread: 32 where that leaves the first launch sixteen workgroups a CU, for
+// half the fixed work of a chunk (32 x 5 x 128000: 55 us for 58), else 16, which
+// spread a small call further (1 x 5 x 32000: 19 us for 24).
+constexpr int kFew = 16, kMany = 32;
+
+template <typename T, int PER>
 hipError_t verify_t(const VerifyArgs &a, hipStream_t s) {
-    const int nch = chunks(a.V, kChunk, sizeof(T)), rows = a.q.p ? 2 * a.K + 1 : a.K + 1;
+    const int nch = chunks(a.V, kThreads * PER, sizeof(T)), rows = a.q.p ? 2 * a.K + 1 : a.K + 1;
     const dim3 thr(kThreads);
-    hipLaunchKernelGGL(verify_sum_kernel<T>, dim3((unsigned)((int64_t)rows * a.B * nch)), thr, 0, s, a, nch, rows);
+    hipLaunchKernelGGL((verify_sum_kernel<T, PER>), dim3((unsigned)((int64_t)rows * a.B * nch)), thr, 0, s, a, nch, rows);
     int across = 1;
     while (across < nch && across < 64) across *= 2;
-    hipLaunchKernelGGL(verify_draw_kernel<T>, dim3((unsigned)((int64_t)a.B * nch)), thr, 0, s, a, nch, rows, across);
+    hipLaunchKernelGGL((verify_draw_kernel<T, PER>), dim3((unsigned)((int64_t)a.B * nch)), thr, 0, s, a, nch, rows, across);
     return hipGetLastError();
+}
+
+template <typename T>
+hipError_t verify_by_size(const VerifyArgs &a, hipStream_t s) {
+    const int64_t rows = a.q.p ? 2 * a.K + 1 : a.K + 1;
+    return rows * a.B * chunks(a.V, kThreads * kMany, sizeof(T)) >= 4096 ? verify_t<T, kMany>(a, s)
+                                                                          : verify_t<T, kFew>(a, s);
 }
 
 }  // namespace
 
 size_t verify_bytes(int K, int B, int V) {
-    // the larger chunk count of the two types
-    const size_t nch = chunks(V, kChunk, 2);
+    // the larger chunk count of the two types and sizes
+    const size_t nch = chunks(V, kThreads * kFew, 2);
     return ((size_t)(2 * K + 1) * nch * sizeof(Part) + nch * sizeof(double) + sizeof(unsigned)) * B;
 }
 
 bool verify_grid_ok(int K, int B, int V) {
-    return grid_ok((int64_t)(2 * K + 1) * B * chunks(V, kChunk, 2), kThreads);
+    return grid_ok((int64_t)(2 * K + 1) * B * chunks(V, kThreads * kFew, 2), kThreads);
 }
 
 hipError_t launch_verify(const VerifyArgs &a, bool bf16, hipStream_t s) {
-    return bf16 ? verify_t<uint16_t>(a, s) : verify_t<float>(a, s);
+    return bf16 ? verify_by_size<uint16_t>(a, s) : verify_by_size<float>(a, s);
 }
 
 }  // namespace lm
