@@ -253,7 +253,7 @@ rnn_status rnn_gated_fwd(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, c
     for (const void *p : ps)
         if (!aligned16(p)) return RNN_ERR_INVALID_ARG;
     const lm::GatedDims n = gated_dims(d, gate);
-    if (!gated_width_ok(d) || !lm::gated_grid_ok(n, dt == RNN_BF16)) return RNN_ERR_UNSUPPORTED;
+    if (!gated_width_ok(d)) return RNN_ERR_UNSUPPORTED;
     const size_t need = lm::gated_bytes(n, dt == RNN_BF16);
     if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;
     return done(lm::launch_gated_fwd(n, dt == RNN_BF16, seq_of(f), seq_of(x), h0, lens, out_of(h), hT,
@@ -268,7 +268,7 @@ rnn_status rnn_gated_step(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, 
         !aligned16(h_out))
         return RNN_ERR_INVALID_ARG;
     const lm::GatedDims n = gated_dims(d, gate);
-    if (!gated_width_ok(d) || !lm::gated_step_grid_ok(n)) return RNN_ERR_UNSUPPORTED;
+    if (!gated_width_ok(d)) return RNN_ERR_UNSUPPORTED;
     return done(lm::launch_gated_step(n, dt == RNN_BF16, seq_of(f), seq_of(x), h, out_of(y), h_out,
                                       stream));
 }
@@ -288,7 +288,7 @@ rnn_status rnn_gated_bwd(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, c
     for (const void *p : ps)
         if (!aligned16(p)) return RNN_ERR_INVALID_ARG;
     const lm::GatedDims n = gated_dims(d, gate);
-    if (!gated_width_ok(d) || !lm::gated_grid_ok(n, dt == RNN_BF16)) return RNN_ERR_UNSUPPORTED;
+    if (!gated_width_ok(d)) return RNN_ERR_UNSUPPORTED;
     const size_t need = lm::gated_bytes(n, dt == RNN_BF16);
     if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;
     return done(lm::launch_gated_bwd(n, dt == RNN_BF16, seq_of(f), seq_or_none(x), seq_of(h), seq_of(dh),

@@ -10,9 +10,11 @@
 // the call, so that a captured call replays what it was given.
 //
 // Memory bounds it: a workgroup takes an equal share of the list, in pieces of a
-// 16-byte unit to a thread, kAhead of them in flight.  The second pass walks each
-// share backwards: what the first read last is then still in the last-level cache.
-// It stores past the caches.
+// 16-byte unit to a thread, kAhead of them in flight.  The first pass leaves what it
+// can in the last-level cache; the second reads and stores past the caches.  86
+// million float32: 171 us, 6.05 TB/s over the two readings and the writing (the second
+// reading through the caches 185, its stores too 217, the first past them 192; the
+// second from the list's end makes no difference).
 //
 // Squares are summed in 64 bits: the largest float32 squared is far inside
 // them, so only a value that is not finite gives such a sum, and there is
@@ -25,6 +27,8 @@ namespace rnn355 {
 namespace lm {
 
 namespace {
+
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256, kAhead = 8;
 constexpr int kPiece = kThreads * 16;  // bytes
@@ -79,7 +83,7 @@ struct Units {
         off = (int)(((uintptr_t)p & 15) / sizeof(T));
         base = (const T *)p - off;
     }
-    // whether piece i (of NT units) holds nothing but whole units
+    // whether units [lo, hi) are all whole
     __device__ __forceinline__ bool whole(int64_t lo, int64_t hi) const { return lo * N >= off && hi * N - off <= n; }
 };
 
@@ -130,7 +134,6 @@ __device__ __forceinline__ void store(T *out, Unit<T, 16 / sizeof(T)> q, float c
 #pragma unroll
     for (int e = 0; e < N; ++e) q.v[e] = from_f32<T>(to_f32<T>(q.v[e]) * c);
     if (whole) {
-        typedef uint32_t u4 __attribute__((ext_vector_type(4)));
         __builtin_nontemporal_store(__builtin_bit_cast(u4, q), (u4 *)out);
     } else {
 #pragma unroll
@@ -138,52 +141,44 @@ __device__ __forceinline__ void store(T *out, Unit<T, 16 / sizeof(T)> q, float c
     }
 }
 
-// out = c p over units [lo, hi), from the end.
+// out = c p over units [lo, hi), NT threads.
 template <typename T, int NT>
 __device__ __forceinline__ void scale(const void *p, void *out_, int64_t n, int64_t lo, int64_t hi, float c) {
     constexpr int N = Units<T>::N;
     const Units<T> t(p, n);
     T *out = (T *)out_ - t.off;
     const bool same = ((uintptr_t)out & 15) == 0;  // at the same place of its 16 bytes
-    for (int64_t end = hi; end > lo;) {
-        if (end - NT * kAhead >= lo && t.whole(end - NT * kAhead, end)) {
-            end -= NT * kAhead;
+    for (int64_t at = lo; at < hi;) {
+        if (at + NT * kAhead <= hi && t.whole(at, at + NT * kAhead)) {
             Unit<T, N> q[kAhead];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) q[j] = *(const Unit<T, N> *)(t.base + (end + j * NT + threadIdx.x) * N);
+            for (int j = 0; j < kAhead; ++j)
+                q[j] = __builtin_bit_cast(
+                    Unit<T, N>, __builtin_nontemporal_load((const u4 *)(t.base + (at + j * NT + threadIdx.x) * N)));
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) store<T>(out + (end + j * NT + threadIdx.x) * N, q[j], c, same);
+            for (int j = 0; j < kAhead; ++j) store<T>(out + (at + j * NT + threadIdx.x) * N, q[j], c, same);
+            at += NT * kAhead;
             continue;
         }
-        // to a multiple of NT from lo, so that what is left is whole pieces
-        const int64_t at = lo + (end - lo - 1) / NT * NT;
         const int64_t u = at + threadIdx.x, i0 = u * N - t.off;
-        if (u < end && i0 >= 0 && i0 + N <= n) {
+        if (u < hi && i0 >= 0 && i0 + N <= n) {
             store<T>(out + u * N, *(const Unit<T, N> *)(t.base + u * N), c, same);
-        } else if (u < end) {
+        } else if (u < hi) {
             for (int e = 0; e < N; ++e)
                 if (i0 + e >= 0 && i0 + e < n) out[u * N + e] = from_f32<T>(to_f32<T>(t.base[u * N + e]) * c);
         }
-        end = at;
+        at += NT;
     }
 }
 
-// Pieces [lo, hi) of the list, tensor by tensor, forwards or from the end:
-// f(tensor, first unit, unit behind the last).
-template <bool BACK, typename F>
+// Pieces [lo, hi) of the list, tensor by tensor: f(tensor, first unit, unit behind the last).
+template <typename F>
 __device__ __forceinline__ void each(const Group &g, int lo, int hi, F f) {
     if (lo >= hi) return;
-    int t = find(g, BACK ? hi - 1 : lo);
-    while (lo < hi) {
-        const int from = max(g.first[t], lo), to = min(g.first[t + 1], hi);
-        f(t, (int64_t)(from - g.first[t]) * kThreads, (int64_t)(to - g.first[t]) * kThreads);
-        if (BACK) {
-            hi = from;
-            --t;
-        } else {
-            lo = to;
-            ++t;
-        }
+    for (int t = find(g, lo); lo < hi; ++t) {
+        const int to = min(g.first[t + 1], hi);
+        f(t, (int64_t)(lo - g.first[t]) * kThreads, (int64_t)(to - g.first[t]) * kThreads);
+        lo = to;
     }
 }
 
@@ -196,7 +191,7 @@ __device__ __forceinline__ void share(int all, int &lo, int &hi) {
 template <int NT>
 __device__ __forceinline__ double share_squares(const Group &g, int lo, int hi) {
     double s = 0.0;
-    each<false>(g, lo, hi, [&](int t, int64_t a, int64_t b) {
+    each(g, lo, hi, [&](int t, int64_t a, int64_t b) {
         s += g.bf16[t] ? squares<uint16_t, NT>(g.p[t], g.n[t], a, b) : squares<float, NT>(g.p[t], g.n[t], a, b);
     });
     return s;
@@ -212,7 +207,7 @@ __device__ __forceinline__ bool factor(double s, float max_norm, float &c) {
 
 template <int NT>
 __device__ __forceinline__ void share_scale(const Group &g, int lo, int hi, bool over, float c) {
-    each<true>(g, lo, hi, [&](int t, int64_t a, int64_t b) {
+    each(g, lo, hi, [&](int t, int64_t a, int64_t b) {
         if (!over && !g.out[t]) return;  // in place, as it is
         void *out = g.out[t] ? g.out[t] : const_cast<void *>(g.p[t]);
         if (g.bf16[t])

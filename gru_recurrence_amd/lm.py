@@ -11,6 +11,7 @@ stream that uses it.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 from typing import Optional
@@ -70,7 +71,7 @@ def load():
     P, I, S, L, F = (ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64,
                      ctypes.c_float)
     ids, seq, dims = ctypes.POINTER(_Ids), ctypes.POINTER(_Seq), ctypes.POINTER(LinDims)
-    gated, grads = ctypes.POINTER(GatedDims), ctypes.POINTER(_Grad)
+    gated, grads = ctypes.POINTER(GatedDims), P  # rnn_grad[count] as its bytes
     for name, res, args in (
             ("rnn_embed_fwd", I, [I, I, I, I, I, ids, P, L, F, P, P]),
             ("rnn_workspace_size_embed_bwd", S, [I] * 4),
@@ -447,7 +448,7 @@ def _row_out(t, name, dtype, shape, dev):
     """An output sequence: (tensor, view); a view given must not overlap itself."""
     if t is None:
         t = torch.empty(shape, dtype=dtype, device=dev)
-        return t, _Seq(t.data_ptr(), shape[1] * shape[2], shape[2])
+        return t, _Seq(t.data_ptr(), shape[1] * shape[2], shape[2])  # dense
     v = _row(t, name, dtype, shape, dev)
     need = shape[2]
     for step, n in sorted(((v.stride_t, shape[0]), (v.stride_b, shape[1]))):
@@ -555,22 +556,26 @@ class GradList:
         outs = grads if out is None else list(out)
         if len(outs) != len(grads):
             raise ValueError("%d outputs for %d gradients" % (len(outs), len(grads)))
-        rows, seen = [], set()
+        flat = []
         for t, o in zip(grads, outs):
-            code, n, at = _DT.get(t.dtype), t.numel(), o.data_ptr()
+            code = _DT.get(t.dtype)
             if code is None:
                 raise TypeError("gradients must be bfloat16 or float32, got %s" % t.dtype)
             if t.device != dev or not t.is_contiguous():
                 raise ValueError("gradients must be contiguous tensors of one device")
-            if o is not t and (o.dtype != t.dtype or o.shape != t.shape or o.device != dev
-                               or not o.is_contiguous()):
-                raise ValueError("outputs must match their gradients")
-            if n and at in seen:
-                raise ValueError("the same output more than once")
-            seen.add(at)
-            rows.append((t.data_ptr(), at, n, code))
-        self.grads, self.out = grads, outs
-        self.count, self.array = len(rows), (_Grad * len(rows))(*rows)
+            at = to = t.data_ptr()
+            if o is not t:
+                if (o.dtype != t.dtype or o.shape != t.shape or o.device != dev
+                        or not o.is_contiguous()):
+                    raise ValueError("outputs must match their gradients")
+                to = o.data_ptr()
+            flat += (at, to, t.numel(), code)
+        written = [to for to, n in zip(flat[1::4], flat[2::4]) if n]
+        self.grads, self.out, self.count = grads, outs, len(grads)
+        self.twice = len(set(written)) != len(written)
+        # rnn_grad has four fields of 8 bytes (the type's upper half is padding)
+        self._rows = array.array("q", flat)
+        self.array = self._rows.buffer_info()[0]
 
     def get_device(self):
         return self.device.index
@@ -613,6 +618,8 @@ def clip_grads(grads, max_norm: float, *, out=None, norm=None, ws=None, stream=N
         g = grads
     else:
         g = GradList(grads, out)
+    if g.twice:
+        raise ValueError("the same output more than once")
     if not max_norm >= 0:
         raise ValueError("max_norm must be 0 or more, got %r" % (max_norm,))
     return _clip(g, float(max_norm), norm, ws, stream=stream)

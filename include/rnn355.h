@@ -554,11 +554,11 @@ rnn_status rnn_linattn_bwd(const rnn_lin_dims *d, rnn_dtype dt, const rnn_seq *q
  * lens (may be NULL: T for all) [B]: only the first lens[b] tokens of row b, at
  * least 0 and at most T, count (other values are taken as the nearest of these).
  * Behind them the state stays as it is, h and the gradients df, dx are 0, and
- * nothing is read from f, x, h or dh.
- * Sums and states are float32 in an order that the dimensions set, so results
- * repeat bit for bit; outputs are rounded once.  Decays are of magnitude 1 at
- * most: the products of up to 256 consecutive ones are formed, which larger
- * ones may carry past float32.  A value that is not finite may reach every
+ * what f, x, h or dh hold does not matter.
+ * Sums and states are float32 in an order that the dimensions and the operands'
+ * alignment set, so results repeat bit for bit; outputs are rounded once.
+ * Decays are of magnitude 1 at most: products of many consecutive ones are
+ * formed, which larger ones may carry past float32.  A value that is not finite may reach every
  * later output of its batch row and channel (backward: every earlier one).
  * B * D at most 2^30, else RNN_ERR_UNSUPPORTED.
  */
