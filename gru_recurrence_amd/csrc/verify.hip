@@ -249,8 +249,11 @@ __device__ __forceinline__ void join(int live, int nch, int across, double scale
     }
 }
 
-// Weight of entry i of the row to draw from, of value x, y (draft's).
+// Weight of entry i of the row to draw from, of value x, y (draft's).  The products are
+// rounded before they are subtracted: where p equals q nothing is left, not the rounding
+// of one of them.
 __device__ __forceinline__ double weight(const Pick &p, float x, float y, int i, bool q) {
+#pragma clang fp contract(off)
     const double w = pow2((double)x - p.mp, p.scale, p.low);
     if (q) return fmax(w * p.ip - pow2((double)y - p.mq, p.scale, p.low) * p.iq, 0.0);
     return i == p.drop ? 0.0 : w;

@@ -558,7 +558,9 @@ rnn_status rnn_linattn_bwd(const rnn_lin_dims *d, rnn_dtype dt, const rnn_seq *q
  * Sums and states are float32 in an order that the dimensions and the operands'
  * alignment set, so results repeat bit for bit; outputs are rounded once.
  * Decays are of magnitude 1 at most: products of many consecutive ones are
- * formed, which larger ones may carry past float32.  A value that is not finite may reach every
+ * formed, which larger ones may carry past float32.  Segments of a long sequence
+ * wait for each other with a bounded spin, as described above (the workspace's
+ * status word, rnn_workspace_status).  A value that is not finite may reach every
  * later output of its batch row and channel (backward: every earlier one).
  * B * D at most 2^30, else RNN_ERR_UNSUPPORTED.
  */

@@ -374,6 +374,22 @@ def test_gated_on_another_stream_and_captured():
         torch.cuda.synchronize()
 
 
+def test_gated_wait_timeout_is_reported(monkeypatch):
+    """With one poll allowed (set from the host) waits between segments give up, the
+    kernels end normally and the workspace reports it; the next call clears it."""
+    f, x, dh, h0, dhT, _ = _case(1, 60000, 1, 96, "f32", "logit")
+    ws = torch.empty(max(g.workspace_size_gated(op, g.GatedDims(60000, 1, 96), g.RNN_F32)
+                         for op in (g.OP_GATED_FWD, g.OP_GATED_BWD)), dtype=torch.uint8, device="cuda")
+    calls = [lambda: g.gated_fwd(f, x, h0, ws=ws), lambda: g.gated_bwd(f, x, x, dh, h0, dhT, ws=ws)]
+    for call in calls:
+        monkeypatch.setenv("RNN355_SPIN_LIMIT", "1")
+        call()
+        assert g.workspace_status(ws) == g.RNN_ERR_BARRIER_TIMEOUT
+        monkeypatch.delenv("RNN355_SPIN_LIMIT")
+        call()
+        assert g.workspace_status(ws) == g.RNN_OK
+
+
 def test_gated_two_calls_at_once():
     """Calls on two streams, each with its workspace, over and over."""
     cases = [_case(s, 6000, 2, 130, "f32", "logit") for s in (1, 2)]

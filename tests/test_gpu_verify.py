@@ -179,6 +179,33 @@ def test_verify_large_vocabularies_and_offsets_past_32_bits():
     assert torch.equal(tokens[0, rest], flat[rest])
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_verify_large_calls(dt):
+    """Calls large enough for the longer chunks, with a mask and temperatures; rows of
+    the two models that start at the same place of their 16 bytes, and elsewhere."""
+    torch.manual_seed(8)
+    K, B, V = 4, 40, 100003
+    x, d, u, y, temp, n = _case(77, K, B, V, dt, "banned")
+    want = _check(x, d, u, y, temp, n)
+    _check(x, d, u, None, temp)
+    yp = torch.nn.functional.pad(y, (3, 0))[..., 3:]
+    got = g.verify_drafts(x, d, u, yp, temperature=temp, n_drafts=n)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("V", [7, 5000, 70001])
+def test_verify_nothing_left_of_the_difference(V):
+    """The same model twice and u = 1: every draft is refused, max(p - q, 0) is 0
+    everywhere, and p itself is drawn from."""
+    torch.manual_seed(9)
+    x, d, u, y, _, _ = _case(V, 2, 9, V, "f32", "equal")
+    u[:2] = 1.0
+    tokens, acc = _check(x, d, u, y)
+    assert not acc.any()
+    want, _ = g.verify_drafts(x[:1], None, u[2:])
+    assert torch.equal(tokens[:1], want)
+
+
 def test_verify_is_distributed_as_the_target():
     """Drafts drawn from q and verified against p: the first token that comes out
     is distributed as p, whatever q is.  Counts of n draws stay within 5 of their
