@@ -8,9 +8,9 @@
 // Two launches.  The first reads every row once, a chunk of it to a workgroup, and
 // leaves the chunk's maximum and sum of weights.  The second joins those, decides how
 // many drafts stand (each workgroup of a sequence for itself) and sums w over the
-// chunks of the row to draw from; the sequence's last workgroup to finish finds the
-// chunk in which the sum passes u, and the entry in it.  Sums are added in the order of
-// the chunks, so nothing depends on which workgroup that is.  A sum is one 64-bit word
+// strips of the row to draw from, a wave a strip; the sequence's last workgroup to
+// finish finds the strip in which the sum passes u, and the entry in it.  Sums are added
+// in the order of the strips, so nothing depends on which workgroup that is.  A sum is one 64-bit word
 // that says by its value that it is there; an ordered counter in its place would write
 // back and empty the caches of every workgroup (70 us for 58 at 32 x 5 x 128000).
 //
@@ -133,12 +133,12 @@ __device__ __forceinline__ const T *row_of(const LinSeq &s, int k, int b) {
     return (const T *)s.p + (int64_t)k * s.st + (int64_t)b * s.sb;
 }
 
-// The workspace: parts [rows][B][nch], sums [B][nch], counters [B].
-__device__ __forceinline__ double *chunk_sums(const VerifyArgs &a, int nch, int rows) {
-    return (double *)((Part *)a.ws + (int64_t)rows * a.B * nch);
+// The workspace: parts [rows][B][nch], sums of strips [B][nch kWaves], counters [B].
+__device__ __forceinline__ uint64_t *strip_sums(const VerifyArgs &a, int nch, int rows) {
+    return (uint64_t *)((Part *)a.ws + (int64_t)rows * a.B * nch);
 }
 __device__ __forceinline__ unsigned *counter(const VerifyArgs &a, int nch, int rows) {
-    return (unsigned *)(chunk_sums(a, nch, rows) + (int64_t)a.B * nch);
+    return (unsigned *)(strip_sums(a, nch, rows) + (int64_t)a.B * nch * kWaves);
 }
 
 // Rows of a sequence: 0 .. K the target's, K + 1 .. 2 K the draft's.
@@ -153,10 +153,8 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs a, int 
     const int n = drafts_of(a, b);
     const double scale = scale_of(a, b), low = lowest(scale);
     const bool draft = r > a.K, greedy = scale == 0.0;
-    if (r == 0 && tid == 0) {
-        ((uint64_t *)chunk_sums(a, nch, rows))[(int64_t)b * nch + ch] = kNone;
-        if (ch == 0) counter(a, nch, rows)[b] = 0;
-    }
+    if (r == 0 && tid < kWaves) strip_sums(a, nch, rows)[((int64_t)b * nch + ch) * kWaves + tid] = kNone;
+    if (r == 0 && ch == 0 && tid == 0) counter(a, nch, rows)[b] = 0;
     if (draft ? r - a.K - 1 >= n || greedy : r > n) return;  // a row that nothing asks for
     const Row<T> row(draft ? row_of<T>(a.q, r - a.K - 1, b) : row_of<T>(a.logits, r, b), a.V);
     const int u0 = ch * (kThreads * U);
@@ -259,113 +257,139 @@ __device__ __forceinline__ double weight(const Pick &p, float x, float y, int i,
     return i == p.drop ? 0.0 : w;
 }
 
-// Values of a chunk of the row to draw from (and of the draft's): unit u0 + j step + tid
-// of the target's aligned start for j = 0, 1, ...; the first is entry i0.
-template <typename T, int PER>
+// NU units of the row to draw from (and of the draft's): units u, u + step, ... from the
+// target's aligned start; the first holds entry i0.
+template <typename T, int NU>
 __device__ __forceinline__ void load_pair(const VerifyArgs &a, const Pick &p, int b, int u, int step, bool q,
                                           float *x, float *y, int &i0) {
-    constexpr int N = Row<T>::N, U = PER / N;
+    constexpr int N = Row<T>::N;
     const Row<T> row(row_of<T>(a.logits, p.acc, b), a.V);
-    row.template load_all<U>(u, step, x);
+    row.template load_all<NU>(u, step, x);
     i0 = u * N - row.off;
     if (!q) return;
     const T *qr = row_of<T>(a.q, p.acc, b);
     if ((int)(((uintptr_t)qr & 15) / sizeof(T)) == row.off) {
-        Row<T>(qr, a.V).template load_all<U>(u, step, y);
+        Row<T>(qr, a.V).template load_all<NU>(u, step, y);
     } else {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
+        for (int i = 0; i < NU * N; ++i) {
             const int at = i0 + (i / N) * step * N + i % N;
             y[i] = at >= 0 && at < a.V ? to_f32<T>(qr[at]) : -INFINITY;
         }
     }
 }
 
-// The chunk in which the sum of v (lane's chunks j 64 + lane) passes u times the whole,
-// and the sum before it; at the very end the last with any weight; -1: no weight at all.
-__device__ __forceinline__ int find_chunk(const double *v, int nch, float u, double &before, double &goal) {
-    double incl[kMaxParts], run = 0.0;
+// The strip in which the sum of v (lane's strips j 64 + lane, n in all) passes u times
+// the whole, and the sum before it; at the very end the last with any weight; -1: no
+// weight at all.
+constexpr int kMaxStrips = kMaxParts * kWaves;  // of a lane
+__device__ __forceinline__ int find_strip(const double *v, int n, float u, double &before, double &goal) {
+    double incl[kMaxStrips], run = 0.0;
 #pragma unroll
-    for (int j = 0; j < kMaxParts; ++j) {
+    for (int j = 0; j < kMaxStrips; ++j) {
         incl[j] = run;
-        if (j * 64 >= nch) continue;
+        if (j * 64 >= n) continue;
         incl[j] = run + scan(v[j]);
         run = from_lane(incl[j], 63);
     }
     goal = (double)u * run;
-    int ch = -1, last = -1;
+    int at = -1, last = -1;
 #pragma unroll
-    for (int j = kMaxParts - 1; j >= 0; --j) {  // the lowest that passes is found last
+    for (int j = kMaxStrips - 1; j >= 0; --j) {  // the lowest that passes is found last
+        if (j * 64 >= n) continue;
         const uint64_t some = __ballot(v[j] > 0.0), over = __ballot(v[j] > 0.0 && incl[j] > goal);
         if (some && last < 0) last = j * 64 + 63 - __clzll((long long)some);
-        if (over) ch = j * 64 + __ffsll((unsigned long long)over) - 1;
+        if (over) at = j * 64 + __ffsll((unsigned long long)over) - 1;
     }
-    if (ch < 0) ch = last;
+    if (at < 0) at = last;
     before = 0.0;
-    if (ch > 0) {
-        const int c = ch - 1;
+    if (at > 0) {
+        const int c = at - 1;
 #pragma unroll
-        for (int j = 0; j < kMaxParts; ++j)
+        for (int j = 0; j < kMaxStrips; ++j)
             if (j == c >> 6) before = from_lane(incl[j], c & 63);
     }
-    return ch;
+    return at;
 }
 
-// One workgroup: the token drawn from the row that p names.
+// One workgroup: the token drawn from the row that p names, given the sums of its strips
+// of 64 U units (and its parts, which are those of p alone).
 template <typename T, int PER>
 __device__ __forceinline__ int draw(const VerifyArgs &a, Pick p, int b, int nch, bool q, const uint64_t *sums,
                                     const Part *parts) {
-    constexpr int U = PER / Row<T>::N;
+    constexpr int N = Row<T>::N, U = PER / N, NU = U >= kWaves ? U / kWaves : 1;
     __shared__ double total[kWaves];
     __shared__ int found, last;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, strips = nch * kWaves;
     if (tid == 0) found = 0x7FFFFFFF, last = -1;
     const float u = fminf(fmaxf(a.u[(int64_t)a.K * a.B + b], 0.0f), 1.0f);
-    double v[kMaxParts], before, goal;
+    double v[kMaxStrips], before, goal;
 #pragma unroll
-    for (int j = 0; j < kMaxParts; ++j) {
+    for (int j = 0; j < kMaxStrips; ++j) {
         uint64_t word = 0;
         // counted already, so stored already: on its way at most
-        for (unsigned spins = 0; j * 64 + lane < nch && spins < kSpins; ++spins) {
+        for (unsigned spins = 0; j * 64 + lane < strips && spins < kSpins; ++spins) {
             word = __hip_atomic_load(sums + j * 64 + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             if (word != kNone) break;
         }
         v[j] = __longlong_as_double((long long)word);
     }
-    int ch = find_chunk(v, nch, u, before, goal);
-    if (ch < 0) {  // nothing of p - q is left: p itself
+    int at = find_strip(v, strips, u, before, goal);
+    if (at < 0) {  // nothing of p - q is left: p itself, first its chunk, then the strip
         p.drop = -1;
         q = false;
 #pragma unroll
-        for (int j = 0; j < kMaxParts; ++j) {
+        for (int j = 0; j < kMaxStrips; ++j) {
             const Part c = j * 64 + lane < nch ? parts[j * 64 + lane] : Part{0.0, -INFINITY, 0};
             v[j] = c.m == -INFINITY ? 0.0 : c.s * pow2((double)c.m - p.mp, p.scale, p.low);
+            if (v[j] < 1e-290) v[j] = 0.0;  // its entries would have none
         }
-        ch = find_chunk(v, nch, u, before, goal);
-    }
-    if (ch < 0) return -1;
-    // a thread takes neighbouring entries: indices grow with the thread
-    float x[PER], y[PER];
-    double wt[PER], s = 0.0;
-    int i0;
-    load_pair<T, PER>(a, p, b, (ch * kThreads + tid) * U, 1, q, x, y, i0);
+        const int ch = find_strip(v, nch, u, before, goal);
+        if (ch < 0) return -1;
+        float x[PER], y[PER];
+        int i0;
+        load_pair<T, U>(a, p, b, (ch * kWaves + w) * 64 * U + lane, 64, false, x, y, i0);
+        double s = 0.0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        wt[i] = weight(p, x[i], y[i], i0 + i, q);
+        for (int i = 0; i < PER; ++i) s += weight(p, x[i], 0.0f, 0, false);
+        s = wave_sum(s);
+        if (lane == 0) total[w] = s;
+        __syncthreads();
+        double sum = before;
+        for (int i = 0; i < kWaves; ++i) {
+            if (!(total[i] > 0.0)) continue;
+            at = ch * kWaves + i;
+            before = sum;
+            sum += total[i];
+            if (sum > goal) break;
+        }
+        __syncthreads();
+        if (at < 0) return -1;
+    }
+    // a thread takes NU neighbouring units of the strip, as far as there are any: indices
+    // grow with the thread
+    const bool some = tid * NU < 64 * U;
+    float x[NU * N], y[NU * N];
+    double wt[NU * N], s = 0.0;
+    int i0;
+    load_pair<T, NU>(a, p, b, at * 64 * U + (some ? tid * NU : 0), 1, q, x, y, i0);
+#pragma unroll
+    for (int i = 0; i < NU * N; ++i) {
+        wt[i] = some ? weight(p, x[i], y[i], i0 + i, q) : 0.0;
         s += wt[i];
     }
     const double incl = scan(s);
     if (lane == 63) total[w] = incl;
     __syncthreads();
-    double at = before + (incl - s);
-    for (int i = 0; i < w; ++i) at += total[i];
+    double sum = before + (incl - s);
+    for (int i = 0; i < w; ++i) sum += total[i];
     int mine = 0x7FFFFFFF, end = -1;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        at += wt[i];
+    for (int i = 0; i < NU * N; ++i) {
+        sum += wt[i];
         if (wt[i] > 0.0) {
             end = i0 + i;
-            if (at > goal) mine = min(mine, i0 + i);
+            if (sum > goal) mine = min(mine, i0 + i);
         }
     }
     mine = wave_min(mine);
@@ -380,10 +404,9 @@ __device__ __forceinline__ int draw(const VerifyArgs &a, Pick p, int b, int nch,
 
 template <typename T, int PER>
 __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int nch, int rows, int across) {
-    constexpr int N = Row<T>::N;
+    constexpr int N = Row<T>::N, U = PER / N;
     __shared__ Joined all[2 * kMaxDrafts + 1];
     __shared__ Pick pick;
-    __shared__ double tmp[kWaves];
     __shared__ int done;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int b = blockIdx.x / nch, ch = blockIdx.x - b * nch;
@@ -448,23 +471,19 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int
         const bool q = has_q && p.acc < n;
         float x[PER], y[PER];
         int i0;
-        load_pair<T, PER>(a, p, b, ch * (kThreads * PER / N) + tid, kThreads, q, x, y, i0);
+        load_pair<T, U>(a, p, b, (ch * kWaves + w) * 64 * U + lane, 64, q, x, y, i0);
         double s = 0.0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) s += weight(p, x[i], y[i], i0 + (i / N) * kThreads * N + i % N, q);
+        for (int i = 0; i < PER; ++i) s += weight(p, x[i], y[i], i0 + (i / N) * 64 * N + i % N, q);
         s = wave_sum(s);
-        if (lane == 0) tmp[w] = s;
-        __syncthreads();
-        uint64_t *sums = (uint64_t *)chunk_sums(a, nch, rows) + (int64_t)b * nch;
-        if (tid == 0) {
-            s = 0.0;
-#pragma unroll
-            for (int i = 0; i < kWaves; ++i) s += tmp[i];
-            __hip_atomic_store(sums + ch, (uint64_t)__double_as_longlong(s), __ATOMIC_RELAXED,
+        uint64_t *sums = strip_sums(a, nch, rows) + (int64_t)b * nch * kWaves;
+        if (lane == 0)
+            __hip_atomic_store(sums + ch * kWaves + w, (uint64_t)__double_as_longlong(s), __ATOMIC_RELAXED,
                                __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (tid == 0)
             done = __hip_atomic_fetch_add(counter(a, nch, rows) + b, 1u, __ATOMIC_RELAXED,
                                           __HIP_MEMORY_SCOPE_AGENT) == (unsigned)nch - 1;
-        }
         __syncthreads();
         if (!done) return;
         token = draw<T, PER>(a, p, b, nch, q, sums, part + ((int64_t)p.acc * a.B + b) * nch);
@@ -510,7 +529,7 @@ hipError_t verify_by_size(const VerifyArgs &a, hipStream_t s) {
 size_t verify_bytes(int K, int B, int V) {
     // the larger chunk count of the two types and sizes
     const size_t nch = chunks(V, kThreads * kFew, 2);
-    return ((size_t)(2 * K + 1) * nch * sizeof(Part) + nch * sizeof(double) + sizeof(unsigned)) * B;
+    return ((size_t)(2 * K + 1) * nch * sizeof(Part) + nch * kWaves * sizeof(double) + sizeof(unsigned)) * B;
 }
 
 bool verify_grid_ok(int K, int B, int V) {
