@@ -14,6 +14,8 @@ from __future__ import annotations
 import array
 import ctypes
 import functools
+import itertools
+import operator
 from typing import Optional
 
 import torch
@@ -98,6 +100,11 @@ def load():
     return lib
 
 
+# The current device's number; the plain call checks each time that CUDA is
+# initialised, which an operand on it says already.
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _on_stream(fn):
     """Run with `stream`, and the first operand's device, current."""
     name = fn.__code__.co_varnames[0]
@@ -114,7 +121,7 @@ def _on_stream(fn):
                 raise ValueError("stream is on %s, the operands on %s" % (stream.device, first.device))
             with torch.cuda.stream(stream):
                 return fn(*args, **kw)
-        if first.get_device() != torch.cuda.current_device():
+        if first.get_device() != _device():
             with torch.cuda.device(first.device):
                 return fn(*args, **kw)
         return fn(*args, **kw)
@@ -459,17 +466,32 @@ def _row_out(t, name, dtype, shape, dev):
     return t, v
 
 
+def _state(t, name, shape, dev):
+    """Pointer of a contiguous float32 state, None for None."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _dense(t, name, torch.float32, shape, dev)  # says what is wrong
+    return t.data_ptr()
+
+
 def _gated(f, x, gate, lens):
-    dev = f.device
-    dt = _dt(f, "f")
-    if f.dim() != 3:
-        raise ValueError("f must be [T, B, D], got %s" % (tuple(f.shape),))
-    shape = f.shape
-    sf = _row(f, "f", f.dtype, shape, dev)
-    sx = None if x is None else _row(x, "x", f.dtype, shape, dev)
-    d = GatedDims(*shape)
-    lp = _dense(lens, "lens", torch.int32, torch.Size((d.B,)), dev)
-    return d, dt, _gate(gate), sf, sx, lp, shape, dev
+    dev, shape, dtype = f.device, f.shape, f.dtype
+    dt, gt = _dt(f, "f"), _GATES.get(gate)
+    if gt is None:
+        raise ValueError("gate must be 'logit' or 'decay', got %r" % (gate,))
+    if len(shape) != 3:
+        raise ValueError("f must be [T, B, D], got %s" % (tuple(shape),))
+    sf = _row(f, "f", dtype, shape, dev)
+    sx = None if x is None else _row(x, "x", dtype, shape, dev)
+    T, B, D = shape
+    lp = None if lens is None else _dense(lens, "lens", torch.int32, (B,), dev)
+    return (T, B, D), dt, gt, sf, sx, lp, shape, dev
+
+
+@functools.lru_cache(maxsize=256)
+def _gated_space(op, T, B, D, dt):
+    return workspace_size_gated(op, GatedDims(T, B, D), dt)
 
 
 def workspace_size_gated(op: int, dims: GatedDims, dtype_code: int) -> int:
@@ -486,14 +508,14 @@ def gated_fwd(f, x, h0=None, *, gate: str = "logit", lens=None, ws=None, out=Non
     token that counts); `out` is a dict with "h" (any view) and "hT" (may be h0)."""
     if x is None:
         raise ValueError("x is required")
-    d, dt, gt, sf, sx, lp, shape, dev = _gated(f, x, gate, lens)
-    state = torch.Size((d.B, d.D))
+    (T, B, D), dt, gt, sf, sx, lp, shape, dev = _gated(f, x, gate, lens)
+    state = (B, D)
     out = out or {}
-    p0 = _dense(h0, "h0", torch.float32, state, dev)
+    p0 = _state(h0, "h0", state, dev)
     h, sh = _row_out(out.get("h"), "h", f.dtype, shape, dev)
     hT = _new(out.get("hT"), "hT", torch.float32, state, dev)
-    ws, wp, wn = _space(ws, workspace_size_gated(OP_GATED_FWD, d, dt), dev)
-    _ok(load().rnn_gated_fwd(d, dt, gt, sf, sx, p0, lp, sh, hT.data_ptr(), wp, wn, _current(dev)),
+    ws, wp, wn = _space(ws, _gated_space(OP_GATED_FWD, T, B, D, dt), dev)
+    _ok(load().rnn_gated_fwd(GatedDims(T, B, D), dt, gt, sf, sx, p0, lp, sh, hT.data_ptr(), wp, wn, _current(dev)),
         "rnn_gated_fwd")
     return h, hT
 
@@ -505,15 +527,16 @@ def gated_step(f, x, h, *, gate: str = "logit", h_out=None, out=None):
     the new state)."""
     if x is None or h is None:
         raise ValueError("x and h are required")
-    d, dt, gt, sf, sx, _, shape, dev = _gated(f, x, gate, None)
-    if d.T != 1:
-        raise ValueError("gated_step takes one token, got T = %d" % d.T)
-    h_out = h if h_out is None else h_out
-    state = torch.Size((d.B, d.D))
-    p0 = _dense(h, "h", torch.float32, state, dev)
-    p1 = _dense(h_out, "h_out", torch.float32, state, dev)
+    (T, B, D), dt, gt, sf, sx, _, shape, dev = _gated(f, x, gate, None)
+    if T != 1:
+        raise ValueError("gated_step takes one token, got T = %d" % T)
+    p0 = _state(h, "h", (B, D), dev)
+    if h_out is None:
+        h_out, p1 = h, p0
+    else:
+        p1 = _state(h_out, "h_out", (B, D), dev)
     y, sy = _row_out(out, "out", f.dtype, shape, dev)
-    _ok(load().rnn_gated_step(d, dt, gt, sf, sx, p0, sy, p1, _current(dev)), "rnn_gated_step")
+    _ok(load().rnn_gated_step(GatedDims(T, B, D), dt, gt, sf, sx, p0, sy, p1, _current(dev)), "rnn_gated_step")
     return y, h_out
 
 
@@ -522,24 +545,27 @@ def gated_bwd(f, x, h, dh, h0=None, dhT=None, *, gate: str = "logit", lens=None,
     """Gradients of sum(dh * h) + sum(dhT * h_T), given gated_fwd's h: dict df, dx
     (in f's type) and dh0 float32.  x may be None with gate "decay"; `out` is a
     dict with "df", "dx" (any views) and "dh0" (may be dhT)."""
-    d, dt, gt, sf, sx, lp, shape, dev = _gated(f, x, gate, lens)
+    (T, B, D), dt, gt, sf, sx, lp, shape, dev = _gated(f, x, gate, lens)
     if x is None and gt == 0:
         raise ValueError("x is required with gate 'logit'")
     sh, sdh = _row(h, "h", f.dtype, shape, dev), _row(dh, "dh", f.dtype, shape, dev)
-    state = torch.Size((d.B, d.D))
-    p0 = _dense(h0, "h0", torch.float32, state, dev)
-    pT = _dense(dhT, "dhT", torch.float32, state, dev)
+    state = (B, D)
+    p0 = _state(h0, "h0", state, dev)
+    pT = _state(dhT, "dhT", state, dev)
     out = out or {}
     df, sdf = _row_out(out.get("df"), "df", f.dtype, shape, dev)
     dx, sdx = _row_out(out.get("dx"), "dx", f.dtype, shape, dev)
     dh0 = _new(out.get("dh0"), "dh0", torch.float32, state, dev)
-    ws, wp, wn = _space(ws, workspace_size_gated(OP_GATED_BWD, d, dt), dev)
-    _ok(load().rnn_gated_bwd(d, dt, gt, sf, sx, sh, sdh, p0, pT, lp, sdf, sdx, dh0.data_ptr(), wp,
+    ws, wp, wn = _space(ws, _gated_space(OP_GATED_BWD, T, B, D, dt), dev)
+    _ok(load().rnn_gated_bwd(GatedDims(T, B, D), dt, gt, sf, sx, sh, sdh, p0, pT, lp, sdf, sdx, dh0.data_ptr(), wp,
                              wn, _current(dev)), "rnn_gated_bwd")
     return {"df": df, "dx": dx, "dh0": dh0}
 
 
 # ------------------------------------------------ gradient norm, clipping
+_get_dtype, _get_shape = operator.attrgetter("dtype"), operator.attrgetter("shape")
+
+
 class GradList:
     """Gradients checked once, for programs whose gradient buffers stay where they
     are: `grads` are contiguous bfloat16 or float32 tensors of one device, `out`
@@ -556,25 +582,27 @@ class GradList:
         outs = grads if out is None else list(out)
         if len(outs) != len(grads):
             raise ValueError("%d outputs for %d gradients" % (len(outs), len(grads)))
-        flat = []
-        for t, o in zip(grads, outs):
-            code = _DT.get(t.dtype)
-            if code is None:
-                raise TypeError("gradients must be bfloat16 or float32, got %s" % t.dtype)
-            if t.device != dev or not t.is_contiguous():
-                raise ValueError("gradients must be contiguous tensors of one device")
-            at = to = t.data_ptr()
-            if o is not t:
-                if (o.dtype != t.dtype or o.shape != t.shape or o.device != dev
-                        or not o.is_contiguous()):
-                    raise ValueError("outputs must match their gradients")
-                to = o.data_ptr()
-            flat += (at, to, t.numel(), code)
-        written = [to for to, n in zip(flat[1::4], flat[2::4]) if n]
+        # a list at a time: half the time of a tensor at a time
+        n, at = list(map(torch.Tensor.numel, grads)), list(map(torch.Tensor.data_ptr, grads))
+        types = list(map(_get_dtype, grads))
+        codes = list(map(_DT.get, types))
+        if None in codes:
+            raise TypeError("gradients must be bfloat16 or float32, got %s" % types[codes.index(None)])
+        if set(map(torch.Tensor.get_device, grads)) != {dev.index} or not all(map(torch.Tensor.is_contiguous, grads)):
+            raise ValueError("gradients must be contiguous tensors of one device")
+        to = at
+        if out is not None:
+            if (list(map(_get_dtype, outs)) != types
+                    or list(map(_get_shape, outs)) != list(map(_get_shape, grads))
+                    or set(map(torch.Tensor.get_device, outs)) != {dev.index}
+                    or not all(map(torch.Tensor.is_contiguous, outs))):
+                raise ValueError("outputs must match their gradients")
+            to = list(map(torch.Tensor.data_ptr, outs))
+        written = [p for p, k in zip(to, n) if k]
         self.grads, self.out, self.count = grads, outs, len(grads)
         self.twice = len(set(written)) != len(written)
         # rnn_grad has four fields of 8 bytes (the type's upper half is padding)
-        self._rows = array.array("q", flat)
+        self._rows = array.array("q", itertools.chain.from_iterable(zip(at, to, n, codes)))
         self.array = self._rows.buffer_info()[0]
 
     def get_device(self):
@@ -630,6 +658,9 @@ def workspace_size_verify(K: int, B: int, V: int) -> int:
     return int(load().rnn_workspace_size_verify(K, B, V))
 
 
+_verify_space = functools.lru_cache(maxsize=256)(workspace_size_verify)
+
+
 @_on_stream
 def verify_drafts(logits, drafts, u, draft_logits=None, *, temperature=None, n_drafts=None, ws=None,
                   out=None):
@@ -641,29 +672,29 @@ def verify_drafts(logits, drafts, u, draft_logits=None, *, temperature=None, n_d
     temperature [B] float32 (0 or less: greedy), n_drafts [B] int32 (None: K).
     Returns (tokens [K+1,B] int32: accepted drafts, the drawn token, then -1;
     accepted [B] int32); `out` is a dict with "tokens" and "accepted"."""
-    dev = logits.device
-    _dev(logits, "logits", dev)
+    dev, shape = logits.device, logits.shape
     dt = _dt(logits, "logits")
-    if logits.dim() != 3 or 0 in logits.shape:
-        raise ValueError("logits must be [K+1, B, V], got %s" % (tuple(logits.shape),))
-    K, B, V = logits.shape[0] - 1, logits.shape[1], logits.shape[2]
-    sl = _row(logits, "logits", logits.dtype, logits.shape, dev)
+    if len(shape) != 3 or 0 in shape:
+        raise ValueError("logits must be [K+1, B, V], got %s" % (tuple(shape),))
+    R, B, V = shape
+    K = R - 1
+    sl = _row(logits, "logits", logits.dtype, shape, dev)
     view = sq = None
     if K:
-        if drafts is None or tuple(drafts.shape) != (K, B):
+        if drafts is None or drafts.shape != (K, B):
             raise ValueError("drafts must be [K, B] = [%d, %d]" % (K, B))
         view = _ids(drafts, dev)[2]
         if draft_logits is not None:
-            sq = _row(draft_logits, "draft_logits", logits.dtype, torch.Size((K, B, V)), dev)
+            sq = _row(draft_logits, "draft_logits", logits.dtype, (K, B, V), dev)
     if u is None:
         raise ValueError("u is required")
-    up = _dense(u, "u", torch.float32, torch.Size((K + 1, B)), dev)
-    tp = _dense(temperature, "temperature", torch.float32, torch.Size((B,)), dev)
-    np_ = _dense(n_drafts, "n_drafts", torch.int32, torch.Size((B,)), dev)
+    up = _state(u, "u", (R, B), dev)
+    tp = _state(temperature, "temperature", (B,), dev)
+    np_ = _dense(n_drafts, "n_drafts", torch.int32, (B,), dev)
     out = out or {}
-    tokens = _new(out.get("tokens"), "tokens", torch.int32, (K + 1, B), dev)
+    tokens = _new(out.get("tokens"), "tokens", torch.int32, (R, B), dev)
     accepted = _new(out.get("accepted"), "accepted", torch.int32, (B,), dev)
-    ws, wp, wn = _space(ws, workspace_size_verify(K, B, V), dev)
+    ws, wp, wn = _space(ws, _verify_space(K, B, V), dev)
     _ok(load().rnn_verify_drafts(K, B, V, dt, sl, view, sq, up, tp, np_, tokens.data_ptr(),
                                  accepted.data_ptr(), wp, wn, _current(dev)), "rnn_verify_drafts")
     return tokens, accepted
