@@ -6,8 +6,8 @@ linear attention with a decay for each head, logits, token log probabilities.
 Trains by plain gradient descent on a synthetic text and then continues a
 prompt token by token.  Every step of the model runs in the library's kernels
 (embed_fwd, lstm_fwd, input_proj, linattn_fwd / linattn_step, token_logprobs)
-and so do their gradients; the gradients of the two projections' weights are
-plain matrix products.  float32 throughout.
+and so do their gradients and the clipping of their norm; the gradients of the
+two projections' weights are plain matrix products.  float32 throughout.
 """
 import argparse
 import os
@@ -78,10 +78,9 @@ class RecurrentLM:
         losses = []
         for _ in range(steps):
             loss, d = self.gradients(ids, targets)
-            norm = torch.stack([t.norm() for t in d.values()]).norm()
-            scale = lr * torch.clamp(clip / norm, max=1.0)
+            g.clip_grads(list(d.values()), clip)
             for n, t in d.items():
-                self.p[n] -= scale * t
+                self.p[n] -= lr * t
             losses.append(loss)
         return [float(x) for x in losses]
 
