@@ -480,7 +480,6 @@ bool gated_grid_ok(const GatedDims &d, bool bf16) {
         if (!grid_ok(segments(d.T, vec) * (((int64_t)d.B * d.D + 64 * vec - 1) / (64 * vec)), kThreads)) return false;
     return true;
 }
-bool gated_step_grid_ok(const GatedDims &d) { return grid_ok(((int64_t)d.B * d.D + 255) / 256, 256); }
 
 hipError_t launch_gated_fwd(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, const float *h0,
                             const int *lens, SeqOut h, float *hT, void *ws, hipStream_t s) {

@@ -550,7 +550,8 @@ rnn_status rnn_linattn_bwd(const rnn_lin_dims *d, rnn_dtype dt, const rnn_seq *q
  * f, x, h and the gradients are sequences of D contiguous values for each
  * (t, b) in dtype dt: views at any strides (rnn_seq; rnn_seq_out for outputs),
  * so the halves of one projection and batch-first arrays are read and written
- * as they are.  Rows of an output must not overlap.  States [B][D] float32.
+ * as they are.  Rows of an output must not overlap each other, nor an input but
+ * where a call says so.  States [B][D] float32.
  * lens (may be NULL: T for all) [B]: only the first lens[b] tokens of row b, at
  * least 0 and at most T, count (other values are taken as the nearest of these).
  * Behind them the state stays as it is, h and the gradients df, dx are 0, and

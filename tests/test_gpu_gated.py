@@ -304,6 +304,24 @@ def test_gated_strides_past_32_bits():
         assert torch.equal(r[k], r1[k])
 
 
+def test_gated_offsets_past_32_bits():
+    """2.5e9 values: the last channels against a call on those alone, whose sums run
+    in the same order."""
+    T, B, D = 300, 128, 65536
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    f, x = (torch.empty((T, B, D), dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(2))
+    h, hT = g.gated_fwd(f, x)
+    r = g.gated_bwd(f, x, h, x)
+    for b, lo in ((0, 0), (63, 65472), (127, 65472)):
+        cut = [t[:, b:b + 1, lo:lo + 64].contiguous() for t in (f, x)]
+        h1, S1 = g.gated_fwd(*cut)
+        assert torch.equal(h[:, b:b + 1, lo:lo + 64], h1) and torch.equal(hT[b:b + 1, lo:lo + 64], S1)
+        r1 = g.gated_bwd(*cut, h1, cut[1])
+        for k in ("df", "dx"):
+            assert torch.equal(r[k][:, b:b + 1, lo:lo + 64], r1[k]), k
+        assert torch.equal(r["dh0"][b:b + 1, lo:lo + 64], r1["dh0"])
+
+
 def test_gated_inputs_shared_by_the_batch():
     """f and x broadcast over the batch (stride 0)."""
     f, x, dh, h0, dhT, _ = _case(2, 90, 4, 32, "f32", "logit")

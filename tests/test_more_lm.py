@@ -79,6 +79,16 @@ def test_gated_workspace_is_asked_for(op):
     assert g.workspace_size_gated(op, lm.GatedDims(1, 8, 64), 1) == 0
 
 
+@pytest.mark.parametrize("dt", [g.RNN_F32, g.RNN_BF16])
+@pytest.mark.parametrize("T,B,D", [(1024, 1 << 20, 1024), (1 << 15, 1 << 15, 1 << 15), (1 << 10, 1 << 20, 600)])
+def test_gated_launches_past_2_32_threads(T, B, D, dt):
+    lib, d, s = lm.load(), lm.GatedDims(T, B, D), [_seq()] * 2
+    assert T * B <= 1 << 30 and B * D <= 1 << 30
+    assert lib.rnn_gated_fwd(d, dt, 0, *s, None, None, _seq(), None, FAKE, BIG, None) == UNS
+    assert lib.rnn_gated_bwd(d, dt, 0, *s, *s, None, None, None, *s, None, FAKE, BIG, None) == UNS
+    assert g.workspace_size_gated(g.OP_GATED_FWD, d, dt) == 0
+
+
 def _list(*rows):
     return (lm._Grad * len(rows))(*rows)
 
