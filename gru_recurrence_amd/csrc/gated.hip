@@ -9,8 +9,8 @@
 // kind of recurrence from the end: e_t = a_t (dh_t + e_{t+1}).
 //
 // Every operand is read once and every output written once; memory bounds it.  A
-// workgroup takes a tile of kWaves S steps (a wave S of them) by 64 lanes of VEC
-// channels, as loaded, in registers.  Each thread composes its S steps; a segment's
+// workgroup takes a tile of 64 lanes of VEC channels by kWaves S steps (a wave S of
+// them), as loaded, in registers.  Each thread composes its S steps; a segment's
 // total goes to memory, the carry into it is composed from the totals of the segments
 // before it, and the steps run again from the carry, from the same registers (the
 // gates are computed twice: kept in float32 they cost the waves that hide the join).
@@ -33,6 +33,7 @@
 // for the calls' 24, 70 and 51; workgroups that stay and load their next tile while
 // they wait for a carry, 34, 87 and 76 (half as many fit).
 #include <algorithm>
+#include <type_traits>
 
 #include "host.h"
 #include "lm.h"
@@ -43,6 +44,7 @@ namespace lm {
 namespace {
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;
+constexpr int kNarrow = 16;  // lanes along the channels where one workgroup has all of a short sequence
 constexpr int kGroup = 16;
 constexpr int kHead = 128;           // bytes before the counters: the status word
 
@@ -84,34 +86,51 @@ __device__ __forceinline__ void place(const Cut &k, int &seg, int &tile) {
     }
 }
 
-// From the threads' own (A, B) to the state that each begins with.  agg, car: LDS,
-// [kWaves][64 VEC].  Returns the state before the thread's first step in h.
-// start: the recurrence's initial state, in the first wave of segment 0.  Nobody
-// else reads that, and all that follows waits for what this wave makes of it, so
+// Parts along time of a workgroup with LN lanes along the channels, and a thread's.
+template <int LN>
+constexpr int parts() { return kThreads / LN; }
+template <int LN>
+__device__ __forceinline__ int part() {
+    const int p = threadIdx.x / LN;
+    return LN == 64 ? __builtin_amdgcn_readfirstlane(p) : p;
+}
+
+// From the threads' own (A, B) to the state that each begins with.  agg, car: LDS.
+// Returns the state before the thread's first step in h.
+// start: the recurrence's initial state, in the first part of segment 0.  Nobody
+// else reads that, and all that follows waits for what this part makes of it, so
 // the last state may be written over the first.
-template <int VEC>
+template <int VEC, int LN>
 __device__ __forceinline__ void join(const Cut &k, int seg, int c0, const float *A, const float *B,
-                                     const float *start, float2 (*agg)[64 * VEC],
-                                     float2 (*car)[64 * VEC], float *h) {
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), at = lane * VEC;
+                                     const float *start, float2 (*agg)[LN * VEC],
+                                     float2 (*car)[LN * VEC], float *h) {
+    const int lane = threadIdx.x & (LN - 1), w = part<LN>(), at = lane * VEC;
     const bool first = seg == 0 && w == 0;
 #pragma unroll
     for (int v = 0; v < VEC; ++v)
         agg[w][at + v] = first ? make_float2(0.0f, apply(A[v], B[v], start[v])) : make_float2(A[v], B[v]);
     lds_barrier();
-    // the steps of this workgroup before this wave
+    // the steps of this workgroup before this part
     float pA[VEC], pB[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) pA[v] = 1.0f, pB[v] = first ? start[v] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWaves - 1; ++i) {
-        if (i >= w) break;
+    for (int i = 0; i < parts<LN>() - 1; ++i) {
+        if (i >= w) {
+            if (LN == 64) break;
+            continue;
+        }
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             const float2 q = agg[i][at + v];
             pB[v] = apply(q.x, q.y, pB[v]);
             pA[v] *= q.x;
         }
+    }
+    if (LN < 64) {  // a single segment
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) h[v] = pB[v];
+        return;
     }
     const bool last = seg == k.nseg - 1;
     float tA[VEC], tB[VEC];  // the whole segment, in the last wave
@@ -225,18 +244,18 @@ __device__ __forceinline__ void forget(V &q) {
     }
 }
 
-template <typename T, bool LOGIT, int VEC, int S>
+template <typename T, bool LOGIT, int VEC, int S, int LN>
 __global__ __launch_bounds__(kThreads) void gated_fwd_kernel(FwdArgs a) {
     typedef Unit<T, VEC> V;
-    __shared__ float2 agg[kWaves][64 * VEC], car[kWaves][64 * VEC];
+    __shared__ float2 agg[parts<LN>()][LN * VEC], car[LN == 64 ? kWaves : 1][LN * VEC];
     const Cut &k = a.k;
     int seg, tile;
     place(k, seg, tile);
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c0 = (tile * 64 + lane) * VEC, c = min(c0, k.C - VEC);
+    const int lane = threadIdx.x & (LN - 1), w = part<LN>();
+    const int c0 = (tile * LN + lane) * VEC, c = min(c0, k.C - VEC);
     const int b = c / k.D, i = c - b * k.D;
     const int len = a.lens ? min(max(a.lens[b], 0), k.T) : k.T;
-    const int t0 = (seg * kWaves + w) * S;  // the grid's limit keeps this in 31 bits
+    const int t0 = (seg * parts<LN>() + w) * S;  // the grid's limit keeps this in 31 bits
     V fr[S], xr[S];
     if (__any(t0 < len)) {
         const T *fp = (const T *)a.f.p + (int64_t)b * a.f.sb + i, *xp = (const T *)a.x.p + (int64_t)b * a.x.sb + i;
@@ -268,7 +287,7 @@ __global__ __launch_bounds__(kThreads) void gated_fwd_kernel(FwdArgs a) {
         }
 #pragma unroll
     for (int s = 0; s < S; ++s) forget(fr[s]), forget(xr[s]);
-    join<VEC>(k, seg, c0, A, B, start, agg, car, h);
+    join<VEC, LN>(k, seg, c0, A, B, start, agg, car, h);
     T *out = (T *)a.h.p + (int64_t)b * a.h.sb + i;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
@@ -284,7 +303,7 @@ __global__ __launch_bounds__(kThreads) void gated_fwd_kernel(FwdArgs a) {
         }
         if (t0 + s < k.T && c0 < k.C) *(V *)(out + (int64_t)(t0 + s) * a.h.st) = o;
     }
-    if (a.hT && seg == k.nseg - 1 && w == kWaves - 1 && c0 < k.C) {
+    if (a.hT && seg == k.nseg - 1 && w == parts<LN>() - 1 && c0 < k.C) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) a.hT[c + v] = h[v];
     }
@@ -313,18 +332,18 @@ struct BwdArgs {
 
 // Backwards in time: step s of a thread is t = T - 1 - (first + s).  The state is
 // e = a_{t+1} g_{t+1}; g_t = dh_t + e, e' = a_t g_t.
-template <typename T, bool LOGIT, int VEC, int S>
+template <typename T, bool LOGIT, int VEC, int S, int LN>
 __global__ __launch_bounds__(kThreads) void gated_bwd_kernel(BwdArgs a) {
     typedef Unit<T, VEC> V;
-    __shared__ float2 agg[kWaves][64 * VEC], car[kWaves][64 * VEC];
+    __shared__ float2 agg[parts<LN>()][LN * VEC], car[LN == 64 ? kWaves : 1][LN * VEC];
     const Cut &k = a.k;
     int seg, tile;
     place(k, seg, tile);
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c0 = (tile * 64 + lane) * VEC, c = min(c0, k.C - VEC);
+    const int lane = threadIdx.x & (LN - 1), w = part<LN>();
+    const int c0 = (tile * LN + lane) * VEC, c = min(c0, k.C - VEC);
     const int b = c / k.D, i = c - b * k.D;
     const int len = a.lens ? min(max(a.lens[b], 0), k.T) : k.T;
-    const int t0 = k.T - 1 - (seg * kWaves + w) * S;  // the thread's last step in time; may be below 0
+    const int t0 = k.T - 1 - (seg * parts<LN>() + w) * S;  // the thread's last step in time; may be below 0
     V fr[S], dr[S], xr[S], hr[S];
     if (__any(t0 - (S - 1) < len && t0 >= 0)) {
         const T *fp = (const T *)a.f.p + (int64_t)b * a.f.sb + i, *dp = (const T *)a.dh.p + (int64_t)b * a.dh.sb + i;
@@ -363,7 +382,7 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_kernel(BwdArgs a) {
         }
 #pragma unroll
     for (int s = 0; s < S; ++s) forget(fr[s]), forget(dr[s]);
-    join<VEC>(k, seg, c0, A, B, start, agg, car, e);
+    join<VEC, LN>(k, seg, c0, A, B, start, agg, car, e);
     T *of = (T *)a.df.p + (int64_t)b * a.df.sb + i, *ox = (T *)a.dx.p + (int64_t)b * a.dx.sb + i;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
@@ -395,7 +414,7 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_kernel(BwdArgs a) {
             *(V *)(ox + (int64_t)t * a.dx.st) = vx;
         }
     }
-    if (a.dh0 && seg == k.nseg - 1 && w == kWaves - 1 && c0 < k.C) {
+    if (a.dh0 && seg == k.nseg - 1 && w == parts<LN>() - 1 && c0 < k.C) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) a.dh0[c + v] = e[v];
     }
@@ -406,14 +425,33 @@ __global__ __launch_bounds__(256) void gated_clear_kernel(uint4 *p, int64_t n) {
         p[i] = make_uint4(0, 0, 0, 0);
 }
 
-// Steps of a thread: with two channels to a lane 8, with one 16.  Longer segments have
-// fewer words to exchange (32768 x 768 float32: 79 us with 8 steps, 70 with 16) until
-// their registers leave too few waves to hide a join.
-constexpr int steps(int vec) { return vec == 2 ? 8 : 16; }
+// How a call is laid out: channels of a lane, steps of a thread, lanes along the channels.
+struct Shape {
+    int vec, steps, lanes;
+};
 
-int64_t segments(int T, int vec) {
-    const int tile = kWaves * steps(vec);
-    return ((int64_t)T + tile - 1) / tile;
+int64_t tiles(const GatedDims &d, const Shape &p) {
+    const int64_t wide = (int64_t)p.vec * p.lanes;
+    return ((int64_t)d.B * d.D + wide - 1) / wide;
+}
+int64_t segments(int T, const Shape &p) {
+    const int64_t tile = (int64_t)(kThreads / p.lanes) * p.steps;
+    return (T + tile - 1) / tile;
+}
+
+// One channel to a lane: 16 steps a thread.  A short sequence of few values, which its
+// launches bound, goes to workgroups that have all of it, and needs no words cleared
+// (500 x 4 x 768 float32 13 us for 16, 500 x 16 x 768 however 27 for 18: narrow rows).
+// Two (bf16): 8 steps up to eight workgroups a CU, and 16 past that or where one segment
+// then does: longer segments have fewer words to exchange but leave fewer waves to hide a join (1024 x 16 x 768:
+// 24 and 26 us, 32768 x 1 x 768: 73 and 55, 8192 x 16 x 2048: 386 and 337).
+Shape shape(const GatedDims &d, bool two) {
+    const int64_t C = (int64_t)d.B * d.D;
+    const Shape one{1, 16, 64}, narrow{1, 16, kNarrow}, few{2, 8, 64}, many{2, 16, 64};
+    if (segments(d.T, one) > 1 && segments(d.T, narrow) == 1 && d.T * C <= (1 << 21)) return narrow;
+    if (!two) return one;
+    const bool alone = segments(d.T, few) > 1 && segments(d.T, many) == 1;
+    return !alone && segments(d.T, few) * tiles(d, few) <= 8 * 256 ? few : many;
 }
 int64_t group_of(int64_t nseg) {
     if (nseg <= kGroup) return nseg;
@@ -426,13 +464,12 @@ int64_t group_of(int64_t nseg) {
 int pitch(int64_t ntile) { return ntile <= 1024 ? 32 : 1; }
 int64_t counter_words(int64_t ntile) { return (ntile * pitch(ntile) + 31) / 32 * 32; }
 
-// vec: channels of a lane
-Cut cut(const GatedDims &d, int vec, void *ws) {
+Cut cut(const GatedDims &d, const Shape &p, void *ws) {
     Cut k{};
     k.T = d.T, k.D = d.D, k.C = d.B * d.D;
-    k.nseg = (int)segments(d.T, vec);
+    k.nseg = (int)segments(d.T, p);
     k.G = (int)group_of(k.nseg);
-    k.ntile = (k.C + 64 * vec - 1) / (64 * vec);
+    k.ntile = (int)tiles(d, p);
     k.pitch = pitch(k.ntile);
     k.spins = host::spin_limit();
     k.flag = (unsigned *)ws;
@@ -466,39 +503,61 @@ bool pairs(int D, size_t e, std::initializer_list<LinSeq> seqs) {
 }
 LinSeq in(const SeqOut &o) { return LinSeq{o.p, o.st, o.sb}; }
 
+// go(type, gate, channels of a lane, steps, lanes) of a call, as values of their types.
+template <int V>
+using Int = std::integral_constant<int, V>;
+template <typename F>
+void by_shape(const Shape &p, bool bf16, bool logit, F go) {
+    auto gate = [&](auto type, auto vec, auto steps, auto lanes) {
+        if (logit)
+            go(type, std::true_type{}, vec, steps, lanes);
+        else
+            go(type, std::false_type{}, vec, steps, lanes);
+    };
+    auto one = [&](auto type) {
+        if (p.lanes == kNarrow)
+            gate(type, Int<1>{}, Int<16>{}, Int<kNarrow>{});
+        else
+            gate(type, Int<1>{}, Int<16>{}, Int<64>{});
+    };
+    if (!bf16)
+        one(float{});
+    else if (p.vec == 1)
+        one(uint16_t{});
+    else if (p.steps == 8)
+        gate(uint16_t{}, Int<2>{}, Int<8>{}, Int<64>{});
+    else
+        gate(uint16_t{}, Int<2>{}, Int<16>{}, Int<64>{});
+}
+
 }  // namespace
 
 size_t gated_bytes(const GatedDims &d, bool bf16) {
     // a bf16 call may have either number of channels to a lane
     int64_t n = 0;
-    for (int vec = 1; vec <= (bf16 ? 2 : 1); ++vec) n = std::max(n, space(cut(d, vec, nullptr)));
+    for (int two = 0; two <= (bf16 ? 1 : 0); ++two) n = std::max(n, space(cut(d, shape(d, two), nullptr)));
     return (size_t)n;
 }
 
 bool gated_grid_ok(const GatedDims &d, bool bf16) {
-    for (int vec = 1; vec <= (bf16 ? 2 : 1); ++vec)
-        if (!grid_ok(segments(d.T, vec) * (((int64_t)d.B * d.D + 64 * vec - 1) / (64 * vec)), kThreads)) return false;
+    for (int two = 0; two <= (bf16 ? 1 : 0); ++two) {
+        const Shape p = shape(d, two);
+        if (!grid_ok(segments(d.T, p) * tiles(d, p), kThreads)) return false;
+    }
     return true;
 }
 
 hipError_t launch_gated_fwd(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, const float *h0,
                             const int *lens, SeqOut h, float *hT, void *ws, hipStream_t s) {
-    const int vec = bf16 && pairs(d.D, 2, {f, x, in(h)}) ? 2 : 1;
-    const FwdArgs a{cut(d, vec, ws), f, x, h0, lens, h, hT};
+    const Shape p = shape(d, bf16 && pairs(d.D, 2, {f, x, in(h)}));
+    const FwdArgs a{cut(d, p, ws), f, x, h0, lens, h, hT};
     const hipError_t e = clear(a.k, s);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)((int64_t)a.k.nseg * a.k.ntile)), thr(kThreads);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, thr, 0, s, a); };
-    if (!bf16) {
-        if (d.logit) go(gated_fwd_kernel<float, true, 1, steps(1)>);
-        else go(gated_fwd_kernel<float, false, 1, steps(1)>);
-    } else if (vec == 2) {
-        if (d.logit) go(gated_fwd_kernel<uint16_t, true, 2, steps(2)>);
-        else go(gated_fwd_kernel<uint16_t, false, 2, steps(2)>);
-    } else {
-        if (d.logit) go(gated_fwd_kernel<uint16_t, true, 1, steps(1)>);
-        else go(gated_fwd_kernel<uint16_t, false, 1, steps(1)>);
-    }
+    by_shape(p, bf16, d.logit, [&](auto type, auto logit, auto vec, auto steps, auto lanes) {
+        go(gated_fwd_kernel<decltype(type), logit.value, vec.value, steps.value, lanes.value>);
+    });
     return hipGetLastError();
 }
 
@@ -506,13 +565,10 @@ hipError_t launch_gated_step(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, 
                              SeqOut y, float *h_out, hipStream_t s) {
     const dim3 grid((unsigned)(((int64_t)d.B * d.D + 255) / 256)), thr(256);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, thr, 0, s, d, f, x, h, y, h_out); };
-    if (bf16) {
-        if (d.logit) go(gated_step_kernel<uint16_t, true>);
-        else go(gated_step_kernel<uint16_t, false>);
-    } else {
-        if (d.logit) go(gated_step_kernel<float, true>);
-        else go(gated_step_kernel<float, false>);
-    }
+    if (bf16 && d.logit) go(gated_step_kernel<uint16_t, true>);
+    if (bf16 && !d.logit) go(gated_step_kernel<uint16_t, false>);
+    if (!bf16 && d.logit) go(gated_step_kernel<float, true>);
+    if (!bf16 && !d.logit) go(gated_step_kernel<float, false>);
     return hipGetLastError();
 }
 
@@ -520,22 +576,15 @@ hipError_t launch_gated_bwd(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, L
                             const float *h0, const float *dhT, const int *lens, SeqOut df, SeqOut dx,
                             float *dh0, void *ws, hipStream_t s) {
     if (!d.logit) x = f;  // not read
-    const int vec = bf16 && pairs(d.D, 2, {f, x, h, dh, in(df), in(dx)}) ? 2 : 1;
-    const BwdArgs a{cut(d, vec, ws), f, x, h, dh, h0, dhT, lens, df, dx, dh0};
+    const Shape p = shape(d, bf16 && pairs(d.D, 2, {f, x, h, dh, in(df), in(dx)}));
+    const BwdArgs a{cut(d, p, ws), f, x, h, dh, h0, dhT, lens, df, dx, dh0};
     const hipError_t e = clear(a.k, s);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)((int64_t)a.k.nseg * a.k.ntile)), thr(kThreads);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, thr, 0, s, a); };
-    if (!bf16) {
-        if (d.logit) go(gated_bwd_kernel<float, true, 1, steps(1)>);
-        else go(gated_bwd_kernel<float, false, 1, steps(1)>);
-    } else if (vec == 2) {
-        if (d.logit) go(gated_bwd_kernel<uint16_t, true, 2, steps(2)>);
-        else go(gated_bwd_kernel<uint16_t, false, 2, steps(2)>);
-    } else {
-        if (d.logit) go(gated_bwd_kernel<uint16_t, true, 1, steps(1)>);
-        else go(gated_bwd_kernel<uint16_t, false, 1, steps(1)>);
-    }
+    by_shape(p, bf16, d.logit, [&](auto type, auto logit, auto vec, auto steps, auto lanes) {
+        go(gated_bwd_kernel<decltype(type), logit.value, vec.value, steps.value, lanes.value>);
+    });
     return hipGetLastError();
 }
 

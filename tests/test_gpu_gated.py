@@ -305,21 +305,57 @@ def test_gated_strides_past_32_bits():
 
 
 def test_gated_offsets_past_32_bits():
-    """2.5e9 values: the last channels against a call on those alone, whose sums run
-    in the same order."""
+    """2.5e9 values: some rows against calls on those alone, which are cut the same
+    way, so that their sums run in the same order."""
     T, B, D = 300, 128, 65536
     gen = torch.Generator(device="cuda").manual_seed(0)
     f, x = (torch.empty((T, B, D), dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(2))
     h, hT = g.gated_fwd(f, x)
     r = g.gated_bwd(f, x, h, x)
-    for b, lo in ((0, 0), (63, 65472), (127, 65472)):
-        cut = [t[:, b:b + 1, lo:lo + 64].contiguous() for t in (f, x)]
+    for b in (0, 60, 120):
+        rows = slice(b, b + 8)
+        cut = [t[:, rows].contiguous() for t in (f, x)]
         h1, S1 = g.gated_fwd(*cut)
-        assert torch.equal(h[:, b:b + 1, lo:lo + 64], h1) and torch.equal(hT[b:b + 1, lo:lo + 64], S1)
+        assert torch.equal(h[:, rows], h1) and torch.equal(hT[rows], S1)
         r1 = g.gated_bwd(*cut, h1, cut[1])
         for k in ("df", "dx"):
-            assert torch.equal(r[k][:, b:b + 1, lo:lo + 64], r1[k]), k
-        assert torch.equal(r["dh0"][b:b + 1, lo:lo + 64], r1["dh0"])
+            assert torch.equal(r[k][:, rows], r1[k]), k
+        assert torch.equal(r["dh0"][rows], r1["dh0"])
+
+
+@pytest.mark.parametrize("D,layout", [(258, "fused"), (257, "dense")])
+def test_gated_many_values_bf16(D, layout):
+    """A call of many workgroups, with and without pairs of channels, against the
+    definition in 64 bits on the device: bounds as in gated_ref, where a step's share
+    u ((2 |f| + 7) s (|x| + M) + 4 M) stays below 16 u M' with M' = M + s |x| (|f| < 9,
+    s (2 |f| + 7) < 9), and the sum over steps forgets at a's pace: carried along."""
+    T, B = 4200, 16
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    f = (torch.randn((T, B, D), generator=gen, device="cuda") + 2.0).bfloat16()
+    x, dh = (torch.randn((T, B, D), generator=gen, device="cuda").bfloat16() for _ in range(2))
+    h0, dhT = (torch.randn((B, D), generator=gen, device="cuda") for _ in range(2))
+    f, x, dh = (_view(t, layout) for t in (f, x, dh))
+    assert f.float().abs().max() < 9
+    h, hT = g.gated_fwd(f, x, h0)
+    r = g.gated_bwd(f, x, h, dh, h0, dhT)
+    a, s = torch.sigmoid(f.double()), torch.sigmoid(-f.double())
+    u, S, M = 2.0 ** -24, h0.double(), h0.double().abs()
+    E = torch.zeros_like(S)
+    ok = torch.ones((), dtype=torch.bool, device="cuda")
+    for t in range(T):
+        xt = x[t].double()
+        S, M = a[t] * S + s[t] * xt, a[t] * M + s[t] * xt.abs()
+        E = a[t] * E + 16 * u * (M + s[t] * xt.abs())
+        ok &= ((h[t].double() - S).abs() <= E + 2.0 ** -8 * (S.abs() + E)).all()
+    assert ok and ((hT - S).abs() <= E).all()
+    e, m, E = dhT.double(), dhT.double().abs(), torch.zeros_like(S)
+    for t in range(T - 1, -1, -1):
+        gt, mt, Et = e + dh[t].double(), m + dh[t].double().abs(), E
+        Et = Et + u * mt
+        dx, bx = s[t] * gt, s[t] * (Et + 26 * u * mt)
+        ok &= ((r["dx"][t].double() - dx).abs() <= bx + 2.0 ** -8 * (dx.abs() + bx)).all()
+        e, m, E = a[t] * gt, a[t] * mt, a[t] * Et + 16 * u * mt
+    assert ok and ((r["dh0"] - e).abs() <= E).all()
 
 
 def test_gated_inputs_shared_by_the_batch():
