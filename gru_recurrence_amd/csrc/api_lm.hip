@@ -241,7 +241,8 @@ size_t rnn_workspace_size_gated(rnn_gated_op op, const rnn_gated_dims *d, rnn_dt
     if (!gated_dims_ok(d) || !dtype_ok(dt) || !gated_width_ok(d)) return 0;
     if (op != RNN_OP_GATED_FWD && op != RNN_OP_GATED_BWD) return 0;
     const lm::GatedDims n = gated_dims(d, RNN_GATE_LOGIT);
-    return lm::gated_grid_ok(n, dt == RNN_BF16) ? lm::gated_bytes(n, dt == RNN_BF16) : 0;
+    const bool bwd = op == RNN_OP_GATED_BWD;
+    return lm::gated_grid_ok(n, dt == RNN_BF16, bwd) ? lm::gated_bytes(n, dt == RNN_BF16, bwd) : 0;
 }
 
 rnn_status rnn_gated_fwd(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, const rnn_seq *f,
@@ -254,8 +255,8 @@ rnn_status rnn_gated_fwd(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, c
     for (const void *p : ps)
         if (!aligned16(p)) return RNN_ERR_INVALID_ARG;
     const lm::GatedDims n = gated_dims(d, gate);
-    if (!gated_width_ok(d) || !lm::gated_grid_ok(n, dt == RNN_BF16)) return RNN_ERR_UNSUPPORTED;
-    const size_t need = lm::gated_bytes(n, dt == RNN_BF16);
+    if (!gated_width_ok(d) || !lm::gated_grid_ok(n, dt == RNN_BF16, false)) return RNN_ERR_UNSUPPORTED;
+    const size_t need = lm::gated_bytes(n, dt == RNN_BF16, false);
     if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;
     return done(lm::launch_gated_fwd(n, dt == RNN_BF16, seq_of(f), seq_of(x), h0, lens, out_of(h), hT,
                                      ws, stream));
@@ -289,8 +290,8 @@ rnn_status rnn_gated_bwd(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, c
     for (const void *p : ps)
         if (!aligned16(p)) return RNN_ERR_INVALID_ARG;
     const lm::GatedDims n = gated_dims(d, gate);
-    if (!gated_width_ok(d) || !lm::gated_grid_ok(n, dt == RNN_BF16)) return RNN_ERR_UNSUPPORTED;
-    const size_t need = lm::gated_bytes(n, dt == RNN_BF16);
+    if (!gated_width_ok(d) || !lm::gated_grid_ok(n, dt == RNN_BF16, true)) return RNN_ERR_UNSUPPORTED;
+    const size_t need = lm::gated_bytes(n, dt == RNN_BF16, true);
     if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;
     return done(lm::launch_gated_bwd(n, dt == RNN_BF16, seq_of(f), seq_or_none(x), seq_of(h), seq_of(dh),
                                      h0, dhT, lens, out_of(df), out_of(dx), dh0, ws, stream));

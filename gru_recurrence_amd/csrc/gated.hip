@@ -66,9 +66,6 @@ __device__ __forceinline__ uint64_t pack(float A, float B) {
 __device__ __forceinline__ void publish(uint64_t *p, float A, float B) {
     __hip_atomic_store(p, pack(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// A h + B; a state of 0 takes no part, whatever the product of the decays is.
-__device__ __forceinline__ float apply(float A, float B, float h) { return h == 0.0f ? B : fmaf(A, h, B); }
-
 // 1 - sigmoid(f)
 __device__ __forceinline__ float shut(float f) { return rcp_fast(1.0f + exp_fast(f)); }
 
@@ -108,7 +105,7 @@ __device__ __forceinline__ void join(const Cut &k, int seg, int c0, const float 
     const bool first = seg == 0 && w == 0;
 #pragma unroll
     for (int v = 0; v < VEC; ++v)
-        agg[w][at + v] = first ? make_float2(0.0f, apply(A[v], B[v], start[v])) : make_float2(A[v], B[v]);
+        agg[w][at + v] = first ? make_float2(0.0f, fmaf(A[v], start[v], B[v])) : make_float2(A[v], B[v]);
     lds_barrier();
     // the steps of this workgroup before this part
     float pA[VEC], pB[VEC];
@@ -123,7 +120,7 @@ __device__ __forceinline__ void join(const Cut &k, int seg, int c0, const float 
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             const float2 q = agg[i][at + v];
-            pB[v] = apply(q.x, q.y, pB[v]);
+            pB[v] = fmaf(q.x, pB[v], q.y);
             pA[v] *= q.x;
         }
     }
@@ -137,7 +134,7 @@ __device__ __forceinline__ void join(const Cut &k, int seg, int c0, const float 
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
         tA[v] = seg == 0 ? 0.0f : pA[v] * A[v];
-        tB[v] = apply(A[v], B[v], pB[v]);
+        tB[v] = fmaf(A[v], pB[v], B[v]);
         if (w == kWaves - 1 && !last && c0 + v < k.C) publish(k.word + (int64_t)seg * k.C + c0 + v, tA[v], tB[v]);
     }
     if (seg == 0) {
@@ -190,7 +187,7 @@ __device__ __forceinline__ void join(const Cut &k, int seg, int c0, const float 
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     const float a = __uint_as_float((uint32_t)(q[i][v] >> 32));
-                    cB[v] = apply(a, __uint_as_float((uint32_t)q[i][v]), cB[v]);
+                    cB[v] = fmaf(a, cB[v], __uint_as_float((uint32_t)q[i][v]));
                     cA[v] *= a;
                 }
             }
@@ -199,25 +196,29 @@ __device__ __forceinline__ void join(const Cut &k, int seg, int c0, const float 
     for (int v = 0; v < VEC; ++v) car[w][at + v] = make_float2(cA[v], cB[v]);
     lds_barrier();
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) h[v] = 0.0f, cA[v] = 1.0f, cB[v] = 0.0f;
+    for (int v = 0; v < VEC; ++v) {
+        h[v] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
+        for (int i = 0; i < kWaves; ++i) {
+            const float2 q = car[i][at + v];
+            h[v] = fmaf(q.x, h[v], q.y);
+        }
+    }
+    if (w == kWaves - 1 && !last && inside == k.G - 1) {  // the group's total
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-            const float2 q = car[i][at + v];
-            h[v] = apply(q.x, q.y, h[v]);
-            if (i >= half) {
-                cB[v] = apply(q.x, q.y, cB[v]);
-                cA[v] *= q.x;
+            float gA = 1.0f, gB = 0.0f;
+            for (int i = half; i < kWaves; ++i) {
+                const float2 q = car[i][at + v];
+                gB = fmaf(q.x, gB, q.y);
+                gA *= q.x;
             }
+            if (c0 + v < k.C)
+                publish(k.gword + (int64_t)group * k.C + c0 + v, group ? tA[v] * gA : 0.0f, fmaf(tA[v], gB, tB[v]));
         }
     }
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-        if (w == kWaves - 1 && !last && inside == k.G - 1 && c0 + v < k.C)
-            publish(k.gword + (int64_t)group * k.C + c0 + v, group ? tA[v] * cA[v] : 0.0f, apply(tA[v], tB[v], cB[v]));
-        h[v] = apply(pA[v], pB[v], h[v]);
-    }
+    for (int v = 0; v < VEC; ++v) h[v] = fmaf(pA[v], h[v], pB[v]);
 }
 
 struct FwdArgs {
@@ -229,7 +230,7 @@ struct FwdArgs {
     float *hT;
 };
 
-// Makes the compiler take a register's value as new, so that what was computed from it
+// Makes the compiler take a register's value as new, so that its conversion to float32
 // is computed again where it is needed again, in place of being kept.
 template <typename V>
 __device__ __forceinline__ void forget(V &q) {
@@ -244,8 +245,31 @@ __device__ __forceinline__ void forget(V &q) {
     }
 }
 
+// f(true_type) or f(false_type): the steps of a tile that counts whole need no masks.
+template <typename F>
+__device__ __forceinline__ void by_flag(bool flag, F f) {
+    if (flag)
+        f(std::true_type{});
+    else
+        f(std::false_type{});
+}
+
+// Values in the sequence's type; two at once to bf16.
+template <typename T, int VEC>
+__device__ __forceinline__ Unit<T, VEC> rounded(const float *v) {
+    Unit<T, VEC> o;
+    if constexpr (sizeof(T) == 2 && VEC == 2) {
+        typedef float f2 __attribute__((ext_vector_type(2)));
+        typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(Unit<T, VEC>, __builtin_convertvector((f2){v[0], v[1]}, b2));
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) o.v[i] = from_f32<T>(v[i]);
+    return o;
+}
+
 template <typename T, bool LOGIT, int VEC, int S, int LN>
-__global__ __launch_bounds__(kThreads) void gated_fwd_kernel(FwdArgs a) {
+__global__ __launch_bounds__(kThreads, 4) void gated_fwd_kernel(FwdArgs a) {
     typedef Unit<T, VEC> V;
     __shared__ float2 agg[parts<LN>()][LN * VEC], car[LN == 64 ? kWaves : 1][LN * VEC];
     const Cut &k = a.k;
@@ -266,43 +290,51 @@ __global__ __launch_bounds__(kThreads) void gated_fwd_kernel(FwdArgs a) {
             xr[s] = *(const V *)(xp + t * a.x.st);
         }
     }
-    const bool full = __all(t0 + S <= len);
-    float A[VEC], B[VEC], h[VEC], start[VEC];
+    // what a step keeps beside x: u (logit) or a (decay)
+    float g[S][VEC], A[VEC], B[VEC], h[VEC], start[VEC];
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float fv = to_f32<T>(fr[s].v[v]);
+            g[s][v] = LOGIT ? shut(fv) : fv;
+        }
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
         A[v] = 1.0f, B[v] = 0.0f;
         start[v] = seg == 0 && w == 0 && a.h0 ? a.h0[c + v] : 0.0f;
     }
+    const bool full = __all(t0 + S <= len);
+    by_flag(full, [&](auto all) {
 #pragma unroll
-    for (int s = 0; s < S; ++s)
+        for (int s = 0; s < S; ++s)
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const bool on = full || t0 + s < len;
-            const float fv = to_f32<T>(fr[s].v[v]), xv = to_f32<T>(xr[s].v[v]);
-            const float g = LOGIT ? shut(fv) : fv;
-            const float hn = LOGIT ? fmaf(g, xv - B[v], B[v]) : fmaf(g, B[v], xv);
-            const float an = LOGIT ? fmaf(-g, A[v], A[v]) : A[v] * g;
-            B[v] = on ? hn : B[v];
-            A[v] = on ? an : A[v];
-        }
+            for (int v = 0; v < VEC; ++v) {
+                if (!all.value && t0 + s >= len) continue;
+                const float xv = to_f32<T>(xr[s].v[v]);
+                B[v] = LOGIT ? fmaf(g[s][v], xv - B[v], B[v]) : fmaf(g[s][v], B[v], xv);
+                A[v] = LOGIT ? fmaf(-g[s][v], A[v], A[v]) : A[v] * g[s][v];
+            }
+    });
 #pragma unroll
-    for (int s = 0; s < S; ++s) forget(fr[s]), forget(xr[s]);
+    for (int s = 0; s < S; ++s) forget(xr[s]);
     join<VEC, LN>(k, seg, c0, A, B, start, agg, car, h);
     T *out = (T *)a.h.p + (int64_t)b * a.h.sb + i;
+    by_flag(full, [&](auto all) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const bool on = full || t0 + s < len;
-        V o;
+        for (int s = 0; s < S; ++s) {
+            float o[VEC];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const float fv = to_f32<T>(fr[s].v[v]), xv = to_f32<T>(xr[s].v[v]);
-            const float g = LOGIT ? shut(fv) : fv;
-            const float hn = LOGIT ? fmaf(g, xv - h[v], h[v]) : fmaf(g, h[v], xv);
-            h[v] = on ? hn : h[v];
-            o.v[v] = from_f32<T>(on ? hn : 0.0f);
+            for (int v = 0; v < VEC; ++v) {
+                const float xv = to_f32<T>(xr[s].v[v]);
+                const float hn = LOGIT ? fmaf(g[s][v], xv - h[v], h[v]) : fmaf(g[s][v], h[v], xv);
+                const bool on = all.value || t0 + s < len;
+                h[v] = on ? hn : h[v];
+                o[v] = on ? hn : 0.0f;
+            }
+            if ((all.value || t0 + s < k.T) && c0 < k.C) *(V *)(out + (int64_t)(t0 + s) * a.h.st) = rounded<T, VEC>(o);
         }
-        if (t0 + s < k.T && c0 < k.C) *(V *)(out + (int64_t)(t0 + s) * a.h.st) = o;
-    }
+    });
     if (a.hT && seg == k.nseg - 1 && w == parts<LN>() - 1 && c0 < k.C) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) a.hT[c + v] = h[v];
@@ -333,7 +365,7 @@ struct BwdArgs {
 // Backwards in time: step s of a thread is t = T - 1 - (first + s).  The state is
 // e = a_{t+1} g_{t+1}; g_t = dh_t + e, e' = a_t g_t.
 template <typename T, bool LOGIT, int VEC, int S, int LN>
-__global__ __launch_bounds__(kThreads) void gated_bwd_kernel(BwdArgs a) {
+__global__ __launch_bounds__(kThreads, 4) void gated_bwd_kernel(BwdArgs a) {
     typedef Unit<T, VEC> V;
     __shared__ float2 agg[parts<LN>()][LN * VEC], car[LN == 64 ? kWaves : 1][LN * VEC];
     const Cut &k = a.k;
@@ -361,59 +393,72 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_kernel(BwdArgs a) {
             hr[s] = *(const V *)(hp + max(t - 1, (int64_t)0) * a.h.st);
         }
     }
-    // steps outside the sequence, or before its start, do not count
-    const bool full = __all(t0 < len && t0 - (S - 1) >= 0);
-    float A[VEC], B[VEC], start[VEC], e[VEC];
+    // what a step keeps beside dh, x and h: u (logit) or a (decay), and a u (logit), to
+    // full relative accuracy where either is small
+    float g[S][VEC], au[LOGIT ? S : 1][VEC], A[VEC], B[VEC], start[VEC], e[VEC];
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float fv = to_f32<T>(fr[s].v[v]);
+            if (LOGIT) {
+                const float ex = exp_fast(fv);
+                g[s][v] = rcp_fast(1.0f + ex);
+                au[LOGIT ? s : 0][v] = fminf(ex, 3e38f) * g[s][v] * g[s][v];
+            } else {
+                g[s][v] = fv;
+            }
+        }
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
         A[v] = 1.0f, B[v] = 0.0f;
         start[v] = seg == 0 && w == 0 && a.dhT ? a.dhT[c + v] : 0.0f;
     }
+    // steps outside the sequence, or before its start, do not count
+    const bool full = __all(t0 < len && t0 - (S - 1) >= 0);
+    by_flag(full, [&](auto all) {
 #pragma unroll
-    for (int s = 0; s < S; ++s)
+        for (int s = 0; s < S; ++s)
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const bool on = full || (t0 - s < len && t0 - s >= 0);
-            const float fv = to_f32<T>(fr[s].v[v]), g = LOGIT ? shut(fv) : fv;
-            const float q = B[v] + to_f32<T>(dr[s].v[v]);
-            const float bn = LOGIT ? fmaf(-g, q, q) : g * q, an = LOGIT ? fmaf(-g, A[v], A[v]) : A[v] * g;
-            B[v] = on ? bn : B[v];
-            A[v] = on ? an : A[v];
-        }
+            for (int v = 0; v < VEC; ++v) {
+                if (!all.value && (t0 - s >= len || t0 - s < 0)) continue;
+                const float q = B[v] + to_f32<T>(dr[s].v[v]);
+                B[v] = LOGIT ? fmaf(-g[s][v], q, q) : g[s][v] * q;
+                A[v] = LOGIT ? fmaf(-g[s][v], A[v], A[v]) : A[v] * g[s][v];
+            }
+    });
 #pragma unroll
-    for (int s = 0; s < S; ++s) forget(fr[s]), forget(dr[s]);
+    for (int s = 0; s < S; ++s) forget(dr[s]);
     join<VEC, LN>(k, seg, c0, A, B, start, agg, car, e);
     T *of = (T *)a.df.p + (int64_t)b * a.df.sb + i, *ox = (T *)a.dx.p + (int64_t)b * a.dx.sb + i;
+    by_flag(full, [&](auto all) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const int t = t0 - s;
-        const bool on = full || (t < len && t >= 0);
-        V vf, vx;
+        for (int s = 0; s < S; ++s) {
+            const int t = t0 - s;
+            const bool on = all.value || (t < len && t >= 0);
+            float df[VEC], dx[VEC];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const float fv = to_f32<T>(fr[s].v[v]), q = e[v] + to_f32<T>(dr[s].v[v]);
-            float before = to_f32<T>(hr[s].v[v]);
-            if (t == 0) before = a.h0 ? a.h0[c + v] : 0.0f;
-            float df, dx, en;
-            if (LOGIT) {
-                const float ex = exp_fast(fv), u = rcp_fast(1.0f + ex);
-                dx = u * q;
-                df = fminf(ex, 3e38f) * u * dx * (before - to_f32<T>(xr[s].v[v]));
-                en = fmaf(-u, q, q);
-            } else {
-                dx = q;
-                df = q * before;
-                en = fv * q;
+            for (int v = 0; v < VEC; ++v) {
+                const float q = e[v] + to_f32<T>(dr[s].v[v]);
+                float before = to_f32<T>(hr[s].v[v]);
+                if (t == 0) before = a.h0 ? a.h0[c + v] : 0.0f;
+                if (LOGIT) {
+                    dx[v] = g[s][v] * q;
+                    df[v] = au[LOGIT ? s : 0][v] * q * (before - to_f32<T>(xr[s].v[v]));
+                    e[v] = on ? fmaf(-g[s][v], q, q) : e[v];
+                } else {
+                    dx[v] = q;
+                    df[v] = q * before;
+                    e[v] = on ? g[s][v] * q : e[v];
+                }
+                if (!on) df[v] = dx[v] = 0.0f;
             }
-            e[v] = on ? en : e[v];
-            vf.v[v] = from_f32<T>(on ? df : 0.0f);
-            vx.v[v] = from_f32<T>(on ? dx : 0.0f);
+            if ((all.value || t >= 0) && c0 < k.C) {
+                *(V *)(of + (int64_t)t * a.df.st) = rounded<T, VEC>(df);
+                *(V *)(ox + (int64_t)t * a.dx.st) = rounded<T, VEC>(dx);
+            }
         }
-        if (t >= 0 && c0 < k.C) {
-            *(V *)(of + (int64_t)t * a.df.st) = vf;
-            *(V *)(ox + (int64_t)t * a.dx.st) = vx;
-        }
-    }
+    });
     if (a.dh0 && seg == k.nseg - 1 && w == parts<LN>() - 1 && c0 < k.C) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) a.dh0[c + v] = e[v];
@@ -439,19 +484,18 @@ int64_t segments(int T, const Shape &p) {
     return (T + tile - 1) / tile;
 }
 
-// One channel to a lane: 16 steps a thread.  A short sequence of few values, which its
-// launches bound, goes to workgroups that have all of it, and needs no words cleared
-// (500 x 4 x 768 float32 13 us for 16, 500 x 16 x 768 however 27 for 18: narrow rows).
-// Two (bf16): 8 steps up to eight workgroups a CU, and 16 past that or where one segment
-// then does: longer segments have fewer words to exchange but leave fewer waves to hide a join (1024 x 16 x 768:
-// 24 and 26 us, 32768 x 1 x 768: 73 and 55, 8192 x 16 x 2048: 386 and 337).
-Shape shape(const GatedDims &d, bool two) {
+// 16 steps a thread, backward of two channels to a lane (bf16) 8: longer segments have
+// fewer words to exchange, until their registers leave too few waves to hide a join
+// (forward 1024 x 16 x 768 bf16 22 us, with 8 steps 24, 32768 x 1 x 768 50 and 75;
+// backward 1000 x 16 x 1024 49 us with 8, with 16 115 or, given the registers, 50).  A
+// short sequence of few values, which its launches bound, goes to workgroups that have
+// all of it, and needs no words cleared (500 x 4 x 768 float32 13 us for 16; 500 x 16 x
+// 768 however 27 for 18: narrow rows).
+constexpr int steps(bool bwd, int vec) { return bwd && vec == 2 ? 8 : 16; }
+Shape shape(const GatedDims &d, bool two, bool bwd) {
+    const Shape wide{two ? 2 : 1, steps(bwd, two ? 2 : 1), 64}, narrow{1, 16, kNarrow};
     const int64_t C = (int64_t)d.B * d.D;
-    const Shape one{1, 16, 64}, narrow{1, 16, kNarrow}, few{2, 8, 64}, many{2, 16, 64};
-    if (segments(d.T, one) > 1 && segments(d.T, narrow) == 1 && d.T * C <= (1 << 21)) return narrow;
-    if (!two) return one;
-    const bool alone = segments(d.T, few) > 1 && segments(d.T, many) == 1;
-    return !alone && segments(d.T, few) * tiles(d, few) <= 8 * 256 ? few : many;
+    return segments(d.T, wide) > 1 && segments(d.T, narrow) == 1 && d.T * C <= (1 << 21) ? narrow : wide;
 }
 int64_t group_of(int64_t nseg) {
     if (nseg <= kGroup) return nseg;
@@ -506,7 +550,7 @@ LinSeq in(const SeqOut &o) { return LinSeq{o.p, o.st, o.sb}; }
 // go(type, gate, channels of a lane, steps, lanes) of a call, as values of their types.
 template <int V>
 using Int = std::integral_constant<int, V>;
-template <typename F>
+template <bool BWD, typename F>
 void by_shape(const Shape &p, bool bf16, bool logit, F go) {
     auto gate = [&](auto type, auto vec, auto steps, auto lanes) {
         if (logit)
@@ -518,30 +562,28 @@ void by_shape(const Shape &p, bool bf16, bool logit, F go) {
         if (p.lanes == kNarrow)
             gate(type, Int<1>{}, Int<16>{}, Int<kNarrow>{});
         else
-            gate(type, Int<1>{}, Int<16>{}, Int<64>{});
+            gate(type, Int<1>{}, Int<steps(BWD, 1)>{}, Int<64>{});
     };
     if (!bf16)
         one(float{});
     else if (p.vec == 1)
         one(uint16_t{});
-    else if (p.steps == 8)
-        gate(uint16_t{}, Int<2>{}, Int<8>{}, Int<64>{});
     else
-        gate(uint16_t{}, Int<2>{}, Int<16>{}, Int<64>{});
+        gate(uint16_t{}, Int<2>{}, Int<steps(BWD, 2)>{}, Int<64>{});
 }
 
 }  // namespace
 
-size_t gated_bytes(const GatedDims &d, bool bf16) {
+size_t gated_bytes(const GatedDims &d, bool bf16, bool bwd) {
     // a bf16 call may have either number of channels to a lane
     int64_t n = 0;
-    for (int two = 0; two <= (bf16 ? 1 : 0); ++two) n = std::max(n, space(cut(d, shape(d, two), nullptr)));
+    for (int two = 0; two <= (bf16 ? 1 : 0); ++two) n = std::max(n, space(cut(d, shape(d, two, bwd), nullptr)));
     return (size_t)n;
 }
 
-bool gated_grid_ok(const GatedDims &d, bool bf16) {
+bool gated_grid_ok(const GatedDims &d, bool bf16, bool bwd) {
     for (int two = 0; two <= (bf16 ? 1 : 0); ++two) {
-        const Shape p = shape(d, two);
+        const Shape p = shape(d, two, bwd);
         if (!grid_ok(segments(d.T, p) * tiles(d, p), kThreads)) return false;
     }
     return true;
@@ -549,13 +591,13 @@ bool gated_grid_ok(const GatedDims &d, bool bf16) {
 
 hipError_t launch_gated_fwd(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, const float *h0,
                             const int *lens, SeqOut h, float *hT, void *ws, hipStream_t s) {
-    const Shape p = shape(d, bf16 && pairs(d.D, 2, {f, x, in(h)}));
+    const Shape p = shape(d, bf16 && pairs(d.D, 2, {f, x, in(h)}), false);
     const FwdArgs a{cut(d, p, ws), f, x, h0, lens, h, hT};
     const hipError_t e = clear(a.k, s);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)((int64_t)a.k.nseg * a.k.ntile)), thr(kThreads);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, thr, 0, s, a); };
-    by_shape(p, bf16, d.logit, [&](auto type, auto logit, auto vec, auto steps, auto lanes) {
+    by_shape<false>(p, bf16, d.logit, [&](auto type, auto logit, auto vec, auto steps, auto lanes) {
         go(gated_fwd_kernel<decltype(type), logit.value, vec.value, steps.value, lanes.value>);
     });
     return hipGetLastError();
@@ -576,13 +618,13 @@ hipError_t launch_gated_bwd(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, L
                             const float *h0, const float *dhT, const int *lens, SeqOut df, SeqOut dx,
                             float *dh0, void *ws, hipStream_t s) {
     if (!d.logit) x = f;  // not read
-    const Shape p = shape(d, bf16 && pairs(d.D, 2, {f, x, h, dh, in(df), in(dx)}));
+    const Shape p = shape(d, bf16 && pairs(d.D, 2, {f, x, h, dh, in(df), in(dx)}), true);
     const BwdArgs a{cut(d, p, ws), f, x, h, dh, h0, dhT, lens, df, dx, dh0};
     const hipError_t e = clear(a.k, s);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)((int64_t)a.k.nseg * a.k.ntile)), thr(kThreads);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, thr, 0, s, a); };
-    by_shape(p, bf16, d.logit, [&](auto type, auto logit, auto vec, auto steps, auto lanes) {
+    by_shape<true>(p, bf16, d.logit, [&](auto type, auto logit, auto vec, auto steps, auto lanes) {
         go(gated_bwd_kernel<decltype(type), logit.value, vec.value, steps.value, lanes.value>);
     });
     return hipGetLastError();

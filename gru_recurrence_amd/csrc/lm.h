@@ -129,8 +129,8 @@ struct SeqOut {
     void *p;
     int64_t st, sb;
 };
-bool gated_grid_ok(const GatedDims &d, bool bf16);
-size_t gated_bytes(const GatedDims &d, bool bf16);
+bool gated_grid_ok(const GatedDims &d, bool bf16, bool bwd);
+size_t gated_bytes(const GatedDims &d, bool bf16, bool bwd);
 hipError_t launch_gated_fwd(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, const float *h0,
                             const int *lens, SeqOut h, float *hT, void *ws, hipStream_t s);
 hipError_t launch_gated_step(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, const float *h,
