@@ -10,10 +10,10 @@
 //
 // Every operand is read once and every output written once; memory bounds it.  A
 // workgroup takes a tile of 64 lanes of VEC channels by kWaves S steps (a wave S of
-// them), as loaded, in registers.  Each thread composes its S steps; a segment's
-// total goes to memory, the carry into it is composed from the totals of the segments
-// before it, and the steps run again from the carry, from the same registers (the
-// gates are computed twice: kept in float32 they cost the waves that hide the join).
+// them) in registers: the gates in float32, the rest as loaded.  Each thread composes
+// its S steps; a segment's total goes to memory, the carry into it is composed from
+// the totals of the segments before it, and the steps run again from the carry, from
+// the same registers.
 //
 // Segments wait for each other inside one launch: a workgroup draws its segment from
 // its tile's counter, so that whatever it waits for belongs to workgroups that run
@@ -25,13 +25,14 @@
 // so that a segment reads no more than twice that many words.  The order of all
 // products is the dimensions' and the alignment's alone.
 //
-// 1024 x 16 x 768 bf16 forward 21.8 us and 2.5 to clear the words (3.5 TB/s; without the
-// join 15.5), 32768 x 1 x 768 float32 68 and 5 (4.4 TB/s; without the join 50), backward
-// of 1000 x 16 x 1024 bf16 48 and 5 (4.1 TB/s): the workgroups on the chip load together
-// and then wait together, a join (4 us of a workgroup's 8 to 12) long.  Two launches,
-// totals first and the inputs read twice, wait for nothing but took 27, 100 and 57 us
-// for the calls' 24, 70 and 51; workgroups that stay and load their next tile while
-// they wait for a carry, 34, 87 and 76 (half as many fit).
+// 1024 x 16 x 768 bf16 forward 19.4 us and 2.4 to clear the words (3.9 TB/s),
+// 32768 x 1 x 768 float32 67 and 4 (4.5 TB/s), backward of 1000 x 16 x 1024 bf16 46 and
+// 5 (4.3 TB/s): the workgroups on the chip load together and then wait together, a join
+// (3 to 5 us of a workgroup's 8 to 12) long.  An earlier form of 8 steps took 26, 80 and
+// 66 us for the calls, and 19, 56 and 45 with its joins left out.  Two launches, totals first and the inputs read twice, wait for nothing but took
+// 27, 100 and 57 us for the calls' 24, 70 and 51 at the time; workgroups that stay and
+// load their next tile while they wait for a carry, 34, 87 and 72.  Tiles of 32 lanes took
+// 28, 73 and 58 with the best of 8, 12 and 16 steps for each.
 #include <algorithm>
 #include <type_traits>
 
