@@ -179,3 +179,19 @@ def test_clip_stream_and_graph():
         assert torch.equal(got[0], g.clip_grads(grads, 1.0, out=eager)), i
         assert all(torch.equal(a, b) for a, b in zip(got[1:], eager)), i
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dts", [["f32"], ["bf16"]], ids=str)
+@pytest.mark.parametrize("sizes", [[(777,), (31,)], [(300000,), (1,), (70000, 3)]], ids=str)
+def test_clip_factor_below_float32(sizes, dts):
+    """Values of 1e37 clipped to a norm of 1e-3: the factor, some 1e-42, is below
+    float32's normal numbers, where it would have ten bits; the results are not."""
+    grads = _grads(9, sizes, dts, 1e37)
+    norm, ref = gated_ref.clip([_np(t) for t in grads], 1e-3)
+    with np.errstate(over="ignore"):
+        want = float(np.float32(norm))  # +inf where float32 ends
+    got = g.clip_grads(grads, 1e-3).item()
+    assert got == want or abs(got - norm) <= (U + 1e-12) * norm, (got, norm)
+    for o, r in zip(grads, ref):
+        lim = (3 * U + (2.0 ** -8 if o.dtype == torch.bfloat16 else 0.0)) * 1.001 * np.abs(r) + 1e-40
+        assert (np.abs(_np(o) - r) <= lim).all()
