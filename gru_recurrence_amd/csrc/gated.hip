@@ -13,7 +13,8 @@
 // them) in registers: the gates in float32, the rest as loaded.  Each thread composes
 // its S steps; a segment's total goes to memory, the carry into it is composed from
 // the totals of the segments before it, and the steps run again from the carry, from
-// the same registers.
+// the same registers.  Where it pays (shape, below) a workgroup has all steps of fewer
+// channels, and nothing goes through memory.
 //
 // Segments wait for each other inside one launch: a workgroup draws its segment from
 // its tile's counter, so that whatever it waits for belongs to workgroups that run
@@ -25,14 +26,20 @@
 // so that a segment reads no more than twice that many words.  The order of all
 // products is the dimensions' and the alignment's alone.
 //
-// 1024 x 16 x 768 bf16 forward 19.4 us and 2.4 to clear the words (3.9 TB/s),
-// 32768 x 1 x 768 float32 67 and 4 (4.5 TB/s), backward of 1000 x 16 x 1024 bf16 46 and
-// 5 (4.3 TB/s): the workgroups on the chip load together and then wait together, a join
-// (3 to 5 us of a workgroup's 8 to 12) long.  An earlier form of 8 steps took 26, 80 and
-// 66 us for the calls, and 19, 56 and 45 with its joins left out.  Two launches, totals first and the inputs read twice, wait for nothing but took
-// 27, 100 and 57 us for the calls' 24, 70 and 51 at the time; workgroups that stay and
-// load their next tile while they wait for a carry, 34, 87 and 72.  Tiles of 32 lanes took
-// 28, 73 and 58 with the best of 8, 12 and 16 steps for each.
+// 32768 x 1 x 768 float32 forward 65 us and 5 to clear the words (4.6 TB/s), backward of
+// 1000 x 16 x 1024 bf16 46 and 5 (4.3 TB/s): the workgroups on the chip load together and
+// then wait together, a join (3 to 5 us of a workgroup's 8 to 12) long.  An earlier form of
+// 8 steps took 80 and 66 us for the calls, and 56 and 45 with its joins left out.  Two
+// launches, totals first and the inputs read twice, wait for nothing but took 100 and 57
+// us for the calls' 70 and 51 at the time; workgroups that stay and load their next tile
+// while they wait for a carry, 87 and 72; tiles of 32 lanes 73 and 58 with the best of 8,
+// 12 and 16 steps for each; rows of 128 bytes and 1024 threads 73 and 52, of 256 bytes 67
+// and 55 (but 8192 x 16 x 2048 bf16 385 for 324).  1024 x 16 x 768 bf16 forward, one
+// workgroup to a sequence, 18.2 us (4.2 TB/s): all load, then all store.
+//
+// Stores go past the caches, but for the backward pass of bf16 (8192 x 16 x 2048 forward
+// 339 us for 324, 32768 x 1 x 768 float32 backward 131 for 125; 1000 x 16 x 1024 bf16
+// backward however 48.9 for 49.8).
 #include <algorithm>
 #include <type_traits>
 
@@ -45,7 +52,8 @@ namespace lm {
 namespace {
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;
-constexpr int kNarrow = 16;  // lanes along the channels where one workgroup has all of a short sequence
+constexpr int kAll = 1024;   // most threads where one workgroup has all of a sequence
+constexpr int kNarrow = 16;  // its lanes along the channels
 constexpr int kGroup = 16;
 constexpr int kHead = 128;           // bytes before the counters: the status word
 
@@ -70,10 +78,18 @@ __device__ __forceinline__ void publish(uint64_t *p, float A, float B) {
 // 1 - sigmoid(f)
 __device__ __forceinline__ float shut(float f) { return rcp_fast(1.0f + exp_fast(f)); }
 
-// This workgroup's segment and tile of channels.
+// This workgroup's segment and tile of channels.  Workgroups go round the eight XCDs:
+// where a tile's rows are short of a few cache lines (LN < 64), neighbouring tiles go to
+// one of them.
+template <int LN>
 __device__ __forceinline__ void place(const Cut &k, int &seg, int &tile) {
     __shared__ unsigned drawn;
     seg = 0;
+    if (LN < 64) {
+        const int xcd = blockIdx.x & 7, each = k.ntile >> 3, more = k.ntile & 7;
+        tile = xcd * each + min(xcd, more) + (int)(blockIdx.x >> 3);
+        return;
+    }
     tile = blockIdx.x % k.ntile;
     if (k.nseg > 1) {
         if (threadIdx.x == 0)
@@ -85,8 +101,8 @@ __device__ __forceinline__ void place(const Cut &k, int &seg, int &tile) {
 }
 
 // Parts along time of a workgroup with LN lanes along the channels, and a thread's.
-template <int LN>
-constexpr int parts() { return kThreads / LN; }
+template <int LN, int NT>
+constexpr int parts() { return NT / LN; }
 template <int LN>
 __device__ __forceinline__ int part() {
     const int p = threadIdx.x / LN;
@@ -98,11 +114,60 @@ __device__ __forceinline__ int part() {
 // start: the recurrence's initial state, in the first part of segment 0.  Nobody
 // else reads that, and all that follows waits for what this part makes of it, so
 // the last state may be written over the first.
-template <int VEC, int LN>
+
+// One segment, LN < 64: a scan over the wave's parts, then the waves before.
+template <int VEC, int LN, int NT>
+__device__ __forceinline__ void join(const float *A, const float *B, const float *start,
+                                     float2 (*agg)[LN * VEC], float *h) {
+    constexpr int P = 64 / LN;
+    const int p = (threadIdx.x & 63) / LN, at = (threadIdx.x & (LN - 1)) * VEC;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool first = threadIdx.x < LN;
+    float sA[VEC], sB[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        sA[v] = first ? 0.0f : A[v];
+        sB[v] = first ? fmaf(A[v], start[v], B[v]) : B[v];
+    }
+#pragma unroll
+    for (int o = 1; o < P; o *= 2)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float qA = __shfl_up(sA[v], o * LN), qB = __shfl_up(sB[v], o * LN);
+            if (p >= o) {
+                sB[v] = fmaf(sA[v], qB, sB[v]);
+                sA[v] *= qA;
+            }
+        }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        if (p == P - 1) agg[wave][at + v] = make_float2(sA[v], sB[v]);
+        h[v] = 0.0f;
+    }
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < NT / 64 - 1; ++i) {
+        if (i >= wave) break;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float2 q = agg[i][at + v];
+            h[v] = fmaf(q.x, h[v], q.y);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        const float qA = __shfl_up(sA[v], LN), qB = __shfl_up(sB[v], LN);
+        if (p) h[v] = fmaf(qA, h[v], qB);
+        if (first) h[v] = start[v];
+    }
+}
+
+// LN = 64: a part is a wave.
+template <int VEC>
 __device__ __forceinline__ void join(const Cut &k, int seg, int c0, const float *A, const float *B,
-                                     const float *start, float2 (*agg)[LN * VEC],
-                                     float2 (*car)[LN * VEC], float *h) {
-    const int lane = threadIdx.x & (LN - 1), w = part<LN>(), at = lane * VEC;
+                                     const float *start, float2 (*agg)[64 * VEC],
+                                     float2 (*car)[64 * VEC], float *h) {
+    const int lane = threadIdx.x & 63, w = part<64>(), at = lane * VEC;
     const bool first = seg == 0 && w == 0;
 #pragma unroll
     for (int v = 0; v < VEC; ++v)
@@ -113,22 +178,14 @@ __device__ __forceinline__ void join(const Cut &k, int seg, int c0, const float 
 #pragma unroll
     for (int v = 0; v < VEC; ++v) pA[v] = 1.0f, pB[v] = first ? start[v] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < parts<LN>() - 1; ++i) {
-        if (i >= w) {
-            if (LN == 64) break;
-            continue;
-        }
+    for (int i = 0; i < kWaves - 1; ++i) {
+        if (i >= w) break;
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             const float2 q = agg[i][at + v];
             pB[v] = fmaf(q.x, pB[v], q.y);
             pA[v] *= q.x;
         }
-    }
-    if (LN < 64) {  // a single segment
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) h[v] = pB[v];
-        return;
     }
     const bool last = seg == k.nseg - 1;
     float tA[VEC], tB[VEC];  // the whole segment, in the last wave
@@ -240,9 +297,11 @@ __device__ __forceinline__ void forget(V &q) {
         asm volatile("" : "+v"(r));
         q = __builtin_bit_cast(V, (uint16_t)r);
     } else {
-        uint32_t r = __builtin_bit_cast(uint32_t, q);
-        asm volatile("" : "+v"(r));
-        q = __builtin_bit_cast(V, r);
+        uint32_t r[sizeof(V) / 4];
+        __builtin_memcpy(r, &q, sizeof q);
+#pragma unroll
+        for (uint32_t &i : r) asm volatile("" : "+v"(i));
+        __builtin_memcpy(&q, r, sizeof q);
     }
 }
 
@@ -255,32 +314,41 @@ __device__ __forceinline__ void by_flag(bool flag, F f) {
         f(std::false_type{});
 }
 
-// Values in the sequence's type; two at once to bf16.
-template <typename T, int VEC>
-__device__ __forceinline__ Unit<T, VEC> rounded(const float *v) {
-    Unit<T, VEC> o;
-    if constexpr (sizeof(T) == 2 && VEC == 2) {
+// Stores values in the sequence's type (two at once to bf16); PAST: past the caches.
+template <bool PAST, typename T, int VEC>
+__device__ __forceinline__ void put(T *p, const float *v) {
+    typedef Unit<T, VEC> V;
+    typedef std::conditional_t<sizeof(V) == 2, uint16_t, std::conditional_t<sizeof(V) == 4, uint32_t, uint64_t>> W;
+    V o;
+    if constexpr (sizeof(T) == 2 && VEC % 2 == 0) {
         typedef float f2 __attribute__((ext_vector_type(2)));
         typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-        return __builtin_bit_cast(Unit<T, VEC>, __builtin_convertvector((f2){v[0], v[1]}, b2));
-    }
+        b2 two[VEC / 2];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) o.v[i] = from_f32<T>(v[i]);
-    return o;
+        for (int i = 0; i < VEC / 2; ++i) two[i] = __builtin_convertvector((f2){v[2 * i], v[2 * i + 1]}, b2);
+        __builtin_memcpy(&o, two, sizeof o);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) o.v[i] = from_f32<T>(v[i]);
+    }
+    if (PAST)
+        __builtin_nontemporal_store(__builtin_bit_cast(W, o), (W *)p);
+    else
+        *(V *)p = o;
 }
 
-template <typename T, bool LOGIT, int VEC, int S, int LN>
-__global__ __launch_bounds__(kThreads, 4) void gated_fwd_kernel(FwdArgs a) {
+template <typename T, bool LOGIT, int VEC, int S, int LN, int NT>
+__global__ __launch_bounds__(NT, 4) void gated_fwd_kernel(FwdArgs a) {
     typedef Unit<T, VEC> V;
-    __shared__ float2 agg[parts<LN>()][LN * VEC], car[LN == 64 ? kWaves : 1][LN * VEC];
+    __shared__ float2 agg[NT / 64][LN * VEC], car[LN == 64 ? kWaves : 1][LN * VEC];
     const Cut &k = a.k;
     int seg, tile;
-    place(k, seg, tile);
+    place<LN>(k, seg, tile);
     const int lane = threadIdx.x & (LN - 1), w = part<LN>();
     const int c0 = (tile * LN + lane) * VEC, c = min(c0, k.C - VEC);
     const int b = c / k.D, i = c - b * k.D;
     const int len = a.lens ? min(max(a.lens[b], 0), k.T) : k.T;
-    const int t0 = (seg * parts<LN>() + w) * S;  // the grid's limit keeps this in 31 bits
+    const int t0 = (seg * parts<LN, NT>() + w) * S;  // the grid's limit keeps this in 31 bits
     V fr[S], xr[S];
     if (__any(t0 < len)) {
         const T *fp = (const T *)a.f.p + (int64_t)b * a.f.sb + i, *xp = (const T *)a.x.p + (int64_t)b * a.x.sb + i;
@@ -291,15 +359,18 @@ __global__ __launch_bounds__(kThreads, 4) void gated_fwd_kernel(FwdArgs a) {
             xr[s] = *(const V *)(xp + t * a.x.st);
         }
     }
-    // what a step keeps beside x: u (logit) or a (decay)
-    float g[S][VEC], A[VEC], B[VEC], h[VEC], start[VEC];
+    // what a step keeps beside x: u (logit) or a (decay); with four channels f, as there
+    // are no registers for them
+    constexpr bool keep = VEC < 4;
+    float g[keep ? S : 1][VEC], A[VEC], B[VEC], h[VEC], start[VEC];
+    auto gate = [&](int s, int v) {
+        const float fv = to_f32<T>(fr[s].v[v]);
+        return LOGIT ? shut(fv) : fv;
+    };
 #pragma unroll
-    for (int s = 0; s < S; ++s)
+    for (int s = 0; s < (keep ? S : 0); ++s)
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const float fv = to_f32<T>(fr[s].v[v]);
-            g[s][v] = LOGIT ? shut(fv) : fv;
-        }
+        for (int v = 0; v < VEC; ++v) g[s][v] = gate(s, v);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
         A[v] = 1.0f, B[v] = 0.0f;
@@ -312,14 +383,20 @@ __global__ __launch_bounds__(kThreads, 4) void gated_fwd_kernel(FwdArgs a) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 if (!all.value && t0 + s >= len) continue;
-                const float xv = to_f32<T>(xr[s].v[v]);
-                B[v] = LOGIT ? fmaf(g[s][v], xv - B[v], B[v]) : fmaf(g[s][v], B[v], xv);
-                A[v] = LOGIT ? fmaf(-g[s][v], A[v], A[v]) : A[v] * g[s][v];
+                const float xv = to_f32<T>(xr[s].v[v]), gv = keep ? g[keep ? s : 0][v] : gate(s, v);
+                B[v] = LOGIT ? fmaf(gv, xv - B[v], B[v]) : fmaf(gv, B[v], xv);
+                A[v] = LOGIT ? fmaf(-gv, A[v], A[v]) : A[v] * gv;
             }
     });
 #pragma unroll
-    for (int s = 0; s < S; ++s) forget(xr[s]);
-    join<VEC, LN>(k, seg, c0, A, B, start, agg, car, h);
+    for (int s = 0; s < S; ++s) {
+        forget(xr[s]);
+        if (!keep) forget(fr[s]);
+    }
+    if constexpr (LN == 64)
+        join<VEC>(k, seg, c0, A, B, start, agg, car, h);
+    else
+        join<VEC, LN, NT>(A, B, start, agg, h);
     T *out = (T *)a.h.p + (int64_t)b * a.h.sb + i;
     by_flag(full, [&](auto all) {
 #pragma unroll
@@ -327,16 +404,16 @@ __global__ __launch_bounds__(kThreads, 4) void gated_fwd_kernel(FwdArgs a) {
             float o[VEC];
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                const float xv = to_f32<T>(xr[s].v[v]);
-                const float hn = LOGIT ? fmaf(g[s][v], xv - h[v], h[v]) : fmaf(g[s][v], h[v], xv);
+                const float xv = to_f32<T>(xr[s].v[v]), gv = keep ? g[keep ? s : 0][v] : gate(s, v);
+                const float hn = LOGIT ? fmaf(gv, xv - h[v], h[v]) : fmaf(gv, h[v], xv);
                 const bool on = all.value || t0 + s < len;
                 h[v] = on ? hn : h[v];
                 o[v] = on ? hn : 0.0f;
             }
-            if ((all.value || t0 + s < k.T) && c0 < k.C) *(V *)(out + (int64_t)(t0 + s) * a.h.st) = rounded<T, VEC>(o);
+            if ((all.value || t0 + s < k.T) && c0 < k.C) put<true, T, VEC>(out + (int64_t)(t0 + s) * a.h.st, o);
         }
     });
-    if (a.hT && seg == k.nseg - 1 && w == parts<LN>() - 1 && c0 < k.C) {
+    if (a.hT && seg == k.nseg - 1 && w == parts<LN, NT>() - 1 && c0 < k.C) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) a.hT[c + v] = h[v];
     }
@@ -365,18 +442,18 @@ struct BwdArgs {
 
 // Backwards in time: step s of a thread is t = T - 1 - (first + s).  The state is
 // e = a_{t+1} g_{t+1}; g_t = dh_t + e, e' = a_t g_t.
-template <typename T, bool LOGIT, int VEC, int S, int LN>
-__global__ __launch_bounds__(kThreads, 4) void gated_bwd_kernel(BwdArgs a) {
+template <typename T, bool LOGIT, int VEC, int S, int LN, int NT>
+__global__ __launch_bounds__(NT, 4) void gated_bwd_kernel(BwdArgs a) {
     typedef Unit<T, VEC> V;
-    __shared__ float2 agg[parts<LN>()][LN * VEC], car[LN == 64 ? kWaves : 1][LN * VEC];
+    __shared__ float2 agg[NT / 64][LN * VEC], car[LN == 64 ? kWaves : 1][LN * VEC];
     const Cut &k = a.k;
     int seg, tile;
-    place(k, seg, tile);
+    place<LN>(k, seg, tile);
     const int lane = threadIdx.x & (LN - 1), w = part<LN>();
     const int c0 = (tile * LN + lane) * VEC, c = min(c0, k.C - VEC);
     const int b = c / k.D, i = c - b * k.D;
     const int len = a.lens ? min(max(a.lens[b], 0), k.T) : k.T;
-    const int t0 = k.T - 1 - (seg * parts<LN>() + w) * S;  // the thread's last step in time; may be below 0
+    const int t0 = k.T - 1 - (seg * parts<LN, NT>() + w) * S;  // the thread's last step in time; may be below 0
     V fr[S], dr[S], xr[S], hr[S];
     if (__any(t0 - (S - 1) < len && t0 >= 0)) {
         const T *fp = (const T *)a.f.p + (int64_t)b * a.f.sb + i, *dp = (const T *)a.dh.p + (int64_t)b * a.dh.sb + i;
@@ -430,7 +507,10 @@ __global__ __launch_bounds__(kThreads, 4) void gated_bwd_kernel(BwdArgs a) {
     });
 #pragma unroll
     for (int s = 0; s < S; ++s) forget(dr[s]);
-    join<VEC, LN>(k, seg, c0, A, B, start, agg, car, e);
+    if constexpr (LN == 64)
+        join<VEC>(k, seg, c0, A, B, start, agg, car, e);
+    else
+        join<VEC, LN, NT>(A, B, start, agg, e);
     T *of = (T *)a.df.p + (int64_t)b * a.df.sb + i, *ox = (T *)a.dx.p + (int64_t)b * a.dx.sb + i;
     by_flag(full, [&](auto all) {
 #pragma unroll
@@ -455,12 +535,12 @@ __global__ __launch_bounds__(kThreads, 4) void gated_bwd_kernel(BwdArgs a) {
                 if (!on) df[v] = dx[v] = 0.0f;
             }
             if ((all.value || t >= 0) && c0 < k.C) {
-                *(V *)(of + (int64_t)t * a.df.st) = rounded<T, VEC>(df);
-                *(V *)(ox + (int64_t)t * a.dx.st) = rounded<T, VEC>(dx);
+                put<sizeof(T) == 4, T, VEC>(of + (int64_t)t * a.df.st, df);
+                put<sizeof(T) == 4, T, VEC>(ox + (int64_t)t * a.dx.st, dx);
             }
         }
     });
-    if (a.dh0 && seg == k.nseg - 1 && w == parts<LN>() - 1 && c0 < k.C) {
+    if (a.dh0 && seg == k.nseg - 1 && w == parts<LN, NT>() - 1 && c0 < k.C) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) a.dh0[c + v] = e[v];
     }
@@ -471,9 +551,10 @@ __global__ __launch_bounds__(256) void gated_clear_kernel(uint4 *p, int64_t n) {
         p[i] = make_uint4(0, 0, 0, 0);
 }
 
-// How a call is laid out: channels of a lane, steps of a thread, lanes along the channels.
+// How a call is laid out: channels of a lane, steps of a thread, lanes along the channels,
+// threads of a workgroup.
 struct Shape {
-    int vec, steps, lanes;
+    int vec, steps, lanes, threads;
 };
 
 int64_t tiles(const GatedDims &d, const Shape &p) {
@@ -481,22 +562,32 @@ int64_t tiles(const GatedDims &d, const Shape &p) {
     return ((int64_t)d.B * d.D + wide - 1) / wide;
 }
 int64_t segments(int T, const Shape &p) {
-    const int64_t tile = (int64_t)(kThreads / p.lanes) * p.steps;
+    const int64_t tile = (int64_t)(p.threads / p.lanes) * p.steps;
     return (T + tile - 1) / tile;
 }
 
 // 16 steps a thread, backward of two channels to a lane (bf16) 8: longer segments have
 // fewer words to exchange, until their registers leave too few waves to hide a join
 // (forward 1024 x 16 x 768 bf16 22 us, with 8 steps 24, 32768 x 1 x 768 50 and 75;
-// backward 1000 x 16 x 1024 49 us with 8, with 16 115 or, given the registers, 50).  A
-// short sequence of few values, which its launches bound, goes to workgroups that have
-// all of it, and needs no words cleared (500 x 4 x 768 float32 13 us for 16; 500 x 16 x
-// 768 however 27 for 18: narrow rows).
+// backward 1000 x 16 x 1024 49 us with 8, with 16 115 or, given the registers, 50).
+// Where 1024 steps or fewer make more than one such segment, a workgroup may take all of
+// them, with nothing to clear and nobody to wait for (device times, wide for narrow or whole):
+// narrow, in rows of a few values, while those are few: forward 1000 x 4 x 1024 bf16 11.6
+// us for 9.1, 700 x 1 x 768 9.1 for 6.1, however 200 x 32 x 1024 13.0 for 15.6; backward,
+// with twice the rows, sooner no longer: 200 x 8 x 1024 bf16 11.5 for 11.3, 300 x 16 x
+// 768 15.6 for 19.3, past 512 steps 700 x 1 x 768 10.0 for 10.8, 1024 x 2 x 768 11.4 for 14.0;
+// whole, the forward pass of bf16 whose channels stand in fours, in rows of 128 bytes,
+// where all workgroups run at once and on most CUs: 1024 x 16 x 1024 23.8 for 20.6, x 12
+// 21.5 for 18.4, however x 8 14.9 for 16.2, x 20 28.3 for 31.9, and 200 x 32 x 1024, two
+// segments, 13.1 for 14.2.
 constexpr int steps(bool bwd, int vec) { return bwd && vec == 2 ? 8 : 16; }
-Shape shape(const GatedDims &d, bool two, bool bwd) {
-    const Shape wide{two ? 2 : 1, steps(bwd, two ? 2 : 1), 64}, narrow{1, 16, kNarrow};
-    const int64_t C = (int64_t)d.B * d.D;
-    return segments(d.T, wide) > 1 && segments(d.T, narrow) == 1 && d.T * C <= (1 << 21) ? narrow : wide;
+Shape shape(const GatedDims &d, int vec, bool bwd) {
+    const int two = std::min(vec, 2), all = d.T <= kThreads / kNarrow * 16 ? kThreads : kAll;
+    const Shape wide{two, steps(bwd, two), 64, kThreads}, narrow{1, 16, kNarrow, all}, whole{4, 16, kNarrow, all};
+    if (segments(d.T, wide) == 1 || segments(d.T, narrow) > 1) return wide;
+    const int64_t n = tiles(d, whole), few = (int64_t)1 << (!bwd ? 22 : all == kThreads ? 21 : 20);
+    if ((int64_t)d.T * d.B * d.D <= few) return narrow;
+    return vec == 4 && !bwd && segments(d.T, wide) > 2 && n >= 160 && n * all <= 256 * 1024 ? whole : wide;
 }
 int64_t group_of(int64_t nseg) {
     if (nseg <= kGroup) return nseg;
@@ -539,67 +630,75 @@ hipError_t clear(const Cut &k, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Whether two channels of every row stand together at a multiple of their size.
-bool pairs(int D, size_t e, std::initializer_list<LinSeq> seqs) {
-    if (D % 2) return false;
+// How many channels of every row stand together at a multiple of their size: 4, 2 or 1.
+int together(int D, size_t e, std::initializer_list<LinSeq> seqs) {
+    int n = 4;
     for (const LinSeq &s : seqs)
-        if ((uintptr_t)s.p % (2 * e) || s.st % 2 || s.sb % 2) return false;
-    return true;
+        while (n > 1 && (D % n || (uintptr_t)s.p % (n * e) || s.st % n || s.sb % n)) n /= 2;
+    return n;
 }
 LinSeq in(const SeqOut &o) { return LinSeq{o.p, o.st, o.sb}; }
 
-// go(type, gate, channels of a lane, steps, lanes) of a call, as values of their types.
+// go(type, gate, channels of a lane, steps, lanes, threads) of a call, as values of their types.
 template <int V>
 using Int = std::integral_constant<int, V>;
 template <bool BWD, typename F>
 void by_shape(const Shape &p, bool bf16, bool logit, F go) {
-    auto gate = [&](auto type, auto vec, auto steps, auto lanes) {
+    auto gate = [&](auto type, auto vec, auto steps, auto lanes, auto threads) {
         if (logit)
-            go(type, std::true_type{}, vec, steps, lanes);
+            go(type, std::true_type{}, vec, steps, lanes, threads);
         else
-            go(type, std::false_type{}, vec, steps, lanes);
+            go(type, std::false_type{}, vec, steps, lanes, threads);
+    };
+    auto all = [&](auto type, auto vec) {
+        if (p.threads == kThreads)
+            gate(type, vec, Int<16>{}, Int<kNarrow>{}, Int<kThreads>{});
+        else
+            gate(type, vec, Int<16>{}, Int<kNarrow>{}, Int<kAll>{});
     };
     auto one = [&](auto type) {
         if (p.lanes == kNarrow)
-            gate(type, Int<1>{}, Int<16>{}, Int<kNarrow>{});
+            all(type, Int<1>{});
         else
-            gate(type, Int<1>{}, Int<steps(BWD, 1)>{}, Int<64>{});
+            gate(type, Int<1>{}, Int<steps(BWD, 1)>{}, Int<64>{}, Int<kThreads>{});
     };
     if (!bf16)
         one(float{});
     else if (p.vec == 1)
         one(uint16_t{});
-    else
-        gate(uint16_t{}, Int<2>{}, Int<steps(BWD, 2)>{}, Int<64>{});
+    else if (p.vec == 2)
+        gate(uint16_t{}, Int<2>{}, Int<steps(BWD, 2)>{}, Int<64>{}, Int<kThreads>{});
+    else if constexpr (!BWD)
+        all(uint16_t{}, Int<4>{});
 }
 
 }  // namespace
 
+// A bf16 call may have any number of channels together.
 size_t gated_bytes(const GatedDims &d, bool bf16, bool bwd) {
-    // a bf16 call may have either number of channels to a lane
     int64_t n = 0;
-    for (int two = 0; two <= (bf16 ? 1 : 0); ++two) n = std::max(n, space(cut(d, shape(d, two, bwd), nullptr)));
+    for (int vec = 1; vec <= (bf16 ? 4 : 1); vec *= 2) n = std::max(n, space(cut(d, shape(d, vec, bwd), nullptr)));
     return (size_t)n;
 }
 
 bool gated_grid_ok(const GatedDims &d, bool bf16, bool bwd) {
-    for (int two = 0; two <= (bf16 ? 1 : 0); ++two) {
-        const Shape p = shape(d, two, bwd);
-        if (!grid_ok(segments(d.T, p) * tiles(d, p), kThreads)) return false;
+    for (int vec = 1; vec <= (bf16 ? 4 : 1); vec *= 2) {
+        const Shape p = shape(d, vec, bwd);
+        if (!grid_ok(segments(d.T, p) * tiles(d, p), p.threads)) return false;
     }
     return true;
 }
 
 hipError_t launch_gated_fwd(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, const float *h0,
                             const int *lens, SeqOut h, float *hT, void *ws, hipStream_t s) {
-    const Shape p = shape(d, bf16 && pairs(d.D, 2, {f, x, in(h)}), false);
+    const Shape p = shape(d, bf16 ? together(d.D, 2, {f, x, in(h)}) : 1, false);
     const FwdArgs a{cut(d, p, ws), f, x, h0, lens, h, hT};
     const hipError_t e = clear(a.k, s);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)((int64_t)a.k.nseg * a.k.ntile)), thr(kThreads);
+    const dim3 grid((unsigned)((int64_t)a.k.nseg * a.k.ntile)), thr(p.threads);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, thr, 0, s, a); };
-    by_shape<false>(p, bf16, d.logit, [&](auto type, auto logit, auto vec, auto steps, auto lanes) {
-        go(gated_fwd_kernel<decltype(type), logit.value, vec.value, steps.value, lanes.value>);
+    by_shape<false>(p, bf16, d.logit, [&](auto type, auto logit, auto vec, auto steps, auto lanes, auto threads) {
+        go(gated_fwd_kernel<decltype(type), logit.value, vec.value, steps.value, lanes.value, threads.value>);
     });
     return hipGetLastError();
 }
@@ -619,14 +718,14 @@ hipError_t launch_gated_bwd(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, L
                             const float *h0, const float *dhT, const int *lens, SeqOut df, SeqOut dx,
                             float *dh0, void *ws, hipStream_t s) {
     if (!d.logit) x = f;  // not read
-    const Shape p = shape(d, bf16 && pairs(d.D, 2, {f, x, h, dh, in(df), in(dx)}), true);
+    const Shape p = shape(d, bf16 ? together(d.D, 2, {f, x, h, dh, in(df), in(dx)}) : 1, true);
     const BwdArgs a{cut(d, p, ws), f, x, h, dh, h0, dhT, lens, df, dx, dh0};
     const hipError_t e = clear(a.k, s);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)((int64_t)a.k.nseg * a.k.ntile)), thr(kThreads);
+    const dim3 grid((unsigned)((int64_t)a.k.nseg * a.k.ntile)), thr(p.threads);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, thr, 0, s, a); };
-    by_shape<true>(p, bf16, d.logit, [&](auto type, auto logit, auto vec, auto steps, auto lanes) {
-        go(gated_bwd_kernel<decltype(type), logit.value, vec.value, steps.value, lanes.value>);
+    by_shape<true>(p, bf16, d.logit, [&](auto type, auto logit, auto vec, auto steps, auto lanes, auto threads) {
+        go(gated_bwd_kernel<decltype(type), logit.value, vec.value, steps.value, lanes.value, threads.value>);
     });
     return hipGetLastError();
 }

@@ -119,6 +119,21 @@ def test_gated_without_state(dt):
 
 
 @pytest.mark.parametrize("gate", ["logit", "decay"])
+@pytest.mark.parametrize("T,B,D,layout,ragged", [(300, 10, 1024, "fused", True), (512, 21, 500, "bt", False),
+                                                 (700, 13, 1000, "dense", True), (1024, 11, 932, "dense", False)])
+def test_gated_many_channels(T, B, D, layout, ragged, gate):
+    """Many channels of some hundred steps each; a last state written over the first."""
+    f, x, _, h0, _, lens = _case(T, T, B, D, "bf16", gate, layout, ragged)
+    n = None if lens is None else lens.cpu().numpy()
+    rh, rT, eh, eT = gated_ref.gated(_np(f), _np(x), _np(h0), gate, n)
+    h, hT = g.gated_fwd(f, x, h0, gate=gate, lens=lens)
+    _within("h", h, rh, eh, "bf16")
+    _within("hT", hT, rT, eT)
+    h1, _ = g.gated_fwd(f, x, h0, gate=gate, lens=lens, out={"hT": h0})
+    assert torch.equal(h1, h) and torch.equal(h0, hT)
+
+
+@pytest.mark.parametrize("gate", ["logit", "decay"])
 @pytest.mark.parametrize("T,B,D", [(40000, 1, 70), (9000, 4, 258), (20011, 1, 129)])
 def test_gated_many_segments(T, B, D, gate):
     """Long sequences, against the definition in 64 bits on the device."""
