@@ -31,28 +31,46 @@ constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr unsigned kSpins = 1u << 20;  // polls of a word that is on its way
 constexpr uint64_t kNone = ~0ull;      // no sum yet (no sum is this NaN)
 constexpr double kLog2eD = 1.4426950408889634;
+constexpr int kAtOnce = 4;             // weights side by side (a lone wave waits for each step otherwise)
 
-// 2^(d k) for d <= 0 < k to a relative 1e-12, exactly 1 at d = 0, with low = -1100 / k; 0
+// d <- 2^(d k) for d <= 0 < k to a relative 1e-12, exactly 1 at d = 0, with low = -1100 / k; 0
 // below -1075 (and for a NaN).  d k = n + r with n the nearest whole number, 2^r = 1 + r q(r)
 // with q of degree 7 fitted on Chebyshev nodes of [-1/2, 1/2] by least squares on the
 // relative error, reweighted towards equal ripple (8e-13).  With the conversion and the
 // sum 16 64-bit instructions, whose issue bounds the sums: one takes a wave 5.3 to 5.9
 // cycles.  Sums of 37 million bf16 weights take 31 us, 23 of them the issue of 25 vector
-// instructions a weight.
-__device__ __forceinline__ double pow2(double d, double k, double low) {
-    d = fmax(d, low);
+// instructions a weight.  M at once: the draw launch has about a wave to a SIMD, which one
+// after another would wait for each instruction (1 x 5 x 32000 11.5 us for 10.3, 32 x 5 x
+// 128000 19.5 for 17.5).
+template <int M>
+__device__ __forceinline__ void pow2s(double *d, double k, double low) {
     const double big = 6755399441055744.0;  // 1.5 * 2^52: its lowest bits then hold n
-    const double s = fma(d, k, big);
-    const double r = fma(d, k, big - s);
-    double q = 0x1.61c51b381035fp-20;
-    q = fma(q, r, 0x1.00d858d17751cp-16);
-    q = fma(q, r, 0x1.430aa865450adp-13);
-    q = fma(q, r, 0x1.5d874cfcc70f3p-10);
-    q = fma(q, r, 0x1.3b2ab5ed76007p-7);
-    q = fma(q, r, 0x1.c6b08dcede4ffp-5);
-    q = fma(q, r, 0x1.ebfbdff8edf23p-3);
-    q = fma(q, r, 0x1.62e42fef89cbbp-1);
-    return __builtin_amdgcn_ldexp(fma(q, r, 1.0), (int)(uint32_t)__double_as_longlong(s));
+    constexpr double c[8] = {0x1.61c51b381035fp-20, 0x1.00d858d17751cp-16, 0x1.430aa865450adp-13, 0x1.5d874cfcc70f3p-10,
+                             0x1.3b2ab5ed76007p-7,  0x1.c6b08dcede4ffp-5,  0x1.ebfbdff8edf23p-3,  0x1.62e42fef89cbbp-1};
+    double s[M], r[M], q[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) d[i] = fmax(d[i], low);
+#pragma unroll
+    for (int i = 0; i < M; ++i) s[i] = fma(d[i], k, big);
+#pragma unroll
+    for (int i = 0; i < M; ++i) r[i] = big - s[i];
+#pragma unroll
+    for (int i = 0; i < M; ++i) r[i] = fma(d[i], k, r[i]);
+#pragma unroll
+    for (int i = 0; i < M; ++i) q[i] = fma(c[0], r[i], c[1]);
+#pragma unroll
+    for (int j = 2; j < 8; ++j) {
+#pragma unroll
+        for (int i = 0; i < M; ++i) q[i] = fma(q[i], r[i], c[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < M; ++i) q[i] = fma(q[i], r[i], 1.0);
+#pragma unroll
+    for (int i = 0; i < M; ++i) d[i] = __builtin_amdgcn_ldexp(q[i], (int)(uint32_t)__double_as_longlong(s[i]));
+}
+__device__ __forceinline__ double pow2(double d, double k, double low) {
+    pow2s<1>(&d, k, low);
+    return d;
 }
 __device__ __forceinline__ double lowest(double k) { return -1100.0 / k; }
 
@@ -183,7 +201,14 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs a, int 
     } else {
         const double ref = m == -INFINITY ? 0.0 : (double)m;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) s += pow2((double)x[i] - ref, scale, low);
+        for (int i = 0; i < PER; i += kAtOnce) {
+            double d[kAtOnce];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) d[j] = (double)x[i + j] - ref;
+            pow2s<kAtOnce>(d, scale, low);
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) s += d[j];
+        }
         s = wave_sum(s);
     }
     if (lane == 0) waves[w] = Part{bad ? NAN : s, m, first};
@@ -248,14 +273,26 @@ __device__ __forceinline__ void join(int live, int nch, int across, double scale
     }
 }
 
-// Weight of entry i of the row to draw from, of value x, y (draft's).  The products are
-// rounded before they are subtracted: where p equals q nothing is left, not the rounding
-// of one of them.
-__device__ __forceinline__ double weight(const Pick &p, float x, float y, int i, bool q) {
+// Weights of M entries from i on of the row to draw from, of values x, y (draft's).  The
+// products are rounded before they are subtracted: where p equals q nothing is left, not
+// the rounding of one of them.
+template <int M>
+__device__ __forceinline__ void weights(const Pick &p, const float *x, const float *y, int i, bool q, double *w) {
 #pragma clang fp contract(off)
-    const double w = pow2((double)x - p.mp, p.scale, p.low);
-    if (q) return fmax(w * p.ip - pow2((double)y - p.mq, p.scale, p.low) * p.iq, 0.0);
-    return i == p.drop ? 0.0 : w;
+    double v[M];
+#pragma unroll
+    for (int j = 0; j < M; ++j) w[j] = (double)x[j] - p.mp;
+    pow2s<M>(w, p.scale, p.low);
+    if (q) {
+#pragma unroll
+        for (int j = 0; j < M; ++j) v[j] = (double)y[j] - p.mq;
+        pow2s<M>(v, p.scale, p.low);
+#pragma unroll
+        for (int j = 0; j < M; ++j) w[j] = fmax(w[j] * p.ip - v[j] * p.iq, 0.0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < M; ++j) w[j] = i + j == p.drop ? 0.0 : w[j];
+    }
 }
 
 // NU units of the row to draw from (and of the draft's): units u, u + step, ... from the
@@ -352,7 +389,12 @@ __device__ __forceinline__ int draw(const VerifyArgs &a, Pick p, int b, int nch,
         load_pair<T, U>(a, p, b, (ch * kWaves + w) * 64 * U + lane, 64, false, x, y, i0);
         double s = 0.0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) s += weight(p, x[i], 0.0f, 0, false);
+        for (int i = 0; i < PER; i += kAtOnce) {
+            double wt[kAtOnce];
+            weights<kAtOnce>(p, x + i, y + i, 0, false, wt);
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) s += wt[j];
+        }
         s = wave_sum(s);
         if (lane == 0) total[w] = s;
         __syncthreads();
@@ -375,9 +417,10 @@ __device__ __forceinline__ int draw(const VerifyArgs &a, Pick p, int b, int nch,
     int i0;
     load_pair<T, NU>(a, p, b, at * 64 * U + (some ? tid * NU : 0), 1, q, x, y, i0);
 #pragma unroll
-    for (int i = 0; i < NU * N; ++i) {
-        wt[i] = some ? weight(p, x[i], y[i], i0 + i, q) : 0.0;
-        s += wt[i];
+    for (int i = 0; i < NU * N; i += kAtOnce) {
+        weights<kAtOnce>(p, x + i, y + i, i0 + i, q, wt + i);
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) s += wt[i + j] = some ? wt[i + j] : 0.0;
     }
     const double incl = scan(s);
     if (lane == 63) total[w] = incl;
@@ -475,7 +518,12 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int
         load_pair<T, U>(a, p, b, (ch * kWaves + w) * 64 * U + lane, 64, q, x, y, i0);
         double s = 0.0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) s += weight(p, x[i], y[i], i0 + (i / N) * 64 * N + i % N, q);
+        for (int i = 0; i < PER; i += kAtOnce) {
+            double wt[kAtOnce];
+            weights<kAtOnce>(p, x + i, y + i, i0 + (i / N) * 64 * N + i % N, q, wt);
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) s += wt[j];
+        }
         s = wave_sum(s);
         uint64_t *sums = strip_sums(a, nch, rows) + (int64_t)b * nch * kWaves;
         if (lane == 0)

@@ -430,13 +430,6 @@ def linattn_bwd(q, k, v, g, do, S0=None, dST=None, *, scale: Optional[float] = N
 
 
 # ------------------------------------------------- gated linear recurrence
-def _gate(gate):
-    c = _GATES.get(gate)
-    if c is None:
-        raise ValueError("gate must be 'logit' or 'decay', got %r" % (gate,))
-    return c
-
-
 def _row(t, name, dtype, shape, dev):
     """[T,B,D] with contiguous rows, any other strides."""
     if t.device != dev:
@@ -451,11 +444,12 @@ def _row(t, name, dtype, shape, dev):
     return _Seq(t.data_ptr(), st, sb)
 
 
-def _row_out(t, name, dtype, shape, dev):
-    """An output sequence: (tensor, view); a view given must not overlap itself."""
+def _row_out(t, name, dtype, shape, dev, like=None):
+    """An output sequence: (tensor, view); a view given must not overlap itself.
+    `like`: an operand of its type and shape, for a new one."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=dev)
-        return t, _Seq(t.data_ptr(), shape[1] * shape[2], shape[2])  # dense
+        t = torch.empty_like(like, memory_format=torch.contiguous_format)  # 0.9 us less than empty(shape)
+        return t, _Seq(t.data_ptr(), shape[1] * shape[2], shape[2])
     v = _row(t, name, dtype, shape, dev)
     need = shape[2]
     for step, n in sorted(((v.stride_t, shape[0]), (v.stride_b, shape[1]))):
@@ -512,7 +506,7 @@ def gated_fwd(f, x, h0=None, *, gate: str = "logit", lens=None, ws=None, out=Non
     state = (B, D)
     out = out or {}
     p0 = _state(h0, "h0", state, dev)
-    h, sh = _row_out(out.get("h"), "h", f.dtype, shape, dev)
+    h, sh = _row_out(out.get("h"), "h", f.dtype, shape, dev, f)
     hT = _new(out.get("hT"), "hT", torch.float32, state, dev)
     ws, wp, wn = _space(ws, _gated_space(OP_GATED_FWD, T, B, D, dt), dev)
     _ok(load().rnn_gated_fwd(GatedDims(T, B, D), dt, gt, sf, sx, p0, lp, sh, hT.data_ptr(), wp, wn, _current(dev)),
@@ -535,7 +529,7 @@ def gated_step(f, x, h, *, gate: str = "logit", h_out=None, out=None):
         h_out, p1 = h, p0
     else:
         p1 = _state(h_out, "h_out", (B, D), dev)
-    y, sy = _row_out(out, "out", f.dtype, shape, dev)
+    y, sy = _row_out(out, "out", f.dtype, shape, dev, f)
     _ok(load().rnn_gated_step(GatedDims(T, B, D), dt, gt, sf, sx, p0, sy, p1, _current(dev)), "rnn_gated_step")
     return y, h_out
 
@@ -553,8 +547,8 @@ def gated_bwd(f, x, h, dh, h0=None, dhT=None, *, gate: str = "logit", lens=None,
     p0 = _state(h0, "h0", state, dev)
     pT = _state(dhT, "dhT", state, dev)
     out = out or {}
-    df, sdf = _row_out(out.get("df"), "df", f.dtype, shape, dev)
-    dx, sdx = _row_out(out.get("dx"), "dx", f.dtype, shape, dev)
+    df, sdf = _row_out(out.get("df"), "df", f.dtype, shape, dev, f)
+    dx, sdx = _row_out(out.get("dx"), "dx", f.dtype, shape, dev, f)
     dh0 = _new(out.get("dh0"), "dh0", torch.float32, state, dev)
     ws, wp, wn = _space(ws, _gated_space(OP_GATED_BWD, T, B, D, dt), dev)
     _ok(load().rnn_gated_bwd(GatedDims(T, B, D), dt, gt, sf, sx, sh, sdh, p0, pT, lp, sdf, sdx, dh0.data_ptr(), wp,
