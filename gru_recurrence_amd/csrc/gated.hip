@@ -1,9 +1,11 @@
 // gated.hip -- gated linear recurrence: forward, single token, backward.
 //
 //   h_t = a_t h_{t-1} + b_t,  elementwise;  a, b from the gate's form:
-//   logit  a = sigmoid(f), b = (1 - a) x:  h + u (x - h) with u = sigmoid(-f), so
-//          that a gate near 1 does not lose its small side: a constant x is a
-//          fixed point, and the memory 1 / (1 - a) is right to float32
+//   logit  a = sigmoid(f), b = (1 - a) x, by the smaller side of the gate, to full
+//          relative accuracy:  h + u (x - h) with u = sigmoid(-f) where a > 1/2, so
+//          that a constant x is a fixed point and the memory 1 / (1 - a) is right to
+//          float32;  x - a (x - h) elsewhere, so that a closed gate leaves of a state,
+//          or lets through of a gradient, what it should and no rounding of the rest
 //   decay  a = f, b = x
 // Steps compose: (A1, B1) then (A2, B2) is (A2 A1, A2 B1 + B2).  Backward is the same
 // kind of recurrence from the end: e_t = a_t (dh_t + e_{t+1}).
@@ -35,7 +37,7 @@
 // while they wait for a carry, 87 and 72; tiles of 32 lanes 73 and 58 with the best of 8,
 // 12 and 16 steps for each; rows of 128 bytes and 1024 threads 73 and 52, of 256 bytes 67
 // and 55 (but 8192 x 16 x 2048 bf16 385 for 324).  1024 x 16 x 768 bf16 forward, one
-// workgroup to a sequence, 18.2 us (4.2 TB/s): all load, then all store.
+// workgroup to a sequence, 17.1 us (4.4 TB/s): all load, then all store.
 //
 // Stores go past the caches, but for the backward pass of bf16 (8192 x 16 x 2048 forward
 // 339 us for 324, 32768 x 1 x 768 float32 backward 131 for 125; 1000 x 16 x 1024 bf16
@@ -55,6 +57,8 @@ constexpr int kThreads = 512, kWaves = kThreads / 64;
 constexpr int kAll = 1024;   // most threads where one workgroup has all of a sequence
 constexpr int kNarrow = 16;  // its lanes along the channels
 constexpr int kGroup = 16;
+constexpr int kKept = 10;  // steps of sixteen whose gates four channels keep: as many as 128 registers
+                           // hold (1024 x 16 x 768 bf16 17.1 us; 8 17.7, none 19.7)
 constexpr int kHead = 128;           // bytes before the counters: the status word
 
 // How a call is cut, and the words that its segments exchange.
@@ -75,8 +79,18 @@ __device__ __forceinline__ uint64_t pack(float A, float B) {
 __device__ __forceinline__ void publish(uint64_t *p, float A, float B) {
     __hip_atomic_store(p, pack(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// 1 - sigmoid(f)
-__device__ __forceinline__ float shut(float f) { return rcp_fast(1.0f + exp_fast(f)); }
+// A gate from its logit: the smaller of sigmoid(f) and sigmoid(-f), with the sign of -f:
+// the gate is open (u stored) where that is set, +inf's zero among them.
+__device__ __forceinline__ float side(float f) {
+    const float e = exp_fast(-fabsf(f));
+    return copysignf(e * rcp_fast(1.0f + e), -f);
+}
+__device__ __forceinline__ float by_side(float s, float open, float shut) {
+    return __float_as_int(s) < 0 ? open : shut;
+}
+// a h + (1 - a) x and a h for the gate s
+__device__ __forceinline__ float mix(float s, float h, float x) { return fmaf(-s, x - h, by_side(s, h, x)); }
+__device__ __forceinline__ float part_of(float s, float h) { return fmaf(s, h, by_side(s, h, 0.0f)); }
 
 // This workgroup's segment and tile of channels.  Workgroups go round the eight XCDs:
 // where a tile's rows are short of a few cache lines (LN < 64), neighbouring tiles go to
@@ -359,16 +373,16 @@ __global__ __launch_bounds__(NT, 4) void gated_fwd_kernel(FwdArgs a) {
             xr[s] = *(const V *)(xp + t * a.x.st);
         }
     }
-    // what a step keeps beside x: u (logit) or a (decay); with four channels f, as there
-    // are no registers for them
-    constexpr bool keep = VEC < 4;
-    float g[keep ? S : 1][VEC], A[VEC], B[VEC], h[VEC], start[VEC];
+    // what a step keeps beside x: the gate's side (logit) or a (decay); with four channels
+    // there are registers for some, and the other steps keep f
+    constexpr int keep = VEC < 4 ? S : kKept;
+    float g[keep][VEC], A[VEC], B[VEC], h[VEC], start[VEC];
     auto gate = [&](int s, int v) {
         const float fv = to_f32<T>(fr[s].v[v]);
-        return LOGIT ? shut(fv) : fv;
+        return LOGIT ? side(fv) : fv;
     };
 #pragma unroll
-    for (int s = 0; s < (keep ? S : 0); ++s)
+    for (int s = 0; s < keep; ++s)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) g[s][v] = gate(s, v);
 #pragma unroll
@@ -383,15 +397,15 @@ __global__ __launch_bounds__(NT, 4) void gated_fwd_kernel(FwdArgs a) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 if (!all.value && t0 + s >= len) continue;
-                const float xv = to_f32<T>(xr[s].v[v]), gv = keep ? g[keep ? s : 0][v] : gate(s, v);
-                B[v] = LOGIT ? fmaf(gv, xv - B[v], B[v]) : fmaf(gv, B[v], xv);
-                A[v] = LOGIT ? fmaf(-gv, A[v], A[v]) : A[v] * gv;
+                const float xv = to_f32<T>(xr[s].v[v]), gv = s < keep ? g[s < keep ? s : 0][v] : gate(s, v);
+                B[v] = LOGIT ? mix(gv, B[v], xv) : fmaf(gv, B[v], xv);
+                A[v] = LOGIT ? part_of(gv, A[v]) : A[v] * gv;
             }
     });
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         forget(xr[s]);
-        if (!keep) forget(fr[s]);
+        if (s >= keep) forget(fr[s]);
     }
     if constexpr (LN == 64)
         join<VEC>(k, seg, c0, A, B, start, agg, car, h);
@@ -404,8 +418,8 @@ __global__ __launch_bounds__(NT, 4) void gated_fwd_kernel(FwdArgs a) {
             float o[VEC];
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                const float xv = to_f32<T>(xr[s].v[v]), gv = keep ? g[keep ? s : 0][v] : gate(s, v);
-                const float hn = LOGIT ? fmaf(gv, xv - h[v], h[v]) : fmaf(gv, h[v], xv);
+                const float xv = to_f32<T>(xr[s].v[v]), gv = s < keep ? g[s < keep ? s : 0][v] : gate(s, v);
+                const float hn = LOGIT ? mix(gv, h[v], xv) : fmaf(gv, h[v], xv);
                 const bool on = all.value || t0 + s < len;
                 h[v] = on ? hn : h[v];
                 o[v] = on ? hn : 0.0f;
@@ -426,7 +440,7 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedDims d, LinSeq f, 
     if (c >= (int64_t)d.B * d.D) return;
     const int b = (int)(c / d.D), i = (int)(c - (int64_t)b * d.D);
     const float fv = to_f32<T>(((const T *)f.p)[b * f.sb + i]), xv = to_f32<T>(((const T *)x.p)[b * x.sb + i]);
-    const float n = LOGIT ? fmaf(shut(fv), xv - h[c], h[c]) : fmaf(fv, h[c], xv);
+    const float n = LOGIT ? mix(side(fv), h[c], xv) : fmaf(fv, h[c], xv);
     h_out[c] = n;
     if (y.p) ((T *)y.p)[b * y.sb + i] = from_f32<T>(n);
 }
@@ -471,21 +485,14 @@ __global__ __launch_bounds__(NT, 4) void gated_bwd_kernel(BwdArgs a) {
             hr[s] = *(const V *)(hp + max(t - 1, (int64_t)0) * a.h.st);
         }
     }
-    // what a step keeps beside dh, x and h: u (logit) or a (decay), and a u (logit), to
-    // full relative accuracy where either is small
-    float g[S][VEC], au[LOGIT ? S : 1][VEC], A[VEC], B[VEC], start[VEC], e[VEC];
+    // what a step keeps beside dh, x and h: the gate's side (logit) or a (decay)
+    float g[S][VEC], A[VEC], B[VEC], start[VEC], e[VEC];
 #pragma unroll
     for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             const float fv = to_f32<T>(fr[s].v[v]);
-            if (LOGIT) {
-                const float ex = exp_fast(fv);
-                g[s][v] = rcp_fast(1.0f + ex);
-                au[LOGIT ? s : 0][v] = fminf(ex, 3e38f) * g[s][v] * g[s][v];
-            } else {
-                g[s][v] = fv;
-            }
+            g[s][v] = LOGIT ? side(fv) : fv;
         }
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
@@ -501,12 +508,12 @@ __global__ __launch_bounds__(NT, 4) void gated_bwd_kernel(BwdArgs a) {
             for (int v = 0; v < VEC; ++v) {
                 if (!all.value && (t0 - s >= len || t0 - s < 0)) continue;
                 const float q = B[v] + to_f32<T>(dr[s].v[v]);
-                B[v] = LOGIT ? fmaf(-g[s][v], q, q) : g[s][v] * q;
-                A[v] = LOGIT ? fmaf(-g[s][v], A[v], A[v]) : A[v] * g[s][v];
+                B[v] = LOGIT ? part_of(g[s][v], q) : g[s][v] * q;
+                A[v] = LOGIT ? part_of(g[s][v], A[v]) : A[v] * g[s][v];
             }
     });
 #pragma unroll
-    for (int s = 0; s < S; ++s) forget(dr[s]);
+    for (int s = 0; s < S; ++s) forget(dr[s]), forget(xr[s]), forget(hr[s]);
     if constexpr (LN == 64)
         join<VEC>(k, seg, c0, A, B, start, agg, car, e);
     else
@@ -524,9 +531,10 @@ __global__ __launch_bounds__(NT, 4) void gated_bwd_kernel(BwdArgs a) {
                 float before = to_f32<T>(hr[s].v[v]);
                 if (t == 0) before = a.h0 ? a.h0[c + v] : 0.0f;
                 if (LOGIT) {
-                    dx[v] = g[s][v] * q;
-                    df[v] = au[LOGIT ? s : 0][v] * q * (before - to_f32<T>(xr[s].v[v]));
-                    e[v] = on ? fmaf(-g[s][v], q, q) : e[v];
+                    const float small = fabsf(g[s][v]), less = small * q, more = fmaf(-small, q, q);
+                    dx[v] = by_side(g[s][v], less, more);
+                    df[v] = small * more * (before - to_f32<T>(xr[s].v[v]));
+                    e[v] = on ? by_side(g[s][v], more, less) : e[v];
                 } else {
                     dx[v] = q;
                     df[v] = q * before;

@@ -496,7 +496,7 @@ def workspace_size_gated(op: int, dims: GatedDims, dtype_code: int) -> int:
 def gated_fwd(f, x, h0=None, *, gate: str = "logit", lens=None, ws=None, out=None):
     """Gated linear recurrence over T tokens, elementwise in [T,B,D] views with
     contiguous rows: gate "logit" h_t = a h_{t-1} + (1 - a) x_t with a =
-    sigmoid(f_t), gate "decay" h_t = f_t h_{t-1} + x_t.  h0 [B,D] float32 or None
+    sigmoid(f_t) (-inf begins a sequence), gate "decay" h_t = f_t h_{t-1} + x_t.  h0 [B,D] float32 or None
     (zeros); lens [B] int32: tokens of each row that count (h is 0 behind them).
     Returns (h [T,B,D] in f's type, h_T [B,D] float32, the state behind the last
     token that counts); `out` is a dict with "h" (any view) and "hT" (may be h0)."""

@@ -3,14 +3,16 @@ and of the verification of drafted tokens, on the CPU, for the tests; they share
 no code with the library.  The recurrence comes with bounds of what float32
 evaluation may be off by.
 
-Its bounds, u = 2^-24 the float32 rounding unit.  1 - sigmoid(f) through
-exponential, sum and reciprocal is off by at most (2 |f| + 6) u relative: the
-exponent's product and constant |f| u each, exponential and reciprocal 2 u each,
-the sum u, and one more for slack.  A step h + s (x - h), s = 1 - a, adds the
-difference's and the step's own rounding; time is cut into segments whose
-products of a and whose joins add as many roundings again.  With M the
-recurrence over magnitudes (what sums and products of either order stay below),
-the error of h obeys E_t = a E_{t-1} + u ((2 |f| + 7) s (|x| + M) + 4 M)."""
+Its bounds, u = 2^-24 the float32 rounding unit.  The smaller side s of a gate, of
+sigmoid(f) and sigmoid(-f), through exponential, sum, reciprocal and product is off
+by at most (2 |f| + 6) u relative: the exponent's product and constant |f| u each,
+exponential and reciprocal 2 u each, the sum u and the product u.  It is all that is
+rounded of the gate: a step is h + s (x - h) or x - s (x - h) and adds the
+difference's and its own rounding; time is cut into segments whose products of a and
+whose joins add as many roundings again.  With M the recurrence over magnitudes (what
+sums and products of either order stay below), the error of h obeys
+E_t = a E_{t-1} + u ((2 |f| + 7) s (|x| + M_{t-1}) + 4 M_t), and that of a gradient
+through the gate En = a E + u ((2 |f| + 7) s + 4 a) M.  Past |f| = 120 s is 0."""
 import numpy as np
 
 U = 2.0 ** -24
@@ -40,7 +42,7 @@ def gated(f, x, h0, gate, lens=None):
             a, s = _sig(f[t])
             new = a * S + s * x[t]
             m = a * M + s * np.abs(x[t])
-            err = a * E + U * ((2 * np.abs(f[t]) + 7) * s * (np.abs(x[t]) + M) + 4 * m)
+            err = a * E + U * ((2 * np.minimum(np.abs(f[t]), 120) + 7) * np.minimum(a, s) * (np.abs(x[t]) + M) + 4 * m)
         else:
             a = np.abs(f[t])
             new = f[t] * S + x[t]
@@ -70,11 +72,11 @@ def gated_grad(f, x, h, dh, h0, dhT, gate, lens=None):
         Eg = Eg + U * mg
         if gate == "logit":
             a, s = _sig(f[t])
-            af = np.abs(f[t])
+            af = np.minimum(np.abs(f[t]), 120)
             df, dx, en = g * (before - x[t]) * a * s, s * g, a * g
             bx = s * (Eg + U * (2 * af + 8) * mg)
             bf = a * s * (np.abs(before) + np.abs(x[t])) * (Eg + U * (4 * af + 16) * mg)
-            En = a * Eg + U * ((2 * af + 7) * s * mg + 4 * mg)
+            En = a * Eg + U * ((2 * af + 7) * np.minimum(a, s) + 4 * a) * mg
         else:
             a = np.abs(f[t])
             df, dx, en = g * before, g, f[t] * g

@@ -279,8 +279,7 @@ def test_gated_extreme_gates():
                           (inf, h0.expand(T, B, D), h0), (200.0, h0.expand(T, B, D), h0)):
         f = torch.full((T, B, D), v, device="cuda")
         h, hT = g.gated_fwd(f, x, h0)
-        # shut: h + (x - h), one rounding of a difference of order 8
-        assert (h - want).abs().max() <= 2e-6 and (hT - last).abs().max() <= 2e-6
+        assert torch.equal(h, want.contiguous()) and torch.equal(hT, last)
         r = g.gated_bwd(f, x, h, torch.ones_like(x), h0, None)
         for k in r:
             assert torch.isfinite(r[k]).all(), (v, k)
@@ -294,6 +293,55 @@ def test_gated_extreme_gates():
     assert not hT.any() and torch.isfinite(h).all()
     h, hT = g.gated_fwd(torch.ones_like(f), torch.ones_like(f), None, gate="decay")
     assert torch.equal(h[:, 0, 0], torch.arange(1.0, T + 1, device="cuda"))
+
+
+@pytest.mark.parametrize("T,D", [(1, 64), (5, 130), (300, 40), (3000, 70), (600, 2048)])
+def test_gated_nearly_shut_gates(T, D):
+    """Gates of 1e-7 to 1e-4 between large and small values, a gradient from the last
+    token alone: what they let through is right relative to itself."""
+    rng = np.random.default_rng(T)
+    f = 3.0 * rng.standard_normal((T, 1, D)) + 3.0
+    low = rng.random(f.shape) < 0.05
+    low[0] = True
+    f[low] = -rng.uniform(9.0, 16.0, low.sum())
+    x = np.abs(rng.standard_normal(f.shape)) * 10.0 ** rng.integers(-4, 5, f.shape)
+    dh = np.zeros(f.shape)
+    dh[-1] = rng.standard_normal((1, D))
+    f, x, dh = (torch.from_numpy(t.astype(np.float32)).cuda() for t in (f, x, dh))
+    h0 = torch.full((1, D), 1e6, device="cuda")
+    h, hT = g.gated_fwd(f, x, h0)
+    rh, rT, eh, eT = gated_ref.gated(_np(f), _np(x), _np(h0), "logit")
+    _within("h", h, rh, eh)
+    _within("hT", hT, rT, eT)
+    if T == 1:
+        y, _ = g.gated_step(f, x, h0.clone())
+        _within("step", y, rh, eh)
+    r = g.gated_bwd(f, x, h, dh, h0)
+    ref, bound = gated_ref.gated_grad(_np(f), _np(x), _np(h), _np(dh), _np(h0), None, "logit")
+    for k in ref:
+        _within(k, r[k], ref[k], bound[k])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,B,D", [(7, 2, 33), (500, 3, 64), (2500, 1, 66), (900, 16, 1024)])
+def test_gated_logits_of_minus_infinity_begin_a_sequence(T, B, D, dt):
+    """Sequences packed along time: nothing passes from one to the next."""
+    rng = np.random.default_rng(T)
+    f, x, dh = (_rand(rng, (T, B, D), dt) for _ in range(3))
+    at = T // 2
+    x[:at] *= 1e6
+    f[at] = -float("inf")
+    h, hT = g.gated_fwd(f, x)
+    assert torch.equal(h[at], x[at])
+    h1, hT1 = g.gated_fwd(f[at:], x[at:])
+    n = [_np(t[at:]) for t in (f, x)]
+    rh, rT, eh, eT = gated_ref.gated(*n, None, "logit")
+    for y, yT in ((h[at:], hT), (h1, hT1)):
+        _within("h", y, rh, eh, dt)
+        _within("hT", yT, rT, eT)
+    dh[:at] = 0.0
+    r = g.gated_bwd(f, x, h, dh)
+    assert not r["dx"][:at].any() and not r["df"][:at].any() and not r["dh0"].any()
 
 
 def test_gated_nan_stays_in_its_channel_and_future():
