@@ -9,10 +9,12 @@
 // leaves the chunk's maximum and sum of weights.  The second joins those, decides how
 // many drafts stand (each workgroup of a sequence for itself) and sums w over the
 // strips of the row to draw from, a wave a strip; the sequence's last workgroup to
-// finish finds the strip in which the sum passes u, and the entry in it.  Sums are added
-// in the order of the strips, so nothing depends on which workgroup that is.  A sum is one 64-bit word
-// that says by its value that it is there; an ordered counter in its place would write
-// back and empty the caches of every workgroup (70 us for 58 at 32 x 5 x 128000).
+// finish finds the strip in which the sum passes u, and the entry in it.  In a large call
+// the first launch's sums serve where w is p, and one workgroup goes from the chunk to
+// the strip.  Sums are added in the order of the strips, so nothing depends on which
+// workgroup is last.  A sum is one 64-bit word that says by its value that it is there; an
+// ordered counter in its place would write back and empty the caches of every workgroup
+// (70 us for 58 at 32 x 5 x 128000).
 //
 // Weights and sums are 64-bit.  The borders between a vocabulary's V entries lie
 // 1/V of the sum apart on average; a sum of 32-bit terms is off by 1e-7 of it, so
@@ -31,6 +33,10 @@ constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr unsigned kSpins = 1u << 20;  // polls of a word that is on its way
 constexpr uint64_t kNone = ~0ull;      // no sum yet (no sum is this NaN)
 constexpr double kLog2eD = 1.4426950408889634;
+// Workgroups of a draw launch from which on a row of p is left to one of them: a longer
+// chain, but less work in all (64 x 1 x 128000, 2048 workgroups, 31 us for 36; 16 x 8 x
+// 50001, 208 of them, 17.5 either way).
+constexpr int kCrowd = 1024;
 constexpr int kAtOnce = 4;             // weights side by side (a lone wave waits for each step otherwise)
 
 // d <- 2^(d k) for d <= 0 < k to a relative 1e-12, exactly 1 at d = 0, with low = -1100 / k; 0
@@ -351,7 +357,7 @@ __device__ __forceinline__ int find_strip(const double *v, int n, float u, doubl
 }
 
 // One workgroup: the token drawn from the row that p names, given the sums of its strips
-// of 64 U units (and its parts, which are those of p alone).
+// of 64 U units (null where w is p) and its parts, which are those of p.
 template <typename T, int PER>
 __device__ __forceinline__ int draw(const VerifyArgs &a, Pick p, int b, int nch, bool q, const uint64_t *sums,
                                     const Part *parts) {
@@ -366,21 +372,21 @@ __device__ __forceinline__ int draw(const VerifyArgs &a, Pick p, int b, int nch,
     for (int j = 0; j < kMaxStrips; ++j) {
         uint64_t word = 0;
         // counted already, so stored already: on its way at most
-        for (unsigned spins = 0; j * 64 + lane < strips && spins < kSpins; ++spins) {
+        for (unsigned spins = 0; sums && j * 64 + lane < strips && spins < kSpins; ++spins) {
             word = __hip_atomic_load(sums + j * 64 + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             if (word != kNone) break;
         }
         v[j] = __longlong_as_double((long long)word);
     }
-    int at = find_strip(v, strips, u, before, goal);
-    if (at < 0) {  // nothing of p - q is left: p itself, first its chunk, then the strip
+    int at = sums ? find_strip(v, strips, u, before, goal) : -1;
+    if (at < 0) {  // p itself (or nothing of p - q is left): first its chunk, then the strip
         p.drop = -1;
         q = false;
 #pragma unroll
         for (int j = 0; j < kMaxStrips; ++j) {
             const Part c = j * 64 + lane < nch ? parts[j * 64 + lane] : Part{0.0, -INFINITY, 0};
+            // above 0 where its largest entry's weight, the same power of two, is
             v[j] = c.m == -INFINITY ? 0.0 : c.s * pow2((double)c.m - p.mp, p.scale, p.low);
-            if (v[j] < 1e-290) v[j] = 0.0;  // its entries would have none
         }
         const int ch = find_strip(v, nch, u, before, goal);
         if (ch < 0) return -1;
@@ -458,6 +464,8 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int
     const double scale = scale_of(a, b), low = lowest(scale);
     const Part *part = (const Part *)a.ws;
     const bool greedy = scale == 0.0, has_q = a.q.p != nullptr && !greedy;
+    const bool crowd = a.B * nch >= kCrowd;
+    if (ch != 0 && (greedy || (n == 0 && crowd))) return;  // one workgroup's work, below
     // the drafts' own logits, on their way while the rows are joined
     int id = a.V;
     float xd = 0.0f, yd = 0.0f, ud = 0.0f;
@@ -512,29 +520,32 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int
     const Pick p = pick;
     int token = p.token;
     if (token == -2) {
-        const bool q = has_q && p.acc < n;
-        float x[PER], y[PER];
-        int i0;
-        load_pair<T, U>(a, p, b, (ch * kWaves + w) * 64 * U + lane, 64, q, x, y, i0);
-        double s = 0.0;
+        const bool q = has_q && p.acc < n, own = crowd && !q && p.drop < 0;  // w is p
+        if (own && ch != 0) return;
+        uint64_t *sums = own ? nullptr : strip_sums(a, nch, rows) + (int64_t)b * nch * kWaves;
+        if (!own) {
+            float x[PER], y[PER];
+            int i0;
+            load_pair<T, U>(a, p, b, (ch * kWaves + w) * 64 * U + lane, 64, q, x, y, i0);
+            double s = 0.0;
 #pragma unroll
-        for (int i = 0; i < PER; i += kAtOnce) {
-            double wt[kAtOnce];
-            weights<kAtOnce>(p, x + i, y + i, i0 + (i / N) * 64 * N + i % N, q, wt);
+            for (int i = 0; i < PER; i += kAtOnce) {
+                double wt[kAtOnce];
+                weights<kAtOnce>(p, x + i, y + i, i0 + (i / N) * 64 * N + i % N, q, wt);
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) s += wt[j];
+                for (int j = 0; j < kAtOnce; ++j) s += wt[j];
+            }
+            s = wave_sum(s);
+            if (lane == 0)
+                __hip_atomic_store(sums + ch * kWaves + w, (uint64_t)__double_as_longlong(s), __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+            __syncthreads();
+            if (tid == 0)
+                done = __hip_atomic_fetch_add(counter(a, nch, rows) + b, 1u, __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_AGENT) == (unsigned)nch - 1;
+            __syncthreads();
+            if (!done) return;
         }
-        s = wave_sum(s);
-        uint64_t *sums = strip_sums(a, nch, rows) + (int64_t)b * nch * kWaves;
-        if (lane == 0)
-            __hip_atomic_store(sums + ch * kWaves + w, (uint64_t)__double_as_longlong(s), __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        if (tid == 0)
-            done = __hip_atomic_fetch_add(counter(a, nch, rows) + b, 1u, __ATOMIC_RELAXED,
-                                          __HIP_MEMORY_SCOPE_AGENT) == (unsigned)nch - 1;
-        __syncthreads();
-        if (!done) return;
         token = draw<T, PER>(a, p, b, nch, q, sums, part + ((int64_t)p.acc * a.B + b) * nch);
     } else if (ch != 0) {
         return;

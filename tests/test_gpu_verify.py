@@ -193,6 +193,20 @@ def test_verify_large_calls(dt):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["plain", "banned", "peaked", "equal"])
+@pytest.mark.parametrize("K", [0, 2])
+def test_verify_many_sequences(K, kind, dt):
+    """Enough sequences that a row of p is left to one workgroup; every place of u."""
+    B, V = 400, 9001
+    x, d, u, y, temp, n = _case(K + 31, K, B, V, dt, kind)
+    u[K] = torch.linspace(0.0, 1.0, B)
+    u[K, -1] = 1.0 - 2.0 ** -24
+    _check(x, d, u, y, temp, n)
+    _check(x, d, u, None, temp, n)
+    _check(x, d, u, y if K else None)
+
+
 @pytest.mark.parametrize("V", [7, 5000, 70001])
 def test_verify_nothing_left_of_the_difference(V):
     """The same model twice and u = 1: every draft is refused, max(p - q, 0) is 0
