@@ -259,7 +259,7 @@ rnn_status rnn_gated_fwd(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, c
     const size_t need = lm::gated_bytes(n, dt == RNN_BF16, false);
     if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;
     return done(lm::launch_gated_fwd(n, dt == RNN_BF16, seq_of(f), seq_of(x), h0, lens, out_of(h), hT,
-                                     ws, stream));
+                                     need ? ws : nullptr, stream));
 }
 
 rnn_status rnn_gated_step(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, const rnn_seq *f,
@@ -294,7 +294,8 @@ rnn_status rnn_gated_bwd(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, c
     const size_t need = lm::gated_bytes(n, dt == RNN_BF16, true);
     if (need && (!ws || ws_bytes < need)) return RNN_ERR_WORKSPACE;
     return done(lm::launch_gated_bwd(n, dt == RNN_BF16, seq_of(f), seq_or_none(x), seq_of(h), seq_of(dh),
-                                     h0, dhT, lens, out_of(df), out_of(dx), dh0, ws, stream));
+                                     h0, dhT, lens, out_of(df), out_of(dx), dh0, need ? ws : nullptr,
+                                     stream));
 }
 
 size_t rnn_workspace_size_clip(int count, const rnn_grad *list) {

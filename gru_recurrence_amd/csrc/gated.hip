@@ -68,7 +68,8 @@ struct Cut {
     int G;            // segments of a group
     int pitch;        // words between the tiles' counters
     unsigned spins;   // polls of a wait before it is given up (seconds), and noted in flag
-    unsigned *flag, *counter;
+    unsigned *flag;   // the status word; null: no workspace
+    unsigned *counter;
     uint64_t *word, *gword;  // [segment][channel], [group][channel]
 };
 
@@ -112,6 +113,12 @@ __device__ __forceinline__ void place(const Cut &k, int &seg, int &tile) {
         __syncthreads();
         seg = __builtin_amdgcn_readfirstlane(drawn);
     }
+}
+
+// A call of one segment waits for nothing and has no launch that clears its workspace:
+// the first workgroup clears the status word.
+__device__ __forceinline__ void no_waits(const Cut &k) {
+    if (k.nseg == 1 && k.flag && blockIdx.x == 0 && threadIdx.x == 0) *k.flag = 0;
 }
 
 // Parts along time of a workgroup with LN lanes along the channels, and a thread's.
@@ -431,6 +438,7 @@ __global__ __launch_bounds__(NT, 4) void gated_fwd_kernel(FwdArgs a) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) a.hT[c + v] = h[v];
     }
+    no_waits(k);
 }
 
 template <typename T, bool LOGIT>
@@ -552,6 +560,7 @@ __global__ __launch_bounds__(NT, 4) void gated_bwd_kernel(BwdArgs a) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) a.dh0[c + v] = e[v];
     }
+    no_waits(k);
 }
 
 __global__ __launch_bounds__(256) void gated_clear_kernel(uint4 *p, int64_t n) {

@@ -577,7 +577,8 @@ typedef struct {
 } rnn_seq_out;
 
 typedef enum { RNN_OP_GATED_FWD = 0, RNN_OP_GATED_BWD = 1 } rnn_gated_op;
-/* 0 where none is needed (then ws may be NULL) or the dims are invalid. */
+/* 0 where none is needed (then ws may be NULL and is not touched) or the dims are
+ * invalid. */
 size_t rnn_workspace_size_gated(rnn_gated_op op, const rnn_gated_dims *d, rnn_dtype dt);
 
 /* Forward over T tokens.  h0 may be NULL (zeros); hT (the state behind the last
