@@ -89,8 +89,10 @@ __device__ __forceinline__ float side(float f) {
 __device__ __forceinline__ float by_side(float s, float open, float shut) {
     return __float_as_int(s) < 0 ? open : shut;
 }
-// a h + (1 - a) x and a h for the gate s
-__device__ __forceinline__ float mix(float s, float h, float x) { return fmaf(-s, x - h, by_side(s, h, x)); }
+// a h + (1 - a) x and a h for the gate s.  s (x - h) as s x less s h, whose rounding the
+// first takes along: x - h may leave float32 where h and x do not, and what lies between
+// them does not either.
+__device__ __forceinline__ float mix(float s, float h, float x) { return by_side(s, h, x) - fmaf(s, x, -(s * h)); }
 __device__ __forceinline__ float part_of(float s, float h) { return fmaf(s, h, by_side(s, h, 0.0f)); }
 
 // This workgroup's segment and tile of channels.  Workgroups go round the eight XCDs:
@@ -541,7 +543,9 @@ __global__ __launch_bounds__(NT, 4) void gated_bwd_kernel(BwdArgs a) {
                 if (LOGIT) {
                     const float small = fabsf(g[s][v]), less = small * q, more = fmaf(-small, q, q);
                     dx[v] = by_side(g[s][v], less, more);
-                    df[v] = small * more * (before - to_f32<T>(xr[s].v[v]));
+                    // half the difference: all of it may leave float32
+                    const float half = fmaf(0.5f, before, -0.5f * to_f32<T>(xr[s].v[v]));
+                    df[v] = 2.0f * (small * more) * half;
                     e[v] = on ? by_side(g[s][v], more, less) : e[v];
                 } else {
                     dx[v] = q;

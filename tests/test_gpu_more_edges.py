@@ -40,3 +40,42 @@ def test_gated_status_is_ok_on_a_workspace_holding_garbage(T, B, D, odd):
         ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
         call(ws)
         assert g.workspace_status(ws) == g.RNN_OK
+
+
+def _huge(T, B, D, dt, seed):
+    """Values up to near the type's largest with both signs, logits of any size and
+    infinite ones."""
+    rng = np.random.default_rng(seed)
+    f = 4.0 * rng.standard_normal((T, B, D))
+    pick = rng.random((T, B, D))
+    f[pick < 0.15], f[pick > 0.85] = -np.inf, np.inf
+
+    def big(shape):
+        return rng.choice([-1.0, 1.0], shape) * 10.0 ** rng.uniform(37.0, 38.5, shape)
+    x, h0 = big((T, B, D)), big((B, D))
+    t = [torch.from_numpy(a.astype(np.float32)).cuda() for a in (f, x)]
+    return [a.to(DT[dt]) for a in t] + [torch.from_numpy(h0.astype(np.float32)).cuda()]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,B,D", [(1, 2, 33), (7, 1, 64), (300, 2, 40), (3000, 1, 66), (700, 13, 1000)])
+def test_gated_values_whose_difference_leaves_float32(T, B, D, dt):
+    """A logit gate's h lies between its state and x, finite where those are; an
+    infinite logit passes the one as it is and nothing of the other."""
+    f, x, h0 = _huge(T, B, D, dt, T)
+    h, hT = g.gated_fwd(f, x, h0)
+    rh, rT, eh, eT = gated_ref.gated(_np(f), _np(x), _np(h0), "logit")
+    _within("h", h, rh, eh, dt)
+    _within("hT", hT, rT, eT)
+    begin = f == -float("inf")
+    assert torch.equal(h[begin], x[begin])
+    if T == 1:
+        y, S = g.gated_step(f, x, h0.clone())
+        _within("step", y, rh, eh, dt)
+        _within("state", S, rT, eT)
+    rng = np.random.default_rng(1)
+    dh = torch.from_numpy((1e-3 * rng.standard_normal((T, B, D))).astype(np.float32)).cuda().to(DT[dt])
+    r = g.gated_bwd(f, x, h, dh, h0)
+    ref, bound = gated_ref.gated_grad(_np(f), _np(x), _np(h), _np(dh), _np(h0), None, "logit")
+    for k in ref:
+        _within(k, r[k], ref[k], bound[k], dt if k != "dh0" else "f32")
