@@ -2,6 +2,10 @@
 // token log probabilities, linear attention, gated linear recurrence, gradient
 // clipping, draft verification): argument checks, workspace sizes and the
 // launches (lm.h).
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "../../include/rnn355.h"
 #include "host.h"
 #include "lm.h"
@@ -90,12 +94,55 @@ bool clip_list_ok(int count, const rnn_grad *list) {
     return true;
 }
 
+// Whether what clipping writes (outputs, the norm) touches no other tensor, nor its own
+// values but at their place: workgroups write while others still read.  Spans by their
+// starts, each against the furthest end so far.
+struct Span {
+    uintptr_t lo, hi;
+    bool written;
+};
+bool apart(int count, const rnn_grad *list, const float *norm, Span *span) {
+    int64_t n = 0;
+    auto add = [&](const void *p, int64_t bytes, bool written) {
+        span[n++] = Span{(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, written};
+    };
+    add(norm, sizeof(float), true);
+    for (int i = 0; i < count; ++i) {
+        const rnn_grad &t = list[i];
+        if (t.n == 0) continue;
+        const int64_t bytes = t.n * elt(t.dtype);
+        const bool in_place = !t.out || t.out == t.data;
+        add(t.data, bytes, in_place);
+        if (!in_place) add(t.out, bytes, true);
+    }
+    std::sort(span, span + n, [](const Span &a, const Span &b) { return a.lo < b.lo; });
+    uintptr_t any = 0, written = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        if (span[i].lo < (span[i].written ? any : written)) return false;
+        any = std::max(any, span[i].hi);
+        if (span[i].written) written = std::max(written, span[i].hi);
+    }
+    return true;
+}
+// RNN_ERR_HIP: no host memory for a long list's spans.
+rnn_status clip_apart(int count, const rnn_grad *list, const float *norm) {
+    constexpr int kFew = 255;
+    Span few[2 * kFew + 1];
+    std::unique_ptr<Span[]> many(count > kFew ? new (std::nothrow) Span[2 * (size_t)count + 1] : nullptr);
+    if (count > kFew && !many) return RNN_ERR_HIP;
+    return apart(count, list, norm, many ? many.get() : few) ? RNN_OK : RNN_ERR_INVALID_ARG;
+}
+
 // max_norm < 0: the norm alone
 rnn_status clip(int count, const rnn_grad *list, float max_norm, float *norm, void *ws,
                 size_t ws_bytes, hipStream_t stream) {
     if (!clip_list_ok(count, list) || !norm || !view_ok(norm, 4) || !aligned16(ws))
         return RNN_ERR_INVALID_ARG;
     if (!ws || ws_bytes < lm::clip_bytes()) return RNN_ERR_WORKSPACE;
+    if (max_norm >= 0.0f) {
+        const rnn_status st = clip_apart(count, list, norm);
+        if (st != RNN_OK) return st;
+    }
     return lm::launch_clip(count, list, max_norm, norm, ws, stream) == hipSuccess ? RNN_OK : RNN_ERR_HIP;
 }
 

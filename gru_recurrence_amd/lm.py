@@ -20,7 +20,7 @@ from typing import Optional
 
 import torch
 
-from . import RNN_BF16, RNN_F32, RNN_OK, RnnError, load as _load
+from . import RNN_BF16, RNN_ERR_INVALID_ARG, RNN_F32, RNN_OK, RnnError, load as _load
 
 __all__ = ["embed_fwd", "embed_bwd", "token_logprobs", "token_logprobs_bwd", "linattn_fwd",
            "linattn_step", "linattn_bwd", "LinDims", "workspace_size_embed_bwd",
@@ -563,7 +563,8 @@ _get_dtype, _get_shape = operator.attrgetter("dtype"), operator.attrgetter("shap
 class GradList:
     """Gradients checked once, for programs whose gradient buffers stay where they
     are: `grads` are contiguous bfloat16 or float32 tensors of one device, `out`
-    (None: in place) tensors of the same types and shapes."""
+    (None: in place) tensors of the same types and shapes.  For clipping an output
+    may be its own gradient, but not overlap another one or another output."""
 
     def __init__(self, grads, out=None):
         grads = list(grads)
@@ -617,8 +618,10 @@ def _clip(g, max_norm, norm, ws):
         _ok(lib.rnn_grad_norm(g.count, g.array, norm.data_ptr(), wp, wn, _current(dev)),
             "rnn_grad_norm")
     else:
-        _ok(lib.rnn_clip_grads(g.count, g.array, max_norm, norm.data_ptr(), wp, wn, _current(dev)),
-            "rnn_clip_grads")
+        s = lib.rnn_clip_grads(g.count, g.array, max_norm, norm.data_ptr(), wp, wn, _current(dev))
+        if s == RNN_ERR_INVALID_ARG and wp % 16 == 0:  # all else is checked
+            raise ValueError("an output, or norm, overlaps another tensor")
+        _ok(s, "rnn_clip_grads")
     return norm
 
 
@@ -631,8 +634,8 @@ def grad_norm(grads, *, norm=None, ws=None, stream=None):
 
 def clip_grads(grads, max_norm: float, *, out=None, norm=None, ws=None, stream=None):
     """Scale gradients by max_norm / norm where their global 2-norm exceeds
-    max_norm, in place or into the tensors of `out` (a GradList brings its own).
-    Returns the norm before that, a float32 scalar on the device; where it is not
+    max_norm, in place or into the tensors of `out` (a GradList brings its own),
+    none of which may overlap another gradient or output.  Returns the norm before that, a float32 scalar on the device; where it is not
     finite the gradients stay as they are."""
     if isinstance(grads, GradList):
         if out is not None:

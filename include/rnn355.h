@@ -616,9 +616,10 @@ rnn_status rnn_gated_bwd(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, c
  * the values as they are (a program drops such a step).  norm: one float.
  * Squares are summed in 64 bits, in an order that the list sets, so results
  * repeat bit for bit and finite gradients always have a finite sum; a norm past
- * float32 is written as +inf, and clips all the same.  max_norm >= 0.  Tensors
- * may overlap none of the outputs but their own.  count >= 1; the values of all
- * tensors at most 2^40.
+ * float32 is written as +inf, and clips all the same.  max_norm >= 0.  Outputs
+ * and norm may not overlap each other or any tensor, but for an output that is
+ * its tensor's `data`: RNN_ERR_INVALID_ARG (tensors that are only read may
+ * overlap).  count >= 1; the values of all tensors at most 2^40.
  */
 typedef struct {
     const void *data;

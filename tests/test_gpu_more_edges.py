@@ -79,3 +79,34 @@ def test_gated_values_whose_difference_leaves_float32(T, B, D, dt):
     ref, bound = gated_ref.gated_grad(_np(f), _np(x), _np(h), _np(dh), _np(h0), None, "logit")
     for k in ref:
         _within(k, r[k], ref[k], bound[k], dt if k != "dh0" else "f32")
+
+
+def test_clip_outputs_next_to_each_other():
+    """Tensors and outputs that touch are apart; those that overlap are refused."""
+    big = torch.randn(40000, device="cuda")
+    keep = big.clone()
+    cut = [100 * i + (i * i) % 100 for i in range(331)]
+    for count in (5, 330):
+        big.copy_(keep)
+        parts = [big[lo:hi] for lo, hi in zip(cut[:count], cut[1:])]
+        norm, ref = gated_ref.clip([_np(t) for t in parts], 1.0)
+        g.clip_grads(parts, 1.0)
+        for o, r in zip(parts, ref):
+            assert (np.abs(_np(o) - r) <= 4 * U * np.abs(r)).all()
+        assert torch.equal(big[cut[count]:], keep[cut[count]:])
+    a, b = keep[:100], keep[100:200]
+    out = torch.full((200,), 7.0, device="cuda")
+    for grads, to in (([a, b], [b, a]), ([a, b], [a, a]), ([a, b], [out[:100], out[99:199]]),
+                      ([a, b], [out[:100], keep[150:250]]), ([a], [keep[1:101]])):
+        with pytest.raises(ValueError):
+            g.clip_grads(grads, 1.0, out=to)
+    with pytest.raises(ValueError):
+        g.clip_grads([a, keep[99:150]], 1.0)
+    with pytest.raises(ValueError):
+        g.clip_grads([a, b], 1.0, norm=keep[5])
+    assert (out == 7.0).all()
+    # what is only read may overlap, and a norm is of any list
+    g.clip_grads([a, keep[50:150]], 1.0, out=[out[:100], out[100:]])
+    norm, ref = gated_ref.clip([_np(a), _np(keep[50:150])], 1.0)
+    assert (np.abs(_np(out) - np.concatenate(ref)) <= 4 * U * np.abs(np.concatenate(ref))).all()
+    assert abs(g.grad_norm([a, a, keep[50:150]]).item() - np.sqrt(norm ** 2 + (_np(a) ** 2).sum())) <= 4 * U * norm * 2
