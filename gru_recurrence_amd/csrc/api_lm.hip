@@ -381,7 +381,7 @@ rnn_status rnn_verify_drafts(int K, int B, int V, rnn_dtype dt, const rnn_seq *l
     if (!ws || ws_bytes < lm::verify_bytes(K, B, V)) return RNN_ERR_WORKSPACE;
     lm::VerifyArgs a{K, B, V, seq_of(logits), K > 0 ? seq_or_none(draft_logits) : lm::LinSeq{nullptr, 0, 0},
                      K > 0 ? ids_of(drafts, K, B) : lm::Ids{nullptr, 0, 0, 1, 1, 0}, u, temperature,
-                     n_drafts, tokens, accepted, ws};
+                     n_drafts, tokens, accepted, ws, spin_limit()};
     return done(lm::launch_verify(a, dt == RNN_BF16, stream));
 }
 

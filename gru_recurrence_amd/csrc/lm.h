@@ -155,6 +155,7 @@ struct VerifyArgs {
     const int *n;           // may be null
     int *tokens, *accepted;
     void *ws;
+    unsigned spins;  // polls of a wait before it is given up, and noted in the workspace's status word
 };
 size_t verify_bytes(int K, int B, int V);
 bool verify_grid_ok(int K, int B, int V);

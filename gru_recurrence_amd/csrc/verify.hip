@@ -30,7 +30,7 @@ namespace lm {
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr unsigned kSpins = 1u << 20;  // polls of a word that is on its way
+constexpr int kHead = 128;             // bytes before the parts: the status word
 constexpr uint64_t kNone = ~0ull;      // no sum yet (no sum is this NaN)
 constexpr double kLog2eD = 1.4426950408889634;
 // Workgroups of a draw launch from which on a row of p is left to one of them: a longer
@@ -158,9 +158,10 @@ __device__ __forceinline__ const T *row_of(const LinSeq &s, int k, int b) {
     return (const T *)s.p + (int64_t)k * s.st + (int64_t)b * s.sb;
 }
 
-// The workspace: parts [rows][B][nch], sums of strips [B][nch kWaves], counters [B].
+// The workspace: status word, parts [rows][B][nch], sums of strips [B][nch kWaves], counters [B].
+__device__ __forceinline__ Part *parts_of(const VerifyArgs &a) { return (Part *)((char *)a.ws + kHead); }
 __device__ __forceinline__ uint64_t *strip_sums(const VerifyArgs &a, int nch, int rows) {
-    return (uint64_t *)((Part *)a.ws + (int64_t)rows * a.B * nch);
+    return (uint64_t *)(parts_of(a) + (int64_t)rows * a.B * nch);
 }
 __device__ __forceinline__ unsigned *counter(const VerifyArgs &a, int nch, int rows) {
     return (unsigned *)(strip_sums(a, nch, rows) + (int64_t)a.B * nch * kWaves);
@@ -179,7 +180,10 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs a, int 
     const double scale = scale_of(a, b), low = lowest(scale);
     const bool draft = r > a.K, greedy = scale == 0.0;
     if (r == 0 && tid < kWaves) strip_sums(a, nch, rows)[((int64_t)b * nch + ch) * kWaves + tid] = kNone;
-    if (r == 0 && ch == 0 && tid == 0) counter(a, nch, rows)[b] = 0;
+    if (r == 0 && ch == 0 && tid == 0) {
+        counter(a, nch, rows)[b] = 0;
+        if (b == 0) *(unsigned *)a.ws = 0;
+    }
     if (draft ? r - a.K - 1 >= n || greedy : r > n) return;  // a row that nothing asks for
     const Row<T> row(draft ? row_of<T>(a.q, r - a.K - 1, b) : row_of<T>(a.logits, r, b), a.V);
     const int u0 = ch * (kThreads * U);
@@ -232,7 +236,7 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs a, int 
             s += greedy ? q.s : q.s * pow2((double)q.m - (double)m, scale, low);
             if (q.m == m) first = min(first, q.at);
         }
-        ((Part *)a.ws)[blockIdx.x] = Part{s, m, first};
+        parts_of(a)[blockIdx.x] = Part{s, m, first};
     }
 }
 
@@ -357,10 +361,10 @@ __device__ __forceinline__ int find_strip(const double *v, int n, float u, doubl
 }
 
 // One workgroup: the token drawn from the row that p names, given the sums of its strips
-// of 64 U units (null where w is p) and its parts, which are those of p.
+// of 64 U units (null where w is p) and its parts, which are those of p.  lost: LDS, 0.
 template <typename T, int PER>
 __device__ __forceinline__ int draw(const VerifyArgs &a, Pick p, int b, int nch, bool q, const uint64_t *sums,
-                                    const Part *parts) {
+                                    const Part *parts, int *lost) {
     constexpr int N = Row<T>::N, U = PER / N, NU = U >= kWaves ? U / kWaves : 1;
     __shared__ double total[kWaves];
     __shared__ int found, last;
@@ -368,18 +372,28 @@ __device__ __forceinline__ int draw(const VerifyArgs &a, Pick p, int b, int nch,
     if (tid == 0) found = 0x7FFFFFFF, last = -1;
     const float u = fminf(fmaxf(a.u[(int64_t)a.K * a.B + b], 0.0f), 1.0f);
     double v[kMaxStrips], before, goal;
+    int at = -1;
+    if (sums) {
 #pragma unroll
-    for (int j = 0; j < kMaxStrips; ++j) {
-        uint64_t word = 0;
-        // counted already, so stored already: on its way at most
-        for (unsigned spins = 0; sums && j * 64 + lane < strips && spins < kSpins; ++spins) {
-            word = __hip_atomic_load(sums + j * 64 + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (word != kNone) break;
+        for (int j = 0; j < kMaxStrips; ++j) {
+            uint64_t word = 0;
+            // counted already, so stored already: on its way at most
+            for (unsigned spins = 0; j * 64 + lane < strips && spins < a.spins; ++spins) {
+                word = __hip_atomic_load(sums + j * 64 + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                if (word != kNone) break;
+            }
+            v[j] = __longlong_as_double((long long)word);
         }
-        v[j] = __longlong_as_double((long long)word);
+        at = find_strip(v, strips, u, before, goal);
+        if (goal != goal) {  // a wave's wait ran out: noted, and nothing drawn, below
+            *lost = 1;
+            __hip_atomic_store((unsigned *)a.ws, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            at = 0;
+        }
     }
-    int at = sums ? find_strip(v, strips, u, before, goal) : -1;
     if (at < 0) {  // p itself (or nothing of p - q is left): first its chunk, then the strip
+        __syncthreads();
+        if (*lost) return -1;  // another wave's
         p.drop = -1;
         q = false;
 #pragma unroll
@@ -449,6 +463,7 @@ __device__ __forceinline__ int draw(const VerifyArgs &a, Pick p, int b, int nch,
         atomicMax(&last, end);
     }
     __syncthreads();
+    if (*lost) return -1;
     return found != 0x7FFFFFFF ? found : last;
 }
 
@@ -457,12 +472,13 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int
     constexpr int N = Row<T>::N, U = PER / N;
     __shared__ Joined all[2 * kMaxDrafts + 1];
     __shared__ Pick pick;
-    __shared__ int done;
+    __shared__ int done, lost;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int b = blockIdx.x / nch, ch = blockIdx.x - b * nch;
     const int n = drafts_of(a, b);
     const double scale = scale_of(a, b), low = lowest(scale);
-    const Part *part = (const Part *)a.ws;
+    const Part *part = parts_of(a);
+    if (tid == 0) lost = 0;
     const bool greedy = scale == 0.0, has_q = a.q.p != nullptr && !greedy;
     const bool crowd = a.B * nch >= kCrowd;
     if (ch != 0 && (greedy || (n == 0 && crowd))) return;  // one workgroup's work, below
@@ -546,7 +562,7 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int
             __syncthreads();
             if (!done) return;
         }
-        token = draw<T, PER>(a, p, b, nch, q, sums, part + ((int64_t)p.acc * a.B + b) * nch);
+        token = draw<T, PER>(a, p, b, nch, q, sums, part + ((int64_t)p.acc * a.B + b) * nch, &lost);
     } else if (ch != 0) {
         return;
     }
@@ -589,7 +605,8 @@ hipError_t verify_by_size(const VerifyArgs &a, hipStream_t s) {
 size_t verify_bytes(int K, int B, int V) {
     // the larger chunk count of the two types and sizes
     const size_t nch = chunks(V, kThreads * kFew, 2);
-    return ((size_t)(2 * K + 1) * nch * sizeof(Part) + nch * kWaves * sizeof(double) + sizeof(unsigned)) * B;
+    const size_t each = (size_t)(2 * K + 1) * nch * sizeof(Part) + nch * kWaves * sizeof(double) + sizeof(unsigned);
+    return std::max<size_t>(4096, kHead + each * B);  // rnn_workspace_status takes no less than 4 KiB
 }
 
 bool verify_grid_ok(int K, int B, int V) {

@@ -661,6 +661,9 @@ rnn_status rnn_clip_grads(int count, const rnn_grad *list, float max_norm, float
  * with any weight is drawn.
  * Weights and sums are 64-bit: 32 bits would move the borders of a long
  * vocabulary's cumulated sum by more than they are apart.
+ * A sequence's last workgroup may wait for a sum that is on its way, with a
+ * bounded spin as described above: should that run out it draws -1, and the
+ * workspace's status word says so (rnn_workspace_status).
  * K <= 63, V <= 1000000, B * (2 K + 1) chunks of 4096 values in one launch, else
  * RNN_ERR_UNSUPPORTED.
  */

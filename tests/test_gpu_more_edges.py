@@ -110,3 +110,29 @@ def test_clip_outputs_next_to_each_other():
     norm, ref = gated_ref.clip([_np(a), _np(keep[50:150])], 1.0)
     assert (np.abs(_np(out) - np.concatenate(ref)) <= 4 * U * np.abs(np.concatenate(ref))).all()
     assert abs(g.grad_norm([a, a, keep[50:150]]).item() - np.sqrt(norm ** 2 + (_np(a) ** 2).sum())) <= 4 * U * norm * 2
+
+
+@pytest.mark.parametrize("K,B,V", [(0, 3, 50), (4, 1, 32000), (2, 400, 9001), (0, 400, 9001)])
+def test_verify_status(K, B, V, monkeypatch):
+    """The workspace reports the call that used it last, whatever it held.  With one
+    poll allowed (set from the host) a sum that is still on its way gives -1 and a
+    status; one that is there gives the token."""
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    x = 2.0 * torch.randn((K + 1, B, V), generator=gen, device="cuda")
+    y = 2.0 * torch.randn((K, B, V), generator=gen, device="cuda")
+    d = torch.randint(0, V, (K, B), generator=gen, device="cuda")
+    u = torch.rand((K + 1, B), generator=gen, device="cuda")
+    n = g.workspace_size_verify(K, B, V)
+    for q in (y, None):
+        ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+        want, acc = g.verify_drafts(x, d, u, q, ws=ws)
+        assert g.workspace_status(ws) == g.RNN_OK
+        rt, ra = gated_ref.verify(_np(x), d.cpu().numpy(), _np(u), None if q is None else _np(q))
+        assert np.array_equal(want.cpu().numpy(), rt) and np.array_equal(acc.cpu().numpy(), ra)
+        monkeypatch.setenv("RNN355_SPIN_LIMIT", "1")
+        tokens, acc1 = g.verify_drafts(x, d, u, q, ws=ws)
+        status = g.workspace_status(ws)
+        monkeypatch.delenv("RNN355_SPIN_LIMIT")
+        lost = tokens != want
+        assert torch.equal(acc, acc1) and (tokens[lost] == -1).all()
+        assert status == (g.RNN_ERR_BARRIER_TIMEOUT if lost.any() else g.RNN_OK)
