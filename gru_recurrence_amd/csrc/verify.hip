@@ -283,9 +283,11 @@ __device__ __forceinline__ void join(int live, int nch, int across, double scale
     }
 }
 
-// Weights of M entries from i on of the row to draw from, of values x, y (draft's).  The
-// products are rounded before they are subtracted: where p equals q nothing is left, not
-// the rounding of one of them.
+// Weights of M entries from i on of the row to draw from, of values x, y (draft's).  A
+// difference of less than kNoise of p counts as nothing: p and q of the same distribution
+// differ by up to four times 8e-13, since their sums run in another order where the rows
+// start at different places of their 16 bytes (and pow2 rounds twice on a sum's way).
+constexpr double kNoise = 0x1p-37;
 template <int M>
 __device__ __forceinline__ void weights(const Pick &p, const float *x, const float *y, int i, bool q, double *w) {
 #pragma clang fp contract(off)
@@ -298,7 +300,10 @@ __device__ __forceinline__ void weights(const Pick &p, const float *x, const flo
         for (int j = 0; j < M; ++j) v[j] = (double)y[j] - p.mq;
         pow2s<M>(v, p.scale, p.low);
 #pragma unroll
-        for (int j = 0; j < M; ++j) w[j] = fmax(w[j] * p.ip - v[j] * p.iq, 0.0);
+        for (int j = 0; j < M; ++j) {
+            const double pj = w[j] * p.ip, left = pj - v[j] * p.iq;
+            w[j] = left > kNoise * pj ? left : 0.0;
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < M; ++j) w[j] = i + j == p.drop ? 0.0 : w[j];

@@ -653,11 +653,12 @@ rnn_status rnn_clip_grads(int count, const rnn_grad *list, float max_norm, float
  * behind them are not read.
  * tokens [K+1][B] int32: the accepted drafts, the drawn token, then -1;
  * accepted [B] int32.
- * -inf rules a token out.  A draft outside [0, V) is refused.  Where no weight is
- * left in max(p - q, 0), p is drawn from.  A row that rules everything out, or
- * holds a NaN or +inf, accepts nothing and draws -1 (as draft: takes nothing
- * from p if it rules everything out, draws -1 otherwise).  u outside [0, 1] is
- * taken as the nearer end, a NaN as 0; at the very end of the sum the last entry
+ * -inf rules a token out.  A draft outside [0, V) is refused.  A difference p - q
+ * of less than 2^-37 of p counts as 0 (the weights are right to 10^-12).  Where no
+ * weight is left in max(p - q, 0), p is drawn from.  A row that rules everything
+ * out, or holds a NaN or +inf, accepts nothing and draws -1 (as draft: takes
+ * nothing from p if it rules everything out, draws -1 otherwise).  u outside [0, 1]
+ * is taken as the nearer end, a NaN as 0; at the very end of the sum the last entry
  * with any weight is drawn.
  * Weights and sums are 64-bit: 32 bits would move the borders of a long
  * vocabulary's cumulated sum by more than they are apart.

@@ -136,3 +136,27 @@ def test_verify_status(K, B, V, monkeypatch):
         lost = tokens != want
         assert torch.equal(acc, acc1) and (tokens[lost] == -1).all()
         assert status == (g.RNN_ERR_BARRIER_TIMEOUT if lost.any() else g.RNN_OK)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [50, 5001, 70001])
+def test_verify_equal_rows_that_start_elsewhere(V, dt):
+    """The same distribution twice, the draft's rows at another place of their 16
+    bytes: nothing is left of the difference, and p itself is drawn from, where a
+    draft is refused that has no probability in either, or is outside."""
+    K, B = 2, 60
+    rng = np.random.default_rng(V)
+    x = torch.from_numpy((2.0 * rng.standard_normal((K + 1, B, V))).astype(np.float32)).to(DT[dt]).cuda()
+    d = torch.from_numpy(rng.integers(0, V, (K, B))).cuda()
+    u = torch.from_numpy(rng.random((K + 1, B)).astype(np.float32)).cuda()
+    d[:, ::2] = -1
+    bidx = torch.arange(1, B, 2, device="cuda")
+    x[0, bidx, d[0, bidx]] = -float("inf")
+    for pad in ((3, 0), (1, 4), (0, 1)):
+        y = torch.nn.functional.pad(x[:K], pad)[..., pad[0]:pad[0] + V]
+        tokens, acc = g.verify_drafts(x, d, u, y)
+        rt, ra = gated_ref.verify(_np(x), d.cpu().numpy(), _np(u), _np(y))
+        assert not ra.any() and np.array_equal(acc.cpu().numpy(), ra)
+        assert np.array_equal(tokens.cpu().numpy(), rt)
+        want, _ = g.verify_drafts(x[:1], None, u[K:])
+        assert torch.equal(tokens[:1], want)
