@@ -134,12 +134,12 @@ rnn_status clip_apart(int count, const rnn_grad *list, const float *norm) {
 }
 
 // max_norm < 0: the norm alone
-rnn_status clip(int count, const rnn_grad *list, float max_norm, float *norm, void *ws,
+rnn_status clip(int count, const rnn_grad *list, double max_norm, float *norm, void *ws,
                 size_t ws_bytes, hipStream_t stream) {
     if (!clip_list_ok(count, list) || !norm || !view_ok(norm, 4) || !aligned16(ws))
         return RNN_ERR_INVALID_ARG;
     if (!ws || ws_bytes < lm::clip_bytes()) return RNN_ERR_WORKSPACE;
-    if (max_norm >= 0.0f) {
+    if (max_norm >= 0.0) {
         const rnn_status st = clip_apart(count, list, norm);
         if (st != RNN_OK) return st;
     }
@@ -351,12 +351,12 @@ size_t rnn_workspace_size_clip(int count, const rnn_grad *list) {
 
 rnn_status rnn_grad_norm(int count, const rnn_grad *list, float *norm, void *ws, size_t ws_bytes,
                          hipStream_t stream) {
-    return clip(count, list, -1.0f, norm, ws, ws_bytes, stream);
+    return clip(count, list, -1.0, norm, ws, ws_bytes, stream);
 }
 
-rnn_status rnn_clip_grads(int count, const rnn_grad *list, float max_norm, float *norm, void *ws,
+rnn_status rnn_clip_grads(int count, const rnn_grad *list, double max_norm, float *norm, void *ws,
                           size_t ws_bytes, hipStream_t stream) {
-    if (!(max_norm >= 0.0f)) return RNN_ERR_INVALID_ARG;
+    if (!(max_norm >= 0.0)) return RNN_ERR_INVALID_ARG;
     return clip(count, list, max_norm, norm, ws, ws_bytes, stream);
 }
 

@@ -205,10 +205,10 @@ __device__ __forceinline__ double share_squares(const Group &g, int lo, int hi) 
 }
 
 // The factor of a sum of squares, and whether the values change.
-__device__ __forceinline__ bool factor(double s, float max_norm, double &c) {
+__device__ __forceinline__ bool factor(double s, double max_norm, double &c) {
     const double n = sqrt(s);
-    const bool over = n > (double)max_norm && n < (double)INFINITY;
-    c = over ? (double)max_norm / n : 1.0;
+    const bool over = n > max_norm && n < (double)INFINITY;
+    c = over ? max_norm / n : 1.0;
     return over;
 }
 
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(kThreads) void norm_only_kernel(const double *slot,
 }
 
 __global__ __launch_bounds__(kThreads) void scale_kernel(Group g, const double *slot, int slots,
-                                                         float max_norm, float *norm) {
+                                                         double max_norm, float *norm) {
     __shared__ double tmp[kThreads / 64];
     const double s = total(slot, slots, tmp);
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = (float)sqrt(s);
@@ -263,12 +263,12 @@ __global__ __launch_bounds__(kThreads) void scale_kernel(Group g, const double *
 }
 
 // A list of few pieces.  max_norm < 0: the norm alone.
-__global__ __launch_bounds__(kOne) void one_kernel(Group g, float max_norm, float *norm) {
+__global__ __launch_bounds__(kOne) void one_kernel(Group g, double max_norm, float *norm) {
     __shared__ double tmp[kOne / 64];
     const int all = g.first[g.count];
     const double s = block_sum<kOne>(share_squares<kOne>(g, 0, all), tmp);
     if (threadIdx.x == 0) norm[0] = (float)sqrt(s);
-    if (max_norm < 0.0f) return;
+    if (max_norm < 0.0) return;
     double c;
     const bool over = factor(s, max_norm, c);
     share_scale<kOne>(g, 0, all, over, c);
@@ -310,7 +310,7 @@ int grid_of(const Group &g, int most) {
 
 size_t clip_bytes() { return kSlots * sizeof(double); }
 
-hipError_t launch_clip(int count, const rnn_grad *list, float max_norm, float *norm, void *ws,
+hipError_t launch_clip(int count, const rnn_grad *list, double max_norm, float *norm, void *ws,
                        hipStream_t s) {
     double *slot = (double *)ws;
     Group g;
@@ -328,7 +328,7 @@ hipError_t launch_clip(int count, const rnn_grad *list, float max_norm, float *n
         if (groups > 1) at = fill(&g, count, list, at);
         hipLaunchKernelGGL(norm_kernel, dim3(i ? grid_of(g, slots) : slots), dim3(kThreads), 0, s, g, slot, i > 0);
     }
-    if (max_norm < 0.0f) {
+    if (max_norm < 0.0) {
         hipLaunchKernelGGL(norm_only_kernel, dim3(1), dim3(kThreads), 0, s, slot, slots, norm);
         return hipGetLastError();
     }

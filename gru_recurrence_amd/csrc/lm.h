@@ -142,7 +142,7 @@ hipError_t launch_gated_bwd(const GatedDims &d, bool bf16, LinSeq f, LinSeq x, L
 // ---- gradient norm and clipping (clip.hip)
 size_t clip_bytes();
 // max_norm < 0: the norm alone
-hipError_t launch_clip(int count, const rnn_grad *list, float max_norm, float *norm, void *ws,
+hipError_t launch_clip(int count, const rnn_grad *list, double max_norm, float *norm, void *ws,
                        hipStream_t s);
 
 // ---- verification of drafted tokens (verify.hip)

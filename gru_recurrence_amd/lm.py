@@ -70,8 +70,8 @@ def load():
     lib = _load()
     if lib is _declared:
         return lib
-    P, I, S, L, F = (ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64,
-                     ctypes.c_float)
+    P, I, S, L, F, D = (ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64,
+                        ctypes.c_float, ctypes.c_double)
     ids, seq, dims = ctypes.POINTER(_Ids), ctypes.POINTER(_Seq), ctypes.POINTER(LinDims)
     gated, grads = ctypes.POINTER(GatedDims), P  # rnn_grad[count] as its bytes
     for name, res, args in (
@@ -91,7 +91,7 @@ def load():
             ("rnn_gated_bwd", I, [gated, I, I, seq, seq, seq, seq, P, P, P, seq, seq, P, P, S, P]),
             ("rnn_workspace_size_clip", S, [I, grads]),
             ("rnn_grad_norm", I, [I, grads, P, P, S, P]),
-            ("rnn_clip_grads", I, [I, grads, F, P, P, S, P]),
+            ("rnn_clip_grads", I, [I, grads, D, P, P, S, P]),
             ("rnn_workspace_size_verify", S, [I] * 3),
             ("rnn_verify_drafts", I, [I, I, I, I, seq, ids, seq, P, P, P, P, P, P, S, P])):
         f = getattr(lib, name)

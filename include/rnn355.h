@@ -616,10 +616,11 @@ rnn_status rnn_gated_bwd(const rnn_gated_dims *d, rnn_dtype dt, rnn_gate gate, c
  * the values as they are (a program drops such a step).  norm: one float.
  * Squares are summed in 64 bits, in an order that the list sets, so results
  * repeat bit for bit and finite gradients always have a finite sum; a norm past
- * float32 is written as +inf, and clips all the same.  max_norm >= 0.  Outputs
- * and norm may not overlap each other or any tensor, but for an output that is
- * its tensor's `data`: RNN_ERR_INVALID_ARG (tensors that are only read may
- * overlap).  count >= 1; the values of all tensors at most 2^40.
+ * float32 is written as +inf, and clips all the same.  max_norm >= 0, which a
+ * double holds as it is given.  Outputs and norm may not overlap each other or any
+ * tensor, but for an output that is its tensor's `data`: RNN_ERR_INVALID_ARG
+ * (tensors that are only read may overlap).  count >= 1; the values of all tensors
+ * at most 2^40.
  */
 typedef struct {
     const void *data;
@@ -630,7 +631,7 @@ typedef struct {
 size_t rnn_workspace_size_clip(int count, const rnn_grad *list);
 rnn_status rnn_grad_norm(int count, const rnn_grad *list, float *norm, void *ws, size_t ws_bytes,
                          hipStream_t stream);
-rnn_status rnn_clip_grads(int count, const rnn_grad *list, float max_norm, float *norm, void *ws,
+rnn_status rnn_clip_grads(int count, const rnn_grad *list, double max_norm, float *norm, void *ws,
                           size_t ws_bytes, hipStream_t stream);
 
 /*

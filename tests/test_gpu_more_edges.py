@@ -160,3 +160,22 @@ def test_verify_equal_rows_that_start_elsewhere(V, dt):
         assert np.array_equal(tokens.cpu().numpy(), rt)
         want, _ = g.verify_drafts(x[:1], None, u[K:])
         assert torch.equal(tokens[:1], want)
+
+
+@pytest.mark.parametrize("sizes", [[(777,), (31,)], [(300000,), (1,), (70000, 3)]], ids=str)
+def test_clip_bound_keeps_its_bits(sizes):
+    """The bound is taken in 64 bits as it is given: a float32 result is off by its
+    own rounding alone, half a step, and a bound past float32 clips."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    grads = [torch.randn(n, generator=gen, device="cuda") for n in sizes]
+    for bound in (0.1, 1.0 / 3.0, 1e-4 * np.pi):
+        norm, ref = gated_ref.clip([_np(t) for t in grads], bound)
+        out = [torch.empty_like(t) for t in grads]
+        g.clip_grads(grads, bound, out=out)
+        for o, r in zip(out, ref):
+            # the sum's, the root's and the factor's 64-bit roundings: below 1e-12
+            assert (np.abs(_np(o) - r) <= (U + 1e-12) * np.abs(r) + 1e-45).all(), bound
+    t = torch.full((300,), 3e38, device="cuda")
+    g.clip_grads([t], 1e39)
+    want = 1e39 / np.sqrt(300)
+    assert (np.abs(_np(t) - want) <= (U + 1e-12) * want).all()
