@@ -130,9 +130,18 @@ __device__ __forceinline__ double squares(const void *p, int64_t n, int64_t lo, 
 }
 
 // g c, rounded once (a factor below float32's normal numbers would lose its bits there).
+// bf16 by way of 21 bits of the product, the last of them set where anything is cut off
+// behind: those are exact in float32 (normal numbers), and lie on a middle of two bf16
+// numbers only where the product does.
 template <typename T>
 __device__ __forceinline__ T scaled(T g, double c) {
-    return from_f32<T>((float)((double)to_f32<T>(g) * c));
+    double v = (double)to_f32<T>(g) * c;
+    if constexpr (sizeof(T) == 2) {
+        const uint64_t b = (uint64_t)__double_as_longlong(v);
+        const uint32_t hi = (uint32_t)(b >> 32) | min((uint32_t)b, 1u);
+        v = __longlong_as_double((long long)((uint64_t)hi << 32));
+    }
+    return from_f32<T>((float)v);
 }
 
 template <typename T>

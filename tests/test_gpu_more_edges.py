@@ -179,3 +179,29 @@ def test_clip_bound_keeps_its_bits(sizes):
     g.clip_grads([t], 1e39)
     want = 1e39 / np.sqrt(300)
     assert (np.abs(_np(t) - want) <= (U + 1e-12) * want).all()
+
+
+@pytest.mark.parametrize("n", [4, 1 << 20])
+def test_clip_bf16_next_to_a_midpoint(n):
+    """Ones of norm sqrt(n), clipped so that the result lies 2^-30 to either side of
+    the middle of two bf16 numbers: the nearer one, whichever is even."""
+    for k in (1, 2):
+        mid = 0.5 + (k + 0.5) * 2.0 ** -8
+        for off, want in ((-2.0 ** -30, 0.5 + k * 2.0 ** -8), (2.0 ** -30, 0.5 + (k + 1) * 2.0 ** -8)):
+            t = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+            out = torch.empty_like(t)
+            g.clip_grads([t], float(np.sqrt(n)) * (mid + off), out=[out])
+            assert (out.double() == want).all(), (k, off, out[0].item())
+
+
+def test_clip_bf16_rounds_once():
+    """Random values and bounds against the 64-bit product rounded to bf16 once, bit for
+    bit (the product is off by less than 2^-45 of itself: one border in 10^10 values)."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    t = torch.randn(40001, generator=gen, device="cuda").bfloat16()
+    v, out = _np(t), torch.empty_like(t)
+    norm = float(np.sqrt((v ** 2).sum()))
+    for share in np.random.default_rng(3).uniform(0.1, 1.0, 40):
+        g.clip_grads([t], share * norm, out=[out])
+        m, e = np.frexp(v * (share * norm / norm))  # |m| in [1/2, 1): eight bits of it
+        assert np.array_equal(_np(out), np.ldexp(np.rint(m * 256.0), e - 8)), share
