@@ -469,6 +469,14 @@ def _state(t, name, shape, dev):
     return t.data_ptr()
 
 
+def _refused(s, what, **states):
+    """Raises what a call of the gated recurrence was refused for."""
+    for name, t in states.items():
+        if s == RNN_ERR_INVALID_ARG and t is not None and t.data_ptr() % 16:
+            raise ValueError("%s must start at a multiple of 16 bytes (a row of a larger tensor may not)" % name)
+    raise RnnError(s, what)
+
+
 def _gated(f, x, gate, lens):
     dev, shape, dtype = f.device, f.shape, f.dtype
     dt, gt = _dt(f, "f"), _GATES.get(gate)
@@ -496,8 +504,9 @@ def workspace_size_gated(op: int, dims: GatedDims, dtype_code: int) -> int:
 def gated_fwd(f, x, h0=None, *, gate: str = "logit", lens=None, ws=None, out=None):
     """Gated linear recurrence over T tokens, elementwise in [T,B,D] views with
     contiguous rows: gate "logit" h_t = a h_{t-1} + (1 - a) x_t with a =
-    sigmoid(f_t) (-inf begins a sequence), gate "decay" h_t = f_t h_{t-1} + x_t.  h0 [B,D] float32 or None
-    (zeros); lens [B] int32: tokens of each row that count (h is 0 behind them).
+    sigmoid(f_t) (-inf begins a sequence), gate "decay" h_t = f_t h_{t-1} + x_t.
+    h0 [B,D] float32 or None (zeros; states start at a multiple of 16 bytes); lens
+    [B] int32: tokens of each row that count (h is 0 behind them).
     Returns (h [T,B,D] in f's type, h_T [B,D] float32, the state behind the last
     token that counts); `out` is a dict with "h" (any view) and "hT" (may be h0)."""
     if x is None:
@@ -509,8 +518,9 @@ def gated_fwd(f, x, h0=None, *, gate: str = "logit", lens=None, ws=None, out=Non
     h, sh = _row_out(out.get("h"), "h", f.dtype, shape, dev, f)
     hT = _new(out.get("hT"), "hT", torch.float32, state, dev)
     ws, wp, wn = _space(ws, _gated_space(OP_GATED_FWD, T, B, D, dt), dev)
-    _ok(load().rnn_gated_fwd(GatedDims(T, B, D), dt, gt, sf, sx, p0, lp, sh, hT.data_ptr(), wp, wn, _current(dev)),
-        "rnn_gated_fwd")
+    s = load().rnn_gated_fwd(GatedDims(T, B, D), dt, gt, sf, sx, p0, lp, sh, hT.data_ptr(), wp, wn, _current(dev))
+    if s != RNN_OK:
+        _refused(s, "rnn_gated_fwd", h0=h0, hT=hT)
     return h, hT
 
 
@@ -530,7 +540,9 @@ def gated_step(f, x, h, *, gate: str = "logit", h_out=None, out=None):
     else:
         p1 = _state(h_out, "h_out", (B, D), dev)
     y, sy = _row_out(out, "out", f.dtype, shape, dev, f)
-    _ok(load().rnn_gated_step(GatedDims(T, B, D), dt, gt, sf, sx, p0, sy, p1, _current(dev)), "rnn_gated_step")
+    s = load().rnn_gated_step(GatedDims(T, B, D), dt, gt, sf, sx, p0, sy, p1, _current(dev))
+    if s != RNN_OK:
+        _refused(s, "rnn_gated_step", h=h, h_out=h_out)
     return y, h_out
 
 
@@ -551,8 +563,10 @@ def gated_bwd(f, x, h, dh, h0=None, dhT=None, *, gate: str = "logit", lens=None,
     dx, sdx = _row_out(out.get("dx"), "dx", f.dtype, shape, dev, f)
     dh0 = _new(out.get("dh0"), "dh0", torch.float32, state, dev)
     ws, wp, wn = _space(ws, _gated_space(OP_GATED_BWD, T, B, D, dt), dev)
-    _ok(load().rnn_gated_bwd(GatedDims(T, B, D), dt, gt, sf, sx, sh, sdh, p0, pT, lp, sdf, sdx, dh0.data_ptr(), wp,
-                             wn, _current(dev)), "rnn_gated_bwd")
+    s = load().rnn_gated_bwd(GatedDims(T, B, D), dt, gt, sf, sx, sh, sdh, p0, pT, lp, sdf, sdx, dh0.data_ptr(), wp,
+                             wn, _current(dev))
+    if s != RNN_OK:
+        _refused(s, "rnn_gated_bwd", h0=h0, dhT=dhT, dh0=dh0)
     return {"df": df, "dx": dx, "dh0": dh0}
 
 

@@ -205,3 +205,20 @@ def test_clip_bf16_rounds_once():
         g.clip_grads([t], share * norm, out=[out])
         m, e = np.frexp(v * (share * norm / norm))  # |m| in [1/2, 1): eight bits of it
         assert np.array_equal(_np(out), np.ldexp(np.rint(m * 256.0), e - 8)), share
+
+
+def test_gated_states_that_start_elsewhere_are_refused_by_name():
+    f, x, dh = (torch.randn((1, 1, 129), device="cuda") for _ in range(3))
+    s = torch.randn((2, 129), device="cuda")[1:]
+    for call, name in ((lambda: g.gated_fwd(f, x, s), "h0"), (lambda: g.gated_fwd(f, x, out={"hT": s}), "hT"),
+                       (lambda: g.gated_step(f, x, s), "h"), (lambda: g.gated_step(f, x, s.clone(), h_out=s), "h_out"),
+                       (lambda: g.gated_bwd(f, x, x, dh, s), "h0"), (lambda: g.gated_bwd(f, x, x, dh, None, s), "dhT"),
+                       (lambda: g.gated_bwd(f, x, x, dh, out={"dh0": s}), "dh0")):
+        with pytest.raises(ValueError, match=name + " must start"):
+            call()
+    # what is read value by value may start anywhere
+    logits = torch.randn((1, 3, 50), device="cuda")
+    u, t = torch.rand((2, 3), device="cuda"), torch.rand(4, device="cuda") + 0.5
+    tokens, _ = g.verify_drafts(logits, None, u[1:], temperature=t[1:])
+    want, _ = g.verify_drafts(logits, None, u[1:].clone(), temperature=t[1:].clone())
+    assert torch.equal(tokens, want)

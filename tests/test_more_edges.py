@@ -44,3 +44,16 @@ def test_clip_refuses_overlapping_outputs(rows, more):
         for lst in (lst + _far(more), _far(more) + lst):
             a = _list(*lst)
             assert lib.rnn_clip_grads(len(lst), a, 1.0, NORM, FAKE + (1 << 40), BIG, None) == g.RNN_ERR_INVALID_ARG
+
+
+def test_states_must_start_at_16_bytes():
+    """Rows of a state whose width is no multiple of four values: the library's refusal
+    is explained by name, others as they come."""
+    many = torch.zeros((5, 129))
+    at = [i for i in range(5) if many[i].data_ptr() % 16]
+    with pytest.raises(ValueError, match="hT must start.*16 bytes"):
+        lm._refused(g.RNN_ERR_INVALID_ARG, "rnn_gated_fwd", h0=None, hT=many[at[0]:at[0] + 1])
+    for s, t in ((g.RNN_ERR_INVALID_ARG, None), (g.RNN_ERR_UNSUPPORTED, many[at[0]])):
+        with pytest.raises(g.RnnError) as e:
+            lm._refused(s, "rnn_gated_fwd", h0=t)
+        assert e.value.status == s
