@@ -1,11 +1,13 @@
 // gated.hip -- gated linear recurrence: forward, single token, backward.
 //
 //   h_t = a_t h_{t-1} + b_t,  elementwise;  a, b from the gate's form:
-//   logit  a = sigmoid(f), b = (1 - a) x, by the smaller side of the gate, to full
-//          relative accuracy:  h + u (x - h) with u = sigmoid(-f) where a > 1/2, so
-//          that a constant x is a fixed point and the memory 1 / (1 - a) is right to
-//          float32;  x - a (x - h) elsewhere, so that a closed gate leaves of a state,
-//          or lets through of a gradient, what it should and no rounding of the rest
+//   logit  a = sigmoid(f), b = (1 - a) x, by the smaller side of the gate, which is right to
+//          (2 |f| + 6) 2^-24 of itself (the exponent's product and constant are rounded to
+//          float32) and 0 below float32's normal numbers (|f| > 87.3):  h + u (x - h) with
+//          u = sigmoid(-f) where a > 1/2, so that a constant x is a fixed point and the
+//          memory 1 / (1 - a) is as right as u;  x - a (x - h) elsewhere, so that a closed
+//          gate leaves of a state, or lets through of a gradient, what it should and no
+//          rounding of the rest
 //   decay  a = f, b = x
 // Steps compose: (A1, B1) then (A2, B2) is (A2 A1, A2 B1 + B2).  Backward is the same
 // kind of recurrence from the end: e_t = a_t (dh_t + e_{t+1}).

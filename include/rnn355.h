@@ -549,6 +549,8 @@ rnn_status rnn_linattn_bwd(const rnn_lin_dims *d, rnn_dtype dt, const rnn_seq *q
  *   RNN_GATE_DECAY  a_t = f_t:           h_t = a_t h_{t-1} + x_t
  * A logit may be infinite: at -inf a_t is 0, nothing of a finite state passes and
  * a new sequence begins; at +inf the state stays as it is.
+ * The smaller of a_t and 1 - a_t is right to (2 |f_t| + 6) 2^-24 of itself, and 0
+ * below float32's normal numbers (|f_t| > 87.3).
  * f, x, h and the gradients are sequences of D contiguous values for each
  * (t, b) in dtype dt: views at any strides (rnn_seq; rnn_seq_out for outputs),
  * so the halves of one projection and batch-first arrays are read and written

@@ -222,3 +222,15 @@ def test_gated_states_that_start_elsewhere_are_refused_by_name():
     tokens, _ = g.verify_drafts(logits, None, u[1:], temperature=t[1:])
     want, _ = g.verify_drafts(logits, None, u[1:].clone(), temperature=t[1:].clone())
     assert torch.equal(tokens, want)
+
+
+def test_gated_smaller_side_of_the_gate():
+    """Read from one step: a itself of a state of 1 and an x of 0 where the gate is shut,
+    1 - a of an x of 1 and a state of 0 where it is open, against sigmoid in 64 bits."""
+    v = np.concatenate([np.linspace(0.0, 87.2, 200001), 2.0 ** np.arange(-20.0, 0.0)])
+    v = torch.from_numpy(v.astype(np.float32)).cuda()[None, None]
+    zero, one = torch.zeros_like(v), torch.ones_like(v)
+    ref = np.exp(-_np(v)) / (1.0 + np.exp(-_np(v)))
+    for f, x, h0 in ((-v, zero, one[0]), (v, one, zero[0])):
+        err = np.abs(_np(g.gated_step(f, x, h0.clone())[0]) - ref)
+        assert (err <= (2 * _np(v) + 6) * U * ref).all()
