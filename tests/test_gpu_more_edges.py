@@ -234,3 +234,49 @@ def test_gated_smaller_side_of_the_gate():
     for f, x, h0 in ((-v, zero, one[0]), (v, one, zero[0])):
         err = np.abs(_np(g.gated_step(f, x, h0.clone())[0]) - ref)
         assert (err <= (2 * _np(v) + 6) * U * ref).all()
+
+
+@pytest.mark.parametrize("gate", ["logit", "decay"])
+@pytest.mark.parametrize("T,B,D", [(6000, 4, 258), (20011, 1, 129)])
+def test_gated_many_segments_bound_carried(T, B, D, gate):
+    """Long float32 sequences within the bounds that gated_ref derives, carried along
+    the 64-bit definition on the device step by step."""
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    f = torch.randn((T, B, D), generator=gen, device="cuda") + 3.0
+    f = f if gate == "logit" else torch.sigmoid(f)
+    x, dh = (torch.randn((T, B, D), generator=gen, device="cuda") for _ in range(2))
+    h0, dhT = (torch.randn((B, D), generator=gen, device="cuda") for _ in range(2))
+    h, hT = g.gated_fwd(f, x, h0, gate=gate)
+    r = g.gated_bwd(f, x, h, dh, h0, dhT, gate=gate)
+    fd = f.double()
+    if gate == "logit":
+        a, s = torch.sigmoid(fd), torch.sigmoid(-fd)
+        w = (2 * fd.abs() + 7) * torch.minimum(a, s)
+    else:
+        a, s, w = fd, torch.ones_like(fd), torch.zeros_like(fd)
+    ok = torch.ones((), dtype=torch.bool, device="cuda")
+    S, M, E = h0.double(), h0.double().abs(), torch.zeros((B, D), dtype=torch.float64, device="cuda")
+    for t in range(T):
+        xt = x[t].double()
+        m = a[t] * M + s[t] * xt.abs()
+        E = a[t] * E + U * (w[t] * (xt.abs() + M) + 4 * m)
+        S, M = a[t] * S + s[t] * xt, m
+        ok &= ((h[t] - S).abs() <= E).all()
+    assert ok and ((hT - S).abs() <= E).all()
+    e, m, E = dhT.double(), dhT.double().abs(), torch.zeros_like(S)
+    af = fd.abs() if gate == "logit" else torch.zeros_like(fd)
+    for t in range(T - 1, -1, -1):
+        gt, mg = e + dh[t].double(), m + dh[t].double().abs()
+        Eg = E + U * mg
+        bx = s[t] * (Eg + U * (2 * af[t] + 8) * mg) if gate == "logit" else Eg
+        ok &= ((r["dx"][t] - s[t] * gt).abs() <= bx).all()
+        before = h[t - 1].double() if t else h0.double()
+        if gate == "logit":
+            w2, df = a[t] * s[t], gt * (before - x[t].double()) * a[t] * s[t]
+            bf = w2 * (before.abs() + x[t].double().abs()) * (Eg + U * (4 * af[t] + 16) * mg)
+        else:
+            df, bf = gt * before, before.abs() * (Eg + U * mg)
+        ok &= ((r["df"][t] - df).abs() <= bf).all()
+        E = a[t] * Eg + U * (w[t] + 4 * a[t]) * mg
+        e, m = a[t] * gt, a[t] * mg
+    assert ok and ((r["dh0"] - e).abs() <= E).all()
