@@ -39,11 +39,11 @@
 // while they wait for a carry, 87 and 72; tiles of 32 lanes 73 and 58 with the best of 8,
 // 12 and 16 steps for each; rows of 128 bytes and 1024 threads 73 and 52, of 256 bytes 67
 // and 55 (but 8192 x 16 x 2048 bf16 385 for 324).  1024 x 16 x 768 bf16 forward, one
-// workgroup to a sequence, 17.1 us (4.4 TB/s): all load, then all store.
+// workgroup to a sequence, 17.7 us (4.3 TB/s): all load, then all store.
 //
 // Stores go past the caches, but for the backward pass of bf16 (8192 x 16 x 2048 forward
-// 339 us for 324, 32768 x 1 x 768 float32 backward 131 for 125; 1000 x 16 x 1024 bf16
-// backward however 48.9 for 49.8).
+// 350 us for 338, 32768 x 1 x 768 float32 backward 131 for 126; 1000 x 16 x 1024 bf16
+// backward however 49.3 for 50.9).
 #include <algorithm>
 #include <type_traits>
 
@@ -60,7 +60,7 @@ constexpr int kAll = 1024;   // most threads where one workgroup has all of a se
 constexpr int kNarrow = 16;  // its lanes along the channels
 constexpr int kGroup = 16;
 constexpr int kKept = 10;  // steps of sixteen whose gates four channels keep: as many as 128 registers
-                           // hold (1024 x 16 x 768 bf16 17.1 us; 8 17.7, none 19.7)
+                           // hold (1024 x 16 x 768 bf16 18.1 us in a graph; 8 19.3, one 21.6)
 constexpr int kHead = 128;           // bytes before the counters: the status word
 
 // How a call is cut, and the words that its segments exchange.
@@ -591,18 +591,22 @@ int64_t segments(int T, const Shape &p) {
 
 // 16 steps a thread, backward of two channels to a lane (bf16) 8: longer segments have
 // fewer words to exchange, until their registers leave too few waves to hide a join
-// (forward 1024 x 16 x 768 bf16 22 us, with 8 steps 24, 32768 x 1 x 768 50 and 75;
-// backward 1000 x 16 x 1024 49 us with 8, with 16 115 or, given the registers, 50).
+// (forward 32768 x 1 x 768 bf16 51 us, with 8 steps 66; backward 1000 x 16 x 1024 49 us with
+// 8, with 16 77).
 // Where 1024 steps or fewer make more than one such segment, a workgroup may take all of
-// them, with nothing to clear and nobody to wait for (device times, wide for narrow or whole):
-// narrow, in rows of a few values, while those are few: forward 1000 x 4 x 1024 bf16 11.6
-// us for 9.1, 700 x 1 x 768 9.1 for 6.1, however 200 x 32 x 1024 13.0 for 15.6; backward,
-// with twice the rows, sooner no longer: 200 x 8 x 1024 bf16 11.5 for 11.3, 300 x 16 x
-// 768 15.6 for 19.3, past 512 steps 700 x 1 x 768 10.0 for 10.8, 1024 x 2 x 768 11.4 for 14.0;
+// them, with nothing to clear and nobody to wait for (times in a graph, wide for narrow or
+// whole):
+// narrow, in rows of a few values, while those are few: forward 1000 x 4 x 1024 bf16 12.1
+// us for 11.0, 700 x 1 x 768 9.7 for 6.8, however 200 x 32 x 1024 14.1 for 19.1; backward,
+// with twice the rows, sooner no longer: 200 x 8 x 1024 float32 12.5 for 10.8, however 300 x
+// 16 x 768 bf16 15.2 for 25.1, past 512 steps 1024 x 2 x 768 11.3 for 16.0.  In a graph the
+// narrow bf16 gradient is behind from about 10^6 values on (200 x 8 x 1024 11.4 for 14.1, 1000
+// x 1 x 1024 10.1 for 13.0), call by call ahead up to the limits (17.6 for 14.4 and 14.1: a
+// launch less for the host).
 // whole, the forward pass of bf16 whose channels stand in fours, in rows of 128 bytes,
-// where all workgroups run at once and on most CUs: 1024 x 16 x 1024 23.8 for 20.6, x 12
-// 21.5 for 18.4, however x 8 14.9 for 16.2, x 20 28.3 for 31.9, and 200 x 32 x 1024, two
-// segments, 13.1 for 14.2.
+// where all workgroups run at once and on most CUs: 1024 x 16 x 1024 25.4 for 21.1, x 12
+// 22.5 for 18.4, however x 8 15.1 for 17.1, x 20 29.7 for 33.2, and 200 x 32 x 1024, two
+// segments, 14.1 for 13.8.
 constexpr int steps(bool bwd, int vec) { return bwd && vec == 2 ? 8 : 16; }
 Shape shape(const GatedDims &d, int vec, bool bwd) {
     const int two = std::min(vec, 2), all = d.T <= kThreads / kNarrow * 16 ? kThreads : kAll;

@@ -14,7 +14,7 @@
 // the strip.  Sums are added in the order of the strips, so nothing depends on which
 // workgroup is last.  A sum is one 64-bit word that says by its value that it is there; an
 // ordered counter in its place would write back and empty the caches of every workgroup
-// (70 us for 58 at 32 x 5 x 128000).
+// (48.1 us for 45.4 at 32 x 5 x 128000 bf16, 22.0 for 20.0 at 8 x 5 x 128000 float32).
 //
 // Weights and sums are 64-bit.  The borders between a vocabulary's V entries lie
 // 1/V of the sum apart on average; a sum of 32-bit terms is off by 1e-7 of it, so
@@ -34,8 +34,8 @@ constexpr int kHead = 128;             // bytes before the parts: the status wor
 constexpr uint64_t kNone = ~0ull;      // no sum yet (no sum is this NaN)
 constexpr double kLog2eD = 1.4426950408889634;
 // Workgroups of a draw launch from which on a row of p is left to one of them: a longer
-// chain, but less work in all (64 x 1 x 128000, 2048 workgroups, 31 us for 36; 16 x 8 x
-// 50001, 208 of them, 17.5 either way).
+// chain, but less work in all (64 x 1 x 128000, 2048 workgroups, 28.9 us for 33.9; 16 x 8 x
+// 50001, 208 of them, 18.4 either way).
 constexpr int kCrowd = 1024;
 constexpr int kAtOnce = 4;             // weights side by side (a lone wave waits for each step otherwise)
 
@@ -44,10 +44,10 @@ constexpr int kAtOnce = 4;             // weights side by side (a lone wave wait
 // with q of degree 7 fitted on Chebyshev nodes of [-1/2, 1/2] by least squares on the
 // relative error, reweighted towards equal ripple (8e-13).  With the conversion and the
 // sum 16 64-bit instructions, whose issue bounds the sums: one takes a wave 5.3 to 5.9
-// cycles.  Sums of 37 million bf16 weights take 31 us, 23 of them the issue of 25 vector
+// cycles.  Sums of 37 million bf16 weights take 32 us, 23 of them the issue of 25 vector
 // instructions a weight.  M at once: the draw launch has about a wave to a SIMD, which one
-// after another would wait for each instruction (1 x 5 x 32000 11.5 us for 10.3, 32 x 5 x
-// 128000 19.5 for 17.5).
+// after another would wait for each instruction (32 x 5 x 128000 47.8 us for 45.4, 16 x 8 x
+// 50001 19.3 for 18.5, 1 x 5 x 32000 17.3 either way).
 template <int M>
 __device__ __forceinline__ void pow2s(double *d, double k, double low) {
     const double big = 6755399441055744.0;  // 1.5 * 2^52: its lowest bits then hold n
@@ -583,8 +583,9 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int
 }
 
 // Values of a thread: 32 where that leaves the first launch sixteen workgroups a CU, for
-// half the fixed work of a chunk (32 x 5 x 128000: 55 us for 58), else 16, which
-// spread a small call further (1 x 5 x 32000: 19 us for 24).
+// half the fixed work of a chunk (32 x 5 x 128000: 45.4 us for 53), else 16, which
+// spread a small call further (16 x 8 x 50001: 18.5 us for 22.2; 1 x 5 x 32000 17 either
+// way; a call of one row a sequence, 64 x 1 x 128000, would be faster with 32, 24.4 for 28.9).
 constexpr int kFew = 16, kMany = 32;
 
 template <typename T, int PER>

@@ -508,7 +508,9 @@ def gated_fwd(f, x, h0=None, *, gate: str = "logit", lens=None, ws=None, out=Non
     h0 [B,D] float32 or None (zeros; states start at a multiple of 16 bytes); lens
     [B] int32: tokens of each row that count (h is 0 behind them).
     Returns (h [T,B,D] in f's type, h_T [B,D] float32, the state behind the last
-    token that counts); `out` is a dict with "h" (any view) and "hT" (may be h0)."""
+    token that counts); `out` is a dict with "h" (any view) and "hT" (may be h0).
+    A wait between segments that runs out (seconds) is noted in the workspace:
+    workspace_status(ws), for a `ws` of workspace_size_gated bytes given here."""
     if x is None:
         raise ValueError("x is required")
     (T, B, D), dt, gt, sf, sx, lp, shape, dev = _gated(f, x, gate, lens)
@@ -550,7 +552,8 @@ def gated_step(f, x, h, *, gate: str = "logit", h_out=None, out=None):
 def gated_bwd(f, x, h, dh, h0=None, dhT=None, *, gate: str = "logit", lens=None, ws=None, out=None):
     """Gradients of sum(dh * h) + sum(dhT * h_T), given gated_fwd's h: dict df, dx
     (in f's type) and dh0 float32.  x may be None with gate "decay"; `out` is a
-    dict with "df", "dx" (any views) and "dh0" (may be dhT)."""
+    dict with "df", "dx" (any views) and "dh0" (may be dhT).  workspace_status(ws)
+    as in gated_fwd."""
     (T, B, D), dt, gt, sf, sx, lp, shape, dev = _gated(f, x, gate, lens)
     if x is None and gt == 0:
         raise ValueError("x is required with gate 'logit'")
@@ -682,7 +685,9 @@ def verify_drafts(logits, drafts, u, draft_logits=None, *, temperature=None, n_d
     [K,B,V] the logits the drafts were drawn from (None: found some other way);
     temperature [B] float32 (0 or less: greedy), n_drafts [B] int32 (None: K).
     Returns (tokens [K+1,B] int32: accepted drafts, the drawn token, then -1;
-    accepted [B] int32); `out` is a dict with "tokens" and "accepted"."""
+    accepted [B] int32); `out` is a dict with "tokens" and "accepted".  A wait
+    that runs out draws -1; workspace_status(ws) says so, for a `ws` of
+    workspace_size_verify bytes given here."""
     dev, shape = logits.device, logits.shape
     dt = _dt(logits, "logits")
     if len(shape) != 3 or 0 in shape:
